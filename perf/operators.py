@@ -407,7 +407,7 @@ def _plain_pages(st):
     want = (j >= a) & (j <= z) & fits & (~held | shared)
     running = want.sum(1).cumsum(0)
     free = torch.nonzero(refs == 0).squeeze(1)
-    served = (running <= free.numel()) & (fits.squeeze(1) | (st["n_new"] <= 0))
+    served = ((running <= free.numel()) | (want.sum(1) == 0)) & (fits.squeeze(1) | (st["n_new"] <= 0))
     want = want & served[:, None]
     give = free[:int(want.sum())]
     was = table[want]
