@@ -457,7 +457,7 @@ def run(st):
                                 k_weight=st["k_weight"], eps=1e-6, interleaved=case["interleaved"])
             return {"q": r["q"], "k": r["k"]}
         if op == "append":
-            sv.cache_append(st["pool"], st["table"], st["start"], st["k"], st["v"], n_new=st["n_new"],
+            sv.cache_append(st["pool"], st["table"], st["start"], st["k"], st["v"], counts=st["n_new"],
                             workspace=st["workspace"])
             r = sv.cache_read(st["pool"], st["table"], st["start"], case["N"], counts=st["n_new"],
                               dtype=st["k"].dtype, workspace=st["workspace"])
