@@ -7,6 +7,9 @@ when not given. There is no CPU path: if the library is missing, importing the c
     verify(target, draft, tokens, seeds, temperature)            standard speculative sampling
     cactus_verify(target, draft, tokens, seeds, delta, temperature)  Cactus constrained acceptance
     counterfactual_gamma(target, drafters, temperature, selected, tokens, seeds)  HedgeSpec gamma
+
+The operators of the scoring step around a verification (head norms and rotation, a paged cache in 4 bits, attention
+over it, its pages) are in cache.py and exported here too.
 """
 from __future__ import annotations
 
@@ -337,3 +340,9 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
                                             _p(out.get("diag")), _p(ws), ws.numel(), _stream(stream)))
     out["workspace"] = ws
     return out
+
+
+# the scoring step's operators (include/speccache.h); imported last, since the module uses the helpers above
+from .cache import (PAGE as CACHE_PAGE, cache_append, cache_attention, cache_read, new_attention_workspace,  # noqa: E402
+                    new_pages_workspace, new_pool, pages_commit, pages_compact, pages_fork, pages_release,
+                    pages_reserve, qk_norm_rope, rope_frequencies)

@@ -9,9 +9,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
-SOURCES = [os.path.join(CSRC, "specverify.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
-    os.path.join(INCLUDE, "specverify.h")]
+CACHE = os.path.join(CSRC, "cache")
+SOURCES = [os.path.join(CSRC, "specverify.cu"), os.path.join(CACHE, "speccache.cu")]
+DEPS = SOURCES + [os.path.join(d, f) for d in (CSRC, CACHE) for f in os.listdir(d) if f.endswith((".cuh", ".h"))] + [
+    os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "speccache.h")]
 
 
 def nvcc_path() -> str:
@@ -32,7 +33,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc_path(), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I" + INCLUDE, "-o", tmp] + SOURCES
+           "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I" + INCLUDE, "-o", tmp] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)

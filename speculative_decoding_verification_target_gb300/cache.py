@@ -1,0 +1,329 @@
+"""Operators of the scoring step around a verification: binding of the C ABI in include/speccache.h.
+
+Argument marshalling only, as for the verification calls. A cache in 4 bits is a pool of pages, uint8
+[pages, Hk, 68 D] (new_pool), a table int32 [sequences, max_pages] of page numbers, lengths int32 [sequences] and
+refs int32 [pages]; the header states the format and every rule. One round of a serving loop:
+
+    pages_reserve(pools, table, lengths, refs, n_new)          room for the last token and K drafts
+    per layer:
+        qk_norm_rope(q, k, positions, freqs, ...)              head norms and rotation
+        cache_append(pool, table, lengths, k, v)               quantised into the pages
+        cache_attention(q, pool, table, lengths + n_new)       the new tokens over the cache
+    verify(logits, ...)                                        accept_len
+    pages_commit(table, lengths, refs, accept_len)             keeps the accepted tokens, frees the rest
+
+and beside it pages_fork (a sequence that shares another's pages), pages_release, pages_compact and cache_read.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+
+import torch
+
+from . import SPEC_OK, SpecError, _need, _p, _stream, load as _load
+
+PAGE, GROUP = 64, 32
+WS_HEADER = 8192
+STATUS_BAD_PAGE, STATUS_BAD_LENGTH, STATUS_NO_PAGES, STATUS_BAD_SLOT = 4, 8, 16, 32
+CACHE_EXPORTS = ("spec_cache_block_bytes", "spec_qk_norm_rope", "spec_cache_append", "spec_cache_read",
+                 "spec_cache_attention_workspace_size", "spec_cache_attention", "spec_pages_workspace_size",
+                 "spec_pages_fork", "spec_pages_reserve", "spec_pages_commit", "spec_pages_release",
+                 "spec_pages_compact", "spec_cache_last_error")
+
+
+class Heads(ctypes.Structure):
+    """spec_heads: [B, N, heads, D] in device memory, element strides over the first three."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_n", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong)]
+
+
+@functools.cache
+def _lib():
+    lib = _load()
+    P, I, F, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
+    H = ctypes.POINTER(Heads)
+    for name, res, args in (
+            ("spec_cache_block_bytes", Z, [I]),
+            ("spec_qk_norm_rope", I, [H, H, I, I, I, I, I, I, P, P, I, I, P, P, F, H, H, P]),
+            ("spec_cache_append", I, [P, I, P, I, P, P, H, H, I, I, I, I, I, P, Z, P]),
+            ("spec_cache_read", I, [P, I, P, I, P, P, H, H, I, I, I, I, I, P, Z, P]),
+            ("spec_cache_attention_workspace_size", Z, [I, I, I, I]),
+            ("spec_cache_attention", I, [H, I, P, I, P, I, P, P, I, I, I, I, I, F, I, I, H, P, P, Z, P]),
+            ("spec_pages_workspace_size", Z, [I, I]),
+            ("spec_pages_fork", I, [P, P, P, I, I, I, P, P, I, P, Z, P]),
+            ("spec_pages_reserve", I, [P, I, L, P, P, P, I, I, I, P, P, P, Z, P]),
+            ("spec_pages_commit", I, [P, P, P, I, I, I, P, I, I, I, P, Z, P]),
+            ("spec_pages_release", I, [P, P, P, I, I, I, P, I, P, Z, P]),
+            ("spec_pages_compact", I, [P, I, L, P, P, I, I, I, P, P, Z, P]),
+            ("spec_cache_last_error", ctypes.c_char_p, [])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = res, args
+    return lib
+
+
+def _ok(code):
+    if code != SPEC_OK:
+        raise SpecError(code, _lib().spec_cache_last_error().decode())
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
+def _code(t, name, fp32=False):
+    code = _DTYPES.get(t.dtype)
+    if code is None or (code == 1 and not fp32):
+        raise TypeError("%s must be bfloat16%s float16%s, got %s" % (name, "," if fp32 else " or",
+                                                                   " or float32" if fp32 else "", t.dtype))
+    return code
+
+
+def _heads(t, name, shape, dtype):
+    """[B, N, heads, D] with any strides but contiguous channels."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    sb, sn, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    return Heads(t.data_ptr(), sb, sn, sh)
+
+
+def _pool(pool, name="pool"):
+    _need(pool, name, torch.uint8)
+    if pool.dim() != 3:
+        raise ValueError("%s must be [pages, Hk, 68 D], got %s" % (name, tuple(pool.shape)))
+    P, H, n = pool.shape
+    if n not in (68 * 64, 68 * 128):
+        raise ValueError("%s's blocks must have 68 D bytes for D = 64 or 128, got %d" % (name, n))
+    return P, H, n // 68
+
+
+def _ints(t, name, shape):
+    _need(t, name, torch.int32, shape)
+
+
+def _table(table):
+    _need(table, "table", torch.int32)
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, max_pages], got %s" % (tuple(table.shape),))
+    return table.shape
+
+
+def new_pool(pages, kv_heads, head_dim, layers=None, device=None):
+    """A pool of free pages: uint8 [pages, Hk, 68 D], or [layers, pages, Hk, 68 D], of which pool[l] is a layer's."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128, got %r" % (head_dim,))
+    shape = (pages, kv_heads, 68 * head_dim)
+    return torch.zeros(shape if layers is None else (layers,) + shape, dtype=torch.uint8, device=device or "cuda")
+
+
+def new_attention_workspace(N, q_heads, kv_heads, head_dim, device=None):
+    """Workspace of cache_attention for up to N new tokens a sequence, ready for its first use."""
+    n = int(_lib().spec_cache_attention_workspace_size(N, q_heads, kv_heads, head_dim))
+    if n == 0:
+        raise ValueError("unsupported sizes N=%d Hq=%d Hk=%d D=%d" % (N, q_heads, kv_heads, head_dim))
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def new_pages_workspace(sequences, pages, device=None):
+    """Workspace of the pages_* calls, cache_append and cache_read, ready for its first use."""
+    n = int(_lib().spec_pages_workspace_size(sequences, pages))
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def rope_frequencies(rotary_dim, theta=10000.0, *, inv_freq=None, device=None):
+    """The rotation's frequencies for qk_norm_rope: each pair's turns a position in 2^-64 of a turn, int64 (the bits of
+    a uint64) [rotary_dim / 2], from theta ** (-2 i / rotary_dim), or from inv_freq (radians a position)."""
+    if inv_freq is None:
+        inv = [theta ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    else:
+        inv = [float(x) for x in inv_freq]
+        if len(inv) != rotary_dim // 2:
+            raise ValueError("inv_freq must have rotary_dim / 2 = %d values, got %d" % (rotary_dim // 2, len(inv)))
+    bits = [int(math.ldexp(math.fmod(x / (2.0 * math.pi), 1.0), 64)) % (1 << 64) for x in inv]
+    return torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64, device=device or "cuda")
+
+
+def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                 k_out=None, stream=None):
+    """Root-mean-square norm of each head of q [B, N, Hq, D] and k [B, N, Hk, D], times a weight [D], and rotation of the
+    first 2 len(freqs) channels by position (int32 [B, N]). bf16, fp16 or fp32. freqs from rope_frequencies, or None
+    for the norm alone. q_out, k_out may be q and k. Returns dict(q, k)."""
+    B, N, Hq, D = q.shape
+    Hk = k.shape[2]
+    dt = q.dtype
+    code = _code(q, "q", True)
+    if q_out is None:
+        q_out = torch.empty((B, N, Hq, D), dtype=dt, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((B, N, Hk, D), dtype=dt, device=q.device)
+    rotary = 0
+    if freqs is not None:
+        _need(freqs, "freqs", torch.int64)
+        _ints(positions, "positions", (B, N))
+        rotary = 2 * freqs.numel()
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, dt, (D,))
+    _ok(_lib().spec_qk_norm_rope(_heads(q, "q", (B, N, Hq, D), dt), _heads(k, "k", (B, N, Hk, D), dt), code, B, N, Hq, Hk,
+                                 D, _p(positions) if rotary else None, _p(freqs) if rotary else None, rotary, interleaved,
+                                 _p(q_weight), _p(k_weight), eps, _heads(q_out, "q_out", (B, N, Hq, D), dt),
+                                 _heads(k_out, "k_out", (B, N, Hk, D), dt), _stream(stream)))
+    return dict(q=q_out, k=k_out)
+
+
+def cache_append(pool, table, start, k, v, *, counts=None, workspace=None, stream=None):
+    """Quantises k and v [B, N, Hk, D] (bf16 or fp16) into pool [pages, Hk, 68 D]: token i of sequence b to position
+    start[b] + i, for i < counts[b] (None: N). Returns the workspace."""
+    P, H, D = _pool(pool)
+    B, M = _table(table)
+    N = k.shape[1]
+    code = _code(k, "k")
+    _ints(start, "start", (B,))
+    if counts is not None:
+        _ints(counts, "counts", (B,))
+    if workspace is None:
+        workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
+    _ok(_lib().spec_cache_append(_p(pool), P, _p(table), M, _p(start), _p(counts), _heads(k, "k", (B, N, H, D), k.dtype),
+                                 _heads(v, "v", (B, N, H, D), k.dtype), code, B, N, H, D, _p(workspace), workspace.numel(),
+                                 _stream(stream)))
+    return workspace
+
+
+def cache_read(pool, table, start, n, *, counts=None, dtype=torch.bfloat16, k=None, v=None, workspace=None, stream=None):
+    """The cached keys and values of positions start[b] .. start[b] + n - 1 as [B, n, Hk, D] in bf16 or fp16, exactly;
+    zeros past counts[b] and where there is no page. Returns dict(k, v, workspace)."""
+    P, H, D = _pool(pool)
+    B, M = _table(table)
+    _ints(start, "start", (B,))
+    if counts is not None:
+        _ints(counts, "counts", (B,))
+    if k is None:
+        k = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+    if v is None:
+        v = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+    code = _code(k, "k")
+    if workspace is None:
+        workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
+    _ok(_lib().spec_cache_read(_p(pool), P, _p(table), M, _p(start), _p(counts), _heads(k, "k", (B, n, H, D), dtype),
+                               _heads(v, "v", (B, n, H, D), dtype), code, B, n, H, D, _p(workspace), workspace.numel(),
+                               _stream(stream)))
+    return dict(k=k, v=v, workspace=workspace)
+
+
+def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0, sinks=0, out=None, lse=None,
+                    want_lse=False, workspace=None, stream=None):
+    """Attention of the newest tokens q [B, N, Hq, D] (bf16 or fp16) over the cache. kv_len [B] counts every cached
+    token, the new ones included; query i of sequence b stands at kv_len[b] - q_len[b] + i (q_len None: N). window > 0
+    limits each query to the window last tokens and the first `sinks`. scale: 1 / sqrt(D) unless given. Returns
+    dict(out, lse, workspace), lse [B, N, Hq] where wanted."""
+    P, H, D = _pool(pool)
+    B, M = _table(table)
+    N, Hq = q.shape[1], q.shape[2]
+    code = _code(q, "q")
+    _ints(kv_len, "kv_len", (B,))
+    if q_len is not None:
+        _ints(q_len, "q_len", (B,))
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _need(lse, "lse", torch.float32, (B, N, Hq))
+    if workspace is None:
+        workspace = new_attention_workspace(N, Hq, H, D, q.device)
+    _ok(_lib().spec_cache_attention(_heads(q, "q", (B, N, Hq, D), q.dtype), code, _p(pool), P, _p(table), M, _p(kv_len),
+                                    _p(q_len), B, N, Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks,
+                                    _heads(out, "out", (B, N, Hq, D), q.dtype), _p(lse), _p(workspace), workspace.numel(),
+                                    _stream(stream)))
+    return dict(out=out, lse=lse, workspace=workspace)
+
+
+def _books(table, lengths, refs):
+    S, M = _table(table)
+    if lengths is not None:
+        _ints(lengths, "lengths", (S,))
+    _need(refs, "refs", torch.int32)
+    return S, M, refs.numel()
+
+
+def _layers(pool, P):
+    """[pages, ...] or [layers, pages, ...] as (layers, bytes of a page)."""
+    _need(pool, "pool", torch.uint8)
+    if pool.dim() not in (3, 4) or pool.shape[-3] != P:
+        raise ValueError("pool must be [%d, Hk, 68 D] or [layers, %d, Hk, 68 D], got %s" % (P, P, tuple(pool.shape)))
+    return (pool.shape[0] if pool.dim() == 4 else 1), pool.shape[-2] * pool.shape[-1]
+
+
+def _pages_ws(workspace, S, P, device):
+    return new_pages_workspace(S, P, device) if workspace is None else workspace
+
+
+def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
+    """Sequence dst[f] becomes a copy of src[f] that shares its pages (int32 [F] each). Returns the workspace."""
+    S, M, P = _books(table, lengths, refs)
+    F = src.numel()
+    _ints(src, "src", (F,))
+    _ints(dst, "dst", (F,))
+    ws = _pages_ws(workspace, S, P, table.device)
+    _ok(_lib().spec_pages_fork(_p(table), _p(lengths), _p(refs), S, M, P, _p(src), _p(dst), F, _p(ws), ws.numel(),
+                               _stream(stream)))
+    return ws
+
+
+def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=None, stream=None):
+    """Pages of its own for each sequence's next n_new[s] tokens; a shared part-filled page is copied in every layer of
+    pool. Returns served, int32 [sequences]: 0 where there was no room."""
+    S, M, P = _books(table, lengths, refs)
+    layers, page_bytes = _layers(pool, P)
+    _ints(n_new, "n_new", (S,))
+    if served is None:
+        served = torch.empty(S, dtype=torch.int32, device=table.device)
+    else:
+        _ints(served, "served", (S,))
+    ws = _pages_ws(workspace, S, P, table.device)
+    _ok(_lib().spec_pages_reserve(_p(pool), layers, page_bytes, _p(table), _p(lengths), _p(refs), S, M, P, _p(n_new),
+                                  _p(served), _p(ws), ws.numel(), _stream(stream)))
+    return served
+
+
+def pages_commit(table, lengths, refs, advance, *, extra=1, window=0, sinks=0, workspace=None, stream=None):
+    """lengths += advance + extra (a verification's accept_len and the token before the drafts); pages past the new
+    lengths, or with window > 0 out of every later query's view, are let go. Returns the workspace."""
+    S, M, P = _books(table, lengths, refs)
+    _ints(advance, "advance", (S,))
+    ws = _pages_ws(workspace, S, P, table.device)
+    _ok(_lib().spec_pages_commit(_p(table), _p(lengths), _p(refs), S, M, P, _p(advance), extra, window, sinks, _p(ws),
+                                 ws.numel(), _stream(stream)))
+    return ws
+
+
+def pages_release(table, lengths, refs, slots, *, workspace=None, stream=None):
+    """Lets go of every page of the sequences slots (int32 [F]). Returns the workspace."""
+    S, M, P = _books(table, lengths, refs)
+    F = slots.numel()
+    _ints(slots, "slots", (F,))
+    ws = _pages_ws(workspace, S, P, table.device)
+    _ok(_lib().spec_pages_release(_p(table), _p(lengths), _p(refs), S, M, P, _p(slots), F, _p(ws), ws.numel(),
+                                  _stream(stream)))
+    return ws
+
+
+def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
+    """Moves the pages in use to the front of the pool, in every layer; table and refs follow. Returns used, int32 [1]:
+    how many there are."""
+    S, M, P = _books(table, None, refs)
+    layers, page_bytes = _layers(pool, P)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=table.device)
+    else:
+        _ints(used, "used", (1,))
+    ws = _pages_ws(workspace, S, P, table.device)
+    _ok(_lib().spec_pages_compact(_p(pool), layers, page_bytes, _p(table), _p(refs), S, M, P, _p(used), _p(ws), ws.numel(),
+                                  _stream(stream)))
+    return used

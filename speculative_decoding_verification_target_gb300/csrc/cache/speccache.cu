@@ -1,0 +1,406 @@
+// Host side of the C ABI declared in include/speccache.h: argument checks and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "speccache.h"
+#include "append.cuh"
+#include "attention.cuh"
+#include "norm_rope.cuh"
+#include "pages.cuh"
+
+namespace specc {
+namespace {
+
+thread_local char g_err[512] = "";
+
+spec_status fail(spec_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+spec_status launched(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
+}
+
+constexpr int MAX_B = 65535, MAX_TOKENS = 1 << 20, MAX_HEADS = 1024, MAX_Q = 1024, MAX_PAIRS = 4096;
+
+size_t elem_bytes(int dtype) { return dtype == SPEC_FP32 ? 4 : 2; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A [B, N, heads, D] argument: present, and every row 16-byte aligned.
+spec_status check_heads(const spec_heads* t, const char* name, int dtype) {
+    if (!t || !t->data) return fail(SPEC_ERR_INVALID, "%s must not be NULL", name);
+    const long long per = 16 / static_cast<long long>(elem_bytes(dtype));
+    if (!aligned16(t->data) || t->stride_b % per || t->stride_n % per || t->stride_h % per)
+        return fail(SPEC_ERR_INVALID, "%s: the pointer and every stride must be a multiple of 16 bytes", name);
+    return SPEC_OK;
+}
+
+spec_status check_sizes(int B, int N, int heads, int max_n) {
+    if (B < 0 || B > MAX_B) return fail(SPEC_ERR_INVALID, "B must be in [0, %d], got %d", MAX_B, B);
+    if (N < 0 || N > max_n) return fail(SPEC_ERR_INVALID, "N must be in [0, %d], got %d", max_n, N);
+    if (heads < 1 || heads > MAX_HEADS) return fail(SPEC_ERR_INVALID, "heads must be in [1, %d], got %d", MAX_HEADS, heads);
+    return SPEC_OK;
+}
+
+spec_status check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (!ws || !aligned16(ws)) return fail(SPEC_ERR_INVALID, "workspace must be 16-byte aligned device memory");
+    if (bytes < need) return fail(SPEC_ERR_INVALID, "workspace has %zu bytes, %zu needed", bytes, need);
+    return SPEC_OK;
+}
+
+spec_status check_cache_dim(int D) {
+    return D == 64 || D == 128 ? SPEC_OK : fail(SPEC_ERR_UNSUPPORTED, "D must be 64 or 128, got %d", D);
+}
+
+spec_status check_half_type(int dtype) {
+    return dtype == SPEC_BF16 || dtype == SPEC_FP16 ? SPEC_OK
+                                                    : fail(SPEC_ERR_UNSUPPORTED, "dtype must be bf16 or fp16, got %d", dtype);
+}
+
+spec_status check_table(const void* pool, int pages, const void* table, int max_pages) {
+    if (!pool || !aligned16(pool)) return fail(SPEC_ERR_INVALID, "pool must be 16-byte aligned device memory");
+    if (!table) return fail(SPEC_ERR_INVALID, "table must not be NULL");
+    if (pages < 1 || max_pages < 1) return fail(SPEC_ERR_INVALID, "pages and max_pages must be at least 1");
+    if (static_cast<long long>(max_pages) * PAGE > 2147483647LL)
+        return fail(SPEC_ERR_INVALID, "max_pages is limited to %d", 2147483647 / PAGE);
+    return SPEC_OK;
+}
+
+Heads heads_of(const spec_heads* t) { return {t->data, t->stride_b, t->stride_n, t->stride_h}; }
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+#define SPECC_TRY(expr)                        \
+    do {                                       \
+        const spec_status try_s = (expr);      \
+        if (try_s != SPEC_OK) return try_s;    \
+    } while (0)
+
+// ------------------------------------------------------------------------------------------------ tokens
+spec_status check_tokens(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start, int dtype,
+                         int B, int N, int Hk, int D, void* ws, size_t ws_bytes) {
+    SPECC_TRY(check_half_type(dtype));
+    SPECC_TRY(check_cache_dim(D));
+    SPECC_TRY(check_sizes(B, N, Hk, MAX_TOKENS));
+    if (B == 0 || N == 0) return SPEC_OK;
+    SPECC_TRY(check_table(pool, pages, table, max_pages));
+    if (!start) return fail(SPEC_ERR_INVALID, "start must not be NULL");
+    return check_workspace(ws, ws_bytes, SPEC_CACHE_WS_HEADER);
+}
+
+TokensParams tokens_params(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start,
+                           const int32_t* counts, const spec_heads* k, const spec_heads* v, int B, int N, int Hk, void* ws) {
+    TokensParams p = {};
+    p.pool = static_cast<unsigned char*>(const_cast<void*>(pool));
+    p.table = table;
+    p.start = start;
+    p.counts = counts;
+    if (k) p.k = heads_of(k);
+    if (v) p.v = heads_of(v);
+    p.pages = pages;
+    p.max_pages = max_pages;
+    p.B = B;
+    p.N = N;
+    p.Hk = Hk;
+    p.status = static_cast<unsigned*>(ws);
+    return p;
+}
+
+// ------------------------------------------------------------------------------------------------- pages
+size_t pages_scratch_ints(int S, int pages) { return 3 * static_cast<size_t>(S) + 3 * static_cast<size_t>(pages) + 16; }
+
+spec_status check_pages(const void* table, const void* refs, int S, int max_pages, int pages, void* ws, size_t ws_bytes,
+                        size_t need) {
+    if (S < 0 || S > (1 << 20)) return fail(SPEC_ERR_INVALID, "S must be in [0, %d], got %d", 1 << 20, S);
+    if (S == 0) return SPEC_OK;
+    if (!table || !refs) return fail(SPEC_ERR_INVALID, "table and refs must not be NULL");
+    if (pages < 1 || max_pages < 1) return fail(SPEC_ERR_INVALID, "pages and max_pages must be at least 1");
+    if (static_cast<long long>(max_pages) * PAGE > 2147483647LL)
+        return fail(SPEC_ERR_INVALID, "max_pages is limited to %d", 2147483647 / PAGE);
+    return check_workspace(ws, ws_bytes, need);
+}
+
+spec_status check_pool(const void* pool, int layers, long long page_bytes) {
+    if (!pool || !aligned16(pool)) return fail(SPEC_ERR_INVALID, "pool must be 16-byte aligned device memory");
+    if (layers < 1 || page_bytes < 16 || page_bytes % 16)
+        return fail(SPEC_ERR_INVALID, "layers must be at least 1 and page_bytes a positive multiple of 16");
+    return SPEC_OK;
+}
+
+PagesParams pages_params(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages, void* ws) {
+    PagesParams p = {};
+    p.table = table;
+    p.lengths = lengths;
+    p.refs = refs;
+    p.S = S;
+    p.M = max_pages;
+    p.P = pages;
+    p.status = static_cast<unsigned*>(ws);
+    p.scratch = reinterpret_cast<int*>(static_cast<unsigned char*>(ws) + SPEC_CACHE_WS_HEADER);
+    return p;
+}
+
+}  // namespace
+}  // namespace specc
+
+using namespace specc;
+
+extern "C" {
+
+const char* spec_cache_last_error(void) { return g_err; }
+
+size_t spec_cache_block_bytes(int D) { return D == 64 || D == 128 ? static_cast<size_t>(68) * D : 0; }
+
+spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtype, int B, int N, int Hq, int Hk, int D,
+                              const int32_t* positions, const uint64_t* freqs, int rotary, int interleaved,
+                              const void* q_weight, const void* k_weight, float eps, const spec_heads* q_out,
+                              const spec_heads* k_out, void* stream) {
+    if (dtype != SPEC_BF16 && dtype != SPEC_FP16 && dtype != SPEC_FP32)
+        return fail(SPEC_ERR_UNSUPPORTED, "dtype must be bf16, fp16 or fp32, got %d", dtype);
+    if (D != 64 && D != 128 && D != 256) return fail(SPEC_ERR_UNSUPPORTED, "D must be 64, 128 or 256, got %d", D);
+    if (Hq < 0 || Hk < 0) return fail(SPEC_ERR_INVALID, "Hq and Hk must not be negative");
+    SPECC_TRY(check_sizes(B, N, Hq + Hk, MAX_TOKENS));
+    if (rotary < 0 || rotary > D || rotary % 16) return fail(SPEC_ERR_INVALID, "rotary must be a multiple of 16 in [0, D], got %d", rotary);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPEC_ERR_INVALID, "eps must be finite and not negative");
+    if (B == 0 || N == 0) return SPEC_OK;
+    if (Hq > 0) {
+        SPECC_TRY(check_heads(q, "q", dtype));
+        SPECC_TRY(check_heads(q_out, "q_out", dtype));
+    }
+    if (Hk > 0) {
+        SPECC_TRY(check_heads(k, "k", dtype));
+        SPECC_TRY(check_heads(k_out, "k_out", dtype));
+    }
+    if (rotary && (!positions || !freqs)) return fail(SPEC_ERR_INVALID, "positions and freqs must not be NULL");
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(SPEC_ERR_INVALID, "weights must be 16-byte aligned");
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    NormParams p = {};
+    if (Hq > 0) p.q = heads_of(q), p.qo = heads_of(q_out);
+    if (Hk > 0) p.k = heads_of(k), p.ko = heads_of(k_out);
+    p.positions = positions;
+    p.freqs = reinterpret_cast<const unsigned long long*>(freqs);
+    p.qw = q_weight;
+    p.kw = k_weight;
+    p.tokens = static_cast<long long>(B) * N;
+    p.N = N;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.rotary = rotary;
+    p.interleaved = interleaved != 0;
+    p.eps = eps;
+    // few tokens: a token's heads are split over warps until the card has 32 warps an SM
+    const int rpw = 256 / D;
+    p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>((Hq + Hk + rpw - 1) / rpw, 32LL * sms / p.tokens)));
+    const long long units = p.tokens * p.parts, ctas = (units + NORM_WARPS - 1) / NORM_WARPS;
+    if (ctas > 2147483647LL) return fail(SPEC_ERR_INVALID, "too many tokens: B N is limited to 2^31");
+    using Fn = void (*)(const NormParams);
+    static const Fn fns[3][3] = {
+        {norm_rope_kernel<__nv_bfloat16, 64>, norm_rope_kernel<__nv_bfloat16, 128>, norm_rope_kernel<__nv_bfloat16, 256>},
+        {norm_rope_kernel<float, 64>, norm_rope_kernel<float, 128>, norm_rope_kernel<float, 256>},
+        {norm_rope_kernel<__half, 64>, norm_rope_kernel<__half, 128>, norm_rope_kernel<__half, 256>}};
+    fns[dtype][D == 64 ? 0 : D == 128 ? 1 : 2]<<<static_cast<unsigned>(ctas), NORM_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("norm and rotation");
+}
+
+spec_status spec_cache_append(void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start,
+                              const int32_t* counts, const spec_heads* k, const spec_heads* v, int dtype, int B, int N, int Hk,
+                              int D, void* workspace, size_t workspace_bytes, void* stream) {
+    SPECC_TRY(check_tokens(pool, pages, table, max_pages, start, dtype, B, N, Hk, D, workspace, workspace_bytes));
+    if (B == 0 || N == 0) return SPEC_OK;
+    SPECC_TRY(check_heads(k, "k", dtype));
+    SPECC_TRY(check_heads(v, "v", dtype));
+    const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, k, v, B, N, Hk, workspace);
+    const dim3 grid(Hk, (N + PAGE - 2) / PAGE + 1, B);   // a run of N tokens touches at most that many pages
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == SPEC_BF16) {
+        if (D == 64) append_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
+        else append_kernel<__nv_bfloat16, 128><<<grid, TOK_THREADS, 0, st>>>(p);
+    } else {
+        if (D == 64) append_kernel<__half, 64><<<grid, TOK_THREADS, 0, st>>>(p);
+        else append_kernel<__half, 128><<<grid, TOK_THREADS, 0, st>>>(p);
+    }
+    return launched("append");
+}
+
+spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start,
+                            const int32_t* counts, const spec_heads* k_out, const spec_heads* v_out, int dtype, int B, int N,
+                            int Hk, int D, void* workspace, size_t workspace_bytes, void* stream) {
+    SPECC_TRY(check_tokens(pool, pages, table, max_pages, start, dtype, B, N, Hk, D, workspace, workspace_bytes));
+    if (B == 0 || N == 0) return SPEC_OK;
+    const bool has_k = k_out && k_out->data, has_v = v_out && v_out->data;
+    if (has_k) SPECC_TRY(check_heads(k_out, "k_out", dtype));
+    if (has_v) SPECC_TRY(check_heads(v_out, "v_out", dtype));
+    if (!has_k && !has_v) return fail(SPEC_ERR_INVALID, "k_out and v_out must not both be NULL");
+    const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, has_k ? k_out : nullptr,
+                                         has_v ? v_out : nullptr, B, N, Hk, workspace);
+    const dim3 grid(Hk, (N + PAGE - 2) / PAGE + 1, B);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == SPEC_BF16) {
+        if (D == 64) read_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
+        else read_kernel<__nv_bfloat16, 128><<<grid, TOK_THREADS, 0, st>>>(p);
+    } else {
+        if (D == 64) read_kernel<__half, 64><<<grid, TOK_THREADS, 0, st>>>(p);
+        else read_kernel<__half, 128><<<grid, TOK_THREADS, 0, st>>>(p);
+    }
+    return launched("read");
+}
+
+size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
+    if (N < 1 || N > MAX_Q || Hk < 1 || Hq < Hk || Hq > MAX_HEADS || Hq % Hk || (D != 64 && D != 128)) return 0;
+    return SPEC_CACHE_WS_HEADER;
+}
+
+spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
+                                 int max_pages, const int32_t* kv_len, const int32_t* q_len, int B, int N, int Hq, int Hk,
+                                 int D, float scale, int window, int sinks, const spec_heads* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    SPECC_TRY(check_half_type(dtype));
+    SPECC_TRY(check_cache_dim(D));
+    SPECC_TRY(check_sizes(B, N, Hq, MAX_Q));
+    if (Hk < 1 || Hq % Hk) return fail(SPEC_ERR_INVALID, "Hq must be a multiple of Hk, got %d and %d", Hq, Hk);
+    if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID, "scale must be finite");
+    if (window < 0 || sinks < 0) return fail(SPEC_ERR_INVALID, "window and sinks must not be negative");
+    if (B == 0 || N == 0) return SPEC_OK;
+    SPECC_TRY(check_heads(q, "q", dtype));
+    SPECC_TRY(check_heads(out, "out", dtype));
+    SPECC_TRY(check_table(pool, pages, table, max_pages));
+    if (!kv_len) return fail(SPEC_ERR_INVALID, "kv_len must not be NULL");
+    SPECC_TRY(check_workspace(workspace, workspace_bytes, spec_cache_attention_workspace_size(N, Hq, Hk, D)));
+    AttnParams p = {};
+    p.q = heads_of(q);
+    p.out = heads_of(out);
+    p.pool = static_cast<const unsigned char*>(pool);
+    p.table = table;
+    p.kv_len = kv_len;
+    p.q_len = q_len;
+    p.lse = lse;
+    p.status = static_cast<unsigned*>(workspace);
+    p.pages = pages;
+    p.max_pages = max_pages;
+    p.B = B;
+    p.N = N;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    const long long ctas = (static_cast<long long>(B) * N * Hq + 3) / 4;
+    if (ctas > 2147483647LL) return fail(SPEC_ERR_INVALID, "B N Hq is limited to 2^33");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned g = static_cast<unsigned>(ctas);
+    if (dtype == SPEC_BF16) {
+        if (D == 64) attention_kernel<__nv_bfloat16, 64><<<g, 128, 0, st>>>(p);
+        else attention_kernel<__nv_bfloat16, 128><<<g, 128, 0, st>>>(p);
+    } else {
+        if (D == 64) attention_kernel<__half, 64><<<g, 128, 0, st>>>(p);
+        else attention_kernel<__half, 128><<<g, 128, 0, st>>>(p);
+    }
+    return launched("attention");
+}
+
+size_t spec_pages_workspace_size(int S, int pages) {
+    if (S < 0 || pages < 0) return 0;
+    return SPEC_CACHE_WS_HEADER + (pages_scratch_ints(S, pages) * sizeof(int) + 15) / 16 * 16;
+}
+
+spec_status spec_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
+                            const int32_t* src, const int32_t* dst, int F, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    if (F < 0 || F > MAX_PAIRS) return fail(SPEC_ERR_INVALID, "F must be in [0, %d], got %d", MAX_PAIRS, F);
+    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, SPEC_CACHE_WS_HEADER));
+    if (F == 0 || S == 0) return SPEC_OK;
+    if (!lengths || !src || !dst) return fail(SPEC_ERR_INVALID, "lengths, src and dst must not be NULL");
+    PagesParams p = pages_params(table, lengths, refs, S, max_pages, pages, workspace);
+    p.a = src;
+    p.b = dst;
+    p.n = F;
+    fork_kernel<<<F, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("fork");
+}
+
+spec_status spec_pages_reserve(void* pool, int layers, long long page_bytes, int32_t* table, const int32_t* lengths,
+                               int32_t* refs, int S, int max_pages, int pages, const int32_t* n_new, int32_t* served,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, spec_pages_workspace_size(S, pages)));
+    if (S == 0) return SPEC_OK;
+    SPECC_TRY(check_pool(pool, layers, page_bytes));
+    if (!lengths || !n_new) return fail(SPEC_ERR_INVALID, "lengths and n_new must not be NULL");
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    PagesParams p = pages_params(table, const_cast<int32_t*>(lengths), refs, S, max_pages, pages, workspace);
+    p.pool = static_cast<unsigned char*>(pool);
+    p.layers = layers;
+    p.page_bytes = page_bytes;
+    p.a = n_new;
+    p.out = served;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    reserve_kernel<<<PG_CLUSTER, PG_THREADS, 0, st>>>(p);
+    SPECC_TRY(launched("reserve"));
+    reserve_copy_kernel<<<4 * sms, COPY_THREADS, 0, st>>>(p);
+    return launched("reserve's copies");
+}
+
+spec_status spec_pages_commit(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
+                              const int32_t* advance, int extra, int window, int sinks, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, SPEC_CACHE_WS_HEADER));
+    if (window < 0 || sinks < 0) return fail(SPEC_ERR_INVALID, "window and sinks must not be negative");
+    if (S == 0) return SPEC_OK;
+    if (!lengths || !advance) return fail(SPEC_ERR_INVALID, "lengths and advance must not be NULL");
+    PagesParams p = pages_params(table, lengths, refs, S, max_pages, pages, workspace);
+    p.a = advance;
+    p.extra = extra;
+    p.window = window;
+    p.sinks = sinks;
+    commit_kernel<<<S, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("commit");
+}
+
+spec_status spec_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
+                               const int32_t* slots, int F, void* workspace, size_t workspace_bytes, void* stream) {
+    if (F < 0 || F > (1 << 20)) return fail(SPEC_ERR_INVALID, "F must be in [0, %d], got %d", 1 << 20, F);
+    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, SPEC_CACHE_WS_HEADER));
+    if (F == 0 || S == 0) return SPEC_OK;
+    if (!lengths || !slots) return fail(SPEC_ERR_INVALID, "lengths and slots must not be NULL");
+    PagesParams p = pages_params(table, lengths, refs, S, max_pages, pages, workspace);
+    p.a = slots;
+    p.n = F;
+    release_kernel<<<F, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("release");
+}
+
+spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int32_t* table, int32_t* refs, int S,
+                               int max_pages, int pages, int32_t* used, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, spec_pages_workspace_size(S, pages)));
+    if (S == 0) return SPEC_OK;
+    SPECC_TRY(check_pool(pool, layers, page_bytes));
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    PagesParams p = pages_params(table, nullptr, refs, S, max_pages, pages, workspace);
+    p.pool = static_cast<unsigned char*>(pool);
+    p.layers = layers;
+    p.page_bytes = page_bytes;
+    p.out = used;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    compact_plan_kernel<<<PG_CLUSTER, PG_THREADS, 0, st>>>(p);
+    SPECC_TRY(launched("compact's plan"));
+    compact_move_kernel<<<8 * sms, COPY_THREADS, 0, st>>>(p);
+    return launched("compact");
+}
+
+}  // extern "C"
