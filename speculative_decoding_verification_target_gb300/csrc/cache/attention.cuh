@@ -1,8 +1,41 @@
 // Attention of the newest tokens over the 4-bit cache.
+//
+// For a sequence, a key head and up to NC of the queries that read it (the query heads of the group times the new
+// tokens), with keys k_t = c_t s_t and values likewise:
+//   S[t, n] = k_t . q_n,  p[t, n] = 2^(S c_n - m_n),  O[d, n] = sum_t v[t, d] p[t, n],  l_n = sum_t p[t, n],  out = O / l.
+// Both products run on the 5th-generation tensor cores with the CACHE as the M side: M = 128 tokens for S, M = 128
+// channels for O, N = NC queries. So the cost of a tile grows with the queries there are (NC = 16, 32 or 64) and
+// not with a padded block of them. The M operand comes from tensor memory, which is what makes 4 bits cheap: a thread is
+// a lane of it, turns its own token's (or channel's) codes into halves in registers and stores them there. Neither
+// operand's 16-bit form passes through shared memory; that would take three times the bandwidth of the
+// codes themselves, more than shared memory has at the rate HBM delivers them.
+//   - Codes to halves: 0x5400 | c << 4 is the half 64 + c, and one fused multiply-add with (s, -72 s) gives (c - 8) s
+//     exactly: s has four significant bits, so 72 s and the result are halves. 1.4 instructions a code.
+//   - Key codes lie so that a token's 16 bytes of a group are one conflict-free load; the order of channels that
+//     falls out, 0 4 1 5 2 6 3 7 in each eight, is given to the queries as well. Value bytes hold channels r and r + D / 2
+//     of one token, so that a token can be appended without touching its neighbours' bytes; lanes of the lower
+//     and the upper half read the same bytes. Their tokens fall out in the order 0 2 1 3 in each four, which the
+//     probabilities' rows follow. A lane's scales change from token to token but are the same for the 32 channels of a
+//     warp: a table of (s, -72 s) pairs, rebuilt per tile, is read as broadcasts. Tokens that hold nothing have s = 0 there,
+//     so that whatever bits they have cannot reach O (0 times a NaN would).
+//   - The softmax works on S^T: a thread has one token and all queries. m_n is not the maximum but a reference that
+//     any value near it may serve as: it is moved, and O and l rescaled, only where a score exceeds it by more than 2^8,
+//     which the barrier before the second product detects at no cost. l_n is kept per thread and added up at the end.
+// A tile is 128 tokens, two pages, fetched as one bulk copy each two tiles ahead. CTAs are small (128 threads, four to an
+// SM; for NC = 64 256 threads, two to an SM), and hide each other's waits.
+// Work is split evenly whatever the lengths: the tiles of all (sequence, key head, query block) units form one line,
+// of which each CTA takes an equal run. A unit that is cut leaves partial (O, m, l) in the workspace, and a second kernel
+// joins them in a fixed order.
 #pragma once
 #include "cache_format.cuh"
+#include "tmem.cuh"
 
 namespace specc {
+
+constexpr int ATT_MAX_CTAS = 640;
+constexpr uint64_t ATT_WAIT_NS = 2000000000ull;
+constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
+constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
 
 struct AttnParams {
     Heads q, out;
@@ -11,59 +44,580 @@ struct AttnParams {
     const int *kv_len, *q_len;
     float* lse;
     unsigned* status;
-    int pages, max_pages, B, N, Hq, Hk, window, sinks;
+    int4* desc;              // per CTA: the cut unit that starts in it: sequence, head RB + block, parts (0: none)
+    float2* part_ml;         // [2 CTAs][NC] (reference, sum)
+    float* part_o;           // [2 CTAs][NC][D]
+    int pages, max_pages, B, N, Hq, Hk, G, window, sinks;
+    int RB, rpb;             // query blocks and rows of each
     float scale;             // times log2 e
 };
 
-// One warp to a query row: a pass over the visible tokens with the running maximum and sum of the softmax.
-template <class T, int D>
-__global__ void __launch_bounds__(128) attention_kernel(const __grid_constant__ AttnParams p) {
+template <int D, int NC>
+struct Att {
+    static constexpr int WG = NC > 32 ? 2 : 1, TH = 128 * WG, CTAS = WG == 1 ? 4 : 2;
+    static constexpr int NW = NC / WG;                    // queries of a thread
+    static constexpr int TILE = 2 * Block<D>::BYTES;
+    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : 2;
+    static constexpr int P = STAGES * TILE;               // byte offsets in dynamic shared memory
+    static constexpr int Q = P + 128 * NC * 2;
+    static constexpr int VS = Q + NC * D * 2;
+    static constexpr int END = VS + 32 * Block<D>::NG * 16;
+    // no more CTAs on an SM than its tensor memory has columns for: a further one would wait for one to end
+    static constexpr int FLOOR = WG == 1 ? 47104 : 78848;
+    static constexpr int SMEM = END > FLOOR ? END : FLOOR;
+    static constexpr int COLS = WG == 1 ? 128 : 256;      // tensor memory: operand, S, O
+    static constexpr int COL_S = 64, COL_O = 64 + NC;
+};
+
+// A sequence's visible pages: [0, a) and [w0, ...), np in all, two to a tile.
+struct Seq {
+    int len, ql, a, w0, np, T;
+};
+__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b, bool report) {
+    Seq s;
+    s.ql = p.q_len ? p.q_len[b] : p.N;
+    s.len = p.kv_len[b];
+    const int room = p.max_pages * PAGE;
+    if (report && (s.ql < 0 || s.ql > p.N || s.len < 0 || s.len > room)) atomicOr(p.status, SPEC_STATUS_BAD_LENGTH);
+    s.ql = min(max(s.ql, 0), p.N);
+    s.len = min(max(s.len, 0), room);
+    s.a = s.w0 = 0;
+    if (p.window > 0) {
+        const long long first = static_cast<long long>(s.len) - s.ql - p.window + 1;
+        s.w0 = first > 0 ? static_cast<int>(first / PAGE) : 0;
+        s.a = min(static_cast<int>((static_cast<long long>(p.sinks) + PAGE - 1) / PAGE), s.w0);
+    }
+    s.np = s.ql > 0 ? s.a + (s.len + PAGE - 1) / PAGE - s.w0 : 0;
+    s.T = max(1, (s.np + 1) / 2);        // one empty tile for a unit that sees nothing: it writes its zeros
+    return s;
+}
+
+// A place in the line of tiles.
+struct Cursor {
+    int b, h, rb, t;
+    Seq s;
+    __device__ void next(const AttnParams& p) {
+        if (++t < s.T) return;
+        t = 0;
+        if (++rb < p.RB) return;
+        rb = 0;
+        if (++h < p.Hk) return;
+        h = 0;
+        if (++b < p.B) s = load_seq(p, b, false);
+    }
+    __device__ int page_index(int i) const {      // of the tile's page i, or -1
+        const int v = 2 * t + i;
+        return v >= s.np ? -1 : v < s.a ? v : s.w0 + v - s.a;
+    }
+};
+
+// Sums (or maxima) of v[0 .. W) over the warp's lanes: lane i ends with that of column i mod W. Halving exchanges: 31
+// shuffles for 32 columns.
+template <int W, class Op>
+__device__ __forceinline__ float fold_columns(float (&v)[W], int lane, Op op) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+            const bool up = lane & o;
+            const float keep = up ? v[k + o] : v[k], send = up ? v[k] : v[k + o];
+            v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    }
+#pragma unroll
+    for (int o = W; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return v[0];
+}
+
+__device__ __forceinline__ uint32_t half_code(uint32_t x, __half2 s, __half2 o) {
+    const uint32_t h = (x & 0x00F000F0u) | 0x54005400u;
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&h), s, o);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Whether a query saw any token, from its reference and sum: a NaN among its scores never becomes the reference.
+__device__ __forceinline__ bool has_seen(float m, float sum) { return m > ATT_NONE || sum != sum; }
+
+template <class T, int D, int NC>
+__global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
+    attention_kernel(const __grid_constant__ AttnParams p) {
+    using C = Att<D, NC>;
     using BL = Block<D>;
+    constexpr int TH = C::TH, WG = C::WG, NW = C::NW, NG = BL::NG;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t s_full[C::STAGES];
+    __shared__ __align__(8) uint64_t s_bar_s, s_bar_o;
+    __shared__ uint32_t s_tmem;
+    __shared__ __align__(8) int2 s_pos[C::STAGES];       // first position of the tile's two pages, -1 where there is none
+    __shared__ __align__(16) float2 s_cm[NC];            // c_n, m_n
+    __shared__ float s_fac[NC], s_red[4][NC], s_sum[NC];
+    __shared__ long long s_off[NC];                      // output row offset, -1: no such row
+    __shared__ int s_lse[NC];                            // lse index within the sequence, -1: a row past q_len
+    __shared__ long long s_scan[TH / 32 + 1];
+    __shared__ long long s_start;
+    __shared__ int s_b;
+    struct Ahead {               // thread 0's own: the next tile to copy, its pages' places and numbers, tiles issued
+        Cursor c;
+        int j0, j1, e0, e1, issued;
+    };
+    __shared__ Ahead s_next;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, wq = warp & 3;
+    const int tok = wq * 32 + lane;                      // this thread's lane of tensor memory
+    const uint32_t sm = specv::smem_addr(smem);
+
+    // ---- the CTA's run of tiles
+    long long mine = 0;
+    for (int b = tid; b < p.B; b += TH) mine += load_seq(p, b, blockIdx.x == 0).T;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_scan[warp] = mine;
+    if (warp == 0) tmem_alloc(&s_tmem, C::COLS);
+    if (tid == 0) {
+        for (int i = 0; i < C::STAGES; ++i) specv::mbar_init(&s_full[i], 1);
+        specv::mbar_init(&s_bar_s, 1);
+        specv::mbar_init(&s_bar_o, 1);
+        specv::fence_mbarrier_init_cluster();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tbase = s_tmem, lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const long long per_t = static_cast<long long>(p.Hk) * p.RB;
+    long long total = 0;
+    for (int w = 0; w < TH / 32; ++w) total += s_scan[w];
+    total *= per_t;
+    const long long A = min(static_cast<long long>(gridDim.x), total);     // CTAs with work
+    const long long g = blockIdx.x;
+    const long long lo = g < A ? g * total / A : 0, hi = g < A ? (g + 1) * total / A : 0;
+    if (lo < hi) {
+        // the sequence that holds tile lo: running sums over chunks of TH sequences
+        long long before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += TH) {
+            const int b = b0 + tid;
+            const long long c = b < p.B ? load_seq(p, b, false).T * per_t : 0;
+            long long x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[warp] = x;
+            __syncthreads();
+            long long end = before + x;
+            for (int w = 0; w < TH / 32; ++w) {
+                if (w < warp) end += s_scan[w];
+                before += s_scan[w];
+            }
+            if (c && lo < end && lo >= end - c) {
+                s_b = b;
+                s_start = end - c;
+            }
+            if (lo < before) break;      // the same for every thread
+        }
+    }
+    __syncthreads();
+
+    Cursor cur = {};
+    if (lo < hi) {
+        cur.b = s_b;
+        cur.s = load_seq(p, cur.b, false);
+        const long long rem = lo - s_start;
+        const int unit = static_cast<int>(rem / cur.s.T);
+        cur.t = static_cast<int>(rem - static_cast<long long>(unit) * cur.s.T);
+        cur.h = unit / p.RB;
+        cur.rb = unit - cur.h * p.RB;
+    }
+
+    const int tiles = static_cast<int>(hi - lo);
+
+    // ---- the copies (thread 0): tile k of the run into slot k mod STAGES. Page numbers are read one tile before they
+    // are needed.
+    auto look = [&] {
+        s_next.j0 = s_next.c.page_index(0);
+        s_next.j1 = s_next.c.page_index(1);
+        const int* const row = p.table + static_cast<size_t>(s_next.c.b) * p.max_pages;
+        s_next.e0 = s_next.j0 >= 0 ? row[s_next.j0] : -1;
+        s_next.e1 = s_next.j1 >= 0 ? row[s_next.j1] : -1;
+    };
+    auto issue = [&] {
+        const int st = s_next.issued % C::STAGES, j0 = s_next.j0, j1 = s_next.j1, e0 = s_next.e0, e1 = s_next.e1;
+        const bool v0 = e0 >= 0 && e0 < p.pages, v1 = e1 >= 0 && e1 < p.pages;
+        const uint64_t policy = p.RB == 1 ? specv::policy_evict_first() : specv::policy_evict_normal();
+        if ((j0 >= 0 && !v0) || (j1 >= 0 && !v1)) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
+        s_pos[st] = make_int2(v0 ? j0 * PAGE : -1, v1 ? j1 * PAGE : -1);
+        unsigned char* const dst = smem + st * C::TILE;
+        specv::mbar_arrive_expect_tx(&s_full[st], (v0 + v1) * BL::BYTES);
+        if (v0) specv::bulk_load(dst, p.pool + (static_cast<size_t>(e0) * p.Hk + s_next.c.h) * BL::BYTES, BL::BYTES, &s_full[st], policy);
+        if (v1)
+            specv::bulk_load(dst + BL::BYTES, p.pool + (static_cast<size_t>(e1) * p.Hk + s_next.c.h) * BL::BYTES, BL::BYTES,
+                             &s_full[st], policy);
+        if (++s_next.issued < tiles) {
+            s_next.c.next(p);
+            look();
+        }
+    };
+    bool dead = false;       // a wait gave up: results are invalid, but every barrier is still met
+    if (tid == 0 && tiles > 0) {
+        s_next.c = cur;
+        s_next.issued = 0;
+        look();
+        for (int i = 0; i < C::STAGES && s_next.issued < tiles; ++i) issue();
+    }
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !specv::mbar_wait_bounded(bar, parity, p.status, SPEC_STATUS_TIMEOUT, ATT_WAIT_NS);
+        __syncwarp();
+    };
+
+    const uint32_t idesc = umma_idesc(NC);
+    constexpr uint32_t KSTRIDE = NC / 8 * 128;            // bytes between neighbouring runs of eight along K, both B operands
+    float l[NW];
+    uint32_t par_s = 0, par_o = 0;
+    int t0 = 0;
+    bool first = true;       // first tile of this CTA's part of a unit
+    int4 desc = make_int4(0, 0, 0, 0);
+
+    for (int k = 0; k < tiles; ++k) {
+        const Seq& s = cur.s;
+        const int st = k % C::STAGES;
+        const unsigned char* const tile = smem + st * C::TILE;
+        const int r0 = cur.rb * p.rpb, rows = min(p.rpb, p.N * p.G - r0);
+        if (first) {
+            // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
+            t0 = cur.t;
+            for (int n = warp; n < NC; n += TH / 32) {
+                const int r = r0 + n, i = r / p.G, hq = cur.h * p.G + (r - i * p.G);
+                const bool live = n < rows && i < s.ql;
+                constexpr int E = D / 32;         // lane: channels E lane ..
+                float x[E], top = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    x[e] = live ? static_cast<float>(static_cast<const T*>(p.q.p)[cur.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane + e]) : 0.f;
+                    top = fmaxf(top, fabsf(x[e]));
+                }
+                top = specv::warp_max(top);
+                const int ex = top > 0.f && top <= 3.4e38f ? min(max(10 - ilogbf(top), -120), 120) : 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int d = E * lane + e, w8 = d & 7, at = (w8 & 3) * 2 + (w8 >> 2);     // 0 4 1 5 2 6 3 7
+                    *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * KSTRIDE + (n >> 3) * 128 + (n & 7) * 16 + at * 2) =
+                        __float2half_rn(ldexpf(x[e], ex));
+                }
+                if (lane == 0) {
+                    s_cm[n] = make_float2(live ? ldexpf(p.scale, -ex) : 0.f, ATT_NONE);
+                    s_off[n] = n < rows ? i * p.out.sn + hq * p.out.sh : -1;
+                    s_lse[n] = live ? i * p.Hq + hq : -1;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NW; ++n) l[n] = 0.f;
+            specv::fence_proxy_async_shared();
+        }
+        // ---- S = K Q: the keys' halves, this thread's token and this warpgroup's groups
+        wait(&s_full[st], static_cast<uint32_t>(k / C::STAGES) & 1u);
+        const int2 pos2 = s_pos[st];
+        if (tid < 32 * NG) {      // the values' scales: four tokens of one group, pairs (0, 2) and (1, 3)
+            const int q = tid / NG, gr = tid % NG, page = q / 16, t4 = (4 * q) % PAGE, from = page ? pos2.y : pos2.x;
+            const unsigned char* const vs = tile + page * BL::BYTES + BL::VS + t4 * NG + gr;
+            uint32_t b[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) b[r] = from >= 0 && from + t4 + r < s.len ? static_cast<uint32_t>(vs[r * NG]) << 7 : 0u;
+            const uint32_t s02 = b[0] | b[2] << 16, s13 = b[1] | b[3] << 16;
+            const __half2 m72 = __float2half2_rn(-72.f);
+            const __half2 o02 = __hmul2(*reinterpret_cast<const __half2*>(&s02), m72);
+            const __half2 o13 = __hmul2(*reinterpret_cast<const __half2*>(&s13), m72);
+            *reinterpret_cast<uint4*>(smem + C::VS + (q * NG + gr) * 16) =
+                make_uint4(s02, *reinterpret_cast<const uint32_t*>(&o02), s13, *reinterpret_cast<const uint32_t*>(&o13));
+        }
+#pragma unroll
+        for (int i = 0; i < NG / WG; ++i) {
+            const int gr = wg * (NG / WG) + i, t = tok % PAGE;
+            const unsigned char* const blk = tile + (tok / PAGE) * BL::BYTES;
+            const uint4 v = *reinterpret_cast<const uint4*>(blk + BL::key(gr, t));
+            const __half sc = __ushort_as_half(static_cast<unsigned short>(blk[BL::KS + t * NG + gr] << 7));
+            const __half2 s2 = __half2half2(sc), o2 = __hmul2(s2, __float2half2_rn(-72.f));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t kr[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                kr[4 * q] = half_code(w[q] << 4, s2, o2);
+                kr[4 * q + 1] = half_code(w[q], s2, o2);
+                kr[4 * q + 2] = half_code(w[q] >> 4, s2, o2);
+                kr[4 * q + 3] = half_code(w[q] >> 8, s2, o2);
+            }
+            if (i == 0 && !first) {       // the values' operand of the tile before is read, its columns are free
+                wait(&s_bar_o, par_o);
+                par_o ^= 1;
+                tmem_fence_after();
+            }
+            tmem_st16(tbase + lane_base + 16 * gr, kr);
+        }
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tmem_fence_after();
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                umma_ts(tbase + C::COL_S, tbase + 8 * i, umma_desc(sm + C::Q + 2 * i * KSTRIDE, KSTRIDE, 128), idesc, i > 0);
+            umma_commit(&s_bar_s);
+        }
+        __syncwarp();
+        // ---- values to halves while the product runs
+        uint32_t vr[64 / WG];
+        const bool has_v = D == 128 || wq < 2;
+        if (has_v) {
+            const int half = D == 128 ? wq >> 1 : wq, shift = half ? 0 : 4;
+            const int r = D == 128 ? (wq & 1) * 32 + lane : lane;
+#pragma unroll
+            for (int u = 0; u < 8 / WG; ++u) {
+                const int run = wg * (8 / WG) + u;
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + (run / 4) * BL::BYTES + BL::value((run % 4) * 16, r));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 sc = *reinterpret_cast<const uint4*>(smem + C::VS + ((run * 4 + q) * NG + wq % NG) * 16);
+                    const uint32_t y = w[q] << shift;
+                    vr[8 * u + 2 * q] = half_code(y, *reinterpret_cast<const __half2*>(&sc.x), *reinterpret_cast<const __half2*>(&sc.y));
+                    vr[8 * u + 2 * q + 1] = half_code(y >> 8, *reinterpret_cast<const __half2*>(&sc.z), *reinterpret_cast<const __half2*>(&sc.w));
+                }
+            }
+        }
+        wait(&s_bar_s, par_s);
+        par_s ^= 1;
+        tmem_fence_after();
+        if (has_v) {
+#pragma unroll
+            for (int i = 0; i < 4 / WG; ++i) tmem_st16(tbase + lane_base + 16 * (wg * (4 / WG) + i), vr + 16 * i);
+        }
+        // ---- which queries see this thread's token: [nlo, nhi), and whether the whole tile is seen by all
+        const int base = s.len - s.ql, at0 = tok < PAGE ? pos2.x : pos2.y, at = at0 + tok % PAGE;
+        const int i_first = r0 / p.G, i_last = (r0 + rows - 1) / p.G;
+        const bool whole = pos2.x >= 0 && pos2.y >= 0 && max(pos2.x, pos2.y) + PAGE - 1 <= base + i_first &&
+                           (p.window == 0 || min(pos2.x, pos2.y) > static_cast<long long>(base) + i_last - p.window);
+        int nlo = 0, nhi = NC;
+        if (!whole) {
+            if (at0 < 0 || at >= s.len) {
+                nhi = 0;
+            } else {
+                nlo = max(at - base, 0) * p.G - r0;
+                if (p.window > 0 && at >= p.sinks)
+                    nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - r0;
+            }
+        }
+        nlo -= wg * NW;
+        nhi -= wg * NW;
+        auto scores = [&](float (&x)[NW]) {
+            uint32_t u[NW];
+            tmem_ld(tbase + lane_base + C::COL_S + wg * NW, u);
+#pragma unroll
+            for (int n = 0; n < NW; ++n) x[n] = __uint_as_float(u[n]);
+        };
+        // Moves the references to the maxima seen so far; l and, unless this is the unit's first tile, O follow.
+        auto move_reference = [&] {
+            float y[NW];
+            scores(y);
+#pragma unroll
+            for (int n = 0; n < NW; ++n) y[n] = n >= nlo && n < nhi ? y[n] * s_cm[wg * NW + n].x : -INFINITY;
+            const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (lane < NW) s_red[wq][wg * NW + lane] = top;
+            __syncthreads();
+            if (tid < NC) {
+                const float old = s_cm[tid].y;
+                const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
+                s_fac[tid] = specv::ex2(old - now);
+                s_cm[tid].y = now;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NW; ++n) l[n] *= s_fac[wg * NW + n];
+            if (!first) {
+#pragma unroll
+                for (int i = 0; i < NW / 16; ++i) {
+                    uint32_t u[16];
+                    const uint32_t a = tbase + lane_base + C::COL_O + wg * NW + 16 * i;
+                    tmem_ld(a, u);
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) u[n] = __float_as_uint(__uint_as_float(u[n]) * s_fac[wg * NW + 16 * i + n]);
+                    tmem_st16(a, u);
+                }
+            }
+        };
+        float x[NW];
+        // Probabilities of this token, to shared memory as the second product's operand; true where a score passed
+        // its reference by too much.
+        auto probabilities = [&] {
+            scores(x);
+            float over = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NW; n += 2) {
+                const float4 cm = *reinterpret_cast<const float4*>(&s_cm[wg * NW + n]);
+                x[n] = fmaf(x[n], cm.x, -cm.y);
+                x[n + 1] = fmaf(x[n + 1], cm.z, -cm.w);
+            }
+            if (!whole) {
+#pragma unroll
+                for (int n = 0; n < NW; ++n) x[n] = n >= nlo && n < nhi ? x[n] : -INFINITY;
+            }
+#pragma unroll
+            for (int n = 0; n < NW; ++n) {
+                over = fmaxf(over, x[n]);
+                x[n] = specv::ex2(x[n]);
+            }
+            const int pos = (tok & ~3) + ((tok & 1) << 1) + ((tok >> 1) & 1);       // 0 2 1 3 in each four
+            unsigned char* const row = smem + C::P + (pos >> 3) * KSTRIDE + (pos & 7) * 16 + wg * (NW / 8) * 128;
+#pragma unroll
+            for (int n = 0; n < NW; n += 8) {
+                uint32_t h[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const __half2 v = __floats2half2_rn(x[n + 2 * q], x[n + 2 * q + 1]);
+                    h[q] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(row + (n / 8) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            return over > ATT_SLACK;
+        };
+        if (first) move_reference();
+        const bool over = probabilities();
+        tmem_wait_st();
+        specv::fence_proxy_async_shared();
+        tmem_fence_before();
+        if (__syncthreads_or(over)) {
+            tmem_fence_after();
+            move_reference();
+            probabilities();
+            tmem_wait_st();
+            specv::fence_proxy_async_shared();
+            tmem_fence_before();
+            __syncthreads();
+        }
+#pragma unroll
+        for (int n = 0; n < NW; ++n) l[n] += x[n];
+        // ---- O += V P; the tile's slot is free for the copy two tiles on
+        if (tid == 0) {
+            tmem_fence_after();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                umma_ts(tbase + C::COL_O, tbase + 8 * i, umma_desc(sm + C::P + 2 * i * KSTRIDE, KSTRIDE, 128),
+                        idesc | UMMA_B_MN_MAJOR, !(first && i == 0));
+            umma_commit(&s_bar_o);
+            if (s_next.issued < tiles && !dead) issue();
+        }
+        __syncwarp();
+        const bool unit_ends = cur.t + 1 == s.T;
+        if (!unit_ends && k + 1 < tiles) {
+            first = false;
+        } else {
+            // ---- the part's end: O and the sums out
+            wait(&s_bar_o, par_o);
+            par_o ^= 1;
+            tmem_fence_after();
+            const float sum = fold_columns(l, lane, [](float a, float b) { return a + b; });
+            if (lane < NW) s_red[wq][wg * NW + lane] = sum;
+            __syncthreads();
+            if (tid < NC) s_sum[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+            __syncthreads();
+            const bool alone = t0 == 0 && unit_ends;
+            const long long slot = 2 * g + (t0 == 0 ? 1 : 0);
+            if (!alone && t0 == 0) {
+                const long long end = lo + k + (s.T - cur.t);       // the unit's tiles end there
+                desc = make_int4(cur.b, cur.h * p.RB + cur.rb, static_cast<int>((end * A - 1) / total - g + 1), 0);
+            }
+            if (has_v) {
+                const int d = tok;
+                T* const out = static_cast<T*>(p.out.p) + cur.b * p.out.sb + d;
+                float* const part = p.part_o + slot * NC * D + d;
+#pragma unroll
+                for (int i = 0; i < NW / 16; ++i) {
+                    uint32_t u[16];
+                    tmem_ld(tbase + lane_base + C::COL_O + wg * NW + 16 * i, u);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const int n = wg * NW + 16 * i + q;
+                        if (s_off[n] < 0) continue;
+                        const float o = __uint_as_float(u[q]);
+                        if (alone) out[s_off[n]] = static_cast<T>(s_lse[n] >= 0 && has_seen(s_cm[n].y, s_sum[n]) ? o / s_sum[n] : 0.f);
+                        else part[n * D] = o;
+                    }
+                }
+            }
+            if (tid < NC && s_off[tid] >= 0) {
+                const bool seen = s_lse[tid] >= 0 && has_seen(s_cm[tid].y, s_sum[tid]);
+                if (!alone) {
+                    p.part_ml[slot * NC + tid] = make_float2(s_cm[tid].y, s_sum[tid]);
+                } else if (p.lse) {
+                    const int r = r0 + tid, i = r / p.G;
+                    p.lse[(static_cast<long long>(cur.b) * p.N + i) * p.Hq + cur.h * p.G + (r - i * p.G)] =
+                        seen ? (s_cm[tid].y + log2f(s_sum[tid])) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+            first = true;
+            tmem_fence_before();
+            __syncthreads();      // the queries' and sums' shared memory is free again
+            tmem_fence_after();
+        }
+        cur.next(p);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        p.desc[g] = desc;
+        // (only after a wait gave up) copies still in flight into this CTA's shared memory
+        if (dead)
+            for (int k = max(0, s_next.issued - C::STAGES); k < s_next.issued; ++k)
+                specv::mbar_wait_bounded(&s_full[k % C::STAGES], static_cast<uint32_t>(k / C::STAGES) & 1u, p.status,
+                                         SPEC_STATUS_TIMEOUT, ATT_WAIT_NS);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 0) tmem_dealloc(tbase, C::COLS);
+}
+
+// Joins the parts of the unit that starts in CTA blockIdx.x of the kernel before and is cut, a warp to a query row, in
+// order of the parts.
+template <class T, int D, int NC>
+__global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= static_cast<long long>(p.B) * p.N * p.Hq) return;
-    const int hq = static_cast<int>(row % p.Hq), i = static_cast<int>(row / p.Hq % p.N), b = static_cast<int>(row / p.Hq / p.N);
-    const int h = hq / (p.Hq / p.Hk);
-    int ql = p.q_len ? p.q_len[b] : p.N;
-    if (ql < 0 || ql > p.N) atomicOr(p.status, SPEC_STATUS_BAD_LENGTH), ql = min(max(ql, 0), p.N);
-    int len = p.kv_len[b];
-    const long long room = static_cast<long long>(p.max_pages) * PAGE;
-    if (len < 0 || len > room) atomicOr(p.status, SPEC_STATUS_BAD_LENGTH), len = static_cast<int>(min(static_cast<long long>(max(len, 0)), room));
-    const int pos = i < ql ? len - ql + i : -1;
-    float q[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = static_cast<float>(static_cast<const T*>(p.q.p)[b * p.q.sb + i * p.q.sn + hq * p.q.sh + e * 32 + lane]);
-        o[e] = 0.f;
-    }
-    float m = -1e30f, l = 0.f;
-    for (int t = 0; t <= pos; ++t) {
-        if (p.window > 0 && t >= p.sinks && t <= pos - p.window) continue;
-        const int page = p.table[static_cast<size_t>(b) * p.max_pages + t / PAGE];
-        if (page < 0 || page >= p.pages) {
-            if (lane == 0) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
-            continue;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 u = p.desc[blockIdx.x];
+    if (u.z == 0) return;
+    const int lane = threadIdx.x & 31, n = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int h = u.y / p.RB, r0 = (u.y - h * p.RB) * p.rpb, r = r0 + n;
+    if (n >= p.rpb || r >= p.N * p.G) return;
+    const int i = r / p.G, hq = h * p.G + (r - i * p.G);
+    const long long g = blockIdx.x;
+    auto slot = [&](int k) { return k == 0 ? 2 * g + 1 : 2 * (g + k); };
+    float m = ATT_NONE;
+    for (int k = lane; k < u.z; k += 32) m = fmaxf(m, p.part_ml[slot(k) * NC + n].x);
+    m = specv::warp_max(m);
+    float o[E] = {}, sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < u.z; ++k) {
+        const float2 ml = p.part_ml[slot(k) * NC + n];
+        const float w = specv::ex2(ml.x - m);
+        const float* const part = p.part_o + (slot(k) * NC + n) * D + E * lane;
+        sum = fmaf(ml.y, w, sum);
+        float v[E];
+        if (E == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(part);
+            v[0] = f.x, v[1] = f.y, v[E - 2] = f.z, v[E - 1] = f.w;
+        } else {
+            const float2 f = *reinterpret_cast<const float2*>(part);
+            v[0] = f.x, v[1] = f.y;
         }
-        const unsigned char* const blk = p.pool + (static_cast<size_t>(page) * p.Hk + h) * BL::BYTES;
-        float s = 0.f, v[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = e * 32 + lane, kb = blk[BL::key(e, t % PAGE) + lane / 2], vb = blk[BL::value(t % PAGE, d % (D / 2))];
-            s += q[e] * (static_cast<float>(((lane & 1) ? kb >> 4 : kb & 15) - 8) * scale_value(blk[BL::KS + t % PAGE * BL::NG + e]));
-            v[e] = static_cast<float>((d < D / 2 ? vb & 15 : vb >> 4) - 8) * scale_value(blk[BL::VS + t % PAGE * BL::NG + e]);
-        }
-        s = specv::warp_sum(s) * p.scale;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * v[e];
-        m = mn;
+        for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], w, o[e]);
     }
+    const int ql = p.q_len ? p.q_len[u.x] : p.N;
+    const bool seen = i < ql && has_seen(m, sum);
+    T* const out = static_cast<T*>(p.out.p) + u.x * p.out.sb + i * p.out.sn + hq * p.out.sh + E * lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        static_cast<T*>(p.out.p)[b * p.out.sb + i * p.out.sn + hq * p.out.sh + e * 32 + lane] = static_cast<T>(l > 0.f ? o[e] / l : 0.f);
-    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : __uint_as_float(0xFF800000u);
+    for (int e = 0; e < E; ++e) out[e] = static_cast<T>(seen ? o[e] / sum : 0.f);
+    if (p.lse && lane == 0)
+        p.lse[(static_cast<long long>(u.x) * p.N + i) * p.Hq + hq] = seen ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace specc

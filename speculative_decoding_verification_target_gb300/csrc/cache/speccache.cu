@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/speccache.h: argument checks and launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -117,6 +118,67 @@ TokensParams tokens_params(const void* pool, int pages, const int32_t* table, in
     p.Hk = Hk;
     p.status = static_cast<unsigned*>(ws);
     return p;
+}
+
+// --------------------------------------------------------------------------------------------- attention
+// The queries that read a key head, in equal blocks of at most 64 rows, and the product's width for a block.
+struct AttSplit {
+    int blocks, rows, nc;
+};
+AttSplit att_split(int rows) {
+    const int blocks = (rows + 63) / 64, per = (rows + blocks - 1) / blocks;
+    return {blocks, per, per <= 16 ? 16 : per <= 32 ? 32 : 64};
+}
+
+// Workspace: header, the cut units' descriptions, and two parts for each CTA that there can be.
+struct AttLayout {
+    size_t desc, ml, o, total;
+};
+AttLayout att_layout(int nc, int D) {
+    const size_t ctas = nc > 32 ? ATT_MAX_CTAS / 2 : ATT_MAX_CTAS;
+    AttLayout w;
+    w.desc = SPEC_CACHE_WS_HEADER;
+    w.ml = w.desc + ctas * sizeof(int4);
+    w.o = w.ml + 2 * ctas * nc * sizeof(float2);
+    w.total = w.o + 2 * ctas * nc * D * sizeof(float);
+    return w;
+}
+
+template <class T, int D, int NC>
+spec_status attend_as(const AttnParams& p, cudaStream_t st) {
+    using C = Att<D, NC>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
+    static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
+    const unsigned bit = dev < 32 ? 1u << dev : 0u;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention kernel attribute failed: %s", cudaGetErrorString(e));
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    const long long tiles = static_cast<long long>(p.B) * p.Hk * p.RB * ((p.max_pages + 1) / 2);     // at most
+    const int ctas = static_cast<int>(std::min<long long>({static_cast<long long>(C::CTAS) * sms, ATT_MAX_CTAS / C::WG, tiles}));
+    attention_kernel<T, D, NC><<<ctas, C::TH, C::SMEM, st>>>(p);
+    SPECC_TRY(launched("attention"));
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (p.rpb + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, NC>, p);
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "attention's join failed: %s", cudaGetErrorString(e));
+}
+
+template <class T>
+spec_status attend(const AttnParams& p, int D, int nc, cudaStream_t st) {
+    if (D == 64) return nc == 16 ? attend_as<T, 64, 16>(p, st) : nc == 32 ? attend_as<T, 64, 32>(p, st) : attend_as<T, 64, 64>(p, st);
+    return nc == 16 ? attend_as<T, 128, 16>(p, st) : nc == 32 ? attend_as<T, 128, 32>(p, st) : attend_as<T, 128, 64>(p, st);
 }
 
 // ------------------------------------------------------------------------------------------------- pages
@@ -261,7 +323,7 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
 
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
     if (N < 1 || N > MAX_Q || Hk < 1 || Hq < Hk || Hq > MAX_HEADS || Hq % Hk || (D != 64 && D != 128)) return 0;
-    return SPEC_CACHE_WS_HEADER;
+    return att_layout(att_split(N * (Hq / Hk)).nc, D).total;
 }
 
 spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
@@ -298,18 +360,17 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     p.window = window;
     p.sinks = sinks;
     p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    const long long ctas = (static_cast<long long>(B) * N * Hq + 3) / 4;
-    if (ctas > 2147483647LL) return fail(SPEC_ERR_INVALID, "B N Hq is limited to 2^33");
+    p.G = Hq / Hk;
+    const AttSplit split = att_split(N * p.G);
+    p.RB = split.blocks;
+    p.rpb = split.rows;
+    const AttLayout w = att_layout(split.nc, D);
+    unsigned char* const ws = static_cast<unsigned char*>(workspace);
+    p.desc = reinterpret_cast<int4*>(ws + w.desc);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned g = static_cast<unsigned>(ctas);
-    if (dtype == SPEC_BF16) {
-        if (D == 64) attention_kernel<__nv_bfloat16, 64><<<g, 128, 0, st>>>(p);
-        else attention_kernel<__nv_bfloat16, 128><<<g, 128, 0, st>>>(p);
-    } else {
-        if (D == 64) attention_kernel<__half, 64><<<g, 128, 0, st>>>(p);
-        else attention_kernel<__half, 128><<<g, 128, 0, st>>>(p);
-    }
-    return launched("attention");
+    return dtype == SPEC_BF16 ? attend<__nv_bfloat16>(p, D, split.nc, st) : attend<__half>(p, D, split.nc, st);
 }
 
 size_t spec_pages_workspace_size(int S, int pages) {

@@ -52,12 +52,13 @@ def block_values(blk):
 
 
 def attention(q, pool, table, kv_len, q_len, scale, window=0, sinks=0):
-    """out, lse, and per output the bound's parts: sum p |v| and the largest sum |q k| scale among visible tokens."""
+    """out, lse, and per output the bound's parts: sum p |v|, the largest sum |q k| scale among visible tokens, sum |v|."""
     B, N, Hq, D = q.shape
     P, H = pool.shape[:2]
     G = Hq // H
     out = np.zeros((B, N, Hq, D))
     mass = np.zeros((B, N, Hq, D))
+    total = np.zeros((B, N, Hq, D))
     big = np.zeros((B, N, Hq))
     lse = np.full((B, N, Hq), -np.inf)
     for b in range(B):
@@ -88,9 +89,10 @@ def attention(q, pool, table, kv_len, q_len, scale, window=0, sinks=0):
                     p = e / e.sum()
                     out[b, i, h * G + g] = p @ v[see]
                     mass[b, i, h * G + g] = p @ np.abs(v[see])
+                    total[b, i, h * G + g] = np.abs(v[see]).sum(0)
                     big[b, i, h * G + g] = (np.abs(k[see]) @ np.abs(x)).max() * abs(scale)
                     lse[b, i, h * G + g] = m + np.log(e.sum())
-    return out, lse, mass, big
+    return out, lse, mass, big, total
 
 
 def fork(table, lengths, refs, src, dst):
