@@ -33,7 +33,7 @@
 namespace specc {
 
 constexpr int ATT_MAX_CTAS = 640;
-constexpr uint64_t ATT_WAIT_NS = 2000000000ull;
+constexpr int ATT_WAIT_TRIES = 2000000;     // of about a microsecond each
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
 constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
 
@@ -50,6 +50,9 @@ struct AttnParams {
     int pages, max_pages, B, N, Hq, Hk, G, window, sinks;
     int RB, rpb;             // query blocks and rows of each
     float scale;             // times log2 e
+    // 16, as a value that the compiler does not know: x 16 then stays a multiplication, for which there is more room
+    // than for shifts
+    uint32_t sixteen;
 };
 
 template <int D, int NC>
@@ -129,14 +132,80 @@ __device__ __forceinline__ float fold_columns(float (&v)[W], int lane, Op op) {
     return v[0];
 }
 
-__device__ __forceinline__ uint32_t half_code(uint32_t x, __half2 s, __half2 o) {
-    const uint32_t h = (x & 0x00F000F0u) | 0x54005400u;
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&h), s, o);
-    return *reinterpret_cast<const uint32_t*>(&r);
+// Two codes, in bits 4 .. 7 of x's halves, as halves (c - 8) s; o = -72 s. One logic instruction and one multiply-add;
+// `sixty_four`, 0x54005400, comes from shared memory, so that it stays in a register: the logic instruction takes one
+// immediate, and the compiler would rather build the other constant anew each time.
+__device__ __forceinline__ uint32_t half_code(uint32_t sixty_four, uint32_t x, uint32_t s, uint32_t o) {
+    uint32_t h, r;
+    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(h) : "r"(x), "r"(sixty_four));     // (x & a) | b
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(s), "r"(o));
+    return r;
+}
+__device__ __forceinline__ uint32_t minus72(uint32_t s) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xD480D480u));
+    return r;
 }
 
 // Whether a query saw any token, from its reference and sum: a NaN among its scores never becomes the reference.
 __device__ __forceinline__ bool has_seen(float m, float sum) { return m > ATT_NONE || sum != sum; }
+
+// Waits, as a warp, for a phase of `bar`, at most `tries` turns; where it gives up it sets the status bit and leaves 0 in
+// `tries`, so that later waits end at once (the results are invalid, but every barrier is still met). A try sleeps in
+// hardware until the phase ends or its time is up, so turns are few.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int& tries, unsigned* status) {
+    int left = tries;
+    while (!__all_sync(0xffffffffu, specv::mbar_try_wait_sleep(bar, parity, 1000))) {
+        if (--left < 0) {
+            if (tries) atomicOr(status, SPEC_STATUS_TIMEOUT);
+            tries = 0;
+            break;
+        }
+    }
+}
+
+// Bits [lo, hi) of 32, the ends clamped.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : hi > 0 ? (1u << hi) - 1u : 0u;
+    return lo >= 32 ? 0u : lo > 0 ? below_hi & (0xFFFFFFFFu << lo) : below_hi;
+}
+// The same value, tied to this place: keeps what is worked out from it inside its branch.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+    asm volatile("" : "+r"(v));
+    return v;
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 template <class T, int D, int NC>
 __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
@@ -147,16 +216,17 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_full[C::STAGES];
     __shared__ __align__(8) uint64_t s_bar_s, s_bar_o;
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_c64;
     __shared__ __align__(8) int2 s_pos[C::STAGES];       // first position of the tile's two pages, -1 where there is none
-    __shared__ __align__(16) float2 s_cm[NC];            // c_n, m_n
-    __shared__ float s_fac[NC], s_red[4][NC], s_sum[NC];
+    __shared__ __align__(16) float s_c[NC], s_nm[NC];    // c_n, -m_n
+    __shared__ __align__(16) float s_fac[NC];
+    __shared__ float s_red[4][NC], s_sum[NC];
     __shared__ long long s_off[NC];                      // output row offset, -1: no such row
     __shared__ int s_lse[NC];                            // lse index within the sequence, -1: a row past q_len
     __shared__ long long s_scan[TH / 32 + 1];
     __shared__ long long s_start;
     __shared__ int s_b;
-    struct Ahead {               // thread 0's own: the next tile to copy, its pages' places and numbers, tiles issued
+    struct Ahead {               // the copying thread's own: the next tile to copy, its pages' places and numbers, tiles issued
         Cursor c;
         int j0, j1, e0, e1, issued;
     };
@@ -175,6 +245,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     if (warp == 0) tmem_alloc(&s_tmem, C::COLS);
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) specv::mbar_init(&s_full[i], 1);
+        s_c64 = 0x54005400u;
         specv::mbar_init(&s_bar_s, 1);
         specv::mbar_init(&s_bar_o, 1);
         specv::fence_mbarrier_init_cluster();
@@ -182,7 +253,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tbase = s_tmem, lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tbase = s_tmem, c64 = *static_cast<volatile uint32_t*>(&s_c64), lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const long long per_t = static_cast<long long>(p.Hk) * p.RB;
     long long total = 0;
     for (int w = 0; w < TH / 32; ++w) total += s_scan[w];
@@ -232,7 +303,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
 
     const int tiles = static_cast<int>(hi - lo);
 
-    // ---- the copies (thread 0): tile k of the run into slot k mod STAGES. Page numbers are read one tile before they
+    // ---- the copies (one thread of the last warp): tile k of the run into slot k mod STAGES. Page numbers are read one tile before they
     // are needed.
     auto look = [&] {
         s_next.j0 = s_next.c.page_index(0);
@@ -258,24 +329,24 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
             look();
         }
     };
-    bool dead = false;       // a wait gave up: results are invalid, but every barrier is still met
-    if (tid == 0 && tiles > 0) {
+    int tries = ATT_WAIT_TRIES;
+    const bool copier = tid == TH - 32;
+    if (copier && tiles > 0) {
         s_next.c = cur;
         s_next.issued = 0;
         look();
         for (int i = 0; i < C::STAGES && s_next.issued < tiles; ++i) issue();
     }
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead) dead = !specv::mbar_wait_bounded(bar, parity, p.status, SPEC_STATUS_TIMEOUT, ATT_WAIT_NS);
-        __syncwarp();
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, tries, p.status); };
 
     const uint32_t idesc = umma_idesc(NC);
     constexpr uint32_t KSTRIDE = NC / 8 * 128;            // bytes between neighbouring runs of eight along K, both B operands
-    float l[NW];
+    unsigned long long l[NW / 2];      // this thread's part of each query's sum
     uint32_t par_s = 0, par_o = 0;
     int t0 = 0;
+    int before_all = 0, seen_by_all = 0;      // a page is seen whole by every query of the block if its first position is
+                                              // past the one and not past the other
     bool first = true;       // first tile of this CTA's part of a unit
     int4 desc = make_int4(0, 0, 0, 0);
 
@@ -287,6 +358,8 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
         if (first) {
             // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
             t0 = cur.t;
+            seen_by_all = s.len - s.ql + r0 / p.G - (PAGE - 1);
+            before_all = p.window == 0 ? -1 : static_cast<int>(max(-1LL, static_cast<long long>(s.len) - s.ql + (r0 + rows - 1) / p.G - p.window));
             for (int n = warp; n < NC; n += TH / 32) {
                 const int r = r0 + n, i = r / p.G, hq = cur.h * p.G + (r - i * p.G);
                 const bool live = n < rows && i < s.ql;
@@ -306,13 +379,14 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                         __float2half_rn(ldexpf(x[e], ex));
                 }
                 if (lane == 0) {
-                    s_cm[n] = make_float2(live ? ldexpf(p.scale, -ex) : 0.f, ATT_NONE);
+                    s_c[n] = live ? ldexpf(p.scale, -ex) : 0.f;
+                    s_nm[n] = -ATT_NONE;
                     s_off[n] = n < rows ? i * p.out.sn + hq * p.out.sh : -1;
                     s_lse[n] = live ? i * p.Hq + hq : -1;
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NW; ++n) l[n] = 0.f;
+            for (int n = 0; n < NW / 2; ++n) l[n] = 0ull;
             specv::fence_proxy_async_shared();
         }
         // ---- S = K Q: the keys' halves, this thread's token and this warpgroup's groups
@@ -325,27 +399,22 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
 #pragma unroll
             for (int r = 0; r < 4; ++r) b[r] = from >= 0 && from + t4 + r < s.len ? static_cast<uint32_t>(vs[r * NG]) << 7 : 0u;
             const uint32_t s02 = b[0] | b[2] << 16, s13 = b[1] | b[3] << 16;
-            const __half2 m72 = __float2half2_rn(-72.f);
-            const __half2 o02 = __hmul2(*reinterpret_cast<const __half2*>(&s02), m72);
-            const __half2 o13 = __hmul2(*reinterpret_cast<const __half2*>(&s13), m72);
-            *reinterpret_cast<uint4*>(smem + C::VS + (q * NG + gr) * 16) =
-                make_uint4(s02, *reinterpret_cast<const uint32_t*>(&o02), s13, *reinterpret_cast<const uint32_t*>(&o13));
+            *reinterpret_cast<uint4*>(smem + C::VS + (q * NG + gr) * 16) = make_uint4(s02, minus72(s02), s13, minus72(s13));
         }
 #pragma unroll
         for (int i = 0; i < NG / WG; ++i) {
             const int gr = wg * (NG / WG) + i, t = tok % PAGE;
             const unsigned char* const blk = tile + (tok / PAGE) * BL::BYTES;
             const uint4 v = *reinterpret_cast<const uint4*>(blk + BL::key(gr, t));
-            const __half sc = __ushort_as_half(static_cast<unsigned short>(blk[BL::KS + t * NG + gr] << 7));
-            const __half2 s2 = __half2half2(sc), o2 = __hmul2(s2, __float2half2_rn(-72.f));
+            const uint32_t s2 = blk[BL::KS + t * NG + gr] * 0x00800080u, o2 = minus72(s2);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t kr[16];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                kr[4 * q] = half_code(w[q] << 4, s2, o2);
-                kr[4 * q + 1] = half_code(w[q], s2, o2);
-                kr[4 * q + 2] = half_code(w[q] >> 4, s2, o2);
-                kr[4 * q + 3] = half_code(w[q] >> 8, s2, o2);
+                kr[4 * q] = half_code(c64, w[q] * p.sixteen, s2, o2);
+                kr[4 * q + 1] = half_code(c64, w[q], s2, o2);
+                kr[4 * q + 2] = half_code(c64, (w[q] >> 8) * p.sixteen, s2, o2);
+                kr[4 * q + 3] = half_code(c64, w[q] >> 8, s2, o2);
             }
             if (i == 0 && !first) {       // the values' operand of the tile before is read, its columns are free
                 wait(&s_bar_o, par_o);
@@ -365,40 +434,46 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
             umma_commit(&s_bar_s);
         }
         __syncwarp();
-        // ---- values to halves while the product runs
-        uint32_t vr[64 / WG];
+        // ---- values to halves, the first half of the tokens while the product runs
         const bool has_v = D == 128 || wq < 2;
-        if (has_v) {
-            const int half = D == 128 ? wq >> 1 : wq, shift = half ? 0 : 4;
+        uint32_t vr[32 / WG];
+        auto values = [&](int part) {
+            const bool half = D == 128 ? wq >> 1 : wq;
+            const uint32_t up = half ? 1u : p.sixteen;
             const int r = D == 128 ? (wq & 1) * 32 + lane : lane;
 #pragma unroll
-            for (int u = 0; u < 8 / WG; ++u) {
-                const int run = wg * (8 / WG) + u;
+            for (int u = 0; u < 4 / WG; ++u) {
+                const int run = wg * (8 / WG) + part * (4 / WG) + u;
                 const uint4 v = *reinterpret_cast<const uint4*>(tile + (run / 4) * BL::BYTES + BL::value((run % 4) * 16, r));
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 sc = *reinterpret_cast<const uint4*>(smem + C::VS + ((run * 4 + q) * NG + wq % NG) * 16);
-                    const uint32_t y = w[q] << shift;
-                    vr[8 * u + 2 * q] = half_code(y, *reinterpret_cast<const __half2*>(&sc.x), *reinterpret_cast<const __half2*>(&sc.y));
-                    vr[8 * u + 2 * q + 1] = half_code(y >> 8, *reinterpret_cast<const __half2*>(&sc.z), *reinterpret_cast<const __half2*>(&sc.w));
+                    const uint32_t y = w[q] * up;
+                    vr[8 * u + 2 * q] = half_code(c64, y, sc.x, sc.y);
+                    vr[8 * u + 2 * q + 1] = half_code(c64, y >> 8, sc.z, sc.w);
                 }
             }
-        }
+        };
+        auto put_values = [&](int part) {
+#pragma unroll
+            for (int i = 0; i < 2 / WG; ++i) tmem_st16(tbase + lane_base + 16 * ((2 * wg + part) * (2 / WG) + i), vr + 16 * i);
+        };
+        if (has_v) values(0);
         wait(&s_bar_s, par_s);
         par_s ^= 1;
         tmem_fence_after();
         if (has_v) {
-#pragma unroll
-            for (int i = 0; i < 4 / WG; ++i) tmem_st16(tbase + lane_base + 16 * (wg * (4 / WG) + i), vr + 16 * i);
+            put_values(0);
+            values(1);
+            put_values(1);
         }
-        // ---- which queries see this thread's token: [nlo, nhi), and whether the whole tile is seen by all
-        const int base = s.len - s.ql, at0 = tok < PAGE ? pos2.x : pos2.y, at = at0 + tok % PAGE;
-        const int i_first = r0 / p.G, i_last = (r0 + rows - 1) / p.G;
-        const bool whole = pos2.x >= 0 && pos2.y >= 0 && max(pos2.x, pos2.y) + PAGE - 1 <= base + i_first &&
-                           (p.window == 0 || min(pos2.x, pos2.y) > static_cast<long long>(base) + i_last - p.window);
+        // ---- which queries see this thread's token: [nlo, nhi); all of them where the whole tile is seen by all
+        const int at0 = tok < PAGE ? pos2.x : pos2.y;
+        const bool whole = min(pos2.x, pos2.y) > before_all && max(pos2.x, pos2.y) <= seen_by_all;
         int nlo = 0, nhi = NC;
         if (!whole) {
+            const int base = s.len - s.ql, at = at0 + tok % PAGE;
             if (at0 < 0 || at >= s.len) {
                 nhi = 0;
             } else {
@@ -407,95 +482,83 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                     nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - r0;
             }
         }
-        nlo -= wg * NW;
-        nhi -= wg * NW;
-        auto scores = [&](float (&x)[NW]) {
+        const uint32_t seen = bit_range(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
+        unsigned long long x[NW / 2];
+        for (bool move = first;; move = true) {
             uint32_t u[NW];
             tmem_ld(tbase + lane_base + C::COL_S + wg * NW, u);
+            if (move) {
+                // the references move to the maxima seen so far; l and, unless this is the unit's first tile, O follow
+                float y[NW];
+                const uint32_t bits = here(seen);
 #pragma unroll
-            for (int n = 0; n < NW; ++n) x[n] = __uint_as_float(u[n]);
-        };
-        // Moves the references to the maxima seen so far; l and, unless this is the unit's first tile, O follow.
-        auto move_reference = [&] {
-            float y[NW];
-            scores(y);
+                for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1u ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
+                const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
+                if (lane < NW) s_red[wq][wg * NW + lane] = top;
+                __syncthreads();
+                if (tid < NC) {
+                    const float old = -s_nm[tid];
+                    const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
+                    s_fac[tid] = specv::ex2(old - now);
+                    s_nm[tid] = -now;
+                }
+                __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NW; ++n) y[n] = n >= nlo && n < nhi ? y[n] * s_cm[wg * NW + n].x : -INFINITY;
-            const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
-            if (lane < NW) s_red[wq][wg * NW + lane] = top;
-            __syncthreads();
-            if (tid < NC) {
-                const float old = s_cm[tid].y;
-                const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
-                s_fac[tid] = specv::ex2(old - now);
-                s_cm[tid].y = now;
-            }
-            __syncthreads();
+                for (int n = 0; n < NW / 2; ++n) l[n] = mul2(l[n], *reinterpret_cast<const unsigned long long*>(&s_fac[wg * NW + 2 * n]));
+                if (!first) {
 #pragma unroll
-            for (int n = 0; n < NW; ++n) l[n] *= s_fac[wg * NW + n];
-            if (!first) {
+                    for (int i = 0; i < NW / 16; ++i) {
+                        uint32_t o[16];
+                        const uint32_t a = tbase + lane_base + C::COL_O + wg * NW + 16 * i;
+                        tmem_ld(a, o);
 #pragma unroll
-                for (int i = 0; i < NW / 16; ++i) {
-                    uint32_t u[16];
-                    const uint32_t a = tbase + lane_base + C::COL_O + wg * NW + 16 * i;
-                    tmem_ld(a, u);
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) u[n] = __float_as_uint(__uint_as_float(u[n]) * s_fac[wg * NW + 16 * i + n]);
-                    tmem_st16(a, u);
+                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[wg * NW + 16 * i + n]);
+                        tmem_st16(a, o);
+                    }
                 }
             }
-        };
-        float x[NW];
-        // Probabilities of this token, to shared memory as the second product's operand; true where a score passed
-        // its reference by too much.
-        auto probabilities = [&] {
-            scores(x);
+            // this token's probabilities, to shared memory as the second product's operand
             float over = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < NW; n += 2) {
-                const float4 cm = *reinterpret_cast<const float4*>(&s_cm[wg * NW + n]);
-                x[n] = fmaf(x[n], cm.x, -cm.y);
-                x[n + 1] = fmaf(x[n + 1], cm.z, -cm.w);
-            }
-            if (!whole) {
-#pragma unroll
-                for (int n = 0; n < NW; ++n) x[n] = n >= nlo && n < nhi ? x[n] : -INFINITY;
-            }
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                over = fmaxf(over, x[n]);
-                x[n] = specv::ex2(x[n]);
-            }
             const int pos = (tok & ~3) + ((tok & 1) << 1) + ((tok >> 1) & 1);       // 0 2 1 3 in each four
             unsigned char* const row = smem + C::P + (pos >> 3) * KSTRIDE + (pos & 7) * 16 + wg * (NW / 8) * 128;
+#pragma unroll
+            for (int n = 0; n < NW; n += 4) {
+                const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[wg * NW + n]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&s_nm[wg * NW + n]);
+                x[n / 2] = fma2(pack2(__uint_as_float(u[n]), __uint_as_float(u[n + 1])), c.x, m.x);
+                x[n / 2 + 1] = fma2(pack2(__uint_as_float(u[n + 2]), __uint_as_float(u[n + 3])), c.y, m.y);
+            }
+            if (!whole) {
+                const uint32_t bits = here(seen);
+#pragma unroll
+                for (int n = 0; n < NW; n += 2) {
+                    const float2 v = unpack2(x[n / 2]);
+                    x[n / 2] = pack2(bits >> n & 1u ? v.x : -INFINITY, bits >> (n + 1) & 1u ? v.y : -INFINITY);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NW; n += 8) {
                 uint32_t h[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const __half2 v = __floats2half2_rn(x[n + 2 * q], x[n + 2 * q + 1]);
-                    h[q] = *reinterpret_cast<const uint32_t*>(&v);
+                    const float2 v = unpack2(x[n / 2 + q]);
+                    over = max3(over, v.x, v.y);
+                    const float e0 = specv::ex2(v.x), e1 = specv::ex2(v.y);
+                    x[n / 2 + q] = pack2(e0, e1);
+                    const __half2 hv = __floats2half2_rn(e0, e1);
+                    h[q] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
                 *reinterpret_cast<uint4*>(row + (n / 8) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            return over > ATT_SLACK;
-        };
-        if (first) move_reference();
-        const bool over = probabilities();
-        tmem_wait_st();
-        specv::fence_proxy_async_shared();
-        tmem_fence_before();
-        if (__syncthreads_or(over)) {
-            tmem_fence_after();
-            move_reference();
-            probabilities();
             tmem_wait_st();
             specv::fence_proxy_async_shared();
             tmem_fence_before();
-            __syncthreads();
+            // a score that passed its reference by too much: once more, with the references moved (after which none does)
+            if (!__syncthreads_or(!move && over > ATT_SLACK)) break;
+            tmem_fence_after();
         }
 #pragma unroll
-        for (int n = 0; n < NW; ++n) l[n] += x[n];
+        for (int n = 0; n < NW / 2; ++n) l[n] = add2(l[n], x[n]);
         // ---- O += V P; the tile's slot is free for the copy two tiles on
         if (tid == 0) {
             tmem_fence_after();
@@ -504,8 +567,8 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                 umma_ts(tbase + C::COL_O, tbase + 8 * i, umma_desc(sm + C::P + 2 * i * KSTRIDE, KSTRIDE, 128),
                         idesc | UMMA_B_MN_MAJOR, !(first && i == 0));
             umma_commit(&s_bar_o);
-            if (s_next.issued < tiles && !dead) issue();
         }
+        if (copier && s_next.issued < tiles && tries) issue();
         __syncwarp();
         const bool unit_ends = cur.t + 1 == s.T;
         if (!unit_ends && k + 1 < tiles) {
@@ -515,7 +578,13 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
             wait(&s_bar_o, par_o);
             par_o ^= 1;
             tmem_fence_after();
-            const float sum = fold_columns(l, lane, [](float a, float b) { return a + b; });
+            float lf[NW];
+#pragma unroll
+            for (int n = 0; n < NW / 2; ++n) {
+                const float2 v = unpack2(l[n]);
+                lf[2 * n] = v.x, lf[2 * n + 1] = v.y;
+            }
+            const float sum = fold_columns(lf, lane, [](float a, float b) { return a + b; });
             if (lane < NW) s_red[wq][wg * NW + lane] = sum;
             __syncthreads();
             if (tid < NC) s_sum[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
@@ -539,19 +608,19 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                         const int n = wg * NW + 16 * i + q;
                         if (s_off[n] < 0) continue;
                         const float o = __uint_as_float(u[q]);
-                        if (alone) out[s_off[n]] = static_cast<T>(s_lse[n] >= 0 && has_seen(s_cm[n].y, s_sum[n]) ? o / s_sum[n] : 0.f);
+                        if (alone) out[s_off[n]] = static_cast<T>(s_lse[n] >= 0 && has_seen(-s_nm[n], s_sum[n]) ? o / s_sum[n] : 0.f);
                         else part[n * D] = o;
                     }
                 }
             }
             if (tid < NC && s_off[tid] >= 0) {
-                const bool seen = s_lse[tid] >= 0 && has_seen(s_cm[tid].y, s_sum[tid]);
+                const bool seen = s_lse[tid] >= 0 && has_seen(-s_nm[tid], s_sum[tid]);
                 if (!alone) {
-                    p.part_ml[slot * NC + tid] = make_float2(s_cm[tid].y, s_sum[tid]);
+                    p.part_ml[slot * NC + tid] = make_float2(-s_nm[tid], s_sum[tid]);
                 } else if (p.lse) {
                     const int r = r0 + tid, i = r / p.G;
                     p.lse[(static_cast<long long>(cur.b) * p.N + i) * p.Hq + cur.h * p.G + (r - i * p.G)] =
-                        seen ? (s_cm[tid].y + log2f(s_sum[tid])) * 0.6931471805599453f : -INFINITY;
+                        seen ? (log2f(s_sum[tid]) - s_nm[tid]) * 0.6931471805599453f : -INFINITY;
                 }
             }
             first = true;
@@ -562,13 +631,12 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
         cur.next(p);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) {
-        p.desc[g] = desc;
-        // (only after a wait gave up) copies still in flight into this CTA's shared memory
-        if (dead)
-            for (int k = max(0, s_next.issued - C::STAGES); k < s_next.issued; ++k)
-                specv::mbar_wait_bounded(&s_full[k % C::STAGES], static_cast<uint32_t>(k / C::STAGES) & 1u, p.status,
-                                         SPEC_STATUS_TIMEOUT, ATT_WAIT_NS);
+    if (tid == 0) p.desc[g] = desc;
+    if (warp == TH / 32 - 1 && !tries) {      // (a wait gave up) copies still in flight into this CTA's shared memory
+        const int issued = __shfl_sync(0xffffffffu, s_next.issued, 0);
+        tries = ATT_WAIT_TRIES;
+        for (int k = max(0, issued - C::STAGES); k < issued; ++k)
+            wait(&s_full[k % C::STAGES], static_cast<uint32_t>(k / C::STAGES) & 1u);
     }
     tmem_fence_before();
     __syncthreads();
