@@ -33,7 +33,7 @@
 namespace specc {
 
 constexpr int ATT_MAX_CTAS = 640;
-constexpr int ATT_WAIT_TRIES = 2000000;     // of about a microsecond each
+constexpr int ATT_WAIT_TRIES = 20000000;    // seconds, whatever a try takes
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
 constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
 
@@ -57,19 +57,27 @@ struct AttnParams {
 
 template <int D, int NC>
 struct Att {
-    static constexpr int WG = NC > 32 ? 2 : 1, TH = 128 * WG, CTAS = WG == 1 ? 4 : 2;
+    static constexpr int WG = NC > 32 ? 2 : 1, CTAS = WG == 1 ? 3 : 2;
+    static constexpr int CT = 128 * WG, TH = CT + 32;     // computing threads; one more warp fetches and issues products
     static constexpr int NW = NC / WG;                    // queries of a thread
     static constexpr int TILE = 2 * Block<D>::BYTES;
-    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : 2;
+    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : 3, INFOS = 2 * STAGES;
+    // the second product: D = 128, 128 channels by 128 tokens; D = 64, both pages' channels as 128 rows by 64 tokens, each
+    // page's probabilities in columns of their own (half of the result is of no use, but all warps have values to convert)
+    static constexpr int ON = D == 128 ? NC : 2 * NC, OK = D == 128 ? 128 : 64;
+    static constexpr int WORDS = OK / 4 / WG;             // a thread's words of value codes, four tokens each
+    static constexpr int VP = WORDS > 16 ? 2 : 1, WPP = WORDS / VP;
+    static constexpr int KQ = NC / 8 * 128, KP = ON / 8 * 128;   // bytes between runs of eight along K, both N operands
     static constexpr int P = STAGES * TILE;               // byte offsets in dynamic shared memory
-    static constexpr int Q = P + 128 * NC * 2;
+    static constexpr int Q = P + OK * ON * 2;
     static constexpr int VS = Q + NC * D * 2;
-    static constexpr int END = VS + 32 * Block<D>::NG * 16;
+    static constexpr int END = VS + CT / 32 * WORDS * 16;
     // no more CTAs on an SM than its tensor memory has columns for: a further one would wait for one to end
-    static constexpr int FLOOR = WG == 1 ? 47104 : 78848;
+    static constexpr int FLOOR = WG == 1 ? 59392 : 78848;
     static constexpr int SMEM = END > FLOOR ? END : FLOOR;
-    static constexpr int COLS = WG == 1 ? 128 : 256;      // tensor memory: operand, S, O
-    static constexpr int COL_S = 64, COL_O = 64 + NC;
+    static constexpr int COL_S = D / 2, COL_O = COL_S + NC;      // tensor memory: operand, S, O
+    static constexpr int COLS = WG == 1 ? 128 : 256;
+    static_assert(COL_O + ON <= COLS, "tensor memory");
 };
 
 // A sequence's visible pages: [0, a) and [w0, ...), np in all, two to a tile.
@@ -150,12 +158,23 @@ __device__ __forceinline__ uint32_t minus72(uint32_t s) {
 // Whether a query saw any token, from its reference and sum: a NaN among its scores never becomes the reference.
 __device__ __forceinline__ bool has_seen(float m, float sum) { return m > ATT_NONE || sum != sum; }
 
+// Without a time of its own: the waits here are short, and a sleep of a microsecond costs more than they do.
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(specv::smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits, as a warp, for a phase of `bar`, at most `tries` turns; where it gives up it sets the status bit and leaves 0 in
 // `tries`, so that later waits end at once (the results are invalid, but every barrier is still met). A try sleeps in
 // hardware until the phase ends or its time is up, so turns are few.
 __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int& tries, unsigned* status) {
     int left = tries;
-    while (!__all_sync(0xffffffffu, specv::mbar_try_wait_sleep(bar, parity, 1000))) {
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
         if (--left < 0) {
             if (tries) atomicOr(status, SPEC_STATUS_TIMEOUT);
             tries = 0;
@@ -207,33 +226,57 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// What the computing warps have to know of a tile, written by the fetching warp before the tile's copies.
+struct __align__(16) TileInfo {
+    int pos0, pos1;          // first position of its two pages, -1 where there is none
+    int b, h, r0, rows;      // sequence, key head, first row of the query block and its rows
+    int len, ql;
+    int flags, slot;         // where its part goes if the unit is cut
+    int before_all, seen_by_all;     // a page is seen whole by every query of the block if its first position is past
+                                     // the one and not past the other
+};
+constexpr int TILE_FIRST = 1, TILE_LAST = 2, TILE_ALONE = 4;    // of this CTA's part of the unit; the part is the unit
+
+// Named barriers: computing threads and the fetching warp (keys stored; probabilities stored, with a vote), computing
+// threads alone.
+constexpr int BAR_KEYS = 1, BAR_PROBS = 2, BAR_COMPUTE = 3;
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_vote(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
 template <class T, int D, int NC>
 __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Att<D, NC>;
     using BL = Block<D>;
-    constexpr int TH = C::TH, WG = C::WG, NW = C::NW, NG = BL::NG;
+    constexpr int TH = C::TH, CT = C::CT, WG = C::WG, NW = C::NW, NG = BL::NG;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_full[C::STAGES];
     __shared__ __align__(8) uint64_t s_bar_s, s_bar_o;
     __shared__ uint32_t s_tmem, s_c64;
-    __shared__ __align__(8) int2 s_pos[C::STAGES];       // first position of the tile's two pages, -1 where there is none
+    __shared__ TileInfo s_info[C::INFOS];
     __shared__ __align__(16) float s_c[NC], s_nm[NC];    // c_n, -m_n
     __shared__ __align__(16) float s_fac[NC];
     __shared__ float s_red[4][NC], s_sum[NC];
     __shared__ long long s_off[NC];                      // output row offset, -1: no such row
-    __shared__ int s_lse[NC];                            // lse index within the sequence, -1: a row past q_len
+    __shared__ int s_live[NC];                            // 1: a row, 0: a row past q_len or none
     __shared__ long long s_scan[TH / 32 + 1];
     __shared__ long long s_start;
     __shared__ int s_b;
-    struct Ahead {               // the copying thread's own: the next tile to copy, its pages' places and numbers, tiles issued
-        Cursor c;
-        int j0, j1, e0, e1, issued;
-    };
-    __shared__ Ahead s_next;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2, wq = warp & 3;
-    const int tok = wq * 32 + lane;                      // this thread's lane of tensor memory
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t sm = specv::smem_addr(smem);
 
     // ---- the CTA's run of tiles
@@ -245,15 +288,15 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     if (warp == 0) tmem_alloc(&s_tmem, C::COLS);
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) specv::mbar_init(&s_full[i], 1);
-        s_c64 = 0x54005400u;
         specv::mbar_init(&s_bar_s, 1);
         specv::mbar_init(&s_bar_o, 1);
         specv::fence_mbarrier_init_cluster();
+        s_c64 = 0x54005400u;
     }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tbase = s_tmem, c64 = *static_cast<volatile uint32_t*>(&s_c64), lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, s_tmem, 0);
     const long long per_t = static_cast<long long>(p.Hk) * p.RB;
     long long total = 0;
     for (int w = 0; w < TH / 32; ++w) total += s_scan[w];
@@ -289,355 +332,376 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
         }
     }
     __syncthreads();
-
-    Cursor cur = {};
-    if (lo < hi) {
-        cur.b = s_b;
-        cur.s = load_seq(p, cur.b, false);
-        const long long rem = lo - s_start;
-        const int unit = static_cast<int>(rem / cur.s.T);
-        cur.t = static_cast<int>(rem - static_cast<long long>(unit) * cur.s.T);
-        cur.h = unit / p.RB;
-        cur.rb = unit - cur.h * p.RB;
-    }
-
     const int tiles = static_cast<int>(hi - lo);
-
-    // ---- the copies (one thread of the last warp): tile k of the run into slot k mod STAGES. Page numbers are read one tile before they
-    // are needed.
-    auto look = [&] {
-        s_next.j0 = s_next.c.page_index(0);
-        s_next.j1 = s_next.c.page_index(1);
-        const int* const row = p.table + static_cast<size_t>(s_next.c.b) * p.max_pages;
-        s_next.e0 = s_next.j0 >= 0 ? row[s_next.j0] : -1;
-        s_next.e1 = s_next.j1 >= 0 ? row[s_next.j1] : -1;
-    };
-    auto issue = [&] {
-        const int st = s_next.issued % C::STAGES, j0 = s_next.j0, j1 = s_next.j1, e0 = s_next.e0, e1 = s_next.e1;
-        const bool v0 = e0 >= 0 && e0 < p.pages, v1 = e1 >= 0 && e1 < p.pages;
-        const uint64_t policy = p.RB == 1 ? specv::policy_evict_first() : specv::policy_evict_normal();
-        if ((j0 >= 0 && !v0) || (j1 >= 0 && !v1)) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
-        s_pos[st] = make_int2(v0 ? j0 * PAGE : -1, v1 ? j1 * PAGE : -1);
-        unsigned char* const dst = smem + st * C::TILE;
-        specv::mbar_arrive_expect_tx(&s_full[st], (v0 + v1) * BL::BYTES);
-        if (v0) specv::bulk_load(dst, p.pool + (static_cast<size_t>(e0) * p.Hk + s_next.c.h) * BL::BYTES, BL::BYTES, &s_full[st], policy);
-        if (v1)
-            specv::bulk_load(dst + BL::BYTES, p.pool + (static_cast<size_t>(e1) * p.Hk + s_next.c.h) * BL::BYTES, BL::BYTES,
-                             &s_full[st], policy);
-        if (++s_next.issued < tiles) {
-            s_next.c.next(p);
-            look();
-        }
-    };
     int tries = ATT_WAIT_TRIES;
-    const bool copier = tid == TH - 32;
-    if (copier && tiles > 0) {
-        s_next.c = cur;
-        s_next.issued = 0;
-        look();
-        for (int i = 0; i < C::STAGES && s_next.issued < tiles; ++i) issue();
-    }
-
     auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, tries, p.status); };
 
-    const uint32_t idesc = umma_idesc(NC);
-    constexpr uint32_t KSTRIDE = NC / 8 * 128;            // bytes between neighbouring runs of eight along K, both B operands
-    unsigned long long l[NW / 2];      // this thread's part of each query's sum
-    uint32_t par_s = 0, par_o = 0;
-    int t0 = 0;
-    int before_all = 0, seen_by_all = 0;      // a page is seen whole by every query of the block if its first position is
-                                              // past the one and not past the other
-    bool first = true;       // first tile of this CTA's part of a unit
-    int4 desc = make_int4(0, 0, 0, 0);
-
-    for (int k = 0; k < tiles; ++k) {
-        const Seq& s = cur.s;
-        const int st = k % C::STAGES;
-        const unsigned char* const tile = smem + st * C::TILE;
-        const int r0 = cur.rb * p.rpb, rows = min(p.rpb, p.N * p.G - r0);
-        if (first) {
-            // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
-            t0 = cur.t;
-            seen_by_all = s.len - s.ql + r0 / p.G - (PAGE - 1);
-            before_all = p.window == 0 ? -1 : static_cast<int>(max(-1LL, static_cast<long long>(s.len) - s.ql + (r0 + rows - 1) / p.G - p.window));
-            for (int n = warp; n < NC; n += TH / 32) {
-                const int r = r0 + n, i = r / p.G, hq = cur.h * p.G + (r - i * p.G);
-                const bool live = n < rows && i < s.ql;
-                constexpr int E = D / 32;         // lane: channels E lane ..
-                float x[E], top = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    x[e] = live ? static_cast<float>(static_cast<const T*>(p.q.p)[cur.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane + e]) : 0.f;
-                    top = fmaxf(top, fabsf(x[e]));
+    if (warp == CT / 32) {
+        // ================ the fetching warp: copies ahead, and both products of each tile
+        Cursor at = {};
+        if (tiles > 0) {
+            at.b = s_b;
+            at.s = load_seq(p, at.b, false);
+            const long long rem = lo - s_start;
+            const int unit = static_cast<int>(rem / at.s.T);
+            at.t = static_cast<int>(rem - static_cast<long long>(unit) * at.s.T);
+            at.h = unit / p.RB;
+            at.rb = unit - at.h * p.RB;
+        }
+        int4 desc = make_int4(0, 0, 0, 0);
+        int issued = 0, t0 = at.t;
+        // the unit's query block: first row, rows, and the positions between which a page is seen whole by all of it
+        int r0 = 0, rows = 0, before_all = 0, seen_by_all = 0;
+        auto enter = [&] {
+            r0 = at.rb * p.rpb;
+            rows = min(p.rpb, p.N * p.G - r0);
+            seen_by_all = at.s.len - at.s.ql + r0 / p.G - (PAGE - 1);
+            before_all = p.window == 0 ? -1 : static_cast<int>(max(-1LL, static_cast<long long>(at.s.len) - at.s.ql + (r0 + rows - 1) / p.G - p.window));
+        };
+        // lanes 0 and 1 have a page of the next tile each; their numbers are read one tile before they are needed
+        int j = -1, e = -1;
+        auto look = [&] {
+            j = lane < 2 ? at.page_index(lane) : -1;
+            e = j >= 0 ? p.table[static_cast<size_t>(at.b) * p.max_pages + j] : -1;
+        };
+        auto issue = [&] {
+            const int st = issued % C::STAGES;
+            const bool valid = e >= 0 && e < p.pages;
+            if (j >= 0 && !valid) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
+            const int pos = valid ? j * PAGE : -1;
+            const int pos1 = __shfl_sync(0xffffffffu, pos, 1);
+            const bool starts = t0 == 0, first = issued == 0 || at.t == 0, ends = at.t + 1 == at.s.T, last = ends || issued + 1 == tiles;
+            if (lane == 0) {
+                TileInfo& f = s_info[issued % C::INFOS];
+                f.pos0 = pos, f.pos1 = pos1;
+                f.b = at.b, f.h = at.h, f.r0 = r0, f.rows = rows;
+                f.len = at.s.len, f.ql = at.s.ql;
+                f.flags = (first ? TILE_FIRST : 0) | (last ? TILE_LAST : 0) | (starts && ends ? TILE_ALONE : 0);
+                f.slot = static_cast<int>(2 * g) + (starts ? 1 : 0);
+                f.before_all = before_all, f.seen_by_all = seen_by_all;
+                specv::mbar_arrive_expect_tx(&s_full[st], ((pos >= 0) + (pos1 >= 0)) * BL::BYTES);
+            }
+            __syncwarp();
+            if (valid) {
+                const uint64_t policy = p.RB == 1 ? specv::policy_evict_first() : specv::policy_evict_normal();
+                specv::bulk_load(smem + st * C::TILE + lane * BL::BYTES, p.pool + (static_cast<size_t>(e) * p.Hk + at.h) * BL::BYTES,
+                                 BL::BYTES, &s_full[st], policy);
+            }
+            if (last && starts && !ends) {       // the unit's tiles end in a later CTA
+                const long long end = lo + issued + (at.s.T - at.t);
+                desc = make_int4(at.b, at.h * p.RB + at.rb, static_cast<int>((end * A - 1) / total - g + 1), 0);
+            }
+            if (++issued < tiles) {
+                at.next(p);
+                if (at.t == 0) {
+                    t0 = 0;
+                    enter();
                 }
-                top = specv::warp_max(top);
-                const int ex = top > 0.f && top <= 3.4e38f ? min(max(10 - ilogbf(top), -120), 120) : 0;
+                look();
+            }
+            __syncwarp();
+        };
+        if (tiles > 0) {
+            enter();
+            look();
+            for (int i = 0; i < C::STAGES && issued < tiles; ++i) issue();
+        }
+        const uint32_t idesc_s = umma_idesc(NC), idesc_o = umma_idesc(C::ON) | UMMA_B_MN_MAJOR;
+        const uint64_t q_desc = umma_desc(sm + C::Q, C::KQ, 128), p_desc = umma_desc(sm + C::P, C::KP, 128);
+        for (int k = 0; k < tiles; ++k) {
+            const bool first = s_info[k % C::INFOS].flags & TILE_FIRST;
+            bar_sync(BAR_KEYS, TH);
+            tmem_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int d = E * lane + e, w8 = d & 7, at = (w8 & 3) * 2 + (w8 >> 2);     // 0 4 1 5 2 6 3 7
-                    *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * KSTRIDE + (n >> 3) * 128 + (n & 7) * 16 + at * 2) =
-                        __float2half_rn(ldexpf(x[e], ex));
+                for (int i = 0; i < D / 16; ++i) umma_ts(tbase + C::COL_S, tbase + 8 * i, q_desc + i * (2 * C::KQ >> 4), idesc_s, i > 0);
+                umma_commit(&s_bar_s);
+            }
+            __syncwarp();
+            while (bar_vote(BAR_PROBS, TH, false)) {}      // at most one turn: see the computing warps
+            tmem_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < C::OK / 16; ++i)
+                    umma_ts(tbase + C::COL_O, tbase + 8 * i, p_desc + i * (2 * C::KP >> 4), idesc_o, i > 0 || !first);
+                umma_commit(&s_bar_o);
+            }
+            __syncwarp();
+            if (issued < tiles) issue();       // into this tile's slot: its values were read before the vote
+        }
+        if (lane == 0) p.desc[g] = desc;
+        // no copy is in flight into this CTA's shared memory when it is given back, even where a wait gave up
+        for (int k = max(0, issued - C::STAGES); k < issued; ++k) wait(&s_full[k % C::STAGES], static_cast<uint32_t>(k / C::STAGES) & 1u);
+    } else {
+        // ================ the computing warps
+        const int wg = warp >> 2, wq = warp & 3;
+        const int tok = wq * 32 + lane;                      // this thread's lane of tensor memory
+        const uint32_t tlane = tbase + (static_cast<uint32_t>(wq * 32) << 16);
+        const uint32_t c64 = *static_cast<volatile uint32_t*>(&s_c64);
+        const uint32_t col_o = tlane + C::COL_O + (D == 64 && wq >= 2 ? NC : 0) + wg * NW;
+        unsigned long long l[NW / 2];      // this thread's part of each query's sum
+#pragma unroll
+        for (int n = 0; n < NW / 2; ++n) l[n] = 0ull;
+        for (int k = 0; k < tiles; ++k) {
+            const int st = k % C::STAGES;
+            const unsigned char* const tile = smem + st * C::TILE;
+            const TileInfo& f = s_info[k % C::INFOS];
+            wait(&s_full[st], static_cast<uint32_t>(k / C::STAGES) & 1u);
+            const int pos0 = f.pos0, pos1 = f.pos1, flags = f.flags;
+            if (flags & TILE_FIRST) {
+                // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
+                const int r0 = f.r0;
+                for (int n = warp; n < NC; n += CT / 32) {
+                    const int r = r0 + n, i = r / p.G, hq = f.h * p.G + (r - i * p.G);
+                    const bool row = n < f.rows, live = row && i < f.ql;
+                    constexpr int E = D / 32;         // lane: channels E lane ..
+                    float x[E], top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        x[e] = live ? static_cast<float>(static_cast<const T*>(p.q.p)[f.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane + e]) : 0.f;
+                        top = fmaxf(top, fabsf(x[e]));
+                    }
+                    top = specv::warp_max(top);
+                    const int ex = top > 0.f && top <= 3.4e38f ? min(max(10 - ilogbf(top), -120), 120) : 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int d = E * lane + e, w8 = d & 7, to = (w8 & 3) * 2 + (w8 >> 2);     // 0 4 1 5 2 6 3 7
+                        *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * C::KQ + (n >> 3) * 128 + (n & 7) * 16 + to * 2) =
+                            __float2half_rn(ldexpf(x[e], ex));
+                    }
+                    if (lane == 0) {
+                        s_c[n] = live ? ldexpf(p.scale, -ex) : 0.f;
+                        s_nm[n] = -ATT_NONE;
+                        s_off[n] = row ? i * p.out.sn + hq * p.out.sh : -1;
+                        s_live[n] = live;
+                    }
                 }
-                if (lane == 0) {
-                    s_c[n] = live ? ldexpf(p.scale, -ex) : 0.f;
-                    s_nm[n] = -ATT_NONE;
-                    s_off[n] = n < rows ? i * p.out.sn + hq * p.out.sh : -1;
-                    s_lse[n] = live ? i * p.Hq + hq : -1;
+                specv::fence_proxy_async_shared();
+                bar_sync(BAR_COMPUTE, CT);
+            }
+            // ---- the scales of this warp's values: a lane has four tokens of the warp's group, pairs (0, 2) and (1, 3)
+            unsigned char* const vs = smem + C::VS + warp * C::WORDS * 16;
+            if (lane < C::WORDS) {
+                const int q = wg * C::WORDS + lane, page = D == 128 ? q / 16 : wq >> 1, t4 = (4 * q) % PAGE, gr = wq % NG;
+                const int from = page ? pos1 : pos0, left = from >= 0 ? f.len - from - t4 : 0;      // tokens that hold something
+                const unsigned char* const b = tile + page * BL::BYTES + BL::VS + t4 * NG + gr;
+                const uint32_t s02 = (left > 0 ? b[0] * 0x80u : 0u) | (left > 2 ? b[2 * NG] * 0x800000u : 0u);
+                const uint32_t s13 = (left > 1 ? b[NG] * 0x80u : 0u) | (left > 3 ? b[3 * NG] * 0x800000u : 0u);
+                *reinterpret_cast<uint4*>(vs + lane * 16) = make_uint4(s02, minus72(s02), s13, minus72(s13));
+            }
+            // ---- keys to halves: this thread's token, this warpgroup's groups
+            {
+                const int t = tok % PAGE;
+                const unsigned char* const blk = tile + (tok / PAGE) * BL::BYTES;
+#pragma unroll
+                for (int i = 0; i < NG / WG; ++i) {
+                    const int gr = wg * (NG / WG) + i;
+                    const uint4 v = *reinterpret_cast<const uint4*>(blk + BL::key(gr, t));
+                    const uint32_t s2 = blk[BL::KS + t * NG + gr] * 0x00800080u, o2 = minus72(s2);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t kr[16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t hi8 = w[q] >> 8;
+                        kr[4 * q] = half_code(c64, w[q] * p.sixteen, s2, o2);
+                        kr[4 * q + 1] = half_code(c64, w[q], s2, o2);
+                        kr[4 * q + 2] = half_code(c64, hi8 * p.sixteen, s2, o2);
+                        kr[4 * q + 3] = half_code(c64, hi8, s2, o2);
+                    }
+                    if (i == 0 && !(flags & TILE_FIRST)) {       // the tile before's values are read, their columns are free
+                        wait(&s_bar_o, (k - 1) & 1);
+                        tmem_fence_after();
+                    }
+                    tmem_st16(tlane + 16 * gr, kr);
                 }
             }
+            tmem_wait_st();
+            tmem_fence_before();
+            bar_arrive(BAR_KEYS, TH);
+            // ---- values to halves, the first part of the tokens while the first product runs
+            uint32_t vr[2 * C::WPP];
+            auto values = [&](int part) {
+                const bool upper = D == 128 ? wq >> 1 : wq & 1;
+                const uint32_t up = upper ? 1u : p.sixteen;
+                const int r = D == 128 ? (wq & 1) * 32 + lane : lane;
 #pragma unroll
-            for (int n = 0; n < NW / 2; ++n) l[n] = 0ull;
-            specv::fence_proxy_async_shared();
-        }
-        // ---- S = K Q: the keys' halves, this thread's token and this warpgroup's groups
-        wait(&s_full[st], static_cast<uint32_t>(k / C::STAGES) & 1u);
-        const int2 pos2 = s_pos[st];
-        if (tid < 32 * NG) {      // the values' scales: four tokens of one group, pairs (0, 2) and (1, 3)
-            const int q = tid / NG, gr = tid % NG, page = q / 16, t4 = (4 * q) % PAGE, from = page ? pos2.y : pos2.x;
-            const unsigned char* const vs = tile + page * BL::BYTES + BL::VS + t4 * NG + gr;
-            uint32_t b[4];
+                for (int u = 0; u < C::WPP / 4; ++u) {
+                    const int run = wg * (C::WORDS / 4) + part * (C::WPP / 4) + u, page = D == 128 ? run / 4 : wq >> 1;
+                    const uint4 v = *reinterpret_cast<const uint4*>(tile + page * BL::BYTES + BL::value((run % 4) * 16, r));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) b[r] = from >= 0 && from + t4 + r < s.len ? static_cast<uint32_t>(vs[r * NG]) << 7 : 0u;
-            const uint32_t s02 = b[0] | b[2] << 16, s13 = b[1] | b[3] << 16;
-            *reinterpret_cast<uint4*>(smem + C::VS + (q * NG + gr) * 16) = make_uint4(s02, minus72(s02), s13, minus72(s13));
-        }
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 sc = *reinterpret_cast<const uint4*>(vs + (part * C::WPP + 4 * u + q) * 16);
+                        const uint32_t y = w[q] * up;
+                        vr[8 * u + 2 * q] = half_code(c64, y, sc.x, sc.y);
+                        vr[8 * u + 2 * q + 1] = half_code(c64, y >> 8, sc.z, sc.w);
+                    }
+                }
+            };
+            auto put_values = [&](int part) {
 #pragma unroll
-        for (int i = 0; i < NG / WG; ++i) {
-            const int gr = wg * (NG / WG) + i, t = tok % PAGE;
-            const unsigned char* const blk = tile + (tok / PAGE) * BL::BYTES;
-            const uint4 v = *reinterpret_cast<const uint4*>(blk + BL::key(gr, t));
-            const uint32_t s2 = blk[BL::KS + t * NG + gr] * 0x00800080u, o2 = minus72(s2);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t kr[16];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                kr[4 * q] = half_code(c64, w[q] * p.sixteen, s2, o2);
-                kr[4 * q + 1] = half_code(c64, w[q], s2, o2);
-                kr[4 * q + 2] = half_code(c64, (w[q] >> 8) * p.sixteen, s2, o2);
-                kr[4 * q + 3] = half_code(c64, w[q] >> 8, s2, o2);
+                for (int i = 0; i < 2 * C::WPP / 16; ++i)
+                    tmem_st16(tlane + 2 * (wg * C::WORDS + part * C::WPP) + 16 * i, vr + 16 * i);
+            };
+            __syncwarp();        // the warp's scales are written
+            values(0);
+            wait(&s_bar_s, k & 1);
+            tmem_fence_after();
+            put_values(0);
+            if (C::VP == 2) {
+                values(1);
+                put_values(1);
             }
-            if (i == 0 && !first) {       // the values' operand of the tile before is read, its columns are free
-                wait(&s_bar_o, par_o);
-                par_o ^= 1;
+            // ---- which queries see this thread's token: all of them where the whole tile is seen by all
+            const bool whole = min(pos0, pos1) > f.before_all && max(pos0, pos1) <= f.seen_by_all;
+            uint32_t seen = 0xFFFFFFFFu;
+            if (!whole) {
+                const int from = tok < PAGE ? pos0 : pos1, at = from + tok % PAGE, base = f.len - f.ql;
+                int nlo = 0, nhi = 0;
+                if (from >= 0 && at < f.len) {
+                    nlo = max(at - base, 0) * p.G - f.r0;
+                    nhi = NC;
+                    if (p.window > 0 && at >= p.sinks)
+                        nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - f.r0;
+                }
+                seen = bit_range(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
+            }
+            unsigned long long x[NW / 2];
+            for (bool move = flags & TILE_FIRST;; move = true) {
+                uint32_t u[NW];
+                tmem_ld(tlane + C::COL_S + wg * NW, u);
+                if (move) {
+                    // the references move to the maxima seen so far; l and, unless this is the part's first tile, O follow
+                    float y[NW];
+                    const uint32_t bits = here(seen);
+#pragma unroll
+                    for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1u ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
+                    const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < NW) s_red[wq][wg * NW + lane] = top;
+                    bar_sync(BAR_COMPUTE, CT);
+                    if (tid < NC) {
+                        const float old = -s_nm[tid];
+                        const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
+                        s_fac[tid] = specv::ex2(old - now);
+                        s_nm[tid] = -now;
+                    }
+                    bar_sync(BAR_COMPUTE, CT);
+#pragma unroll
+                    for (int n = 0; n < NW / 2; ++n) l[n] = mul2(l[n], *reinterpret_cast<const unsigned long long*>(&s_fac[wg * NW + 2 * n]));
+                    if (!(flags & TILE_FIRST)) {
+#pragma unroll
+                        for (int i = 0; i < NW / 16; ++i) {
+                            uint32_t o[16];
+                            tmem_ld(col_o + 16 * i, o);
+#pragma unroll
+                            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[wg * NW + 16 * i + n]);
+                            tmem_st16(col_o + 16 * i, o);
+                        }
+                    }
+                }
+                // this token's probabilities, to shared memory as the second product's operand
+                float over = -INFINITY;
+                const int pt = tok % C::OK, pos = (pt & ~3) + ((pt & 1) << 1) + ((pt >> 1) & 1);       // 0 2 1 3 in each four
+                unsigned char* const row = smem + C::P + (pos >> 3) * C::KP + (pos & 7) * 16 + ((D == 64 ? tok / PAGE * NC : 0) + wg * NW) / 8 * 128;
+#pragma unroll
+                for (int n = 0; n < NW; n += 4) {
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[wg * NW + n]);
+                    const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&s_nm[wg * NW + n]);
+                    x[n / 2] = fma2(pack2(__uint_as_float(u[n]), __uint_as_float(u[n + 1])), c.x, m.x);
+                    x[n / 2 + 1] = fma2(pack2(__uint_as_float(u[n + 2]), __uint_as_float(u[n + 3])), c.y, m.y);
+                }
+                if (!whole) {
+                    const uint32_t bits = here(seen);
+#pragma unroll
+                    for (int n = 0; n < NW; n += 2) {
+                        const float2 v = unpack2(x[n / 2]);
+                        x[n / 2] = pack2(bits >> n & 1u ? v.x : -INFINITY, bits >> (n + 1) & 1u ? v.y : -INFINITY);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NW; n += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 v = unpack2(x[n / 2 + q]);
+                        over = max3(over, v.x, v.y);
+                        const float e0 = specv::ex2(v.x), e1 = specv::ex2(v.y);
+                        x[n / 2 + q] = pack2(e0, e1);
+                        const __half2 hv = __floats2half2_rn(e0, e1);
+                        h[q] = *reinterpret_cast<const uint32_t*>(&hv);
+                    }
+                    *reinterpret_cast<uint4*>(row + (n / 8) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                tmem_wait_st();
+                specv::fence_proxy_async_shared();
+                tmem_fence_before();
+                // a score that passed its reference by too much: once more, with the references moved (after which none does)
+                if (!bar_vote(BAR_PROBS, TH, !move && over > ATT_SLACK)) break;
                 tmem_fence_after();
             }
-            tmem_st16(tbase + lane_base + 16 * gr, kr);
-        }
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tmem_fence_after();
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                umma_ts(tbase + C::COL_S, tbase + 8 * i, umma_desc(sm + C::Q + 2 * i * KSTRIDE, KSTRIDE, 128), idesc, i > 0);
-            umma_commit(&s_bar_s);
-        }
-        __syncwarp();
-        // ---- values to halves, the first half of the tokens while the product runs
-        const bool has_v = D == 128 || wq < 2;
-        uint32_t vr[32 / WG];
-        auto values = [&](int part) {
-            const bool half = D == 128 ? wq >> 1 : wq;
-            const uint32_t up = half ? 1u : p.sixteen;
-            const int r = D == 128 ? (wq & 1) * 32 + lane : lane;
+            for (int n = 0; n < NW / 2; ++n) l[n] = add2(l[n], x[n]);
+            if (flags & TILE_LAST) {
+                // ---- the part's end: O and the sums out
+                wait(&s_bar_o, k & 1);
+                tmem_fence_after();
+                float lf[NW];
 #pragma unroll
-            for (int u = 0; u < 4 / WG; ++u) {
-                const int run = wg * (8 / WG) + part * (4 / WG) + u;
-                const uint4 v = *reinterpret_cast<const uint4*>(tile + (run / 4) * BL::BYTES + BL::value((run % 4) * 16, r));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 sc = *reinterpret_cast<const uint4*>(smem + C::VS + ((run * 4 + q) * NG + wq % NG) * 16);
-                    const uint32_t y = w[q] * up;
-                    vr[8 * u + 2 * q] = half_code(c64, y, sc.x, sc.y);
-                    vr[8 * u + 2 * q + 1] = half_code(c64, y >> 8, sc.z, sc.w);
+                for (int n = 0; n < NW / 2; ++n) {
+                    const float2 v = unpack2(l[n]);
+                    lf[2 * n] = v.x, lf[2 * n + 1] = v.y;
+                    l[n] = 0ull;
                 }
-            }
-        };
-        auto put_values = [&](int part) {
-#pragma unroll
-            for (int i = 0; i < 2 / WG; ++i) tmem_st16(tbase + lane_base + 16 * ((2 * wg + part) * (2 / WG) + i), vr + 16 * i);
-        };
-        if (has_v) values(0);
-        wait(&s_bar_s, par_s);
-        par_s ^= 1;
-        tmem_fence_after();
-        if (has_v) {
-            put_values(0);
-            values(1);
-            put_values(1);
-        }
-        // ---- which queries see this thread's token: [nlo, nhi); all of them where the whole tile is seen by all
-        const int at0 = tok < PAGE ? pos2.x : pos2.y;
-        const bool whole = min(pos2.x, pos2.y) > before_all && max(pos2.x, pos2.y) <= seen_by_all;
-        int nlo = 0, nhi = NC;
-        if (!whole) {
-            const int base = s.len - s.ql, at = at0 + tok % PAGE;
-            if (at0 < 0 || at >= s.len) {
-                nhi = 0;
-            } else {
-                nlo = max(at - base, 0) * p.G - r0;
-                if (p.window > 0 && at >= p.sinks)
-                    nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - r0;
-            }
-        }
-        const uint32_t seen = bit_range(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
-        unsigned long long x[NW / 2];
-        for (bool move = first;; move = true) {
-            uint32_t u[NW];
-            tmem_ld(tbase + lane_base + C::COL_S + wg * NW, u);
-            if (move) {
-                // the references move to the maxima seen so far; l and, unless this is the unit's first tile, O follow
-                float y[NW];
-                const uint32_t bits = here(seen);
-#pragma unroll
-                for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1u ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
-                const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
-                if (lane < NW) s_red[wq][wg * NW + lane] = top;
-                __syncthreads();
-                if (tid < NC) {
-                    const float old = -s_nm[tid];
-                    const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
-                    s_fac[tid] = specv::ex2(old - now);
-                    s_nm[tid] = -now;
-                }
-                __syncthreads();
-#pragma unroll
-                for (int n = 0; n < NW / 2; ++n) l[n] = mul2(l[n], *reinterpret_cast<const unsigned long long*>(&s_fac[wg * NW + 2 * n]));
-                if (!first) {
+                const float sum = fold_columns(lf, lane, [](float a, float b) { return a + b; });
+                if (lane < NW) s_red[wq][wg * NW + lane] = sum;
+                if (D == 64 && wq >= 2) {      // the second page's share of O, to the lanes that write
 #pragma unroll
                     for (int i = 0; i < NW / 16; ++i) {
                         uint32_t o[16];
-                        const uint32_t a = tbase + lane_base + C::COL_O + wg * NW + 16 * i;
-                        tmem_ld(a, o);
+                        tmem_ld(col_o + 16 * i, o);
 #pragma unroll
-                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[wg * NW + 16 * i + n]);
-                        tmem_st16(a, o);
+                        for (int q = 0; q < 16; ++q)
+                            *reinterpret_cast<uint32_t*>(smem + C::P + ((wg * NW + 16 * i + q) * 64 + tok - 64) * 4) = o[q];
                     }
                 }
-            }
-            // this token's probabilities, to shared memory as the second product's operand
-            float over = -INFINITY;
-            const int pos = (tok & ~3) + ((tok & 1) << 1) + ((tok >> 1) & 1);       // 0 2 1 3 in each four
-            unsigned char* const row = smem + C::P + (pos >> 3) * KSTRIDE + (pos & 7) * 16 + wg * (NW / 8) * 128;
+                bar_sync(BAR_COMPUTE, CT);
+                if (tid < NC) s_sum[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+                bar_sync(BAR_COMPUTE, CT);
+                const bool alone = flags & TILE_ALONE;
+                if (D == 128 || wq < 2) {
+                    T* const out = static_cast<T*>(p.out.p) + f.b * p.out.sb + tok;
+                    float* const part = p.part_o + static_cast<size_t>(f.slot) * NC * D + tok;
 #pragma unroll
-            for (int n = 0; n < NW; n += 4) {
-                const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s_c[wg * NW + n]);
-                const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&s_nm[wg * NW + n]);
-                x[n / 2] = fma2(pack2(__uint_as_float(u[n]), __uint_as_float(u[n + 1])), c.x, m.x);
-                x[n / 2 + 1] = fma2(pack2(__uint_as_float(u[n + 2]), __uint_as_float(u[n + 3])), c.y, m.y);
-            }
-            if (!whole) {
-                const uint32_t bits = here(seen);
+                    for (int i = 0; i < NW / 16; ++i) {
+                        uint32_t o[16];
+                        tmem_ld(col_o + 16 * i, o);
 #pragma unroll
-                for (int n = 0; n < NW; n += 2) {
-                    const float2 v = unpack2(x[n / 2]);
-                    x[n / 2] = pack2(bits >> n & 1u ? v.x : -INFINITY, bits >> (n + 1) & 1u ? v.y : -INFINITY);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NW; n += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float2 v = unpack2(x[n / 2 + q]);
-                    over = max3(over, v.x, v.y);
-                    const float e0 = specv::ex2(v.x), e1 = specv::ex2(v.y);
-                    x[n / 2 + q] = pack2(e0, e1);
-                    const __half2 hv = __floats2half2_rn(e0, e1);
-                    h[q] = *reinterpret_cast<const uint32_t*>(&hv);
-                }
-                *reinterpret_cast<uint4*>(row + (n / 8) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            tmem_wait_st();
-            specv::fence_proxy_async_shared();
-            tmem_fence_before();
-            // a score that passed its reference by too much: once more, with the references moved (after which none does)
-            if (!__syncthreads_or(!move && over > ATT_SLACK)) break;
-            tmem_fence_after();
-        }
-#pragma unroll
-        for (int n = 0; n < NW / 2; ++n) l[n] = add2(l[n], x[n]);
-        // ---- O += V P; the tile's slot is free for the copy two tiles on
-        if (tid == 0) {
-            tmem_fence_after();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                umma_ts(tbase + C::COL_O, tbase + 8 * i, umma_desc(sm + C::P + 2 * i * KSTRIDE, KSTRIDE, 128),
-                        idesc | UMMA_B_MN_MAJOR, !(first && i == 0));
-            umma_commit(&s_bar_o);
-        }
-        if (copier && s_next.issued < tiles && tries) issue();
-        __syncwarp();
-        const bool unit_ends = cur.t + 1 == s.T;
-        if (!unit_ends && k + 1 < tiles) {
-            first = false;
-        } else {
-            // ---- the part's end: O and the sums out
-            wait(&s_bar_o, par_o);
-            par_o ^= 1;
-            tmem_fence_after();
-            float lf[NW];
-#pragma unroll
-            for (int n = 0; n < NW / 2; ++n) {
-                const float2 v = unpack2(l[n]);
-                lf[2 * n] = v.x, lf[2 * n + 1] = v.y;
-            }
-            const float sum = fold_columns(lf, lane, [](float a, float b) { return a + b; });
-            if (lane < NW) s_red[wq][wg * NW + lane] = sum;
-            __syncthreads();
-            if (tid < NC) s_sum[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
-            __syncthreads();
-            const bool alone = t0 == 0 && unit_ends;
-            const long long slot = 2 * g + (t0 == 0 ? 1 : 0);
-            if (!alone && t0 == 0) {
-                const long long end = lo + k + (s.T - cur.t);       // the unit's tiles end there
-                desc = make_int4(cur.b, cur.h * p.RB + cur.rb, static_cast<int>((end * A - 1) / total - g + 1), 0);
-            }
-            if (has_v) {
-                const int d = tok;
-                T* const out = static_cast<T*>(p.out.p) + cur.b * p.out.sb + d;
-                float* const part = p.part_o + slot * NC * D + d;
-#pragma unroll
-                for (int i = 0; i < NW / 16; ++i) {
-                    uint32_t u[16];
-                    tmem_ld(tbase + lane_base + C::COL_O + wg * NW + 16 * i, u);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const int n = wg * NW + 16 * i + q;
-                        if (s_off[n] < 0) continue;
-                        const float o = __uint_as_float(u[q]);
-                        if (alone) out[s_off[n]] = static_cast<T>(s_lse[n] >= 0 && has_seen(-s_nm[n], s_sum[n]) ? o / s_sum[n] : 0.f);
-                        else part[n * D] = o;
+                        for (int q = 0; q < 16; ++q) {
+                            const int n = wg * NW + 16 * i + q;
+                            if (s_off[n] < 0) continue;
+                            float v = __uint_as_float(o[q]);
+                            if (D == 64) v += *reinterpret_cast<const float*>(smem + C::P + (n * 64 + tok) * 4);
+                            if (alone) out[s_off[n]] = static_cast<T>(s_live[n] && has_seen(-s_nm[n], s_sum[n]) ? v / s_sum[n] : 0.f);
+                            else part[n * D] = v;
+                        }
                     }
                 }
-            }
-            if (tid < NC && s_off[tid] >= 0) {
-                const bool seen = s_lse[tid] >= 0 && has_seen(-s_nm[tid], s_sum[tid]);
-                if (!alone) {
-                    p.part_ml[slot * NC + tid] = make_float2(-s_nm[tid], s_sum[tid]);
-                } else if (p.lse) {
-                    const int r = r0 + tid, i = r / p.G;
-                    p.lse[(static_cast<long long>(cur.b) * p.N + i) * p.Hq + cur.h * p.G + (r - i * p.G)] =
-                        seen ? (log2f(s_sum[tid]) - s_nm[tid]) * 0.6931471805599453f : -INFINITY;
+                if (tid < NC && s_off[tid] >= 0) {
+                    if (!alone) {
+                        p.part_ml[static_cast<size_t>(f.slot) * NC + tid] = make_float2(-s_nm[tid], s_sum[tid]);
+                    } else if (p.lse) {
+                        const int r = f.r0 + tid, i = r / p.G;
+                        p.lse[(static_cast<long long>(f.b) * p.N + i) * p.Hq + f.h * p.G + (r - i * p.G)] =
+                            s_live[tid] && has_seen(-s_nm[tid], s_sum[tid]) ? (log2f(s_sum[tid]) - s_nm[tid]) * 0.6931471805599453f : -INFINITY;
+                    }
                 }
+                tmem_fence_before();
+                bar_sync(BAR_COMPUTE, CT);      // the queries' and sums' shared memory is free again
+                tmem_fence_after();
             }
-            first = true;
-            tmem_fence_before();
-            __syncthreads();      // the queries' and sums' shared memory is free again
-            tmem_fence_after();
         }
-        cur.next(p);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) p.desc[g] = desc;
-    if (warp == TH / 32 - 1 && !tries) {      // (a wait gave up) copies still in flight into this CTA's shared memory
-        const int issued = __shfl_sync(0xffffffffu, s_next.issued, 0);
-        tries = ATT_WAIT_TRIES;
-        for (int k = max(0, issued - C::STAGES); k < issued; ++k)
-            wait(&s_full[k % C::STAGES], static_cast<uint32_t>(k / C::STAGES) & 1u);
-    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
