@@ -27,6 +27,8 @@
 // of which each CTA takes an equal run. A unit that is cut leaves partial (O, m, l) in the workspace, and a second kernel
 // joins them in a fixed order.
 #pragma once
+#include <type_traits>
+
 #include "cache_format.cuh"
 #include "tmem.cuh"
 
@@ -45,23 +47,26 @@ struct AttnParams {
     float* lse;
     unsigned* status;
     int4* desc;              // per CTA: the cut unit that starts in it: sequence, head RB + block, parts (0: none)
-    float2* part_ml;         // [2 CTAs][NC] (reference, sum)
-    float* part_o;           // [2 CTAs][NC][D]
+    float2* part_ml;         // [2 CTAs][width] (reference, sum)
+    float* part_o;           // [2 CTAs][width][D]
     int pages, max_pages, B, N, Hq, Hk, G, window, sinks;
     int RB, rpb;             // query blocks and rows of each
+    int width, fp16;         // queries of a part in the workspace; activations in fp16 (else bf16)
     float scale;             // times log2 e
     // 16, as a value that the compiler does not know: x 16 then stays a multiplication, for which there is more room
     // than for shifts
     uint32_t sixteen;
 };
 
-template <int D, int NC>
+// WG warpgroups share a tile's tokens, each with NW of the queries.
+template <int D, int WG_, int NW_>
 struct Att {
-    static constexpr int WG = NC > 32 ? 2 : 1, CTAS = WG == 1 ? 3 : 2;
+    static constexpr int WG = WG_, NW = NW_;
+    static constexpr int CTAS = WG == 2 ? 2 : NW <= 24 ? 4 : 3;      // on an SM, as registers allow
     static constexpr int CT = 128 * WG, TH = CT + 32;     // computing threads; one more warp fetches and issues products
-    static constexpr int NW = NC / WG;                    // queries of a thread
+    static constexpr int NQ = WG * NW, NC = (NQ + 15) / 16 * 16;     // queries, and the products' width for them
     static constexpr int TILE = 2 * Block<D>::BYTES;
-    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : 3, INFOS = 2 * STAGES;
+    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : CTAS == 4 ? 2 : 3, INFOS = 2 * STAGES;
     // the second product: D = 128, 128 channels by 128 tokens; D = 64, both pages' channels as 128 rows by 64 tokens, each
     // page's probabilities in columns of their own (half of the result is of no use, but all warps have values to convert)
     static constexpr int ON = D == 128 ? NC : 2 * NC, OK = D == 128 ? 128 : 64;
@@ -73,11 +78,11 @@ struct Att {
     static constexpr int VS = Q + NC * D * 2;
     static constexpr int END = VS + CT / 32 * WORDS * 16;
     // no more CTAs on an SM than its tensor memory has columns for: a further one would wait for one to end
-    static constexpr int FLOOR = WG == 1 ? 59392 : 78848;
+    static constexpr int FLOOR = CTAS == 2 ? 78848 : CTAS == 3 ? 59392 : 47104;
     static constexpr int SMEM = END > FLOOR ? END : FLOOR;
     static constexpr int COL_S = D / 2, COL_O = COL_S + NC;      // tensor memory: operand, S, O
     static constexpr int COLS = WG == 1 ? 128 : 256;
-    static_assert(COL_O + ON <= COLS, "tensor memory");
+    static_assert(COL_O + ON <= COLS && COLS * CTAS <= 512, "tensor memory");
 };
 
 // A sequence's visible pages: [0, a) and [w0, ...), np in all, two to a tile.
@@ -122,12 +127,13 @@ struct Cursor {
     }
 };
 
-// Sums (or maxima) of v[0 .. W) over the warp's lanes: lane i ends with that of column i mod W. Halving exchanges: 31
-// shuffles for 32 columns.
+// Sums (or maxima) of each of v[0 .. W) over the warp's lanes, to out[0 .. W). Halving exchanges, 31 shuffles for 32
+// columns: 32, 16 or 8 at a time.
 template <int W, class Op>
-__device__ __forceinline__ float fold_columns(float (&v)[W], int lane, Op op) {
+__device__ __forceinline__ void fold_columns(float (&v)[W], int lane, float* out, Op op) {
+    constexpr int B = W >= 32 ? 32 : W >= 16 ? 16 : 8;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
+    for (int o = B / 2; o > 0; o >>= 1) {
 #pragma unroll
         for (int k = 0; k < o; ++k) {
             const bool up = lane & o;
@@ -136,8 +142,30 @@ __device__ __forceinline__ float fold_columns(float (&v)[W], int lane, Op op) {
         }
     }
 #pragma unroll
-    for (int o = W; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    return v[0];
+    for (int o = B; o < 32; o <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    if (lane < B) out[lane] = v[0];
+    if constexpr (W > B) {
+        float rest[W - B];
+#pragma unroll
+        for (int k = 0; k < W - B; ++k) rest[k] = v[B + k];
+        fold_columns(rest, lane, out + B, op);
+    }
+}
+
+// W columns of this thread's lane: 8, 16, 24, 32 or 40.
+template <int W>
+__device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[W]) {
+    constexpr int B = W >= 32 ? 32 : W >= 16 ? 16 : 8;
+    uint32_t part[B];
+    tmem_ld(a, part);
+#pragma unroll
+    for (int k = 0; k < B; ++k) v[k] = part[k];
+    if constexpr (W > B) {
+        uint32_t rest[W - B];
+        tmem_load<W - B>(a + B, rest);
+#pragma unroll
+        for (int k = 0; k < W - B; ++k) v[B + k] = rest[k];
+    }
 }
 
 // Two codes, in bits 4 .. 7 of x's halves, as halves (c - 8) s; o = -72 s. One logic instruction and one multiply-add;
@@ -183,15 +211,31 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int& 
     }
 }
 
-// Bits [lo, hi) of 32, the ends clamped.
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-    const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : hi > 0 ? (1u << hi) - 1u : 0u;
-    return lo >= 32 ? 0u : lo > 0 ? below_hi & (0xFFFFFFFFu << lo) : below_hi;
+// Bits [lo, hi) of a word, the ends clamped.
+template <class U>
+__device__ __forceinline__ U bit_range(int lo, int hi) {
+    constexpr int W = 8 * sizeof(U);
+    const U below_hi = hi >= W ? ~U(0) : hi > 0 ? (U(1) << hi) - 1 : U(0);
+    return lo >= W ? U(0) : lo > 0 ? below_hi & (~U(0) << lo) : below_hi;
 }
 // The same value, tied to this place: keeps what is worked out from it inside its branch.
 __device__ __forceinline__ uint32_t here(uint32_t v) {
     asm volatile("" : "+r"(v));
     return v;
+}
+__device__ __forceinline__ unsigned long long here(unsigned long long v) {
+    asm volatile("" : "+l"(v));
+    return v;
+}
+
+// Two neighbouring bf16 or fp16 values, and back (rounded to nearest).
+__device__ __forceinline__ float2 two_of(uint32_t v, int fp16) {
+    if (fp16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ unsigned short one_out(float v, int fp16) {
+    if (fp16) return __half_as_ushort(__float2half_rn(v));
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // Two fp32 values in one 64-bit register pair: one instruction for both.
@@ -256,12 +300,13 @@ __device__ __forceinline__ bool bar_vote(int id, int threads, bool v) {
     return r != 0;
 }
 
-template <class T, int D, int NC>
-__global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
+template <int D, int WG, int NW>
+__global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
-    using C = Att<D, NC>;
+    using C = Att<D, WG, NW>;
     using BL = Block<D>;
-    constexpr int TH = C::TH, CT = C::CT, WG = C::WG, NW = C::NW, NG = BL::NG;
+    using Bits = std::conditional_t<(NW > 32), unsigned long long, uint32_t>;      // one for each query of a thread
+    constexpr int TH = C::TH, CT = C::CT, NC = C::NC, NQ = C::NQ, NG = BL::NG;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_full[C::STAGES];
     __shared__ __align__(8) uint64_t s_bar_s, s_bar_o;
@@ -269,7 +314,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
     __shared__ TileInfo s_info[C::INFOS];
     __shared__ __align__(16) float s_c[NC], s_nm[NC];    // c_n, -m_n
     __shared__ __align__(16) float s_fac[NC];
-    __shared__ float s_red[4][NC], s_sum[NC];
+    __shared__ float s_red[4][NC], s_inv[NC];
     __shared__ long long s_off[NC];                      // output row offset, -1: no such row
     __shared__ int s_live[NC];                            // 1: a row, 0: a row past q_len or none
     __shared__ long long s_scan[TH / 32 + 1];
@@ -450,31 +495,43 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
             const int pos0 = f.pos0, pos1 = f.pos1, flags = f.flags;
             if (flags & TILE_FIRST) {
                 // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
-                const int r0 = f.r0;
-                for (int n = warp; n < NC; n += CT / 32) {
-                    const int r = r0 + n, i = r / p.G, hq = f.h * p.G + (r - i * p.G);
+                constexpr int E = D / 32, NR = NQ / (CT / 32);         // lane: channels E lane ..; the warp's rows
+                uint32_t raw[NR][E / 2];
+#pragma unroll
+                for (int m = 0; m < NR; ++m) {
+                    const int n = warp + m * (CT / 32), r = f.r0 + n, i = r / p.G, hq = f.h * p.G + (r - i * p.G);
                     const bool row = n < f.rows, live = row && i < f.ql;
-                    constexpr int E = D / 32;         // lane: channels E lane ..
+                    const uint32_t* const q = reinterpret_cast<const uint32_t*>(
+                        static_cast<const unsigned char*>(p.q.p) + 2 * (f.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane));
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) raw[m][e] = live ? q[e] : 0u;
+                    if (lane == 0) {
+                        s_off[n] = row ? i * p.out.sn + hq * p.out.sh : -1;
+                        s_live[n] = live;
+                        s_nm[n] = -ATT_NONE;
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < NR; ++m) {
+                    const int n = warp + m * (CT / 32);
                     float x[E], top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        x[e] = live ? static_cast<float>(static_cast<const T*>(p.q.p)[f.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane + e]) : 0.f;
-                        top = fmaxf(top, fabsf(x[e]));
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 v = two_of(raw[m][e / 2], p.fp16);
+                        x[e] = v.x, x[e + 1] = v.y;
+                        top = max3(top, fabsf(v.x), fabsf(v.y));
                     }
                     top = specv::warp_max(top);
-                    const int ex = top > 0.f && top <= 3.4e38f ? min(max(10 - ilogbf(top), -120), 120) : 0;
+                    // 2^ex brings the largest magnitude to 2^10 .. 2^11 (and an infinite one nowhere)
+                    const int ex = top > 0.f && top <= 3.4e38f ? 137 - max(static_cast<int>(__float_as_uint(top) >> 23), 20) : 0;
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         const int d = E * lane + e, w8 = d & 7, to = (w8 & 3) * 2 + (w8 >> 2);     // 0 4 1 5 2 6 3 7
                         *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * C::KQ + (n >> 3) * 128 + (n & 7) * 16 + to * 2) =
-                            __float2half_rn(ldexpf(x[e], ex));
+                            __float2half_rn(x[e] * up);
                     }
-                    if (lane == 0) {
-                        s_c[n] = live ? ldexpf(p.scale, -ex) : 0.f;
-                        s_nm[n] = -ATT_NONE;
-                        s_off[n] = row ? i * p.out.sn + hq * p.out.sh : -1;
-                        s_live[n] = live;
-                    }
+                    if (lane == 0) s_c[n] = s_live[n] ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
                 }
                 specv::fence_proxy_async_shared();
                 bar_sync(BAR_COMPUTE, CT);
@@ -554,7 +611,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
             }
             // ---- which queries see this thread's token: all of them where the whole tile is seen by all
             const bool whole = min(pos0, pos1) > f.before_all && max(pos0, pos1) <= f.seen_by_all;
-            uint32_t seen = 0xFFFFFFFFu;
+            Bits seen = ~Bits(0);
             if (!whole) {
                 const int from = tok < PAGE ? pos0 : pos1, at = from + tok % PAGE, base = f.len - f.ql;
                 int nlo = 0, nhi = 0;
@@ -564,22 +621,21 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                     if (p.window > 0 && at >= p.sinks)
                         nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - f.r0;
                 }
-                seen = bit_range(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
+                seen = bit_range<Bits>(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
             }
             unsigned long long x[NW / 2];
             for (bool move = flags & TILE_FIRST;; move = true) {
                 uint32_t u[NW];
-                tmem_ld(tlane + C::COL_S + wg * NW, u);
+                tmem_load<NW>(tlane + C::COL_S + wg * NW, u);
                 if (move) {
                     // the references move to the maxima seen so far; l and, unless this is the part's first tile, O follow
                     float y[NW];
-                    const uint32_t bits = here(seen);
+                    const Bits bits = here(seen);
 #pragma unroll
-                    for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1u ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
-                    const float top = fold_columns(y, lane, [](float a, float b) { return fmaxf(a, b); });
-                    if (lane < NW) s_red[wq][wg * NW + lane] = top;
+                    for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1 ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
+                    fold_columns(y, lane, &s_red[wq][wg * NW], [](float a, float b) { return fmaxf(a, b); });
                     bar_sync(BAR_COMPUTE, CT);
-                    if (tid < NC) {
+                    if (tid < NQ) {
                         const float old = -s_nm[tid];
                         const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
                         s_fac[tid] = specv::ex2(old - now);
@@ -590,12 +646,12 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                     for (int n = 0; n < NW / 2; ++n) l[n] = mul2(l[n], *reinterpret_cast<const unsigned long long*>(&s_fac[wg * NW + 2 * n]));
                     if (!(flags & TILE_FIRST)) {
 #pragma unroll
-                        for (int i = 0; i < NW / 16; ++i) {
-                            uint32_t o[16];
-                            tmem_ld(col_o + 16 * i, o);
+                        for (int i = 0; i < NW; i += 8) {
+                            uint32_t o[8];
+                            tmem_ld(col_o + i, o);
 #pragma unroll
-                            for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[wg * NW + 16 * i + n]);
-                            tmem_st16(col_o + 16 * i, o);
+                            for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * s_fac[wg * NW + i + n]);
+                            tmem_st8(col_o + i, o);
                         }
                     }
                 }
@@ -611,11 +667,11 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                     x[n / 2 + 1] = fma2(pack2(__uint_as_float(u[n + 2]), __uint_as_float(u[n + 3])), c.y, m.y);
                 }
                 if (!whole) {
-                    const uint32_t bits = here(seen);
+                    const Bits bits = here(seen);
 #pragma unroll
                     for (int n = 0; n < NW; n += 2) {
                         const float2 v = unpack2(x[n / 2]);
-                        x[n / 2] = pack2(bits >> n & 1u ? v.x : -INFINITY, bits >> (n + 1) & 1u ? v.y : -INFINITY);
+                        x[n / 2] = pack2(bits >> n & 1 ? v.x : -INFINITY, bits >> (n + 1) & 1 ? v.y : -INFINITY);
                     }
                 }
 #pragma unroll
@@ -652,47 +708,49 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
                     lf[2 * n] = v.x, lf[2 * n + 1] = v.y;
                     l[n] = 0ull;
                 }
-                const float sum = fold_columns(lf, lane, [](float a, float b) { return a + b; });
-                if (lane < NW) s_red[wq][wg * NW + lane] = sum;
+                fold_columns(lf, lane, &s_red[wq][wg * NW], [](float a, float b) { return a + b; });
                 if (D == 64 && wq >= 2) {      // the second page's share of O, to the lanes that write
 #pragma unroll
-                    for (int i = 0; i < NW / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld(col_o + 16 * i, o);
+                    for (int i = 0; i < NW; i += 8) {
+                        uint32_t o[8];
+                        tmem_ld(col_o + i, o);
 #pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            *reinterpret_cast<uint32_t*>(smem + C::P + ((wg * NW + 16 * i + q) * 64 + tok - 64) * 4) = o[q];
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint32_t*>(smem + C::P + ((wg * NW + i + q) * 64 + tok - 64) * 4) = o[q];
                     }
                 }
-                bar_sync(BAR_COMPUTE, CT);
-                if (tid < NC) s_sum[tid] = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
                 bar_sync(BAR_COMPUTE, CT);
                 const bool alone = flags & TILE_ALONE;
-                if (D == 128 || wq < 2) {
-                    T* const out = static_cast<T*>(p.out.p) + f.b * p.out.sb + tok;
-                    float* const part = p.part_o + static_cast<size_t>(f.slot) * NC * D + tok;
-#pragma unroll
-                    for (int i = 0; i < NW / 16; ++i) {
-                        uint32_t o[16];
-                        tmem_ld(col_o + 16 * i, o);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const int n = wg * NW + 16 * i + q;
-                            if (s_off[n] < 0) continue;
-                            float v = __uint_as_float(o[q]);
-                            if (D == 64) v += *reinterpret_cast<const float*>(smem + C::P + (n * 64 + tok) * 4);
-                            if (alone) out[s_off[n]] = static_cast<T>(s_live[n] && has_seen(-s_nm[n], s_sum[n]) ? v / s_sum[n] : 0.f);
-                            else part[n * D] = v;
-                        }
+                if (tid < NQ) {
+                    const float sum = (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]), m = -s_nm[tid];
+                    const bool some = s_live[tid] && has_seen(m, sum);
+                    s_inv[tid] = some ? 1.f / sum : 0.f;
+                    if (tid < f.rows) {
+                        const int r = f.r0 + tid, i = r / p.G;
+                        if (!alone) p.part_ml[static_cast<size_t>(f.slot) * p.width + tid] = make_float2(m, sum);
+                        else if (p.lse)
+                            p.lse[(static_cast<long long>(f.b) * p.N + i) * p.Hq + f.h * p.G + (r - i * p.G)] =
+                                some ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
                     }
                 }
-                if (tid < NC && s_off[tid] >= 0) {
-                    if (!alone) {
-                        p.part_ml[static_cast<size_t>(f.slot) * NC + tid] = make_float2(-s_nm[tid], s_sum[tid]);
-                    } else if (p.lse) {
-                        const int r = f.r0 + tid, i = r / p.G;
-                        p.lse[(static_cast<long long>(f.b) * p.N + i) * p.Hq + f.h * p.G + (r - i * p.G)] =
-                            s_live[tid] && has_seen(-s_nm[tid], s_sum[tid]) ? (log2f(s_sum[tid]) - s_nm[tid]) * 0.6931471805599453f : -INFINITY;
+                bar_sync(BAR_COMPUTE, CT);
+                if (D == 128 || wq < 2) {
+                    unsigned short* const out = static_cast<unsigned short*>(p.out.p) + f.b * p.out.sb + tok;
+                    float* const part = p.part_o + (static_cast<size_t>(f.slot) * p.width + wg * NW) * D + tok;
+#pragma unroll
+                    for (int i = 0; i < NW; i += 8) {
+                        uint32_t o[8];
+                        tmem_ld(col_o + i, o);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int n = wg * NW + i + q;
+                            float v = __uint_as_float(o[q]);
+                            if (D == 64) v += *reinterpret_cast<const float*>(smem + C::P + (n * 64 + tok) * 4);
+                            if (n >= f.rows) continue;
+                            // a row that sees nothing is 0 whatever its O: its columns may hold what no token's weight stands for
+                            if (alone) out[s_off[n]] = one_out(s_inv[n] != 0.f ? v * s_inv[n] : 0.f, p.fp16);
+                            else part[(i + q) * D] = v;
+                        }
                     }
                 }
                 tmem_fence_before();
@@ -710,7 +768,7 @@ __global__ void __launch_bounds__(Att<D, NC>::TH, Att<D, NC>::CTAS)
 
 // Joins the parts of the unit that starts in CTA blockIdx.x of the kernel before and is cut, a warp to a query row, in
 // order of the parts.
-template <class T, int D, int NC>
+template <int D>
 __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int E = D / 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -723,31 +781,28 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
     const long long g = blockIdx.x;
     auto slot = [&](int k) { return k == 0 ? 2 * g + 1 : 2 * (g + k); };
     float m = ATT_NONE;
-    for (int k = lane; k < u.z; k += 32) m = fmaxf(m, p.part_ml[slot(k) * NC + n].x);
+    for (int k = lane; k < u.z; k += 32) m = fmaxf(m, p.part_ml[slot(k) * p.width + n].x);
     m = specv::warp_max(m);
     float o[E] = {}, sum = 0.f;
 #pragma unroll 4
     for (int k = 0; k < u.z; ++k) {
-        const float2 ml = p.part_ml[slot(k) * NC + n];
+        const float2 ml = p.part_ml[slot(k) * p.width + n];
         const float w = specv::ex2(ml.x - m);
-        const float* const part = p.part_o + (slot(k) * NC + n) * D + E * lane;
+        const float2* const part = reinterpret_cast<const float2*>(p.part_o + (slot(k) * p.width + n) * D + E * lane);
         sum = fmaf(ml.y, w, sum);
-        float v[E];
-        if (E == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(part);
-            v[0] = f.x, v[1] = f.y, v[E - 2] = f.z, v[E - 1] = f.w;
-        } else {
-            const float2 f = *reinterpret_cast<const float2*>(part);
-            v[0] = f.x, v[1] = f.y;
-        }
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], w, o[e]);
+        for (int e = 0; e < E; e += 2) {
+            const float2 v = part[e / 2];
+            o[e] = fmaf(v.x, w, o[e]);
+            o[e + 1] = fmaf(v.y, w, o[e + 1]);
+        }
     }
     const int ql = p.q_len ? p.q_len[u.x] : p.N;
     const bool seen = i < ql && has_seen(m, sum);
-    T* const out = static_cast<T*>(p.out.p) + u.x * p.out.sb + i * p.out.sn + hq * p.out.sh + E * lane;
+    const float inv = 1.f / sum;
+    unsigned short* const out = static_cast<unsigned short*>(p.out.p) + u.x * p.out.sb + i * p.out.sn + hq * p.out.sh + E * lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = static_cast<T>(seen ? o[e] / sum : 0.f);
+    for (int e = 0; e < E; ++e) out[e] = one_out(seen ? o[e] * inv : 0.f, p.fp16);
     if (p.lse && lane == 0)
         p.lse[(static_cast<long long>(u.x) * p.N + i) * p.Hq + hq] = seen ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }

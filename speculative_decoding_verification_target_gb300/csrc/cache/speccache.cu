@@ -121,46 +121,49 @@ TokensParams tokens_params(const void* pool, int pages, const int32_t* table, in
 }
 
 // --------------------------------------------------------------------------------------------- attention
-// The queries that read a key head, in equal blocks of at most 64 rows, and the product's width for a block.
+// The queries that read a key head, in equal blocks: as many as the widest kernel takes (80 rows, 64 where D = 64: the
+// tensor memory's columns), each in the narrowest one that holds it. A block costs the conversion of its tiles once, so
+// one wide block is cheaper than two narrow ones.
 struct AttSplit {
-    int blocks, rows, nc;
+    int blocks, rows, wg, nw;
 };
-AttSplit att_split(int rows) {
-    const int blocks = (rows + 63) / 64, per = (rows + blocks - 1) / blocks;
-    return {blocks, per, per <= 16 ? 16 : per <= 32 ? 32 : 64};
+AttSplit att_split(int rows, int D) {
+    const int most = D == 64 ? 64 : 80, blocks = (rows + most - 1) / most, per = (rows + blocks - 1) / blocks;
+    const int wg = per > 32 ? 2 : 1;
+    return {blocks, per, wg, wg == 1 ? (per + 7) / 8 * 8 : per <= 48 ? 24 : per <= 64 ? 32 : 40};
 }
 
 // Workspace: header, the cut units' descriptions, and two parts for each CTA that there can be.
 struct AttLayout {
     size_t desc, ml, o, total;
 };
-AttLayout att_layout(int nc, int D) {
-    const size_t ctas = nc > 32 ? ATT_MAX_CTAS / 2 : ATT_MAX_CTAS;
+AttLayout att_layout(const AttSplit& s, int D) {
+    const size_t ctas = ATT_MAX_CTAS / s.wg, width = s.wg * s.nw;
     AttLayout w;
     w.desc = SPEC_CACHE_WS_HEADER;
     w.ml = w.desc + ctas * sizeof(int4);
-    w.o = w.ml + 2 * ctas * nc * sizeof(float2);
-    w.total = w.o + 2 * ctas * nc * D * sizeof(float);
+    w.o = w.ml + 2 * ctas * width * sizeof(float2);
+    w.total = w.o + 2 * ctas * width * D * sizeof(float);
     return w;
 }
 
-template <class T, int D, int NC>
+template <int D, int WG, int NW>
 spec_status attend_as(const AttnParams& p, cudaStream_t st) {
-    using C = Att<D, NC>;
+    using C = Att<D, WG, NW>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
     static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
     const unsigned bit = dev < 32 ? 1u << dev : 0u;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(attention_kernel<T, D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(attention_kernel<D, WG, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention kernel attribute failed: %s", cudaGetErrorString(e));
         ready.fetch_or(bit, std::memory_order_release);
     }
     const int sms = sm_count();
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
     const long long tiles = static_cast<long long>(p.B) * p.Hk * p.RB * ((p.max_pages + 1) / 2);     // at most
-    const int ctas = static_cast<int>(std::min<long long>({static_cast<long long>(C::CTAS) * sms, ATT_MAX_CTAS / C::WG, tiles}));
-    attention_kernel<T, D, NC><<<ctas, C::TH, C::SMEM, st>>>(p);
+    const int ctas = static_cast<int>(std::min<long long>({static_cast<long long>(C::CTAS) * sms, ATT_MAX_CTAS / WG, tiles}));
+    attention_kernel<D, WG, NW><<<ctas, C::TH, C::SMEM, st>>>(p);
     SPECC_TRY(launched("attention"));
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -171,14 +174,22 @@ spec_status attend_as(const AttnParams& p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_join_kernel<T, D, NC>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, p);
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "attention's join failed: %s", cudaGetErrorString(e));
 }
 
-template <class T>
-spec_status attend(const AttnParams& p, int D, int nc, cudaStream_t st) {
-    if (D == 64) return nc == 16 ? attend_as<T, 64, 16>(p, st) : nc == 32 ? attend_as<T, 64, 32>(p, st) : attend_as<T, 64, 64>(p, st);
-    return nc == 16 ? attend_as<T, 128, 16>(p, st) : nc == 32 ? attend_as<T, 128, 32>(p, st) : attend_as<T, 128, 64>(p, st);
+template <int D>
+spec_status attend(const AttnParams& p, const AttSplit& s, cudaStream_t st) {
+    if (s.wg == 1) {
+        if (s.nw == 8) return attend_as<D, 1, 8>(p, st);
+        if (s.nw == 16) return attend_as<D, 1, 16>(p, st);
+        if (s.nw == 24) return attend_as<D, 1, 24>(p, st);
+        return attend_as<D, 1, 32>(p, st);
+    }
+    if (s.nw == 24) return attend_as<D, 2, 24>(p, st);
+    if constexpr (D == 128)
+        if (s.nw == 40) return attend_as<D, 2, 40>(p, st);
+    return attend_as<D, 2, 32>(p, st);
 }
 
 // ------------------------------------------------------------------------------------------------- pages
@@ -323,7 +334,7 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
 
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
     if (N < 1 || N > MAX_Q || Hk < 1 || Hq < Hk || Hq > MAX_HEADS || Hq % Hk || (D != 64 && D != 128)) return 0;
-    return att_layout(att_split(N * (Hq / Hk)).nc, D).total;
+    return att_layout(att_split(N * (Hq / Hk), D), D).total;
 }
 
 spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
@@ -362,16 +373,18 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.sixteen = 16u;
     p.G = Hq / Hk;
-    const AttSplit split = att_split(N * p.G);
+    const AttSplit split = att_split(N * p.G, D);
     p.RB = split.blocks;
     p.rpb = split.rows;
-    const AttLayout w = att_layout(split.nc, D);
+    p.width = split.wg * split.nw;
+    p.fp16 = dtype == SPEC_FP16;
+    const AttLayout w = att_layout(split, D);
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
     p.desc = reinterpret_cast<int4*>(ws + w.desc);
     p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == SPEC_BF16 ? attend<__nv_bfloat16>(p, D, split.nc, st) : attend<__half>(p, D, split.nc, st);
+    return D == 64 ? attend<64>(p, split, st) : attend<128>(p, split, st);
 }
 
 size_t spec_pages_workspace_size(int S, int pages) {
