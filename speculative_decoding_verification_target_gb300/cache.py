@@ -22,7 +22,7 @@ import math
 
 import torch
 
-from . import SPEC_OK, SpecError, _need, _p, _stream, load as _load
+from . import SPEC_OK, SpecError, _need, load as _load
 
 PAGE, GROUP = 64, 32
 WS_HEADER = 8192
@@ -69,6 +69,20 @@ def _ok(code):
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# The serving loop calls these once per layer and token, so the checks are written to cost little where they pass: one
+# condition, and the words for what is wrong only after it.
+def _on(t, stream):
+    """The stream's handle: the caller's, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(t.device.index) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _code(t, name, fp32=False):
@@ -81,11 +95,11 @@ def _code(t, name, fp32=False):
 
 def _heads(t, name, shape, dtype):
     """[B, N, heads, D] with any strides but contiguous channels."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape):
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     sb, sn, sh, sd = t.stride()
     if sd != 1:
@@ -94,7 +108,8 @@ def _heads(t, name, shape, dtype):
 
 
 def _pool(pool, name="pool"):
-    _need(pool, name, torch.uint8)
+    if not (pool.is_cuda and pool.dtype is torch.uint8 and pool.is_contiguous()):
+        _need(pool, name, torch.uint8)
     if pool.dim() != 3:
         raise ValueError("%s must be [pages, Hk, 68 D], got %s" % (name, tuple(pool.shape)))
     P, H, n = pool.shape
@@ -104,11 +119,13 @@ def _pool(pool, name="pool"):
 
 
 def _ints(t, name, shape):
-    _need(t, name, torch.int32, shape)
+    if not (t.is_cuda and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
+        _need(t, name, torch.int32, shape)
 
 
 def _table(table):
-    _need(table, "table", torch.int32)
+    if not (table.is_cuda and table.dtype is torch.int32 and table.is_contiguous()):
+        _need(table, "table", torch.int32)
     if table.dim() != 2:
         raise ValueError("table must be [sequences, max_pages], got %s" % (tuple(table.shape),))
     return table.shape
@@ -159,9 +176,9 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     dt = q.dtype
     code = _code(q, "q", True)
     if q_out is None:
-        q_out = torch.empty((B, N, Hq, D), dtype=dt, device=q.device)
+        q_out = q.new_empty((B, N, Hq, D))
     if k_out is None:
-        k_out = torch.empty((B, N, Hk, D), dtype=dt, device=q.device)
+        k_out = k.new_empty((B, N, Hk, D))
     rotary = 0
     if freqs is not None:
         _need(freqs, "freqs", torch.int64)
@@ -171,9 +188,9 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
         if w is not None:
             _need(w, name, dt, (D,))
     _ok(_lib().spec_qk_norm_rope(_heads(q, "q", (B, N, Hq, D), dt), _heads(k, "k", (B, N, Hk, D), dt), code, B, N, Hq, Hk,
-                                 D, _p(positions) if rotary else None, _p(freqs) if rotary else None, rotary, interleaved,
-                                 _p(q_weight), _p(k_weight), eps, _heads(q_out, "q_out", (B, N, Hq, D), dt),
-                                 _heads(k_out, "k_out", (B, N, Hk, D), dt), _stream(stream)))
+                                 D, positions.data_ptr() if rotary else None, freqs.data_ptr() if rotary else None, rotary, interleaved,
+                                 _ptr(q_weight), _ptr(k_weight), eps, _heads(q_out, "q_out", (B, N, Hq, D), dt),
+                                 _heads(k_out, "k_out", (B, N, Hk, D), dt), _on(q, stream)))
     return dict(q=q_out, k=k_out)
 
 
@@ -189,9 +206,9 @@ def cache_append(pool, table, start, k, v, *, counts=None, workspace=None, strea
         _ints(counts, "counts", (B,))
     if workspace is None:
         workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
-    _ok(_lib().spec_cache_append(_p(pool), P, _p(table), M, _p(start), _p(counts), _heads(k, "k", (B, N, H, D), k.dtype),
-                                 _heads(v, "v", (B, N, H, D), k.dtype), code, B, N, H, D, _p(workspace), workspace.numel(),
-                                 _stream(stream)))
+    _ok(_lib().spec_cache_append(_ptr(pool), P, _ptr(table), M, _ptr(start), _ptr(counts), _heads(k, "k", (B, N, H, D), k.dtype),
+                                 _heads(v, "v", (B, N, H, D), k.dtype), code, B, N, H, D, _ptr(workspace), workspace.numel(),
+                                 _on(pool, stream)))
     return workspace
 
 
@@ -210,9 +227,9 @@ def cache_read(pool, table, start, n, *, counts=None, dtype=torch.bfloat16, k=No
     code = _code(k, "k")
     if workspace is None:
         workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
-    _ok(_lib().spec_cache_read(_p(pool), P, _p(table), M, _p(start), _p(counts), _heads(k, "k", (B, n, H, D), dtype),
-                               _heads(v, "v", (B, n, H, D), dtype), code, B, n, H, D, _p(workspace), workspace.numel(),
-                               _stream(stream)))
+    _ok(_lib().spec_cache_read(_ptr(pool), P, _ptr(table), M, _ptr(start), _ptr(counts), _heads(k, "k", (B, n, H, D), dtype),
+                               _heads(v, "v", (B, n, H, D), dtype), code, B, n, H, D, _ptr(workspace), workspace.numel(),
+                               _on(pool, stream)))
     return dict(k=k, v=v, workspace=workspace)
 
 
@@ -230,17 +247,17 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     if q_len is not None:
         _ints(q_len, "q_len", (B,))
     if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((B, N, Hq, D))
     if lse is None and want_lse:
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
     elif lse is not None:
         _need(lse, "lse", torch.float32, (B, N, Hq))
     if workspace is None:
         workspace = new_attention_workspace(N, Hq, H, D, q.device)
-    _ok(_lib().spec_cache_attention(_heads(q, "q", (B, N, Hq, D), q.dtype), code, _p(pool), P, _p(table), M, _p(kv_len),
-                                    _p(q_len), B, N, Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks,
-                                    _heads(out, "out", (B, N, Hq, D), q.dtype), _p(lse), _p(workspace), workspace.numel(),
-                                    _stream(stream)))
+    _ok(_lib().spec_cache_attention(_heads(q, "q", (B, N, Hq, D), q.dtype), code, _ptr(pool), P, _ptr(table), M, _ptr(kv_len),
+                                    _ptr(q_len), B, N, Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks,
+                                    _heads(out, "out", (B, N, Hq, D), q.dtype), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                    _on(q, stream)))
     return dict(out=out, lse=lse, workspace=workspace)
 
 
@@ -271,8 +288,8 @@ def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
     _ints(src, "src", (F,))
     _ints(dst, "dst", (F,))
     ws = _pages_ws(workspace, S, P, table.device)
-    _ok(_lib().spec_pages_fork(_p(table), _p(lengths), _p(refs), S, M, P, _p(src), _p(dst), F, _p(ws), ws.numel(),
-                               _stream(stream)))
+    _ok(_lib().spec_pages_fork(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(src), _ptr(dst), F, _ptr(ws), ws.numel(),
+                               _on(table, stream)))
     return ws
 
 
@@ -283,12 +300,12 @@ def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=N
     layers, page_bytes = _layers(pool, P)
     _ints(n_new, "n_new", (S,))
     if served is None:
-        served = torch.empty(S, dtype=torch.int32, device=table.device)
+        served = table.new_empty(S)
     else:
         _ints(served, "served", (S,))
     ws = _pages_ws(workspace, S, P, table.device)
-    _ok(_lib().spec_pages_reserve(_p(pool), layers, page_bytes, _p(table), _p(lengths), _p(refs), S, M, P, _p(n_new),
-                                  _p(served), _p(ws), ws.numel(), _stream(stream)))
+    _ok(_lib().spec_pages_reserve(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(n_new),
+                                  _ptr(served), _ptr(ws), ws.numel(), _on(pool, stream)))
     return served
 
 
@@ -298,8 +315,8 @@ def pages_commit(table, lengths, refs, advance, *, extra=1, window=0, sinks=0, w
     S, M, P = _books(table, lengths, refs)
     _ints(advance, "advance", (S,))
     ws = _pages_ws(workspace, S, P, table.device)
-    _ok(_lib().spec_pages_commit(_p(table), _p(lengths), _p(refs), S, M, P, _p(advance), extra, window, sinks, _p(ws),
-                                 ws.numel(), _stream(stream)))
+    _ok(_lib().spec_pages_commit(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(advance), extra, window, sinks, _ptr(ws),
+                                 ws.numel(), _on(table, stream)))
     return ws
 
 
@@ -309,8 +326,8 @@ def pages_release(table, lengths, refs, slots, *, workspace=None, stream=None):
     F = slots.numel()
     _ints(slots, "slots", (F,))
     ws = _pages_ws(workspace, S, P, table.device)
-    _ok(_lib().spec_pages_release(_p(table), _p(lengths), _p(refs), S, M, P, _p(slots), F, _p(ws), ws.numel(),
-                                  _stream(stream)))
+    _ok(_lib().spec_pages_release(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(slots), F, _ptr(ws), ws.numel(),
+                                  _on(table, stream)))
     return ws
 
 
@@ -320,10 +337,10 @@ def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
     S, M, P = _books(table, None, refs)
     layers, page_bytes = _layers(pool, P)
     if used is None:
-        used = torch.empty(1, dtype=torch.int32, device=table.device)
+        used = table.new_empty(1)
     else:
         _ints(used, "used", (1,))
     ws = _pages_ws(workspace, S, P, table.device)
-    _ok(_lib().spec_pages_compact(_p(pool), layers, page_bytes, _p(table), _p(refs), S, M, P, _p(used), _p(ws), ws.numel(),
-                                  _stream(stream)))
+    _ok(_lib().spec_pages_compact(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(refs), S, M, P, _ptr(used), _ptr(ws), ws.numel(),
+                                  _on(pool, stream)))
     return used

@@ -66,7 +66,7 @@ struct Att {
     static constexpr int CT = 128 * WG, TH = CT + 32;     // computing threads; one more warp fetches and issues products
     static constexpr int NQ = WG * NW, NC = (NQ + 15) / 16 * 16;     // queries, and the products' width for them
     static constexpr int TILE = 2 * Block<D>::BYTES;
-    static constexpr int STAGES = D == 64 || WG == 2 ? 4 : CTAS == 4 ? 2 : 3, INFOS = 2 * STAGES;
+    static constexpr int STAGES = D == 64 ? 4 : CTAS == 4 ? 2 : 3, INFOS = 2 * STAGES;      // what shared memory has room for
     // the second product: D = 128, 128 channels by 128 tokens; D = 64, both pages' channels as 128 rows by 64 tokens, each
     // page's probabilities in columns of their own (half of the result is of no use, but all warps have values to convert)
     static constexpr int ON = D == 128 ? NC : 2 * NC, OK = D == 128 ? 128 : 64;
@@ -463,6 +463,9 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 umma_commit(&s_bar_s);
             }
             __syncwarp();
+            // the slot of the tile before is free: its values were read before the vote. Here, not right after its second
+            // product, so that the next tile's first product does not wait for this.
+            if (k > 0 && issued < tiles) issue();
             while (bar_vote(BAR_PROBS, TH, false)) {}      // at most one turn: see the computing warps
             tmem_fence_after();
             if (elect_one()) {
@@ -472,7 +475,6 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 umma_commit(&s_bar_o);
             }
             __syncwarp();
-            if (issued < tiles) issue();       // into this tile's slot: its values were read before the vote
         }
         if (lane == 0) p.desc[g] = desc;
         // no copy is in flight into this CTA's shared memory when it is given back, even where a wait gave up
