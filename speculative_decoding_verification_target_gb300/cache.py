@@ -176,9 +176,9 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     dt = q.dtype
     code = _code(q, "q", True)
     if q_out is None:
-        q_out = q.new_empty((B, N, Hq, D))
+        q_out = torch.empty((B, N, Hq, D), dtype=dt, device=q.device)
     if k_out is None:
-        k_out = k.new_empty((B, N, Hk, D))
+        k_out = torch.empty((B, N, Hk, D), dtype=dt, device=q.device)
     rotary = 0
     if freqs is not None:
         _need(freqs, "freqs", torch.int64)
@@ -247,7 +247,7 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     if q_len is not None:
         _ints(q_len, "q_len", (B,))
     if out is None:
-        out = q.new_empty((B, N, Hq, D))
+        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
     elif lse is not None:
@@ -300,7 +300,7 @@ def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=N
     layers, page_bytes = _layers(pool, P)
     _ints(n_new, "n_new", (S,))
     if served is None:
-        served = table.new_empty(S)
+        served = torch.empty(S, dtype=torch.int32, device=table.device)
     else:
         _ints(served, "served", (S,))
     ws = _pages_ws(workspace, S, P, table.device)
@@ -337,7 +337,7 @@ def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
     S, M, P = _books(table, None, refs)
     layers, page_bytes = _layers(pool, P)
     if used is None:
-        used = table.new_empty(1)
+        used = torch.empty(1, dtype=torch.int32, device=table.device)
     else:
         _ints(used, "used", (1,))
     ws = _pages_ws(workspace, S, P, table.device)

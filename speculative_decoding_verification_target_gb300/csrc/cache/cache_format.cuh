@@ -1,6 +1,7 @@
 // The 4-bit cache's format (include/speccache.h) on the device, and the element types of the activations.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,14 +40,52 @@ __device__ __forceinline__ int scale_bits(float v) {
 __device__ __forceinline__ float scale_value(int b) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7)));
 }
-// Code + 8 of x under scale s. The quotient is the correctly rounded one: x has at most 11 significant bits and
-// s four, so x / s is a tie exactly where the true quotient is one, and the code is that of exact arithmetic.
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-    const float c = s > 0.f && x == x ? rintf(__fdiv_rn(x, s)) : 0.f;   // a NaN is 0
-    return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -7.f), 7.f)) + 8);
+// Codes + 8 of eight values under scale s, the i-th in bits 4 i; inv the rounded reciprocal of s, or 0 where s is 0.
+// Exact arithmetic's codes: x has at most 11 significant bits and s four, so a quotient of at most 7.5 that is no tie lies
+// 2^-14 or more from one, and x inv, off by 2^-20, is brought onto the grid of 2^-16 (adding 192, whose last place that is) before
+// it is rounded to an integer. Four codes are put together as one fp32 number below 2^16.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float inv) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = __fsub_rn(__fmaf_rn(x[i], inv, 192.f), 192.f);
+        const float c = fminf(fmaxf(rintf(q), -7.f), 7.f) + 8.f;
+        v[i] = x[i] == x[i] ? c : 8.f;      // a NaN is 0
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w |= static_cast<uint32_t>(fmaf(fmaf(fmaf(v[4 * i + 3], 16.f, v[4 * i + 2]), 16.f, v[4 * i + 1]), 16.f, v[4 * i])) << (16 * i);
+    return w;
 }
 
-// Eight neighbouring channels: 16 bytes of bf16 or fp16, 32 of fp32.
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Eight neighbouring channels: 16 bytes of bf16 or fp16.
 template <class T>
 struct Eight;
 template <>
@@ -96,24 +135,46 @@ struct Eight<__half> {
     }
     __device__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = r; }
 };
+// Four neighbouring channels: 8 bytes of bf16 or fp16, 16 of fp32.
+template <class T>
+struct Four {
+    uint2 r;
+    __device__ void load(const T* p) { r = *reinterpret_cast<const uint2*>(p); }
+    __device__ void get(float* x) const {
+        const uint32_t w[2] = {r.x, r.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+    __device__ void set(const float* x) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        r = make_uint2(w[0], w[1]);
+    }
+    __device__ void store(T* p) const { *reinterpret_cast<uint2*>(p) = r; }
+};
 template <>
-struct Eight<float> {
-    float4 a, b;
-    __device__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-    __device__ void set(const float (&x)[8]) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
-    }
-    __device__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
-    }
+struct Four<float> {
+    float4 r;
+    __device__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+    __device__ void get(float* x) const { x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w; }
+    __device__ void set(const float* x) { r = make_float4(x[0], x[1], x[2], x[3]); }
+    __device__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
 };
 
 }  // namespace specc

@@ -10,21 +10,24 @@ struct NormParams {
     const unsigned long long* freqs;
     const void *qw, *kw;
     long long tokens;
-    int N, Hq, Hk, rotary, interleaved, parts;
+    int N, Hq, Hk, rotary, parts;
     float eps;
 };
 
 constexpr int NORM_WARPS = 4;
 
-// A warp takes one token and 1 / parts of its heads, D / 8 lanes to a head with eight channels each. The token's
-// angles are worked out once per warp: turns = position x frequency in 2^-64 of a turn wraps exactly in integer
-// arithmetic, its top 32 bits are the angle to 2^-32 of a turn, so a far position costs no precision and no
-// table is read. A lane's channels are the same in every head, so it keeps their cosines and sines (and both
-// weights) in registers. In the half-split form a pair's two channels sit in lanes rotary / 16 apart.
-template <class T, int D>
+// A warp takes one token and 1 / parts of its heads, D / 8 lanes to a head with eight channels each: four and the four
+// that they are paired with (rotary / 2 further on in the half-split form, the next four otherwise), so that a rotation
+// stays within the lane. The token's angles are worked out once per warp: turns = position x frequency in 2^-64 of a
+// turn wraps exactly in integer arithmetic, its top 32 bits are the angle to 2^-32 of a turn, so a far position costs no
+// precision and no table is read. A lane's channels are the same in every head: y_i = r (x_i P_i + x_mate Q_i), where P
+// and Q hold the weights and the cosines and sines, once for the query heads and once for the key heads.
+// Bandwidth bounds many tokens: U heads a lane are in flight. Few tokens are split into parts.
+template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int LPH = D / 8, RPW = 32 / LPH;   // lanes per head, heads per warp at a time
-    constexpr int U = 2;                         // heads per lane in flight
+    constexpr int U = 4;                         // heads per lane in flight
+    constexpr int MATE = INTER ? 1 : 4;
     __shared__ float2 s_cs[NORM_WARPS][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long unit = static_cast<long long>(blockIdx.x) * NORM_WARPS + warp;
@@ -33,11 +36,10 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid
     const int part = static_cast<int>(unit - tok * p.parts);
     const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
     const int c = lane % LPH, sub = lane / LPH;
-    const int half = p.rotary >> 1;
     float2* const cs = s_cs[warp];
     if (p.rotary) {
         const long long pos = p.positions[tok];
-        for (int i = lane; i < half; i += 32) {
+        for (int i = lane; i < p.rotary / 2; i += 32) {
             const unsigned long long turn = static_cast<unsigned long long>(pos) * p.freqs[i];
             const float x = static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f;   // half turns
             float s, co;
@@ -47,80 +49,89 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid
         __syncwarp();
     }
     const bool rot = 8 * c < p.rotary;
-    float co[8], si[8];
-    int mate = lane;
+    const int oa = rot && !INTER ? 4 * c : 8 * c, ob = rot && !INTER ? p.rotary / 2 + 4 * c : 8 * c + 4;
+    // heads of this part, queries and keys in one count
+    const int H = p.Hq + p.Hk, step = p.parts * RPW;
+    for (int group = 0; group < 2; ++group) {
+        const Heads &in = group ? p.k : p.q, &out = group ? p.ko : p.qo;
+        const int lo = group ? p.Hq : 0, hi = group ? H : p.Hq;
+        // the part's first head past lo, in steps: its heads are part RPW + sub + m step
+        const int first = part * RPW + (lo > part * RPW ? (lo - part * RPW + step - 1) / step * step : 0);
+        // a step's heads can straddle the two groups: one earlier where its last ones are past lo
+        const int begin = first - step + RPW > lo && first - step >= 0 ? first - step : first;
+        if (begin >= hi) continue;
+        const T* const w = static_cast<const T*>(group ? p.kw : p.qw);
+        float v[8];
+        unsigned long long P[4], Q[4];
+        {
+            float wt[8], pc[8], qc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
-    if (rot) {
-        if (p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 t = cs[4 * c + i];
-                co[2 * i] = co[2 * i + 1] = t.x;
-                si[2 * i] = -t.y;
-                si[2 * i + 1] = t.y;
+            for (int i = 0; i < 8; ++i) wt[i] = 1.f;
+            if (w) {
+                Four<T> e;
+                e.load(w + oa);
+                e.get(wt);
+                e.load(w + ob);
+                e.get(wt + 4);
             }
-        } else {
-            const bool low = 8 * c < half;
-            mate = low ? lane + half / 8 : lane - half / 8;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 t = cs[(low ? 8 * c : 8 * c - half) + i];
-                co[i] = t.x;
-                si[i] = low ? -t.y : t.y;
+                const float2 t = rot ? cs[INTER ? 4 * c + i / 2 : 4 * c + i % 4] : make_float2(1.f, 0.f);
+                pc[i] = wt[i] * t.x;
+                qc[i] = i & MATE ? wt[i ^ MATE] * t.y : -wt[i ^ MATE] * t.y;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) P[i] = pack2(pc[2 * i], pc[2 * i + 1]), Q[i] = pack2(qc[2 * i], qc[2 * i + 1]);
         }
-    }
-    float qw[8], kw[8];
+        const T* const src = static_cast<const T*>(in.p) + b * in.sb + n * in.sn;
+        T* const dst = static_cast<T*>(out.p) + b * out.sb + n * out.sn;
+        for (int h0 = begin + sub; h0 - sub < hi; h0 += U * step) {
+            Four<T> ea[U], eb[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) qw[i] = kw[i] = 1.f;
-    if (p.qw) {
-        Eight<T> e;
-        e.load(static_cast<const T*>(p.qw) + 8 * c);
-        e.get(qw);
-    }
-    if (p.kw) {
-        Eight<T> e;
-        e.load(static_cast<const T*>(p.kw) + 8 * c);
-        e.get(kw);
-    }
-    const T* const q = static_cast<const T*>(p.q.p) + b * p.q.sb + n * p.q.sn + 8 * c;
-    const T* const k = static_cast<const T*>(p.k.p) + b * p.k.sb + n * p.k.sn + 8 * c;
-    T* const qo = static_cast<T*>(p.qo.p) + b * p.qo.sb + n * p.qo.sn + 8 * c;
-    T* const ko = static_cast<T*>(p.ko.p) + b * p.ko.sb + n * p.ko.sn + 8 * c;
-    const int H = p.Hq + p.Hk, step = p.parts * RPW;
-    for (int h0 = part * RPW; h0 < H; h0 += U * step) {
-        Eight<T> e[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * step + sub;
-            if (h < H) e[u].load(h < p.Hq ? q + h * p.q.sh : k + (h - p.Hq) * p.k.sh);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * step + sub;
-            float x[8], y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.f;
-            if (h < H) e[u].get(x);
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-#pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            const float r = __frsqrt_rn(fmaf(s, 1.f / D, p.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (h < p.Hq ? qw[i] : kw[i]);
-            if (p.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], co[i], x[i ^ 1] * si[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], co[i], __shfl_sync(0xffffffffu, x[i], mate) * si[i]);
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * step;
+                if (h >= lo && h < hi) {
+                    const T* const x = src + (h - lo) * in.sh;
+                    ea[u].load(x + oa);
+                    eb[u].load(x + ob);
+                }
             }
-            if (h < H) {
-                e[u].set(y);
-                e[u].store(h < p.Hq ? qo + h * p.qo.sh : ko + (h - p.Hq) * p.ko.sh);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * step;
+                if (h - sub >= hi) break;          // the same for every lane
+                const bool live = h >= lo && h < hi;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                if (live) {
+                    ea[u].get(v);
+                    eb[u].get(v + 4);
+                }
+                unsigned long long x[4], m[4], s2 = 0ull;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = pack2(v[2 * i], v[2 * i + 1]);
+                    m[i] = pack2(v[2 * i ^ MATE], v[(2 * i + 1) ^ MATE]);
+                    s2 = fma2(x[i], x[i], s2);
+                }
+                const float2 sp = unpack2(s2);
+                float s = sp.x + sp.y;
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                const float r = __frsqrt_rn(fmaf(s, 1.f / D, p.eps));
+                const unsigned long long r2 = pack2(r, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = unpack2(mul2(fma2(x[i], P[i], mul2(m[i], Q[i])), r2));
+                    v[2 * i] = y.x, v[2 * i + 1] = y.y;
+                }
+                if (live) {
+                    T* const y = dst + (h - lo) * out.sh;
+                    ea[u].set(v);
+                    ea[u].store(y + oa);
+                    eb[u].set(v + 4);
+                    eb[u].store(y + ob);
+                }
             }
         }
     }

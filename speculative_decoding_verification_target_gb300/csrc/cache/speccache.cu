@@ -273,7 +273,6 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
     p.Hq = Hq;
     p.Hk = Hk;
     p.rotary = rotary;
-    p.interleaved = interleaved != 0;
     p.eps = eps;
     // few tokens: a token's heads are split over warps until the card has 32 warps an SM
     const int rpw = 256 / D;
@@ -281,11 +280,18 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
     const long long units = p.tokens * p.parts, ctas = (units + NORM_WARPS - 1) / NORM_WARPS;
     if (ctas > 2147483647LL) return fail(SPEC_ERR_INVALID, "too many tokens: B N is limited to 2^31");
     using Fn = void (*)(const NormParams);
-    static const Fn fns[3][3] = {
-        {norm_rope_kernel<__nv_bfloat16, 64>, norm_rope_kernel<__nv_bfloat16, 128>, norm_rope_kernel<__nv_bfloat16, 256>},
-        {norm_rope_kernel<float, 64>, norm_rope_kernel<float, 128>, norm_rope_kernel<float, 256>},
-        {norm_rope_kernel<__half, 64>, norm_rope_kernel<__half, 128>, norm_rope_kernel<__half, 256>}};
-    fns[dtype][D == 64 ? 0 : D == 128 ? 1 : 2]<<<static_cast<unsigned>(ctas), NORM_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    static const Fn fns[3][3][2] = {
+        {{norm_rope_kernel<__nv_bfloat16, 64, false>, norm_rope_kernel<__nv_bfloat16, 64, true>},
+         {norm_rope_kernel<__nv_bfloat16, 128, false>, norm_rope_kernel<__nv_bfloat16, 128, true>},
+         {norm_rope_kernel<__nv_bfloat16, 256, false>, norm_rope_kernel<__nv_bfloat16, 256, true>}},
+        {{norm_rope_kernel<float, 64, false>, norm_rope_kernel<float, 64, true>},
+         {norm_rope_kernel<float, 128, false>, norm_rope_kernel<float, 128, true>},
+         {norm_rope_kernel<float, 256, false>, norm_rope_kernel<float, 256, true>}},
+        {{norm_rope_kernel<__half, 64, false>, norm_rope_kernel<__half, 64, true>},
+         {norm_rope_kernel<__half, 128, false>, norm_rope_kernel<__half, 128, true>},
+         {norm_rope_kernel<__half, 256, false>, norm_rope_kernel<__half, 256, true>}}};
+    const Fn fn = fns[dtype][D == 64 ? 0 : D == 128 ? 1 : 2][interleaved ? 1 : 0];
+    fn<<<static_cast<unsigned>(ctas), NORM_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return launched("norm and rotation");
 }
 
