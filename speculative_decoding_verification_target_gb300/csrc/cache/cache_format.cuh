@@ -29,34 +29,40 @@ struct Heads {
     long long sb, sn, sh;
 };
 
-// Non-negative fp32 to the nearest scale's bits, ties to even. Above 2^-14 by integer rounding of the float's own
-// bits, below it as a multiple of 2^-17 (a carry out of either gives the next scale's bits).
-__device__ __forceinline__ int scale_bits(float v) {
+__device__ __forceinline__ float scale_value(int b) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7)));
+}
+
+// Bits of the scale nearest (even on ties) to a seventh of `top`, the group's largest magnitude, a bf16 or fp16 value. The
+// seventh need not be the correctly rounded quotient: top has at most 11 significant bits, so a quotient that is no tie
+// between two scales is 2^-15 of itself or more away from one, and the product, off by 2^-23, is first rounded to 16 bits (by
+// adding and taking away 2^8 of itself). Above 2^-14 by integer rounding of the float's own bits, below as a multiple of
+// 2^-17 (a carry out of either gives the next scale's bits).
+__device__ __forceinline__ int scale_bits(float top) {
+    const float t = fminf(top, 8192.f) * 0.14285714924335479736328125f, far = t * 257.f;
+    const float v = __fsub_rn(far, __fsub_rn(far, t));
     const uint32_t u = __float_as_uint(v);
     const int normal = static_cast<int>((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - (112 << 3);
     const int small = __float2int_rn(v * 131072.f);
     return min(v < 6.103515625e-05f ? small : normal, SCALE_TOP);
 }
-__device__ __forceinline__ float scale_value(int b) {
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(b << 7)));
-}
-// Codes + 8 of eight values under scale s, the i-th in bits 4 i; inv the rounded reciprocal of s, or 0 where s is 0.
-// Exact arithmetic's codes: x has at most 11 significant bits and s four, so a quotient of at most 7.5 that is no tie lies
-// 2^-14 or more from one, and x inv, off by 2^-20, is brought onto the grid of 2^-16 (adding 192, whose last place that is) before
-// it is rounded to an integer. Four codes are put together as one fp32 number below 2^16.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float inv) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = __fsub_rn(__fmaf_rn(x[i], inv, 192.f), 192.f);
-        const float c = fminf(fmaxf(rintf(q), -7.f), 7.f) + 8.f;
-        v[i] = x[i] == x[i] ? c : 8.f;      // a NaN is 0
-    }
+
+// Codes + 8 of eight values (no NaN) under scale s, the i-th in bits 4 i. Exact arithmetic's codes: x has at most 11
+// significant bits and s four, so a quotient of at most 7.5 that is no tie lies 2^-14 or more from one; x times the approximate
+// reciprocal is off by 2^-19 and is brought onto the grid of 2^-16 (by adding 192, whose last place that is). Adding
+// 1.5 2^23 then rounds to an integer, ties to even, which stands in the last bits of the sum: they are put together as they are,
+// and what the sums' upper bits add up to is taken away at once.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = s > 0.f ? inv : 0.f;
     uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w |= static_cast<uint32_t>(fmaf(fmaf(fmaf(v[4 * i + 3], 16.f, v[4 * i + 2]), 16.f, v[4 * i + 1]), 16.f, v[4 * i])) << (16 * i);
-    return w;
+    for (int i = 0; i < 8; ++i) {
+        const float q = fminf(fmaxf(__fmaf_rn(x[i], inv, 192.f), 185.f), 199.f);
+        w += __float_as_uint(__fadd_rn(q, 12582912.f - 184.f)) << (4 * i);
+    }
+    return w - 0x3F400000u;      // the sum of 0x4B400000 << 4 i, modulo 2^32
 }
 
 // Two fp32 values in one 64-bit register pair: one instruction for both.

@@ -24,7 +24,7 @@ constexpr int NORM_WARPS = 4;
 // and Q hold the weights and the cosines and sines, once for the query heads and once for the key heads.
 // Bandwidth bounds many tokens: U heads a lane are in flight. Few tokens are split into parts.
 template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int LPH = D / 8, RPW = 32 / LPH;   // lanes per head, heads per warp at a time
     constexpr int U = 4;                         // heads per lane in flight
     constexpr int MATE = INTER ? 1 : 4;
@@ -61,7 +61,6 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid
         const int begin = first - step + RPW > lo && first - step >= 0 ? first - step : first;
         if (begin >= hi) continue;
         const T* const w = static_cast<const T*>(group ? p.kw : p.qw);
-        float v[8];
         unsigned long long P[4], Q[4];
         {
             float wt[8], pc[8], qc[8];
@@ -83,30 +82,28 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) P[i] = pack2(pc[2 * i], pc[2 * i + 1]), Q[i] = pack2(qc[2 * i], qc[2 * i + 1]);
         }
-        const T* const src = static_cast<const T*>(in.p) + b * in.sb + n * in.sn;
-        T* const dst = static_cast<T*>(out.p) + b * out.sb + n * out.sn;
-        for (int h0 = begin + sub; h0 - sub < hi; h0 += U * step) {
-            Four<T> ea[U], eb[U];
+        const long long is = step * in.sh, os = step * out.sh;
+        const T* src = static_cast<const T*>(in.p) + b * in.sb + n * in.sn + (begin + sub - lo) * in.sh;
+        T* dst = static_cast<T*>(out.p) + b * out.sb + n * out.sn + (begin + sub - lo) * out.sh;
+        for (int h0 = begin; h0 < hi; h0 += U * step) {
+            Four<T> ea[U], eb[U];      // a lane without a head computes on what is there: only its own head's lanes see it
+            bool live[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * step;
-                if (h >= lo && h < hi) {
-                    const T* const x = src + (h - lo) * in.sh;
-                    ea[u].load(x + oa);
-                    eb[u].load(x + ob);
+                const int h = h0 + u * step + sub;
+                live[u] = h >= lo && h < hi;
+                if (live[u]) {
+                    ea[u].load(src + u * is + oa);
+                    eb[u].load(src + u * is + ob);
                 }
             }
+            src += U * is;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * step;
-                if (h - sub >= hi) break;          // the same for every lane
-                const bool live = h >= lo && h < hi;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                if (live) {
-                    ea[u].get(v);
-                    eb[u].get(v + 4);
-                }
+                if (h0 + u * step >= hi) break;          // the same for every lane
+                float v[8];
+                ea[u].get(v);
+                eb[u].get(v + 4);
                 unsigned long long x[4], m[4], s2 = 0ull;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -125,14 +122,14 @@ __global__ void __launch_bounds__(NORM_WARPS * 32) norm_rope_kernel(const __grid
                     const float2 y = unpack2(mul2(fma2(x[i], P[i], mul2(m[i], Q[i])), r2));
                     v[2 * i] = y.x, v[2 * i + 1] = y.y;
                 }
-                if (live) {
-                    T* const y = dst + (h - lo) * out.sh;
+                if (live[u]) {
                     ea[u].set(v);
-                    ea[u].store(y + oa);
+                    ea[u].store(dst + u * os + oa);
                     eb[u].set(v + 4);
-                    eb[u].store(y + ob);
+                    eb[u].store(dst + u * os + ob);
                 }
             }
+            dst += U * os;
         }
     }
 }

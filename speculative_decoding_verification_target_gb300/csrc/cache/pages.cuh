@@ -17,9 +17,8 @@ struct PagesParams {
     int layers, S, M, P, n, extra, window, sinks;
 };
 
-constexpr int PG_CLUSTER = 8;            // CTAs of the cluster that reserves or compacts
+constexpr int PG_CLUSTER = 8;            // CTAs of the cluster that reserves or compacts, at most
 constexpr int PG_THREADS = 1024;
-constexpr int PG_WARPS = PG_CLUSTER * PG_THREADS / 32;
 constexpr int COPY_THREADS = 256;
 constexpr int COPY_BYTES = COPY_THREADS * 16 * 4;   // what a CTA copies at a time, four vectors a thread
 
@@ -121,7 +120,7 @@ __device__ __forceinline__ unsigned long long cluster_scan(ClusterScan* sh, unsi
     __syncthreads();
     specv::cluster_sync_all();
     unsigned long long before = 0, all = 0;
-    for (unsigned r = 0; r < PG_CLUSTER; ++r) {
+    for (unsigned r = 0; r < specv::cluster_nctarank(); ++r) {
         const uint32_t a = specv::map_to_rank(specv::smem_addr(&sh->cta), r);
         unsigned long long t;
         asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(t) : "r"(a) : "memory");
@@ -140,7 +139,7 @@ struct Run {
 };
 __device__ __forceinline__ Run run_of(int n, unsigned rank) {
     const long long t = static_cast<long long>(rank) * PG_THREADS + threadIdx.x;
-    constexpr long long T = PG_CLUSTER * PG_THREADS;
+    const long long T = specv::cluster_nctarank() * PG_THREADS;
     return {static_cast<int>(t * n / T), static_cast<int>((t + 1) * n / T)};
 }
 
@@ -172,11 +171,11 @@ __device__ __forceinline__ bool wants_page(const PagesParams& p, int e) {
 // found it until every sequence has read it.
 //   scratch: need [S], free list [P], former page [P], copies' source and destination [S] each, then the number of
 //   copies and of pages given (the copy kernel reads the first).
-__global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
-    reserve_kernel(const __grid_constant__ PagesParams p) {
+__global__ void __launch_bounds__(PG_THREADS) reserve_kernel(const __grid_constant__ PagesParams p) {
     __shared__ ClusterScan s_scan;
     __shared__ int s_given;
     const unsigned rank = specv::cluster_ctarank();
+    const int threads = specv::cluster_nctarank() * PG_THREADS, warps = threads / 32;
     const int lane = threadIdx.x & 31, gw = rank * (PG_THREADS / 32) + (threadIdx.x >> 5);
     int* const need = p.scratch;
     int* const free_list = need + p.S;
@@ -188,7 +187,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     if (threadIdx.x == 0) s_given = 0;
 
     // pages wanted by each sequence, a warp to a sequence
-    for (int s = gw; s < p.S; s += PG_WARPS) {
+    for (int s = gw; s < p.S; s += warps) {
         Want w;
         int c = 0;
         if (want_of(p, s, w)) {
@@ -235,7 +234,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     if (threadIdx.x == 0 && s_given) atomicMax(&counts[1], s_given);
     specv::cluster_sync_all();
     // hand them out
-    for (int s = gw; s < p.S; s += PG_WARPS) {
+    for (int s = gw; s < p.S; s += warps) {
         int k = need[s];
         Want w;
         if (k < 0 || !want_of(p, s, w)) continue;
@@ -261,7 +260,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     }
     specv::cluster_sync_all();
     const int n = *static_cast<volatile int*>(&counts[1]);
-    for (int k = static_cast<int>(rank) * PG_THREADS + threadIdx.x; k < n; k += PG_CLUSTER * PG_THREADS) {
+    for (int k = static_cast<int>(rank) * PG_THREADS + threadIdx.x; k < n; k += threads) {
         p.refs[free_list[k]] = 1;
         if (former[k] >= 0) atomicSub(&p.refs[former[k]], 1);
     }
@@ -296,10 +295,10 @@ __global__ void __launch_bounds__(COPY_THREADS) reserve_copy_kernel(const __grid
 // The moves of a compaction, by one cluster. With n pages in use, movers (used, number >= n) and holes (free,
 // number < n) are as many, and the i-th of the one goes to the i-th of the other.
 //   scratch: movers [P], holes [P], new number of pages n .. P - 1 [P], number of moves, n.
-__global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
-    compact_plan_kernel(const __grid_constant__ PagesParams p) {
+__global__ void __launch_bounds__(PG_THREADS) compact_plan_kernel(const __grid_constant__ PagesParams p) {
     __shared__ ClusterScan s_scan;
     const unsigned rank = specv::cluster_ctarank();
+    const int threads = specv::cluster_nctarank() * PG_THREADS;
     int* const movers = p.scratch;
     int* const holes = movers + p.P;
     int* const remap = holes + p.P;
@@ -325,7 +324,7 @@ __global__ void __cluster_dims__(PG_CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     }
     specv::cluster_sync_all();
     const int moves = static_cast<int>(both >> 32);
-    for (int k = static_cast<int>(rank) * PG_THREADS + threadIdx.x; k < moves; k += PG_CLUSTER * PG_THREADS) {
+    for (int k = static_cast<int>(rank) * PG_THREADS + threadIdx.x; k < moves; k += threads) {
         const int from = movers[k], to = holes[k];
         remap[from - n] = to;
         p.refs[to] = p.refs[from];

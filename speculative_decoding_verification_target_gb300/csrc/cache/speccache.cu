@@ -226,6 +226,22 @@ PagesParams pages_params(int32_t* table, int32_t* lengths, int32_t* refs, int S,
     return p;
 }
 
+// The bookkeeping kernels run as one cluster: two CTAs up to 8192 pages, where barriers cost more than the walk over the
+// counts (reserving over 8192: 15.5 us with two or four CTAs, 17.6 with eight), else eight (over 65536: 59.5, 28.6 and 20.5 us).
+cudaError_t launch_cluster(void (*fn)(const PagesParams), const PagesParams& p, int ctas, cudaStream_t st) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(PG_THREADS);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+int cluster_for(int pages) { return pages <= 8192 ? 2 : PG_CLUSTER; }
+
 }  // namespace
 }  // namespace specc
 
@@ -303,7 +319,7 @@ spec_status spec_cache_append(void* pool, int pages, const int32_t* table, int m
     SPECC_TRY(check_heads(k, "k", dtype));
     SPECC_TRY(check_heads(v, "v", dtype));
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, k, v, B, N, Hk, workspace);
-    const dim3 grid(Hk, (N + PAGE - 2) / PAGE + 1, B);   // a run of N tokens touches at most that many pages
+    const dim3 grid(2 * Hk, (N + PAGE - 2) / PAGE + 1, B);   // a run of N tokens touches at most that many pages
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == SPEC_BF16) {
         if (D == 64) append_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
@@ -326,7 +342,7 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
     if (!has_k && !has_v) return fail(SPEC_ERR_INVALID, "k_out and v_out must not both be NULL");
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, has_k ? k_out : nullptr,
                                          has_v ? v_out : nullptr, B, N, Hk, workspace);
-    const dim3 grid(Hk, (N + PAGE - 2) / PAGE + 1, B);
+    const dim3 grid(2 * Hk, (N + PAGE - 2) / PAGE + 1, B);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == SPEC_BF16) {
         if (D == 64) read_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
@@ -429,8 +445,8 @@ spec_status spec_pages_reserve(void* pool, int layers, long long page_bytes, int
     p.a = n_new;
     p.out = served;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    reserve_kernel<<<PG_CLUSTER, PG_THREADS, 0, st>>>(p);
-    SPECC_TRY(launched("reserve"));
+    const cudaError_t e = launch_cluster(reserve_kernel, p, cluster_for(pages), st);
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "reserve failed: %s", cudaGetErrorString(e));
     reserve_copy_kernel<<<4 * sms, COPY_THREADS, 0, st>>>(p);
     return launched("reserve's copies");
 }
@@ -478,8 +494,8 @@ spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int
     p.page_bytes = page_bytes;
     p.out = used;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    compact_plan_kernel<<<PG_CLUSTER, PG_THREADS, 0, st>>>(p);
-    SPECC_TRY(launched("compact's plan"));
+    const cudaError_t e = launch_cluster(compact_plan_kernel, p, cluster_for(pages), st);
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "compact's plan failed: %s", cudaGetErrorString(e));
     compact_move_kernel<<<8 * sms, COPY_THREADS, 0, st>>>(p);
     return launched("compact");
 }
