@@ -24,7 +24,7 @@ constexpr int NORM_WARPS = 4;
 // and Q hold the weights and the cosines and sines, once for the query heads and once for the key heads.
 // Bandwidth bounds many tokens: U heads a lane are in flight. Few tokens are split into parts.
 template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_rope_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int LPH = D / 8, RPW = 32 / LPH;   // lanes per head, heads per warp at a time
     constexpr int U = 4;                         // heads per lane in flight
     constexpr int MATE = INTER ? 1 : 4;
@@ -37,6 +37,31 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_
     const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
     const int c = lane % LPH, sub = lane / LPH;
     float2* const cs = s_cs[warp];
+    const bool rot = 8 * c < p.rotary;
+    const int oa = rot && !INTER ? 4 * c : 8 * c, ob = rot && !INTER ? p.rotary / 2 + 4 * c : 8 * c + 4;
+    // The part's heads are part RPW + sub + m step, query and key heads in one count; queries first, then keys. A step's
+    // heads can straddle the two: a group begins with the step that holds its first head.
+    const int H = p.Hq + p.Hk, step = p.parts * RPW, at = part * RPW;
+    const int begin_k = at + (p.Hq - RPW + 1 > at ? (p.Hq - RPW + 1 - at + step - 1) / step * step : 0);
+    auto row = [&](const Heads& t, int h) { return static_cast<T*>(t.p) + b * t.sb + n * t.sn + h * t.sh; };
+    Four<T> na[U], nb[U];      // the next heads, on their way
+    auto fetch = [&](int group, int h0) {
+        const Heads& in = group ? p.k : p.q;
+        const int lo = group ? p.Hq : 0, hi = group ? H : p.Hq;
+        const T* src = row(in, h0 + sub - lo);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * step + sub;
+            if (h >= lo && h < hi) {
+                na[u].load(src + oa);
+                nb[u].load(src + ob);
+            }
+            src += step * in.sh;
+        }
+    };
+    int group = at < p.Hq ? 0 : 1, h0 = group ? begin_k : at;
+    if (group && h0 >= H) return;
+    fetch(group, h0);          // ahead of the angles
     if (p.rotary) {
         const long long pos = p.positions[tok];
         for (int i = lane; i < p.rotary / 2; i += 32) {
@@ -48,21 +73,11 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_
         }
         __syncwarp();
     }
-    const bool rot = 8 * c < p.rotary;
-    const int oa = rot && !INTER ? 4 * c : 8 * c, ob = rot && !INTER ? p.rotary / 2 + 4 * c : 8 * c + 4;
-    // heads of this part, queries and keys in one count
-    const int H = p.Hq + p.Hk, step = p.parts * RPW;
-    for (int group = 0; group < 2; ++group) {
-        const Heads &in = group ? p.k : p.q, &out = group ? p.ko : p.qo;
+    while (true) {
         const int lo = group ? p.Hq : 0, hi = group ? H : p.Hq;
-        // the part's first head past lo, in steps: its heads are part RPW + sub + m step
-        const int first = part * RPW + (lo > part * RPW ? (lo - part * RPW + step - 1) / step * step : 0);
-        // a step's heads can straddle the two groups: one earlier where its last ones are past lo
-        const int begin = first - step + RPW > lo && first - step >= 0 ? first - step : first;
-        if (begin >= hi) continue;
-        const T* const w = static_cast<const T*>(group ? p.kw : p.qw);
         unsigned long long P[4], Q[4];
         {
+            const T* const w = static_cast<const T*>(group ? p.kw : p.qw);
             float wt[8], pc[8], qc[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) wt[i] = 1.f;
@@ -82,22 +97,14 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_
 #pragma unroll
             for (int i = 0; i < 4; ++i) P[i] = pack2(pc[2 * i], pc[2 * i + 1]), Q[i] = pack2(qc[2 * i], qc[2 * i + 1]);
         }
-        const long long is = step * in.sh, os = step * out.sh;
-        const T* src = static_cast<const T*>(in.p) + b * in.sb + n * in.sn + (begin + sub - lo) * in.sh;
-        T* dst = static_cast<T*>(out.p) + b * out.sb + n * out.sn + (begin + sub - lo) * out.sh;
-        for (int h0 = begin; h0 < hi; h0 += U * step) {
+        const Heads& out = group ? p.ko : p.qo;
+        T* dst = row(out, h0 + sub - lo);
+        for (; h0 < hi; h0 += U * step) {
             Four<T> ea[U], eb[U];      // a lane without a head computes on what is there: only its own head's lanes see it
-            bool live[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * step + sub;
-                live[u] = h >= lo && h < hi;
-                if (live[u]) {
-                    ea[u].load(src + u * is + oa);
-                    eb[u].load(src + u * is + ob);
-                }
-            }
-            src += U * is;
+            for (int u = 0; u < U; ++u) ea[u] = na[u], eb[u] = nb[u];
+            if (h0 + U * step < hi) fetch(group, h0 + U * step);
+            else if (!group && begin_k < H) fetch(1, begin_k);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (h0 + u * step >= hi) break;          // the same for every lane
@@ -115,22 +122,26 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 6 : 4) norm_
                 float s = sp.x + sp.y;
 #pragma unroll
                 for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const float r = __frsqrt_rn(fmaf(s, 1.f / D, p.eps));
+                const float r = rsqrtf(fmaf(s, 1.f / D, p.eps));
                 const unsigned long long r2 = pack2(r, r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 y = unpack2(mul2(fma2(x[i], P[i], mul2(m[i], Q[i])), r2));
                     v[2 * i] = y.x, v[2 * i + 1] = y.y;
                 }
-                if (live[u]) {
+                const int h = h0 + u * step + sub;
+                if (h >= lo && h < hi) {
                     ea[u].set(v);
-                    ea[u].store(dst + u * os + oa);
+                    ea[u].store(dst + oa);
                     eb[u].set(v + 4);
-                    eb[u].store(dst + u * os + ob);
+                    eb[u].store(dst + ob);
                 }
+                dst += step * out.sh;
             }
-            dst += U * os;
         }
+        if (group || begin_k >= H) return;
+        group = 1;
+        h0 = begin_k;
     }
 }
 
