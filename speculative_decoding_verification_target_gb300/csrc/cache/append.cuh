@@ -159,17 +159,30 @@ __global__ void __launch_bounds__(TOK_THREADS) read_kernel(const __grid_constant
 #pragma unroll 4
         for (int i = tid / LPT; i < n; i += PER) {
             const int t = sp.t0 + i;
-            const float s = scale_value(blk[(val ? B::VS : B::KS) + t * B::NG + c / 4]);
-            float x[8];
+            // 0x6400 | c + 8 is the half 1032 + c: less 1032 and times the scale, both exactly
+            const uint32_t s = blk[(val ? B::VS : B::KS) + t * B::NG + c / 4] * 0x00800080u;
+            uint32_t h[4];
             if (val) {
-                const int up = 8 * c >= D / 2 ? 4 : 0;
                 const uint2 w = *reinterpret_cast<const uint2*>(&s_codes[t][8 * c % (D / 2)]);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(static_cast<int>(((q < 4 ? w.x : w.y) >> (q % 4 * 8 + up)) & 15u) - 8) * s;
+                const int up = 8 * c >= D / 2 ? 4 : 0;
+                const uint32_t a = w.x >> up & 0x0F0F0F0Fu, z = w.y >> up & 0x0F0F0F0Fu;
+                h[0] = __byte_perm(a, 0x64u, 0x4140), h[1] = __byte_perm(a, 0x64u, 0x4342);
+                h[2] = __byte_perm(z, 0x64u, 0x4140), h[3] = __byte_perm(z, 0x64u, 0x4342);
             } else {
                 const uint32_t w = *reinterpret_cast<const uint32_t*>(blk + B::key(c / 4, t) + (c % 4) * 4);
+                uint32_t g[4];      // codes q and q + 4
 #pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = static_cast<float>(static_cast<int>((w >> (4 * q)) & 15u) - 8) * s;
+                for (int q = 0; q < 4; ++q) g[q] = (w >> (4 * q) & 0x000F000Fu) | 0x64006400u;
+                h[0] = __byte_perm(g[0], g[1], 0x5410), h[1] = __byte_perm(g[2], g[3], 0x5410);
+                h[2] = __byte_perm(g[0], g[1], 0x7632), h[3] = __byte_perm(g[2], g[3], 0x7632);
+            }
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h[q]), __float2half2_rn(1032.f)),
+                                          *reinterpret_cast<const __half2*>(&s));
+                const float2 f = __half22float2(v);
+                x[2 * q] = f.x, x[2 * q + 1] = f.y;
             }
             Eight<T> e;
             e.set(x);
