@@ -36,6 +36,7 @@ namespace specc {
 
 constexpr int ATT_MAX_CTAS = 640;
 constexpr int ATT_WAIT_TRIES = 20000000;    // seconds, whatever a try takes
+constexpr int ATT_UNIT = 2;             // what beginning and ending a unit costs, in tiles
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
 constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
 
@@ -255,6 +256,11 @@ struct __align__(16) TileInfo {
 };
 constexpr int TILE_FIRST = 1, TILE_LAST = 2, TILE_ALONE = 4;    // of this CTA's part of the unit; the part is the unit
 
+struct Place {
+    long long start;         // of the sequence, on the line
+    int b;
+};
+
 // Named barriers: computing threads and the fetching warp (keys stored; probabilities stored, with a vote), computing
 // threads alone.
 constexpr int BAR_KEYS = 1, BAR_PROBS = 2, BAR_COMPUTE = 3;
@@ -292,15 +298,14 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     __shared__ long long s_off[NC];                      // output row offset, -1: no such row
     __shared__ int s_live[NC];                            // 1: a row, 0: a row past q_len or none
     __shared__ long long s_scan[TH / 32 + 1];
-    __shared__ long long s_start;
-    __shared__ int s_b;
+    __shared__ Place s_place[2];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t sm = specv::smem_addr(smem);
 
-    // ---- the CTA's run of tiles
+    // ---- the CTA's run of tiles: an equal share of the line on which each unit takes its tiles and ATT_UNIT more in front
     long long mine = 0;
-    for (int b = tid; b < p.B; b += TH) mine += load_seq(p, b, blockIdx.x == 0).T;
+    for (int b = tid; b < p.B; b += TH) mine += load_seq(p, b, blockIdx.x == 0).T + ATT_UNIT;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) s_scan[warp] = mine;
@@ -316,19 +321,19 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, s_tmem, 0);
-    const long long per_t = static_cast<long long>(p.Hk) * p.RB;
-    long long total = 0;
-    for (int w = 0; w < TH / 32; ++w) total += s_scan[w];
-    total *= per_t;
-    const long long A = min(static_cast<long long>(gridDim.x), total);     // CTAs with work
-    const long long g = blockIdx.x;
-    const long long lo = g < A ? g * total / A : 0, hi = g < A ? (g + 1) * total / A : 0;
-    if (lo < hi) {
-        // the sequence that holds tile lo: running sums over chunks of TH sequences
+    const long long per_t = static_cast<long long>(p.Hk) * p.RB;      // units of a sequence
+    long long line = 0;
+    for (int w = 0; w < TH / 32; ++w) line += s_scan[w];
+    line *= per_t;
+    const long long A = min(static_cast<long long>(gridDim.x), line), g = blockIdx.x;     // CTAs with a share
+    const long long lo = g < A ? g * line / A : line, hi = g < A ? (g + 1) * line / A : line;
+    {
+        // the sequences that hold places lo and hi: running sums over chunks of TH sequences
+        if (tid < 2) s_place[tid].b = p.B;
         long long before = 0;
         for (int b0 = 0; b0 < p.B; b0 += TH) {
             const int b = b0 + tid;
-            const long long c = b < p.B ? load_seq(p, b, false).T * per_t : 0;
+            const long long c = b < p.B ? (load_seq(p, b, false).T + ATT_UNIT) * per_t : 0;
             long long x = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -343,30 +348,37 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 if (w < warp) end += s_scan[w];
                 before += s_scan[w];
             }
-            if (c && lo < end && lo >= end - c) {
-                s_b = b;
-                s_start = end - c;
-            }
-            if (lo < before) break;      // the same for every thread
+            if (c && lo < end && lo >= end - c) s_place[0] = {end - c, b};
+            if (c && hi < end && hi >= end - c) s_place[1] = {end - c, b};
+            if (hi < before) break;      // the same for every thread
         }
     }
     __syncthreads();
-    const int tiles = static_cast<int>(hi - lo);
+    // tiles before each place (a unit's own come after its ATT_UNIT), and the one to begin with
+    Cursor at = {};
+    long long from = 0, to = 0;
+    for (int i = 1; i >= 0; --i) {
+        const Place pl = s_place[i];
+        at.b = pl.b;
+        long long& n = i ? to : from;
+        if (pl.b >= p.B) {
+            n = line - ATT_UNIT * per_t * p.B;
+        } else {
+            at.s = load_seq(p, pl.b, false);
+            const long long rem = (i ? hi : lo) - pl.start, len = at.s.T + ATT_UNIT;
+            const int unit = static_cast<int>(rem / len);
+            at.t = max(static_cast<int>(rem - unit * len) - ATT_UNIT, 0);
+            at.h = unit / p.RB;
+            at.rb = unit - at.h * p.RB;
+            n = pl.start - ATT_UNIT * per_t * pl.b + static_cast<long long>(unit) * at.s.T + at.t;
+        }
+    }
+    const int tiles = static_cast<int>(to - from);
     int tries = ATT_WAIT_TRIES;
     auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, tries, p.status); };
 
     if (warp == CT / 32) {
         // ================ the fetching warp: copies ahead, and both products of each tile
-        Cursor at = {};
-        if (tiles > 0) {
-            at.b = s_b;
-            at.s = load_seq(p, at.b, false);
-            const long long rem = lo - s_start;
-            const int unit = static_cast<int>(rem / at.s.T);
-            at.t = static_cast<int>(rem - static_cast<long long>(unit) * at.s.T);
-            at.h = unit / p.RB;
-            at.rb = unit - at.h * p.RB;
-        }
         int4 desc = make_int4(0, 0, 0, 0);
         int issued = 0, t0 = at.t;
         // the unit's query block: first row, rows, and the positions between which a page is seen whole by all of it
@@ -376,6 +388,13 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
             rows = min(p.rpb, p.N * p.G - r0);
             seen_by_all = at.s.len - at.s.ql + r0 / p.G - (PAGE - 1);
             before_all = p.window == 0 ? -1 : static_cast<int>(max(-1LL, static_cast<long long>(at.s.len) - at.s.ql + (r0 + rows - 1) / p.G - p.window));
+            for (int n = lane; n < rows; n += 32) {        // its queries, which are read when its first tile is there
+                const int r = r0 + n, i = r / p.G;
+                const unsigned char* const q = static_cast<const unsigned char*>(p.q.p) +
+                                               2 * (at.b * p.q.sb + i * p.q.sn + (at.h * p.G + (r - i * p.G)) * p.q.sh);
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128));
+            }
         };
         // lanes 0 and 1 have a page of the next tile each; their numbers are read one tile before they are needed
         int j = -1, e = -1;
@@ -407,8 +426,8 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                                  BL::BYTES, &s_full[st], policy);
             }
             if (last && starts && !ends) {       // the unit's tiles end in a later CTA
-                const long long end = lo + issued + (at.s.T - at.t);
-                desc = make_int4(at.b, at.h * p.RB + at.rb, static_cast<int>((end * A - 1) / total - g + 1), 0);
+                const long long end = hi + (at.s.T - at.t - 1);        // the place behind the unit's last tile: this one's is hi - 1
+                desc = make_int4(at.b, at.h * p.RB + at.rb, static_cast<int>((end * A - 1) / line - g + 1), 0);
             }
             if (++issued < tiles) {
                 at.next(p);
