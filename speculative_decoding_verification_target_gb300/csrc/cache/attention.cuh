@@ -9,8 +9,8 @@
 // a lane of it, turns its own token's (or channel's) codes into halves in registers and stores them there. Neither
 // operand's 16-bit form passes through shared memory; that would take three times the bandwidth of the
 // codes themselves, more than shared memory has at the rate HBM delivers them.
-//   - Codes to halves: 0x5400 | c << 4 is the half 64 + c, and one fused multiply-add with (s, -72 s) gives (c - 8) s
-//     exactly: s has four significant bits, so 72 s and the result are halves. 1.4 instructions a code.
+//   - Codes to halves: one logic and one multiply-add instruction for two, exactly (half_code), and a shift for every
+//     second pair: 1.1 instructions a key code, 1.5 a value code with its scales.
 //   - Key codes lie so that a token's 16 bytes of a group are one conflict-free load; the order of channels that
 //     falls out, 0 4 1 5 2 6 3 7 in each eight, is given to the queries as well. Value bytes hold channels r and r + D / 2
 //     of one token, so that a token can be appended without touching its neighbours' bytes; lanes of the lower
@@ -54,9 +54,6 @@ struct AttnParams {
     int RB, rpb;             // query blocks and rows of each
     int width, fp16;         // queries of a part in the workspace; activations in fp16 (else bf16)
     float scale;             // times log2 e
-    // 16, as a value that the compiler does not know: x 16 then stays a multiplication, for which there is more room
-    // than for shifts
-    uint32_t sixteen;
 };
 
 // WG warpgroups share a tile's tokens, each with NW of the queries.
@@ -77,7 +74,7 @@ struct Att {
     static constexpr int P = STAGES * TILE;               // byte offsets in dynamic shared memory
     static constexpr int Q = P + OK * ON * 2;
     static constexpr int VS = Q + NC * D * 2;
-    static constexpr int END = VS + CT / 32 * WORDS * 16;
+    static constexpr int END = VS + CT / 32 * WORDS * 8;
     // no more CTAs on an SM than its tensor memory has columns for: a further one would wait for one to end
     static constexpr int FLOOR = CTAS == 2 ? 78848 : CTAS == 3 ? 59392 : 47104;
     static constexpr int SMEM = END > FLOOR ? END : FLOOR;
@@ -169,18 +166,30 @@ __device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[W]) {
     }
 }
 
-// Two codes, in bits 4 .. 7 of x's halves, as halves (c - 8) s; o = -72 s. One logic instruction and one multiply-add;
-// `sixty_four`, 0x54005400, comes from shared memory, so that it stays in a register: the logic instruction takes one
-// immediate, and the compiler would rather build the other constant anew each time.
-__device__ __forceinline__ uint32_t half_code(uint32_t sixty_four, uint32_t x, uint32_t s, uint32_t o) {
+// Two codes, in the bits `mask` of x's halves, as halves (c - 8) s. Bits 0 .. 3 under 0x6400 are the half 1024 + c, bits
+// 4 .. 7 under 0x5400 the half 64 + c: one logic instruction, and one multiply-add with (s, o = -1032 s or -72 s), both exact: s
+// has four significant bits, and 129 and 9 times them fit a half's eleven. For keys, scales are taken 2^-4 smaller, so that
+// 1032 s stays a half (and the smallest ones are still exact).
+__device__ __forceinline__ uint32_t half_code(uint32_t x, uint32_t mask, uint32_t base, uint32_t s, uint32_t o) {
     uint32_t h, r;
-    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(h) : "r"(x), "r"(sixty_four));     // (x & a) | b
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(h) : "r"(x), "r"(mask), "r"(base));     // (x & mask) | base
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(s), "r"(o));
     return r;
 }
-__device__ __forceinline__ uint32_t minus72(uint32_t s) {
+// The same in two steps, with off = -1032 or -72: where s changes from code to code, o would have to be fetched with it.
+__device__ __forceinline__ uint32_t half_code_apart(uint32_t x, uint32_t mask, uint32_t base, uint32_t off, uint32_t s) {
+    uint32_t h, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(h) : "r"(x), "r"(mask), "r"(base));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(off));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(s));
+    return r;
+}
+constexpr uint32_t CODES_LOW = 0x000F000Fu, CODES_HIGH = 0x00F000F0u;
+constexpr uint32_t H2_1024 = 0x64006400u, H2_64 = 0x54005400u, H2_SMALLER = 0x2C002C00u, H2_M1032 = 0xE408E408u, H2_M72 = 0xD480D480u;
+constexpr float ATT_LARGER = 16.f;       // what keys are too small by
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xD480D480u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_full[C::STAGES];
     __shared__ __align__(8) uint64_t s_bar_s, s_bar_o;
-    __shared__ uint32_t s_tmem, s_c64;
+    __shared__ uint32_t s_tmem, s_base[2];
     __shared__ TileInfo s_info[C::INFOS];
     __shared__ __align__(16) float s_c[NC], s_nm[NC];    // c_n, -m_n
     __shared__ __align__(16) float s_fac[NC];
@@ -315,7 +324,8 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
         specv::mbar_init(&s_bar_s, 1);
         specv::mbar_init(&s_bar_o, 1);
         specv::fence_mbarrier_init_cluster();
-        s_c64 = 0x54005400u;
+        s_base[0] = H2_1024;
+        s_base[1] = H2_64;
     }
     tmem_fence_before();
     __syncthreads();
@@ -477,7 +487,12 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
         const int wg = warp >> 2, wq = warp & 3;
         const int tok = wq * 32 + lane;                      // this thread's lane of tensor memory
         const uint32_t tlane = tbase + (static_cast<uint32_t>(wq * 32) << 16);
-        const uint32_t c64 = *static_cast<volatile uint32_t*>(&s_c64);
+        // from shared memory, so that they stay in registers: the logic instruction takes one immediate, and the compiler would
+        // rather build the other constant anew each time
+        const uint32_t low = *static_cast<volatile uint32_t*>(&s_base[0]), high = *static_cast<volatile uint32_t*>(&s_base[1]);
+        // of the value bytes' two codes, this warp's channels have the lower or the upper one
+        const bool upper = D == 128 ? wq >> 1 : wq & 1;
+        const uint32_t v_mask = upper ? CODES_HIGH : CODES_LOW, v_base = upper ? high : low, v_off = upper ? H2_M72 : H2_M1032;
         const uint32_t col_o = tlane + C::COL_O + (D == 64 && wq >= 2 ? NC : 0) + wg * NW;
         unsigned long long l[NW / 2];      // this thread's part of each query's sum
 #pragma unroll
@@ -526,20 +541,20 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                         *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * C::KQ + (n >> 3) * 128 + (n & 7) * 16 + to * 2) =
                             __float2half_rn(x[e] * up);
                     }
-                    if (lane == 0) s_c[n] = s_live[n] ? p.scale * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
+                    if (lane == 0) s_c[n] = s_live[n] ? p.scale * ATT_LARGER * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
                 }
                 specv::fence_proxy_async_shared();
                 bar_sync(BAR_COMPUTE, CT);
             }
             // ---- the scales of this warp's values: a lane has four tokens of the warp's group, pairs (0, 2) and (1, 3)
-            unsigned char* const vs = smem + C::VS + warp * C::WORDS * 16;
+            unsigned char* const vs = smem + C::VS + warp * C::WORDS * 8;
             if (lane < C::WORDS) {
                 const int q = wg * C::WORDS + lane, page = D == 128 ? q / 16 : wq >> 1, t4 = (4 * q) % PAGE, gr = wq % NG;
                 const int from = page ? pos1 : pos0, left = from >= 0 ? f.len - from - t4 : 0;      // tokens that hold something
                 const unsigned char* const b = tile + page * BL::BYTES + BL::VS + t4 * NG + gr;
                 const uint32_t s02 = (left > 0 ? b[0] * 0x80u : 0u) | (left > 2 ? b[2 * NG] * 0x800000u : 0u);
                 const uint32_t s13 = (left > 1 ? b[NG] * 0x80u : 0u) | (left > 3 ? b[3 * NG] * 0x800000u : 0u);
-                *reinterpret_cast<uint4*>(vs + lane * 16) = make_uint4(s02, minus72(s02), s13, minus72(s13));
+                *reinterpret_cast<uint2*>(vs + lane * 8) = make_uint2(s02, s13);
             }
             // ---- keys to halves: this thread's token, this warpgroup's groups
             {
@@ -549,16 +564,17 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 for (int i = 0; i < NG / WG; ++i) {
                     const int gr = wg * (NG / WG) + i;
                     const uint4 v = *reinterpret_cast<const uint4*>(blk + BL::key(gr, t));
-                    const uint32_t s2 = blk[BL::KS + t * NG + gr] * 0x00800080u, o2 = minus72(s2);
+                    const uint32_t s2 = half2_mul(blk[BL::KS + t * NG + gr] * 0x00800080u, H2_SMALLER);
+                    const uint32_t ol = half2_mul(s2, H2_M1032), oh = half2_mul(s2, H2_M72);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     uint32_t kr[16];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t hi8 = w[q] >> 8;
-                        kr[4 * q] = half_code(c64, w[q] * p.sixteen, s2, o2);
-                        kr[4 * q + 1] = half_code(c64, w[q], s2, o2);
-                        kr[4 * q + 2] = half_code(c64, hi8 * p.sixteen, s2, o2);
-                        kr[4 * q + 3] = half_code(c64, hi8, s2, o2);
+                        const uint32_t w8 = w[q] >> 8;
+                        kr[4 * q] = half_code(w[q], CODES_LOW, low, s2, ol);
+                        kr[4 * q + 1] = half_code(w[q], CODES_HIGH, high, s2, oh);
+                        kr[4 * q + 2] = half_code(w8, CODES_LOW, low, s2, ol);
+                        kr[4 * q + 3] = half_code(w8, CODES_HIGH, high, s2, oh);
                     }
                     if (i == 0 && !(flags & TILE_FIRST)) {       // the tile before's values are read, their columns are free
                         wait(&s_bar_o, (k - 1) & 1);
@@ -573,8 +589,6 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
             // ---- values to halves, the first part of the tokens while the first product runs
             uint32_t vr[2 * C::WPP];
             auto values = [&](int part) {
-                const bool upper = D == 128 ? wq >> 1 : wq & 1;
-                const uint32_t up = upper ? 1u : p.sixteen;
                 const int r = D == 128 ? (wq & 1) * 32 + lane : lane;
 #pragma unroll
                 for (int u = 0; u < C::WPP / 4; ++u) {
@@ -582,11 +596,12 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                     const uint4 v = *reinterpret_cast<const uint4*>(tile + page * BL::BYTES + BL::value((run % 4) * 16, r));
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 sc = *reinterpret_cast<const uint4*>(vs + (part * C::WPP + 4 * u + q) * 16);
-                        const uint32_t y = w[q] * up;
-                        vr[8 * u + 2 * q] = half_code(c64, y, sc.x, sc.y);
-                        vr[8 * u + 2 * q + 1] = half_code(c64, y >> 8, sc.z, sc.w);
+                    for (int q = 0; q < 4; q += 2) {
+                        const uint4 sc = *reinterpret_cast<const uint4*>(vs + (part * C::WPP + 4 * u + q) * 8);
+                        vr[8 * u + 2 * q] = half_code_apart(w[q], v_mask, v_base, v_off, sc.x);
+                        vr[8 * u + 2 * q + 1] = half_code_apart(w[q] >> 8, v_mask, v_base, v_off, sc.y);
+                        vr[8 * u + 2 * q + 2] = half_code_apart(w[q + 1], v_mask, v_base, v_off, sc.z);
+                        vr[8 * u + 2 * q + 3] = half_code_apart(w[q + 1] >> 8, v_mask, v_base, v_off, sc.w);
                     }
                 }
             };

@@ -393,7 +393,6 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     p.window = window;
     p.sinks = sinks;
     p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    p.sixteen = 16u;
     p.G = Hq / Hk;
     const AttSplit split = att_split(N * p.G, D);
     p.RB = split.blocks;
