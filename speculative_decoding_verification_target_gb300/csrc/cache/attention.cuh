@@ -27,8 +27,6 @@
 // of which each CTA takes an equal run. A unit that is cut leaves partial (O, m, l) in the workspace, and a second kernel
 // joins them in a fixed order.
 #pragma once
-#include <type_traits>
-
 #include "cache_format.cuh"
 #include "tmem.cuh"
 
@@ -150,7 +148,7 @@ __device__ __forceinline__ void fold_columns(float (&v)[W], int lane, float* out
     }
 }
 
-// W columns of this thread's lane: 8, 16, 24, 32 or 40.
+// W columns of this thread's lane: 8, 16, 24 or 32.
 template <int W>
 __device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&v)[W]) {
     constexpr int B = W >= 32 ? 32 : W >= 16 ? 16 : 8;
@@ -222,19 +220,13 @@ __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int& 
 }
 
 // Bits [lo, hi) of a word, the ends clamped.
-template <class U>
-__device__ __forceinline__ U bit_range(int lo, int hi) {
-    constexpr int W = 8 * sizeof(U);
-    const U below_hi = hi >= W ? ~U(0) : hi > 0 ? (U(1) << hi) - 1 : U(0);
-    return lo >= W ? U(0) : lo > 0 ? below_hi & (~U(0) << lo) : below_hi;
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+    const uint32_t below_hi = hi >= 32 ? ~0u : hi > 0 ? (1u << hi) - 1u : 0u;
+    return lo >= 32 ? 0u : lo > 0 ? below_hi & (~0u << lo) : below_hi;
 }
 // The same value, tied to this place: keeps what is worked out from it inside its branch.
 __device__ __forceinline__ uint32_t here(uint32_t v) {
     asm volatile("" : "+r"(v));
-    return v;
-}
-__device__ __forceinline__ unsigned long long here(unsigned long long v) {
-    asm volatile("" : "+l"(v));
     return v;
 }
 
@@ -294,7 +286,6 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Att<D, WG, NW>;
     using BL = Block<D>;
-    using Bits = std::conditional_t<(NW > 32), unsigned long long, uint32_t>;      // one for each query of a thread
     constexpr int TH = C::TH, CT = C::CT, NC = C::NC, NQ = C::NQ, NG = BL::NG;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_full[C::STAGES];
@@ -621,7 +612,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
             }
             // ---- which queries see this thread's token: all of them where the whole tile is seen by all
             const bool whole = min(pos0, pos1) > f.before_all && max(pos0, pos1) <= f.seen_by_all;
-            Bits seen = ~Bits(0);
+            uint32_t seen = ~0u;
             if (!whole) {
                 const int from = tok < PAGE ? pos0 : pos1, at = from + tok % PAGE, base = f.len - f.ql;
                 int nlo = 0, nhi = 0;
@@ -631,7 +622,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                     if (p.window > 0 && at >= p.sinks)
                         nhi = static_cast<int>(min(max(static_cast<long long>(at) - base + p.window, 0LL), static_cast<long long>(p.N)) * p.G) - f.r0;
                 }
-                seen = bit_range<Bits>(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
+                seen = bit_range(nlo - wg * NW, nhi - wg * NW);      // of this thread's queries
             }
             unsigned long long x[NW / 2];
             for (bool move = flags & TILE_FIRST;; move = true) {
@@ -640,7 +631,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 if (move) {
                     // the references move to the maxima seen so far; l and, unless this is the part's first tile, O follow
                     float y[NW];
-                    const Bits bits = here(seen);
+                    const uint32_t bits = here(seen);
 #pragma unroll
                     for (int n = 0; n < NW; ++n) y[n] = bits >> n & 1 ? __uint_as_float(u[n]) * s_c[wg * NW + n] : -INFINITY;
                     fold_columns(y, lane, &s_red[wq][wg * NW], [](float a, float b) { return fmaxf(a, b); });
@@ -677,7 +668,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                     x[n / 2 + 1] = fma2(pack2(__uint_as_float(u[n + 2]), __uint_as_float(u[n + 3])), c.y, m.y);
                 }
                 if (!whole) {
-                    const Bits bits = here(seen);
+                    const uint32_t bits = here(seen);
 #pragma unroll
                     for (int n = 0; n < NW; n += 2) {
                         const float2 v = unpack2(x[n / 2]);

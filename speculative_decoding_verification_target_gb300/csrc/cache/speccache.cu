@@ -121,16 +121,16 @@ TokensParams tokens_params(const void* pool, int pages, const int32_t* table, in
 }
 
 // --------------------------------------------------------------------------------------------- attention
-// The queries that read a key head, in equal blocks: as many as the widest kernel takes (80 rows, 64 where D = 64: the
-// tensor memory's columns), each in the narrowest one that holds it. A block costs the conversion of its tiles once, so
-// one wide block is cheaper than two narrow ones.
+// The queries that read a key head, in equal blocks of at most 64 rows, each in the narrowest kernel that holds it: a block
+// costs the conversion of its tiles once, so one wide block is cheaper than two narrow ones (four sequences of 100001 to 131072
+// tokens, 8 key heads of 128: 64 rows 288 us as one block, 321 us as two of 32; 48 rows 228 and 288 us as two of 24).
 struct AttSplit {
     int blocks, rows, wg, nw;
 };
-AttSplit att_split(int rows, int D) {
-    const int most = D == 64 ? 64 : 80, blocks = (rows + most - 1) / most, per = (rows + blocks - 1) / blocks;
+AttSplit att_split(int rows) {
+    const int blocks = (rows + 63) / 64, per = (rows + blocks - 1) / blocks;
     const int wg = per > 32 ? 2 : 1;
-    return {blocks, per, wg, wg == 1 ? (per + 7) / 8 * 8 : per <= 48 ? 24 : per <= 64 ? 32 : 40};
+    return {blocks, per, wg, wg == 1 ? (per + 7) / 8 * 8 : per <= 48 ? 24 : 32};
 }
 
 // Workspace: header, the cut units' descriptions, and two parts for each CTA that there can be.
@@ -187,8 +187,6 @@ spec_status attend(const AttnParams& p, const AttSplit& s, cudaStream_t st) {
         return attend_as<D, 1, 32>(p, st);
     }
     if (s.nw == 24) return attend_as<D, 2, 24>(p, st);
-    if constexpr (D == 128)
-        if (s.nw == 40) return attend_as<D, 2, 40>(p, st);
     return attend_as<D, 2, 32>(p, st);
 }
 
@@ -356,7 +354,7 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
 
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
     if (N < 1 || N > MAX_Q || Hk < 1 || Hq < Hk || Hq > MAX_HEADS || Hq % Hk || (D != 64 && D != 128)) return 0;
-    return att_layout(att_split(N * (Hq / Hk), D), D).total;
+    return att_layout(att_split(N * (Hq / Hk)), D).total;
 }
 
 spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
@@ -394,7 +392,7 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     p.sinks = sinks;
     p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.G = Hq / Hk;
-    const AttSplit split = att_split(N * p.G, D);
+    const AttSplit split = att_split(N * p.G);
     p.RB = split.blocks;
     p.rpb = split.rows;
     p.width = split.wg * split.nw;
