@@ -457,9 +457,6 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 umma_commit(&s_bar_s);
             }
             __syncwarp();
-            // the slot of the tile before is free: its values were read before the vote. Here, not right after its second
-            // product, so that the next tile's first product does not wait for this.
-            if (k > 0 && issued < tiles) issue();
             while (bar_vote(BAR_PROBS, TH, false)) {}      // at most one turn: see the computing warps
             tmem_fence_after();
             if (elect_one()) {
@@ -469,6 +466,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 umma_commit(&s_bar_o);
             }
             __syncwarp();
+            if (issued < tiles) issue();       // into this tile's slot: its values were read before the vote
         }
         if (lane == 0) p.desc[g] = desc;
         // no copy is in flight into this CTA's shared memory when it is given back, even where a wait gave up
@@ -542,9 +540,21 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
             if (lane < C::WORDS) {
                 const int q = wg * C::WORDS + lane, page = D == 128 ? q / 16 : wq >> 1, t4 = (4 * q) % PAGE, gr = wq % NG;
                 const int from = page ? pos1 : pos0, left = from >= 0 ? f.len - from - t4 : 0;      // tokens that hold something
-                const unsigned char* const b = tile + page * BL::BYTES + BL::VS + t4 * NG + gr;
-                const uint32_t s02 = (left > 0 ? b[0] * 0x80u : 0u) | (left > 2 ? b[2 * NG] * 0x800000u : 0u);
-                const uint32_t s13 = (left > 1 ? b[NG] * 0x80u : 0u) | (left > 3 ? b[3 * NG] * 0x800000u : 0u);
+                // the tokens' scales of all groups, this one's picked out of them: a byte's place in a half is 7 up
+                const unsigned char* const b = tile + page * BL::BYTES + BL::VS + t4 * NG;
+                uint32_t s02, s13;
+                if constexpr (D == 128) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(b);
+                    s02 = __byte_perm(w.x, w.z, gr * 0x11 + 0x40), s13 = __byte_perm(w.y, w.w, gr * 0x11 + 0x40);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(b);
+                    s02 = __byte_perm(w.x, w.y, gr * 0x11 + 0x40), s13 = __byte_perm(w.x, w.y, gr * 0x11 + 0x62);
+                }
+                if (left < 4) {
+                    s02 &= (left > 0 ? 0xFFu : 0u) | (left > 2 ? 0xFF00u : 0u);
+                    s13 &= (left > 1 ? 0xFFu : 0u) | (left > 3 ? 0xFF00u : 0u);
+                }
+                s02 = (s02 & 0xFFu) << 7 | (s02 & 0xFF00u) << 15, s13 = (s13 & 0xFFu) << 7 | (s13 & 0xFF00u) << 15;
                 *reinterpret_cast<uint2*>(vs + lane * 8) = make_uint2(s02, s13);
             }
             // ---- keys to halves: this thread's token, this warpgroup's groups

@@ -90,6 +90,21 @@ int sm_count() {
         if (try_s != SPEC_OK) return try_s;    \
     } while (0)
 
+// A launch whose CTAs may take their places while the kernel before still runs; it waits for that kernel's end by itself.
+template <class P>
+cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
 // ------------------------------------------------------------------------------------------------ tokens
 spec_status check_tokens(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start, int dtype,
                          int B, int N, int Hk, int D, void* ws, size_t ws_bytes) {
@@ -165,16 +180,7 @@ spec_status attend_as(const AttnParams& p, cudaStream_t st) {
     const int ctas = static_cast<int>(std::min<long long>({static_cast<long long>(C::CTAS) * sms, ATT_MAX_CTAS / WG, tiles}));
     attention_kernel<D, WG, NW><<<ctas, C::TH, C::SMEM, st>>>(p);
     SPECC_TRY(launched("attention"));
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (p.rpb + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, p);
+    const cudaError_t e = launch_behind(attention_join_kernel<D>, p, dim3(ctas, (p.rpb + 3) / 4), 128, st);
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "attention's join failed: %s", cudaGetErrorString(e));
 }
 
@@ -442,10 +448,10 @@ spec_status spec_pages_reserve(void* pool, int layers, long long page_bytes, int
     p.a = n_new;
     p.out = served;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_cluster(reserve_kernel, p, cluster_for(pages), st);
+    cudaError_t e = launch_cluster(reserve_kernel, p, cluster_for(pages), st);
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "reserve failed: %s", cudaGetErrorString(e));
-    reserve_copy_kernel<<<4 * sms, COPY_THREADS, 0, st>>>(p);
-    return launched("reserve's copies");
+    e = launch_behind(reserve_copy_kernel, p, dim3(2 * sms), COPY_THREADS, st);
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "reserve's copies failed: %s", cudaGetErrorString(e));
 }
 
 spec_status spec_pages_commit(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
@@ -491,10 +497,10 @@ spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int
     p.page_bytes = page_bytes;
     p.out = used;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_cluster(compact_plan_kernel, p, cluster_for(pages), st);
+    cudaError_t e = launch_cluster(compact_plan_kernel, p, cluster_for(pages), st);
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "compact's plan failed: %s", cudaGetErrorString(e));
-    compact_move_kernel<<<8 * sms, COPY_THREADS, 0, st>>>(p);
-    return launched("compact");
+    e = launch_behind(compact_move_kernel, p, dim3(6 * sms), COPY_THREADS, st);
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "compact's moves failed: %s", cudaGetErrorString(e));
 }
 
 }  // extern "C"
