@@ -15,9 +15,9 @@ struct TokensParams {
 
 constexpr int TOK_THREADS = 256;
 
-__device__ __forceinline__ float max_nan(float a, float b) {      // a NaN if either is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {      // a NaN if any is
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -71,13 +71,13 @@ __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_consta
     const int n = sp.t1 - sp.t0, c = tid % LPT;
     const Heads& in = val ? p.v : p.k;
     unsigned char* const blk = p.pool + (static_cast<size_t>(sp.page) * p.Hk + h) * B::BYTES;
-    const T* const src = static_cast<const T*>(in.p) + b * in.sb + sp.i0 * in.sn + h * in.sh + 8 * c;
+    const T* src = static_cast<const T*>(in.p) + b * in.sb + (sp.i0 + tid / LPT) * in.sn + h * in.sh + 8 * c;
     Eight<T> e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int i = u * PER + tid / LPT;
         e[u] = {};
-        if (i < n) e[u].load(src + i * in.sn);
+        if (u * PER + tid / LPT < n) e[u].load(src);
+        src += PER * in.sn;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_consta
         float x[8], top = 0.f;
         e[u].get(x);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) top = max_nan(top, fabsf(x[q]));
+        for (int q = 0; q < 8; q += 2) top = max3_nan(top, fabsf(x[q]), fabsf(x[q + 1]));
         if (top != top) {             // a NaN counts as 0
             top = 0.f;
 #pragma unroll
@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_consta
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int sb = scale_bits(top);
-        const uint32_t w = codes_of(x, scale_value(sb));
+        const float s = scale_value(sb);
+        const uint32_t w = sb >= 8 && sb < SCALE_TOP ? codes_of<false>(x, s) : codes_of<true>(x, s);
         if (i < n) {
             if (val) s_codes[t][c] = w;
             else *reinterpret_cast<uint32_t*>(blk + B::key(c / 4, t) + (c % 4) * 4) = w;

@@ -52,6 +52,9 @@ __device__ __forceinline__ int scale_bits(float top) {
 // reciprocal is off by 2^-19 and is brought onto the grid of 2^-16 (by adding 192, whose last place that is). Adding
 // 1.5 2^23 then rounds to an integer, ties to even, which stands in the last bits of the sum: they are put together as they are,
 // and what the sums' upper bits add up to is taken away at once.
+// LIMIT: quotients may pass 7.5 (only where the scale is not the nearest 4-bit number to top / 7: in the subnormal range or at
+// its top; elsewhere top / s is at most 7 (1 + 1 / 16)).
+template <bool LIMIT>
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s) {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -59,7 +62,8 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float s) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(__fmaf_rn(x[i], inv, 192.f), 185.f), 199.f);
+        float q = __fmaf_rn(x[i], inv, 192.f);
+        if (LIMIT) q = fminf(fmaxf(q, 185.f), 199.f);
         w += __float_as_uint(__fadd_rn(q, 12582912.f - 184.f)) << (4 * i);
     }
     return w - 0x3F400000u;      // the sum of 0x4B400000 << 4 i, modulo 2^32

@@ -499,7 +499,7 @@ spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_cluster(compact_plan_kernel, p, cluster_for(pages), st);
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "compact's plan failed: %s", cudaGetErrorString(e));
-    e = launch_behind(compact_move_kernel, p, dim3(6 * sms), COPY_THREADS, st);
+    e = launch_behind(compact_move_kernel, p, dim3(16 * sms), COPY_THREADS, st);
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "compact's moves failed: %s", cudaGetErrorString(e));
 }
 
