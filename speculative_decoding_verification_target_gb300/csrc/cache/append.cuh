@@ -58,6 +58,8 @@ __device__ __forceinline__ bool span_of(const TokensParams& p, int b, int y, boo
 // warp fill a sector of each group. A value's codes lie with those of 15 other tokens, so they pass through shared
 // memory: there as words of eight channels by token, from there a thread gathers the 16 tokens of a byte row, two
 // channels, and writes 16 bytes (or, in a run that the range does not fill, the bytes that are its own).
+// 17400 tokens of 8 heads of 128 take 26 us (2.7 TB/s of 71 MB in and 19 MB out): instructions bound it, 79% of the slots are
+// taken; 41 us with divisions for the codes and keys and values in one CTA.
 template <class T, int D>
 __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_constant__ TokensParams p) {
     using B = Block<D>;
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_consta
 // The reverse, again keys and values apart: D / 8 lanes write a token, eight channels each. Keys are read where they lie;
 // value codes, 16 tokens of two channels at a time, go through shared memory as bytes by token. Positions without a page,
 // outside the table or past the count give zeros: CTA y clears those among inputs 64 y ...
+// Writes bound it: 32768 tokens, 17400 of them cached, of 8 heads of 128 take 30 us (153 MB, 5 TB/s).
 template <class T, int D>
 __global__ void __launch_bounds__(TOK_THREADS) read_kernel(const __grid_constant__ TokensParams p) {
     using B = Block<D>;

@@ -4,28 +4,37 @@
 // tokens), with keys k_t = c_t s_t and values likewise:
 //   S[t, n] = k_t . q_n,  p[t, n] = 2^(S c_n - m_n),  O[d, n] = sum_t v[t, d] p[t, n],  l_n = sum_t p[t, n],  out = O / l.
 // Both products run on the 5th-generation tensor cores with the CACHE as the M side: M = 128 tokens for S, M = 128
-// channels for O, N = NC queries. So the cost of a tile grows with the queries there are (NC = 16, 32 or 64) and
-// not with a padded block of them. The M operand comes from tensor memory, which is what makes 4 bits cheap: a thread is
-// a lane of it, turns its own token's (or channel's) codes into halves in registers and stores them there. Neither
-// operand's 16-bit form passes through shared memory; that would take three times the bandwidth of the
-// codes themselves, more than shared memory has at the rate HBM delivers them.
+// channels for O, N = NC queries. So the cost of a tile grows with the queries there are (NC = 16, 32, 48 or 64) and not with
+// a padded block of them. The M operand comes from tensor memory, which is what makes 4 bits cheap: a thread is a lane of
+// it, turns its own token's (or channel's) codes into halves in registers and stores them there. Neither operand's 16-bit
+// form passes through shared memory; that would take three times the bandwidth of the codes themselves, more than shared
+// memory has at the rate HBM delivers them.
 //   - Codes to halves: one logic and one multiply-add instruction for two, exactly (half_code), and a shift for every
-//     second pair: 1.1 instructions a key code, 1.5 a value code with its scales.
+//     second pair; a value code, whose scale changes from code to code, takes one instruction more a pair.
 //   - Key codes lie so that a token's 16 bytes of a group are one conflict-free load; the order of channels that
 //     falls out, 0 4 1 5 2 6 3 7 in each eight, is given to the queries as well. Value bytes hold channels r and r + D / 2
 //     of one token, so that a token can be appended without touching its neighbours' bytes; lanes of the lower
 //     and the upper half read the same bytes. Their tokens fall out in the order 0 2 1 3 in each four, which the
 //     probabilities' rows follow. A lane's scales change from token to token but are the same for the 32 channels of a
-//     warp: a table of (s, -72 s) pairs, rebuilt per tile, is read as broadcasts. Tokens that hold nothing have s = 0 there,
-//     so that whatever bits they have cannot reach O (0 times a NaN would).
+//     warp: a table of them, rebuilt per tile, is read as broadcasts (scales alone, 8 bytes for four tokens: with their
+//     offsets beside them it took 195 us where it takes 182, since broadcasts cost shared memory by their bytes). Tokens that
+//     hold nothing have s = 0 there, so that whatever bits they have cannot reach O (0 times a NaN would).
 //   - The softmax works on S^T: a thread has one token and all queries. m_n is not the maximum but a reference that
 //     any value near it may serve as: it is moved, and O and l rescaled, only where a score exceeds it by more than 2^8,
 //     which the barrier before the second product detects at no cost. l_n is kept per thread and added up at the end.
-// A tile is 128 tokens, two pages, fetched as one bulk copy each two tiles ahead. CTAs are small (128 threads, four to an
-// SM; for NC = 64 256 threads, two to an SM), and hide each other's waits.
-// Work is split evenly whatever the lengths: the tiles of all (sequence, key head, query block) units form one line,
-// of which each CTA takes an equal run. A unit that is cut leaves partial (O, m, l) in the workspace, and a second kernel
-// joins them in a fixed order.
+//     Probabilities are rounded to fp16 for the product, l is the sum of the unrounded ones.
+// A tile is 128 tokens, two pages, fetched as one bulk copy each, STAGES tiles ahead, by a warp that also issues the products:
+// with that in the computing warps, everyone waited for the one that did it. CTAs are small (four computing warps, four CTAs to
+// an SM, as many as the tensor memory has columns for; eight warps and two CTAs for over 32 queries) and hide each other's
+// waits.
+// Work is split evenly whatever the lengths: the tiles of all (sequence, key head, query block) units form one line, with
+// ATT_UNIT places more for each unit's beginning and end, of which each CTA takes an equal run (places of 0, 1, 2, 3 and 4
+// tiles: 75, 64, 65, 66 and 67 us on 48 sequences of 130 to 8191 tokens, 74, 66, 63, 62 and 63 us on 96 windows). A unit that is
+// cut leaves partial (O, m, l) in the workspace, and a second kernel joins them in a fixed order.
+// Measured, 8 key heads of 128: 48 sequences, one query row of four heads each, 219 MB of cache: 62 us, 3.5 TB/s; 64 sequences,
+// 24 rows, 627 MB: 178 us, 3.5 TB/s, half of the copy rate. What bounds it: 3800 (24 rows) warp instructions a tile where
+// HBM delivers one in 765 cycles, issued at 62% of the slots by four warps a scheduler; integer pipe 46%, shared memory
+// 51%, tensor pipe 16%, DRAM 39%.
 #pragma once
 #include "cache_format.cuh"
 #include "tmem.cuh"
@@ -33,7 +42,7 @@
 namespace specc {
 
 constexpr int ATT_MAX_CTAS = 640;
-constexpr int ATT_WAIT_TRIES = 20000000;    // seconds, whatever a try takes
+constexpr int ATT_WAIT_TRIES = 20000000;    // turns of a wait before it gives up: seconds
 constexpr int ATT_UNIT = 2;             // what beginning and ending a unit costs, in tiles
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
 constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
@@ -194,7 +203,7 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
 // Whether a query saw any token, from its reference and sum: a NaN among its scores never becomes the reference.
 __device__ __forceinline__ bool has_seen(float m, float sum) { return m > ATT_NONE || sum != sum; }
 
-// Without a time of its own: the waits here are short, and a sleep of a microsecond costs more than they do.
+// Without a time of its own: the waits here are short.
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(

@@ -22,7 +22,10 @@ constexpr int NORM_WARPS = 4;
 // turn wraps exactly in integer arithmetic, its top 32 bits are the angle to 2^-32 of a turn, so a far position costs no
 // precision and no table is read. A lane's channels are the same in every head: y_i = r (x_i P_i + x_mate Q_i), where P
 // and Q hold the weights and the cosines and sines, once for the query heads and once for the key heads.
-// Bandwidth bounds many tokens: U heads a lane are in flight. Few tokens are split into parts.
+// Bandwidth bounds many tokens: U heads a lane are on their way while U are worked on, the first of them before the angles
+// are. 16384 tokens of 32 + 8 heads of 128 in bf16 take 58 us, 5.8 TB/s, 86% of the copy rate (70 us without the loads ahead,
+// 86 us with a head's eight channels side by side in a lane and shuffles for the rotation). Few tokens are split into parts;
+// there latency counts: 384 tokens 6.9 us.
 template <class T, int D, bool INTER>
 __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int LPH = D / 8, RPW = 32 / LPH;   // lanes per head, heads per warp at a time
