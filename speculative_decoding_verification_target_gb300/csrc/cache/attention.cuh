@@ -42,7 +42,7 @@
 namespace specc {
 
 constexpr int ATT_MAX_CTAS = 640;
-constexpr int ATT_WAIT_TRIES = 20000000;    // turns of a wait before it gives up: seconds
+constexpr uint64_t ATT_WAIT_NS = 2000000000ull;      // after which a wait gives up
 constexpr int ATT_UNIT = 2;             // what beginning and ending a unit costs, in tiles
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
 constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
@@ -214,16 +214,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits, as a warp, for a phase of `bar`, at most `tries` turns; where it gives up it sets the status bit and leaves 0 in
-// `tries`, so that later waits end at once (the results are invalid, but every barrier is still met). A try sleeps in
-// hardware until the phase ends or its time is up, so turns are few.
-__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, int& tries, unsigned* status) {
-    int left = tries;
-    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-        if (--left < 0) {
-            if (tries) atomicOr(status, SPEC_STATUS_TIMEOUT);
-            tries = 0;
-            break;
+// Waits, as a warp, for a phase of `bar`. Where it gives up it sets the status bit and clears `alive`, so that later waits
+// end at once (the results are invalid, but every barrier is still met). A try sleeps in hardware until the phase ends or
+// its time is up, so turns are few; the clock is looked at every 256 of them.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, bool& alive, unsigned* status) {
+    uint64_t since = 0;
+    for (int i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) && alive; ++i) {
+        if (i % 256 == 0) {
+            const uint64_t now = specv::global_timer_ns();
+            if (since == 0) since = now;
+            if (!__all_sync(0xffffffffu, now - since < ATT_WAIT_NS)) {
+                atomicOr(status, SPEC_STATUS_TIMEOUT);
+                alive = false;
+            }
         }
     }
 }
@@ -384,8 +387,8 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
         }
     }
     const int tiles = static_cast<int>(to - from);
-    int tries = ATT_WAIT_TRIES;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, tries, p.status); };
+    bool alive = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, alive, p.status); };
 
     if (warp == CT / 32) {
         // ================ the fetching warp: copies ahead, and both products of each tile

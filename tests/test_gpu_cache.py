@@ -229,6 +229,65 @@ def test_attention_window_and_sinks(window, sinks, N, D):
     check_attention(*attention_case(rng, 4, N, 6, 2, D, [1, 64, 400, 777], torch.bfloat16, window, sinks), window=window, sinks=sinks)
 
 
+def device_check(q, pool, table, lens, window=0, sinks=0):
+    """As check_attention, with the plain form in fp64 on the GPU over what cache_read gives (exact)."""
+    B, N, Hq, D = q.shape
+    H, n = pool.shape[1], int(lens.max())
+    G = Hq // H
+    r = sv.cache_attention(q, pool, table, lens, window=window, sinks=sinks, want_lse=True)
+    assert sv.read_status(r["workspace"]) == 0
+    held = sv.cache_read(pool, table, torch.zeros_like(lens), n, counts=lens, dtype=torch.float16)
+    at = torch.arange(n, device="cuda")
+    for b in range(B):
+        k, v = held["k"][b].double().transpose(0, 1), held["v"][b].double().transpose(0, 1)          # [H, n, D]
+        x = q[b].double().view(N, H, G, D).permute(1, 0, 2, 3).reshape(H, N * G, D)
+        pos = (int(lens[b]) - N + torch.arange(N, device="cuda"))[:, None]
+        see = at <= pos
+        if window:
+            see &= (at > pos - window) | (at < sinks)
+        see = see.repeat_interleave(G, 0)[None]
+        sc = (x @ k.transpose(1, 2) * D ** -0.5).masked_fill(~see, -torch.inf)
+        lse = sc.logsumexp(-1)
+        p = torch.where(see, (sc - torch.where(lse.isinf(), 0, lse)[..., None]).exp(), 0)
+        ref, mass = p @ v, p @ v.abs()
+        delta = 2.0 ** -17 * ((x.abs() @ k.abs().transpose(1, 2)) * see).amax(-1) * D ** -0.5
+        total = see.double().expand(H, -1, -1) @ v.abs()
+        out = r["out"][b].double().view(N, H, G, D).permute(1, 0, 2, 3).reshape(H, N * G, D)
+        tol = torch.finfo(q.dtype).eps / 2 * ref.abs() + (2.0 ** -11 + 2.0 ** -13 + 2 * delta[..., None]) * mass + 2.0 ** -25 * total
+        assert ((out - ref).abs() <= tol + torch.finfo(q.dtype).tiny).all(), b
+        got = r["lse"][b].double().view(N, H, G).permute(1, 0, 2).reshape(H, N * G)
+        assert torch.equal(got.isinf(), lse.isinf()) and ((got - lse).abs()[~lse.isinf()] <= (delta + 2.0 ** -20 * (1 + lse.abs()))[~lse.isinf()]).all(), b
+
+
+def device_case(seed, B, N, Hq, H, D, lens, dt):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    M = (int(lens.max()) + 63) // 64
+    table = torch.randperm(B * M, generator=g, device="cuda").to(torch.int32).view(B, M)
+    pool = sv.new_pool(B * M, H, D)
+    step = 8192
+    for a in range(0, M * 64, step):
+        n = min(step, M * 64 - a)
+        kv = torch.randn((2, B, n, H, D), generator=g, device="cuda").to(dt)
+        sv.cache_append(pool, table, torch.full_like(lens, a), kv[0], kv[1])
+    return torch.randn((B, N, Hq, D), generator=g, device="cuda").to(dt), pool, table, lens
+
+
+@pytest.mark.parametrize("B,N,Hq,H,D,lens,window,sinks", [
+    (400, 2, 4, 2, 64, [(37 * b) % 301 for b in range(400)], 0, 0),              # more sequences than a CTA has threads, empty ones too
+    (200, 1, 8, 1, 128, [1 + (91 * b) % 777 for b in range(200)], 100, 3),
+    (1, 3, 4, 1, 128, [131035], 0, 0),                                           # one unit over all CTAs
+    (2, 1, 1, 1, 64, [65536, 3], 0, 0),
+    (1, 300, 4, 2, 128, [1000], 0, 0),                                           # many query blocks
+    (2, 1024, 2, 2, 64, [1024, 2500], 300, 70),
+    (3, 20, 2, 1, 128, [5000, 40, 129], 0, 0), (2, 7, 8, 1, 64, [700, 3000], 1000, 10),    # widths 48 and 64
+])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_attention_on_larger_shapes(dtype, B, N, Hq, H, D, lens, window, sinks):
+    q, pool, table, lens = device_case(B + N, B, N, Hq, H, D, lens, DT[dtype])
+    device_check(q, pool, table, lens, window, sinks)
+
+
 def test_attention_ragged_queries():
     rng = np.random.default_rng(7)
     check_attention(*attention_case(rng, 6, 5, 8, 2, 128, [0, 1, 3, 70, 128, 500], torch.bfloat16, q_len=[5, 0, 5, 1, 3, 5]))
