@@ -39,8 +39,8 @@
  * not overlap on the GPU. Empty calls (B, N or the number of pairs 0) do nothing.
  *
  * Activations are bf16, fp16 or, for the norm and rotation, fp32 (dtype: SPEC_BF16, SPEC_FP16, SPEC_FP32), as
- * [B, N, heads, D] with any strides over B, N and heads and contiguous channels; pointers and strides are
- * multiples of 16 bytes. D is 64 or 128 (the norm and rotation also 256).
+ * [B, N, heads, D] with any strides over B, N and heads and contiguous channels; pointers and strides (of more than
+ * one entry) are multiples of 16 bytes. D is 64 or 128 (the norm and rotation also 256).
  */
 #ifndef SPECCACHE_H
 #define SPECCACHE_H

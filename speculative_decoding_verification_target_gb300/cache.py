@@ -107,6 +107,17 @@ def _heads(t, name, shape, dtype):
     return Heads(t.data_ptr(), sb, sn, sh)
 
 
+def _own(t):
+    """The same for an output made here, which needs no check."""
+    sb, sn, sh, _ = t.stride()
+    return Heads(t.data_ptr(), sb, sn, sh)
+
+
+def _vector(t, name, dtype, shape):
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+
+
 def _pool(pool, name="pool"):
     if not (pool.is_cuda and pool.dtype is torch.uint8 and pool.is_contiguous()):
         _need(pool, name, torch.uint8)
@@ -170,27 +181,34 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
                  k_out=None, stream=None):
     """Root-mean-square norm of each head of q [B, N, Hq, D] and k [B, N, Hk, D], times a weight [D], and rotation of the
     first 2 len(freqs) channels by position (int32 [B, N]). bf16, fp16 or fp32. freqs from rope_frequencies, or None
-    for the norm alone. q_out, k_out may be q and k. Returns dict(q, k)."""
+    for the norm alone. q_out, k_out may be q and k; unless given they are laid out in q's and k's order. Returns
+    dict(q, k)."""
     B, N, Hq, D = q.shape
     Hk = k.shape[2]
     dt = q.dtype
     code = _code(q, "q", True)
-    if q_out is None:
-        q_out = torch.empty((B, N, Hq, D), dtype=dt, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((B, N, Hk, D), dtype=dt, device=q.device)
-    rotary = 0
+    qi, ki = _heads(q, "q", (B, N, Hq, D), dt), _heads(k, "k", (B, N, Hk, D), dt)
+    rotary, pos, fr = 0, None, None
     if freqs is not None:
-        _need(freqs, "freqs", torch.int64)
+        _vector(freqs, "freqs", torch.int64, (freqs.numel(),))
         _ints(positions, "positions", (B, N))
-        rotary = 2 * freqs.numel()
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, dt, (D,))
-    _ok(_lib().spec_qk_norm_rope(_heads(q, "q", (B, N, Hq, D), dt), _heads(k, "k", (B, N, Hk, D), dt), code, B, N, Hq, Hk,
-                                 D, positions.data_ptr() if rotary else None, freqs.data_ptr() if rotary else None, rotary, interleaved,
-                                 _ptr(q_weight), _ptr(k_weight), eps, _heads(q_out, "q_out", (B, N, Hq, D), dt),
-                                 _heads(k_out, "k_out", (B, N, Hk, D), dt), _on(q, stream)))
+        rotary, pos, fr = 2 * freqs.numel(), positions.data_ptr(), freqs.data_ptr()
+    if q_weight is not None:
+        _vector(q_weight, "q_weight", dt, (D,))
+    if k_weight is not None:
+        _vector(k_weight, "k_weight", dt, (D,))
+    if q_out is None:
+        q_out = torch.empty_like(q)
+        qo = _own(q_out)
+    else:
+        qo = _heads(q_out, "q_out", (B, N, Hq, D), dt)
+    if k_out is None:
+        k_out = torch.empty_like(k)
+        ko = _own(k_out)
+    else:
+        ko = _heads(k_out, "k_out", (B, N, Hk, D), dt)
+    _ok(_lib().spec_qk_norm_rope(qi, ki, code, B, N, Hq, Hk, D, pos, fr, rotary, interleaved, _ptr(q_weight),
+                                 _ptr(k_weight), eps, qo, ko, _on(q, stream)))
     return dict(q=q_out, k=k_out)
 
 
@@ -222,14 +240,19 @@ def cache_read(pool, table, start, n, *, counts=None, dtype=torch.bfloat16, k=No
         _ints(counts, "counts", (B,))
     if k is None:
         k = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+        ki = _own(k)
+    else:
+        ki = _heads(k, "k", (B, n, H, D), dtype)
     if v is None:
         v = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+        vi = _own(v)
+    else:
+        vi = _heads(v, "v", (B, n, H, D), dtype)
     code = _code(k, "k")
     if workspace is None:
         workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
-    _ok(_lib().spec_cache_read(_ptr(pool), P, _ptr(table), M, _ptr(start), _ptr(counts), _heads(k, "k", (B, n, H, D), dtype),
-                               _heads(v, "v", (B, n, H, D), dtype), code, B, n, H, D, _ptr(workspace), workspace.numel(),
-                               _on(pool, stream)))
+    _ok(_lib().spec_cache_read(pool.data_ptr(), P, table.data_ptr(), M, start.data_ptr(), _ptr(counts), ki, vi, code, B, n, H, D,
+                               workspace.data_ptr(), workspace.numel(), _on(pool, stream)))
     return dict(k=k, v=v, workspace=workspace)
 
 
@@ -246,18 +269,21 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     _ints(kv_len, "kv_len", (B,))
     if q_len is not None:
         _ints(q_len, "q_len", (B,))
+    qi = _heads(q, "q", (B, N, Hq, D), q.dtype)
     if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-    if lse is None and want_lse:
+        out = torch.empty_like(q)
+        oi = _own(out)
+    else:
+        oi = _heads(out, "out", (B, N, Hq, D), q.dtype)
+    if lse is not None:
+        _vector(lse, "lse", torch.float32, (B, N, Hq))
+    elif want_lse:
         lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
-    elif lse is not None:
-        _need(lse, "lse", torch.float32, (B, N, Hq))
     if workspace is None:
         workspace = new_attention_workspace(N, Hq, H, D, q.device)
-    _ok(_lib().spec_cache_attention(_heads(q, "q", (B, N, Hq, D), q.dtype), code, _ptr(pool), P, _ptr(table), M, _ptr(kv_len),
-                                    _ptr(q_len), B, N, Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks,
-                                    _heads(out, "out", (B, N, Hq, D), q.dtype), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                    _on(q, stream)))
+    _ok(_lib().spec_cache_attention(qi, code, pool.data_ptr(), P, table.data_ptr(), M, kv_len.data_ptr(), _ptr(q_len), B, N,
+                                    Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks, oi, _ptr(lse),
+                                    workspace.data_ptr(), workspace.numel(), _on(q, stream)))
     return dict(out=out, lse=lse, workspace=workspace)
 
 
@@ -265,13 +291,15 @@ def _books(table, lengths, refs):
     S, M = _table(table)
     if lengths is not None:
         _ints(lengths, "lengths", (S,))
-    _need(refs, "refs", torch.int32)
-    return S, M, refs.numel()
+    P = refs.numel()
+    _ints(refs, "refs", (P,))
+    return S, M, P
 
 
 def _layers(pool, P):
     """[pages, ...] or [layers, pages, ...] as (layers, bytes of a page)."""
-    _need(pool, "pool", torch.uint8)
+    if not (pool.is_cuda and pool.dtype is torch.uint8 and pool.is_contiguous()):
+        _need(pool, "pool", torch.uint8)
     if pool.dim() not in (3, 4) or pool.shape[-3] != P:
         raise ValueError("pool must be [%d, Hk, 68 D] or [layers, %d, Hk, 68 D], got %s" % (P, P, tuple(pool.shape)))
     return (pool.shape[0] if pool.dim() == 4 else 1), pool.shape[-2] * pool.shape[-1]

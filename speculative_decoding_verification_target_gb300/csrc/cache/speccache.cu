@@ -35,11 +35,11 @@ size_t elem_bytes(int dtype) { return dtype == SPEC_FP32 ? 4 : 2; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A [B, N, heads, D] argument: present, and every row 16-byte aligned.
-spec_status check_heads(const spec_heads* t, const char* name, int dtype) {
+// A [B, N, heads, D] argument: present, and every row 16-byte aligned (the stride of a single entry says nothing).
+spec_status check_heads(const spec_heads* t, const char* name, int dtype, int B, int N, int heads) {
     if (!t || !t->data) return fail(SPEC_ERR_INVALID, "%s must not be NULL", name);
     const long long per = 16 / static_cast<long long>(elem_bytes(dtype));
-    if (!aligned16(t->data) || t->stride_b % per || t->stride_n % per || t->stride_h % per)
+    if (!aligned16(t->data) || (B > 1 && t->stride_b % per) || (N > 1 && t->stride_n % per) || (heads > 1 && t->stride_h % per))
         return fail(SPEC_ERR_INVALID, "%s: the pointer and every stride must be a multiple of 16 bytes", name);
     return SPEC_OK;
 }
@@ -270,12 +270,12 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPEC_ERR_INVALID, "eps must be finite and not negative");
     if (B == 0 || N == 0) return SPEC_OK;
     if (Hq > 0) {
-        SPECC_TRY(check_heads(q, "q", dtype));
-        SPECC_TRY(check_heads(q_out, "q_out", dtype));
+        SPECC_TRY(check_heads(q, "q", dtype, B, N, Hq));
+        SPECC_TRY(check_heads(q_out, "q_out", dtype, B, N, Hq));
     }
     if (Hk > 0) {
-        SPECC_TRY(check_heads(k, "k", dtype));
-        SPECC_TRY(check_heads(k_out, "k_out", dtype));
+        SPECC_TRY(check_heads(k, "k", dtype, B, N, Hk));
+        SPECC_TRY(check_heads(k_out, "k_out", dtype, B, N, Hk));
     }
     if (rotary && (!positions || !freqs)) return fail(SPEC_ERR_INVALID, "positions and freqs must not be NULL");
     if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(SPEC_ERR_INVALID, "weights must be 16-byte aligned");
@@ -320,8 +320,8 @@ spec_status spec_cache_append(void* pool, int pages, const int32_t* table, int m
                               int D, void* workspace, size_t workspace_bytes, void* stream) {
     SPECC_TRY(check_tokens(pool, pages, table, max_pages, start, dtype, B, N, Hk, D, workspace, workspace_bytes));
     if (B == 0 || N == 0) return SPEC_OK;
-    SPECC_TRY(check_heads(k, "k", dtype));
-    SPECC_TRY(check_heads(v, "v", dtype));
+    SPECC_TRY(check_heads(k, "k", dtype, B, N, Hk));
+    SPECC_TRY(check_heads(v, "v", dtype, B, N, Hk));
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, k, v, B, N, Hk, workspace);
     const dim3 grid(2 * Hk, (N + PAGE - 2) / PAGE + 1, B);   // a run of N tokens touches at most that many pages
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -341,8 +341,8 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
     SPECC_TRY(check_tokens(pool, pages, table, max_pages, start, dtype, B, N, Hk, D, workspace, workspace_bytes));
     if (B == 0 || N == 0) return SPEC_OK;
     const bool has_k = k_out && k_out->data, has_v = v_out && v_out->data;
-    if (has_k) SPECC_TRY(check_heads(k_out, "k_out", dtype));
-    if (has_v) SPECC_TRY(check_heads(v_out, "v_out", dtype));
+    if (has_k) SPECC_TRY(check_heads(k_out, "k_out", dtype, B, N, Hk));
+    if (has_v) SPECC_TRY(check_heads(v_out, "v_out", dtype, B, N, Hk));
     if (!has_k && !has_v) return fail(SPEC_ERR_INVALID, "k_out and v_out must not both be NULL");
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, has_k ? k_out : nullptr,
                                          has_v ? v_out : nullptr, B, N, Hk, workspace);
@@ -374,8 +374,8 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID, "scale must be finite");
     if (window < 0 || sinks < 0) return fail(SPEC_ERR_INVALID, "window and sinks must not be negative");
     if (B == 0 || N == 0) return SPEC_OK;
-    SPECC_TRY(check_heads(q, "q", dtype));
-    SPECC_TRY(check_heads(out, "out", dtype));
+    SPECC_TRY(check_heads(q, "q", dtype, B, N, Hq));
+    SPECC_TRY(check_heads(out, "out", dtype, B, N, Hq));
     SPECC_TRY(check_table(pool, pages, table, max_pages));
     if (!kv_len) return fail(SPEC_ERR_INVALID, "kv_len must not be NULL");
     SPECC_TRY(check_workspace(workspace, workspace_bytes, spec_cache_attention_workspace_size(N, Hq, Hk, D)));
