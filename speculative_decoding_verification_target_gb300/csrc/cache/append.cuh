@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(TOK_THREADS) append_kernel(const __grid_consta
     constexpr int LPT = D / 8, PER = TOK_THREADS / LPT;      // lanes of a token, tokens of a pass
     constexpr int U = PAGE / PER;                            // passes of a page
     __shared__ uint32_t s_codes[PAGE][LPT];
+    after_previous();
     const bool val = blockIdx.x >= p.Hk;
     const int h = val ? blockIdx.x - p.Hk : blockIdx.x, b = blockIdx.z, tid = threadIdx.x;
     Span sp;
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(TOK_THREADS) read_kernel(const __grid_constant
     using B = Block<D>;
     constexpr int LPT = D / 8, PER = TOK_THREADS / LPT;
     __shared__ __align__(16) unsigned char s_codes[PAGE][D / 2];
+    after_previous();
     const bool val = blockIdx.x >= p.Hk;
     const int h = val ? blockIdx.x - p.Hk : blockIdx.x, b = blockIdx.z, tid = threadIdx.x, c = tid % LPT;
     const Heads& o = val ? p.v : p.k;

@@ -32,7 +32,7 @@
 // tiles: 75, 64, 65, 66 and 67 us on 48 sequences of 130 to 8191 tokens, 74, 66, 63, 62 and 63 us on 96 windows). A unit that is
 // cut leaves partial (O, m, l) in the workspace, and a second kernel joins them in a fixed order.
 // Measured, 8 key heads of 128: 48 sequences, one query row of four heads each, 219 MB of cache: 62 us, 3.5 TB/s; 64 sequences,
-// 24 rows, 627 MB: 178 us, 3.5 TB/s, half of the copy rate. What bounds it: 3800 (24 rows) warp instructions a tile where
+// 24 rows, 627 MB: 180 us, 3.5 TB/s, half of the copy rate. What bounds it: 3800 (24 rows) warp instructions a tile where
 // HBM delivers one in 765 cycles, issued at 62% of the slots by four warps a scheduler; integer pipe 46%, shared memory
 // 51%, tensor pipe 16%, DRAM 39%.
 #pragma once
@@ -315,12 +315,6 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t sm = specv::smem_addr(smem);
 
-    // ---- the CTA's run of tiles: an equal share of the line on which each unit takes its tiles and ATT_UNIT more in front
-    long long mine = 0;
-    for (int b = tid; b < p.B; b += TH) mine += load_seq(p, b, blockIdx.x == 0).T + ATT_UNIT;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_scan[warp] = mine;
     if (warp == 0) tmem_alloc(&s_tmem, C::COLS);
     if (tid == 0) {
         for (int i = 0; i < C::STAGES; ++i) specv::mbar_init(&s_full[i], 1);
@@ -330,6 +324,13 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
         s_base[0] = H2_1024;
         s_base[1] = H2_64;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // after_previous, the next kernel let in at this one's end
+    // ---- the CTA's run of tiles: an equal share of the line on which each unit takes its tiles and ATT_UNIT more in front
+    long long mine = 0;
+    for (int b = tid; b < p.B; b += TH) mine += load_seq(p, b, blockIdx.x == 0).T + ATT_UNIT;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_scan[warp] = mine;
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
 template <int D>
 __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int E = D / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int4 u = p.desc[blockIdx.x];
     if (u.z == 0) return;
     const int lane = threadIdx.x & 31, n = blockIdx.y * 4 + (threadIdx.x >> 5);

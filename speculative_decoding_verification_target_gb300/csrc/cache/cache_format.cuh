@@ -14,6 +14,13 @@ constexpr int PAGE = SPEC_CACHE_PAGE;
 constexpr int GROUP = SPEC_CACHE_GROUP;
 constexpr int SCALE_TOP = 198;            // bits of the largest scale, 896: 72 x 896 is still a finite half
 
+// Every kernel here is launched so that its CTAs may take their places before the kernel in front of it has ended, and begins
+// with this: it waits for that end (so for all that came before, since that kernel waited likewise), and lets the next one's
+// CTAs in. Nothing in global memory is read or written before it.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Byte offsets of a block's four parts for head size D.
 template <int D>
 struct Block {

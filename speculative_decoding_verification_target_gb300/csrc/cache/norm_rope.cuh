@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_
     constexpr int U = 4;                         // heads per lane in flight
     constexpr int MATE = INTER ? 1 : 4;
     __shared__ float2 s_cs[NORM_WARPS][D / 2];
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long unit = static_cast<long long>(blockIdx.x) * NORM_WARPS + warp;
     const long long tok = unit / p.parts;

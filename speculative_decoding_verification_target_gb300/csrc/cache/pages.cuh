@@ -39,6 +39,7 @@ __device__ __forceinline__ void drop_entry(const PagesParams& p, int* e) {
 // One CTA per pair. A destination is never a source of the call (such pairs are left out), so no CTA reads a row
 // that another one writes.
 __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesParams p) {
+    after_previous();
     const int f = blockIdx.x, src = p.a[f], dst = p.b[f];
     bool bad = src < 0 || src >= p.S || dst < 0 || dst >= p.S;
     for (int i = threadIdx.x; i < p.n; i += blockDim.x) bad |= p.a[i] == dst || (i < f && p.b[i] == dst);
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
 
 // One CTA per sequence: its new length, then the entries past it and those before every later query's window.
 __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ PagesParams p) {
+    after_previous();
     const int s = blockIdx.x;
     __shared__ int s_len;
     if (threadIdx.x == 0) {
@@ -79,6 +81,7 @@ __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ Pag
 }
 
 __global__ void __launch_bounds__(128) release_kernel(const __grid_constant__ PagesParams p) {
+    after_previous();
     const int s = p.a[blockIdx.x];
     if (s < 0 || s >= p.S) {
         if (threadIdx.x == 0) atomicOr(p.status, SPEC_STATUS_BAD_SLOT);
@@ -172,7 +175,7 @@ __device__ __forceinline__ bool wants_page(const PagesParams& p, int e) {
 //   scratch: need [S], free list [P], former page [P], copies' source and destination [S] each, then the number of
 //   copies and of pages given (the copy kernel reads the first).
 __global__ void __launch_bounds__(PG_THREADS) reserve_kernel(const __grid_constant__ PagesParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // the copies' CTAs may take their places and wait
+    after_previous();
     __shared__ ClusterScan s_scan;
     __shared__ int s_given;
     const unsigned rank = specv::cluster_ctarank();
@@ -291,7 +294,7 @@ __device__ __forceinline__ void copy_pages(const PagesParams& p, const int* src,
 }
 
 __global__ void __launch_bounds__(COPY_THREADS) reserve_copy_kernel(const __grid_constant__ PagesParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int* const copy_src = p.scratch + p.S + 2 * static_cast<long long>(p.P);
     copy_pages(p, copy_src, copy_src + p.S, copy_src[2 * p.S]);
 }
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(COPY_THREADS) reserve_copy_kernel(const __grid
 // number < n) are as many, and the i-th of the one goes to the i-th of the other.
 //   scratch: movers [P], holes [P], new number of pages n .. P - 1 [P], number of moves, n.
 __global__ void __launch_bounds__(PG_THREADS) compact_plan_kernel(const __grid_constant__ PagesParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // the moves' CTAs may take their places and wait
+    after_previous();
     __shared__ ClusterScan s_scan;
     const unsigned rank = specv::cluster_ctarank();
     const int threads = specv::cluster_nctarank() * PG_THREADS;
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(PG_THREADS) compact_plan_kernel(const __grid_c
 // The copies and the table's new page numbers. Holes are free and movers are in use, so no copy reads a page that
 // another one writes.
 __global__ void __launch_bounds__(COPY_THREADS) compact_move_kernel(const __grid_constant__ PagesParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int* const movers = p.scratch;
     const int* const remap = movers + 2 * static_cast<long long>(p.P);
     const int moves = remap[p.P], n = remap[p.P + 1];

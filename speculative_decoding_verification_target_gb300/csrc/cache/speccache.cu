@@ -24,8 +24,7 @@ spec_status fail(spec_status s, const char* fmt, ...) {
     return s;
 }
 
-spec_status launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
+spec_status launched(const char* what, cudaError_t e) {
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
 }
 
@@ -90,15 +89,16 @@ int sm_count() {
         if (try_s != SPEC_OK) return try_s;    \
     } while (0)
 
-// A launch whose CTAs may take their places while the kernel before still runs; it waits for that kernel's end by itself.
+// A launch whose CTAs may take their places while the kernel before still runs; each waits for that kernel's end by itself.
 template <class P>
-cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st) {
+cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st, size_t smem = 0) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -178,10 +178,8 @@ spec_status attend_as(const AttnParams& p, cudaStream_t st) {
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
     const long long tiles = static_cast<long long>(p.B) * p.Hk * p.RB * ((p.max_pages + 1) / 2);     // at most
     const int ctas = static_cast<int>(std::min<long long>({static_cast<long long>(C::CTAS) * sms, ATT_MAX_CTAS / WG, tiles}));
-    attention_kernel<D, WG, NW><<<ctas, C::TH, C::SMEM, st>>>(p);
-    SPECC_TRY(launched("attention"));
-    const cudaError_t e = launch_behind(attention_join_kernel<D>, p, dim3(ctas, (p.rpb + 3) / 4), 128, st);
-    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "attention's join failed: %s", cudaGetErrorString(e));
+    SPECC_TRY(launched("attention", launch_behind(attention_kernel<D, WG, NW>, p, dim3(ctas), C::TH, st, C::SMEM)));
+    return launched("attention's join", launch_behind(attention_join_kernel<D>, p, dim3(ctas, (p.rpb + 3) / 4), 128, st));
 }
 
 template <int D>
@@ -233,15 +231,17 @@ PagesParams pages_params(int32_t* table, int32_t* lengths, int32_t* refs, int S,
 // The bookkeeping kernels run as one cluster: two CTAs up to 8192 pages, where barriers cost more than the walk over the
 // counts (reserving over 8192: 15.5 us with two or four CTAs, 17.6 with eight), else eight (over 65536: 59.5, 28.6 and 20.5 us).
 cudaError_t launch_cluster(void (*fn)(const PagesParams), const PagesParams& p, int ctas, cudaStream_t st) {
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(PG_THREADS);
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 int cluster_for(int pages) { return pages <= 8192 ? 2 : PG_CLUSTER; }
@@ -311,8 +311,7 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
          {norm_rope_kernel<__half, 128, false>, norm_rope_kernel<__half, 128, true>},
          {norm_rope_kernel<__half, 256, false>, norm_rope_kernel<__half, 256, true>}}};
     const Fn fn = fns[dtype][D == 64 ? 0 : D == 128 ? 1 : 2][interleaved ? 1 : 0];
-    fn<<<static_cast<unsigned>(ctas), NORM_WARPS * 32, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched("norm and rotation");
+    return launched("norm and rotation", launch_behind(fn, p, dim3(static_cast<unsigned>(ctas)), NORM_WARPS * 32, static_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_cache_append(void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start,
@@ -324,15 +323,9 @@ spec_status spec_cache_append(void* pool, int pages, const int32_t* table, int m
     SPECC_TRY(check_heads(v, "v", dtype, B, N, Hk));
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, k, v, B, N, Hk, workspace);
     const dim3 grid(2 * Hk, (N + PAGE - 2) / PAGE + 1, B);   // a run of N tokens touches at most that many pages
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == SPEC_BF16) {
-        if (D == 64) append_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
-        else append_kernel<__nv_bfloat16, 128><<<grid, TOK_THREADS, 0, st>>>(p);
-    } else {
-        if (D == 64) append_kernel<__half, 64><<<grid, TOK_THREADS, 0, st>>>(p);
-        else append_kernel<__half, 128><<<grid, TOK_THREADS, 0, st>>>(p);
-    }
-    return launched("append");
+    void (*const fn)(const TokensParams) = dtype == SPEC_BF16 ? (D == 64 ? append_kernel<__nv_bfloat16, 64> : append_kernel<__nv_bfloat16, 128>)
+                                                             : (D == 64 ? append_kernel<__half, 64> : append_kernel<__half, 128>);
+    return launched("append", launch_behind(fn, p, grid, TOK_THREADS, static_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start,
@@ -347,15 +340,9 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, has_k ? k_out : nullptr,
                                          has_v ? v_out : nullptr, B, N, Hk, workspace);
     const dim3 grid(2 * Hk, (N + PAGE - 2) / PAGE + 1, B);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == SPEC_BF16) {
-        if (D == 64) read_kernel<__nv_bfloat16, 64><<<grid, TOK_THREADS, 0, st>>>(p);
-        else read_kernel<__nv_bfloat16, 128><<<grid, TOK_THREADS, 0, st>>>(p);
-    } else {
-        if (D == 64) read_kernel<__half, 64><<<grid, TOK_THREADS, 0, st>>>(p);
-        else read_kernel<__half, 128><<<grid, TOK_THREADS, 0, st>>>(p);
-    }
-    return launched("read");
+    void (*const fn)(const TokensParams) = dtype == SPEC_BF16 ? (D == 64 ? read_kernel<__nv_bfloat16, 64> : read_kernel<__nv_bfloat16, 128>)
+                                                             : (D == 64 ? read_kernel<__half, 64> : read_kernel<__half, 128>);
+    return launched("read", launch_behind(fn, p, grid, TOK_THREADS, static_cast<cudaStream_t>(stream)));
 }
 
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
@@ -428,8 +415,7 @@ spec_status spec_pages_fork(int32_t* table, int32_t* lengths, int32_t* refs, int
     p.a = src;
     p.b = dst;
     p.n = F;
-    fork_kernel<<<F, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched("fork");
+    return launched("fork", launch_behind(fork_kernel, p, dim3(F), 256, static_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_pages_reserve(void* pool, int layers, long long page_bytes, int32_t* table, const int32_t* lengths,
@@ -448,10 +434,8 @@ spec_status spec_pages_reserve(void* pool, int layers, long long page_bytes, int
     p.a = n_new;
     p.out = served;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_cluster(reserve_kernel, p, cluster_for(pages), st);
-    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "reserve failed: %s", cudaGetErrorString(e));
-    e = launch_behind(reserve_copy_kernel, p, dim3(2 * sms), COPY_THREADS, st);
-    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "reserve's copies failed: %s", cudaGetErrorString(e));
+    SPECC_TRY(launched("reserve", launch_cluster(reserve_kernel, p, cluster_for(pages), st)));
+    return launched("reserve's copies", launch_behind(reserve_copy_kernel, p, dim3(2 * sms), COPY_THREADS, st));
 }
 
 spec_status spec_pages_commit(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
@@ -466,8 +450,7 @@ spec_status spec_pages_commit(int32_t* table, int32_t* lengths, int32_t* refs, i
     p.extra = extra;
     p.window = window;
     p.sinks = sinks;
-    commit_kernel<<<S, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched("commit");
+    return launched("commit", launch_behind(commit_kernel, p, dim3(S), 128, static_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, int S, int max_pages, int pages,
@@ -479,8 +462,7 @@ spec_status spec_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, 
     PagesParams p = pages_params(table, lengths, refs, S, max_pages, pages, workspace);
     p.a = slots;
     p.n = F;
-    release_kernel<<<F, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched("release");
+    return launched("release", launch_behind(release_kernel, p, dim3(F), 128, static_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int32_t* table, int32_t* refs, int S,
@@ -497,10 +479,8 @@ spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int
     p.page_bytes = page_bytes;
     p.out = used;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_cluster(compact_plan_kernel, p, cluster_for(pages), st);
-    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "compact's plan failed: %s", cudaGetErrorString(e));
-    e = launch_behind(compact_move_kernel, p, dim3(16 * sms), COPY_THREADS, st);
-    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "compact's moves failed: %s", cudaGetErrorString(e));
+    SPECC_TRY(launched("compact's plan", launch_cluster(compact_plan_kernel, p, cluster_for(pages), st)));
+    return launched("compact's moves", launch_behind(compact_move_kernel, p, dim3(16 * sms), COPY_THREADS, st));
 }
 
 }  // extern "C"
