@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     __shared__ __align__(16) float s_c[NC], s_nm[NC];    // c_n, -m_n
     __shared__ __align__(16) float s_fac[NC];
     __shared__ float s_red[4][NC], s_inv[NC];
-    __shared__ long long s_off[NC];                      // output row offset, -1: no such row
+    __shared__ long long s_off[NC];                      // output row offset
     __shared__ int s_live[NC];                            // 1: a row, 0: a row past q_len or none
     __shared__ long long s_scan[TH / 32 + 1];
     __shared__ Place s_place[2];
@@ -507,43 +507,42 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
             const int pos0 = f.pos0, pos1 = f.pos1, flags = f.flags;
             if (flags & TILE_FIRST) {
                 // ---- a new unit: its queries as halves, each row scaled by a power of two into a half's range
-                constexpr int E = D / 32, NR = NQ / (CT / 32);         // lane: channels E lane ..; the warp's rows
-                uint32_t raw[NR][E / 2];
+                // (rarely run, so short: its instructions are not in the cache.) A thread takes eight channels of a row.
+                constexpr int CH = D / 8, PER = (NQ * CH + CT - 1) / CT;
+                uint4 raw[PER];
 #pragma unroll
-                for (int m = 0; m < NR; ++m) {
-                    const int n = warp + m * (CT / 32), r = f.r0 + n, i = r / p.G, hq = f.h * p.G + (r - i * p.G);
+                for (int u = 0; u < PER; ++u) {
+                    const int n = (u * CT + tid) / CH, r = f.r0 + n, i = r / p.G, hq = f.h * p.G + (r - i * p.G);
                     const bool row = n < f.rows, live = row && i < f.ql;
-                    const uint32_t* const q = reinterpret_cast<const uint32_t*>(
-                        static_cast<const unsigned char*>(p.q.p) + 2 * (f.b * p.q.sb + i * p.q.sn + hq * p.q.sh + E * lane));
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e) raw[m][e] = live ? q[e] : 0u;
-                    if (lane == 0) {
-                        s_off[n] = row ? i * p.out.sn + hq * p.out.sh : -1;
+                    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live)
+                        raw[u] = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.q.p) +
+                                                                 2 * (f.b * p.q.sb + i * p.q.sn + hq * p.q.sh + 8 * (tid % CH)));
+                    if (tid % CH == 0 && n < NQ) {
+                        s_off[n] = i * p.out.sn + hq * p.out.sh;
                         s_live[n] = live;
                         s_nm[n] = -ATT_NONE;
                     }
                 }
 #pragma unroll
-                for (int m = 0; m < NR; ++m) {
-                    const int n = warp + m * (CT / 32);
-                    float x[E], top = 0.f;
+                for (int u = 0; u < PER; ++u) {
+                    const int n = (u * CT + tid) / CH;
+                    const float2 v[4] = {two_of(raw[u].x, p.fp16), two_of(raw[u].y, p.fp16), two_of(raw[u].z, p.fp16), two_of(raw[u].w, p.fp16)};
+                    float top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float2 v = two_of(raw[m][e / 2], p.fp16);
-                        x[e] = v.x, x[e + 1] = v.y;
-                        top = max3(top, fabsf(v.x), fabsf(v.y));
-                    }
-                    top = specv::warp_max(top);
+                    for (int q = 0; q < 4; ++q) top = max3(top, fabsf(v[q].x), fabsf(v[q].y));
+#pragma unroll
+                    for (int o = CH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     // 2^ex brings the largest magnitude to 2^10 .. 2^11 (and an infinite one nowhere)
                     const int ex = top > 0.f && top <= 3.4e38f ? 137 - max(static_cast<int>(__float_as_uint(top) >> 23), 20) : 0;
                     const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int d = E * lane + e, w8 = d & 7, to = (w8 & 3) * 2 + (w8 >> 2);     // 0 4 1 5 2 6 3 7
-                        *reinterpret_cast<__half*>(smem + C::Q + (d >> 3) * C::KQ + (n >> 3) * 128 + (n & 7) * 16 + to * 2) =
-                            __float2half_rn(x[e] * up);
+                    // channels in the order 0 4 1 5 2 6 3 7
+                    const __half2 h[4] = {__floats2half2_rn(v[0].x * up, v[2].x * up), __floats2half2_rn(v[0].y * up, v[2].y * up),
+                                          __floats2half2_rn(v[1].x * up, v[3].x * up), __floats2half2_rn(v[1].y * up, v[3].y * up)};
+                    if (n < NQ) {
+                        *reinterpret_cast<uint4*>(smem + C::Q + (tid % CH) * C::KQ + (n >> 3) * 128 + (n & 7) * 16) = *reinterpret_cast<const uint4*>(h);
+                        if (tid % CH == 0) s_c[n] = s_live[n] ? p.scale * ATT_LARGER * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
                     }
-                    if (lane == 0) s_c[n] = s_live[n] ? p.scale * ATT_LARGER * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : 0.f;
                 }
                 specv::fence_proxy_async_shared();
                 bar_sync(BAR_COMPUTE, CT);
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
 #pragma unroll
                     for (int n = 0; n < NW / 2; ++n) l[n] = mul2(l[n], *reinterpret_cast<const unsigned long long*>(&s_fac[wg * NW + 2 * n]));
                     if (!(flags & TILE_FIRST)) {
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < NW; i += 8) {
                             uint32_t o[8];
                             tmem_ld(col_o + i, o);
@@ -734,7 +733,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 }
                 fold_columns(lf, lane, &s_red[wq][wg * NW], [](float a, float b) { return a + b; });
                 if (D == 64 && wq >= 2) {      // the second page's share of O, to the lanes that write
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < NW; i += 8) {
                         uint32_t o[8];
                         tmem_ld(col_o + i, o);
@@ -761,7 +760,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 if (D == 128 || wq < 2) {
                     unsigned short* const out = static_cast<unsigned short*>(p.out.p) + f.b * p.out.sb + tok;
                     float* const part = p.part_o + (static_cast<size_t>(f.slot) * p.width + wg * NW) * D + tok;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < NW; i += 8) {
                         uint32_t o[8];
                         tmem_ld(col_o + i, o);
