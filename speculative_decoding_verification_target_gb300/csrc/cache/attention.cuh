@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
     __shared__ __align__(16) float s_fac[NC];
     __shared__ float s_red[4][NC], s_inv[NC];
     __shared__ long long s_off[NC];                      // output row offset
-    __shared__ int s_live[NC];                            // 1: a row, 0: a row past q_len or none
+    __shared__ int s_live[NC];                           // whether it is a query, not a row past q_len or none
     __shared__ long long s_scan[TH / 32 + 1];
     __shared__ Place s_place[2];
 
