@@ -168,13 +168,14 @@ def rope_frequencies(rotary_dim, theta=10000.0, *, inv_freq=None, device=None):
     """The rotation's frequencies for qk_norm_rope: each pair's turns a position in 2^-64 of a turn, int64 (the bits of
     a uint64) [rotary_dim / 2], from theta ** (-2 i / rotary_dim), or from inv_freq (radians a position)."""
     if inv_freq is None:
-        inv = [theta ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+        inv = theta ** (torch.arange(0, rotary_dim, 2, dtype=torch.float64) / -rotary_dim)
     else:
-        inv = [float(x) for x in inv_freq]
-        if len(inv) != rotary_dim // 2:
-            raise ValueError("inv_freq must have rotary_dim / 2 = %d values, got %d" % (rotary_dim // 2, len(inv)))
-    bits = [int(math.ldexp(math.fmod(x / (2.0 * math.pi), 1.0), 64)) % (1 << 64) for x in inv]
-    return torch.tensor([b - (1 << 64) if b >> 63 else b for b in bits], dtype=torch.int64, device=device or "cuda")
+        inv = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu")
+        if inv.numel() != rotary_dim // 2:
+            raise ValueError("inv_freq must have rotary_dim / 2 = %d values, got %d" % (rotary_dim // 2, inv.numel()))
+    high = torch.remainder(inv / (2.0 * math.pi), 1.0) * 2.0 ** 32
+    low = (high - high.floor()) * 2.0 ** 32      # exact: a double's 53 bits, in two steps
+    return (high.floor().long() << 32 | low.floor().long()).to(device or "cuda")
 
 
 def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
