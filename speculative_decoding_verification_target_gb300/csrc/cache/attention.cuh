@@ -71,7 +71,9 @@ struct Att {
     static constexpr int CT = 128 * WG, TH = CT + 32;     // computing threads; one more warp fetches and issues products
     static constexpr int NQ = WG * NW, NC = (NQ + 15) / 16 * 16;     // queries, and the products' width for them
     static constexpr int TILE = 2 * Block<D>::BYTES;
-    static constexpr int STAGES = D == 64 ? 4 : CTAS == 4 ? 2 : 3, INFOS = 2 * STAGES;      // what shared memory has room for
+    // tiles on their way; more gains nothing (72 rows, heads of 128: 389 us with two, 397 with three; heads of 64, 24 rows: 57.0,
+    // 56.5 and 57.2 us with two, three and four)
+    static constexpr int STAGES = D == 64 || CTAS == 3 ? 3 : 2, INFOS = 2 * STAGES;
     // the second product: D = 128, 128 channels by 128 tokens; D = 64, both pages' channels as 128 rows by 64 tokens, each
     // page's probabilities in columns of their own (half of the result is of no use, but all warps have values to convert)
     static constexpr int ON = D == 128 ? NC : 2 * NC, OK = D == 128 ? 128 : 64;
