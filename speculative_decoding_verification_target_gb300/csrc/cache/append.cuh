@@ -35,15 +35,14 @@ __device__ __forceinline__ bool span_of(const TokensParams& p, int b, int y, boo
     }
     if (cnt == 0) return false;
     // positions below 0 or past the table hold no page
-    const long long end = static_cast<long long>(start) + cnt, room = static_cast<long long>(p.max_pages) * PAGE;
-    const long long lo = max(start, 0);
-    const long long hi = min(end, room);
-    if ((start < 0 || end > room) && report) atomicOr(p.status, SPEC_STATUS_BAD_LENGTH);
-    const long long j = lo / PAGE + y;
-    if (j * PAGE >= hi) return false;
-    s.t0 = static_cast<int>(max(lo - j * PAGE, 0LL));
-    s.t1 = static_cast<int>(min(hi - j * PAGE, static_cast<long long>(PAGE)));
-    s.i0 = static_cast<int>(j * PAGE + s.t0 - start);
+    const int room = p.max_pages * PAGE;      // below 2^31
+    const int lo = max(start, 0), hi = start > room - cnt ? room : start + cnt;
+    if ((start < 0 || start > room - cnt) && report) atomicOr(p.status, SPEC_STATUS_BAD_LENGTH);
+    const int j = lo / PAGE + y;
+    if (j > (hi - 1) / PAGE || hi <= lo) return false;
+    s.t0 = max(lo - j * PAGE, 0);
+    s.t1 = min(hi - j * PAGE, PAGE);
+    s.i0 = j * PAGE + s.t0 - start;
     s.page = p.table[static_cast<size_t>(b) * p.max_pages + j];
     if (s.page < 0 || s.page >= p.pages) {
         if (report) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);

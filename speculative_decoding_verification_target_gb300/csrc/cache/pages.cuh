@@ -93,8 +93,7 @@ __global__ void __launch_bounds__(128) release_kernel(const __grid_constant__ Pa
     if (threadIdx.x == 0) p.lengths[s] = 0;
 }
 
-// Exclusive sum over the cluster's threads, in order of (CTA, thread), of up to two counts at once (packed by
-// the caller into 64 bits, 32 each), and their total. Every thread of the cluster calls it.
+// Exclusive sum over the cluster's threads, in order of (CTA, thread), and their total. Every thread of the cluster calls it.
 struct ClusterScan {
     unsigned long long warp[32];
     unsigned long long cta;      // this CTA's total, read by the others
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(PG_THREADS) reserve_kernel(const __grid_consta
     // the free pages of each thread's run
     const Run r = run_of(p.P, rank);
     int mine = 0;
+#pragma unroll 4
     for (int i = r.lo; i < r.hi; ++i) mine += p.refs[i] <= 0;
     unsigned long long all_free;
     const unsigned long long first_free = cluster_scan(&s_scan, static_cast<unsigned long long>(mine), rank, &all_free);
@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(COPY_THREADS) reserve_copy_kernel(const __grid
     copy_pages(p, copy_src, copy_src + p.S, copy_src[2 * p.S]);
 }
 
-// The moves of a compaction, by one cluster. With n pages in use, movers (used, number >= n) and holes (free,
-// number < n) are as many, and the i-th of the one goes to the i-th of the other.
-//   scratch: movers [P], holes [P], new number of pages n .. P - 1 [P], number of moves, n.
+// The moves of a compaction, by one cluster. With n pages in use, movers (used, number >= n) and holes (free, number < n) are
+// as many, and the i-th of the one goes to the i-th of the other. One sum serves both: with u used pages before it, a hole i is
+// the (i - u)-th, and a mover stands at u of the used pages, of which the movers are the last.
+//   scratch: used pages from n on, by rank [P], holes [P], new number of pages n .. P - 1 [P], number of moves, n.
 __global__ void __launch_bounds__(PG_THREADS) compact_plan_kernel(const __grid_constant__ PagesParams p) {
     after_previous();
     __shared__ ClusterScan s_scan;
@@ -312,36 +313,35 @@ __global__ void __launch_bounds__(PG_THREADS) compact_plan_kernel(const __grid_c
     int* const remap = holes + p.P;
     int* const counts = remap + p.P;
     const Run r = run_of(p.P, rank);
-    unsigned long long used = 0, n64, both;
+    unsigned long long used = 0, n64;
+#pragma unroll 4
     for (int i = r.lo; i < r.hi; ++i) used += p.refs[i] > 0;
-    cluster_scan(&s_scan, used, rank, &n64);
+    int u = static_cast<int>(cluster_scan(&s_scan, used, rank, &n64));
     const int n = static_cast<int>(n64);
-    unsigned long long mine = 0;
+#pragma unroll 4
     for (int i = r.lo; i < r.hi; ++i) {
-        const bool u = p.refs[i] > 0;
-        if (u && i >= n) mine += 1ull << 32;
-        if (!u && i < n) mine += 1ull;
+        if (i == n) counts[0] = n - u;
+        if (p.refs[i] > 0) {
+            if (i >= n) movers[u] = i;
+            ++u;
+        } else if (i < n) {
+            holes[i - u] = i;
+        } else {
+            remap[i - n] = i;
+        }
     }
-    const unsigned long long at = cluster_scan(&s_scan, mine, rank, &both);
-    int m = static_cast<int>(at >> 32), h = static_cast<int>(at & 0xffffffffull);
-    for (int i = r.lo; i < r.hi; ++i) {
-        const bool u = p.refs[i] > 0;
-        if (u && i >= n) movers[m++] = i;
-        if (!u && i < n) holes[h++] = i;
-        if (!u && i >= n) remap[i - n] = i;
+    if (rank == 0 && threadIdx.x == 0) {
+        if (n == p.P) counts[0] = 0;
+        counts[1] = n;
+        if (p.out) p.out[0] = n;
     }
     specv::cluster_sync_all();
-    const int moves = static_cast<int>(both >> 32);
+    const int moves = *static_cast<volatile int*>(&counts[0]);
     for (int k = static_cast<int>(rank) * PG_THREADS + threadIdx.x; k < moves; k += threads) {
-        const int from = movers[k], to = holes[k];
+        const int from = movers[n - moves + k], to = holes[k];
         remap[from - n] = to;
         p.refs[to] = p.refs[from];
         p.refs[from] = 0;
-    }
-    if (rank == 0 && threadIdx.x == 0) {
-        counts[0] = moves;
-        counts[1] = n;
-        if (p.out) p.out[0] = n;
     }
 }
 
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(COPY_THREADS) compact_move_kernel(const __grid
         if (e >= n && e < p.P) p.table[i] = remap[e - n];
         if (e >= p.P) atomicOr(p.status, SPEC_STATUS_BAD_PAGE);
     }
-    copy_pages(p, movers, movers + p.P, moves);
+    copy_pages(p, movers + (n - moves), movers + p.P, moves);
 }
 
 }  // namespace specc
