@@ -31,10 +31,10 @@
 // ATT_UNIT places more for each unit's beginning and end, of which each CTA takes an equal run (places of 0, 1, 2, 3 and 4
 // tiles: 75, 64, 65, 66 and 67 us on 48 sequences of 130 to 8191 tokens, 74, 66, 63, 62 and 63 us on 96 windows). A unit that is
 // cut leaves partial (O, m, l) in the workspace, and a second kernel joins them in a fixed order.
-// Measured, 8 key heads of 128: 48 sequences, one query row of four heads each, 219 MB of cache: 62 us, 3.5 TB/s; 64 sequences,
-// 24 rows, 627 MB: 180 us, 3.5 TB/s, half of the copy rate. What bounds it: 3800 (24 rows) warp instructions a tile where
-// HBM delivers one in 765 cycles, issued at 62% of the slots by four warps a scheduler; integer pipe 46%, shared memory
-// 51%, tensor pipe 16%, DRAM 39%.
+// Measured, 8 key heads of 128: 48 sequences, one query row of four heads each, 219 MB of cache: 61 us, 3.6 TB/s; 64 sequences,
+// 24 rows, 627 MB: 180 us, 3.5 TB/s, half of the copy rate. What bounds it: 3900 (24 rows) warp instructions a tile where
+// HBM delivers one in 765 cycles, issued at 64% of the slots by four warps a scheduler; integer pipe 49%, shared memory
+// 48%, tensor pipe 16%, DRAM 39%.
 #pragma once
 #include "cache_format.cuh"
 #include "tmem.cuh"
