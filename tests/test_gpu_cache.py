@@ -75,6 +75,15 @@ def test_norm_rope_in_place_and_on_another_stream():
     assert torch.equal(qkv[:, :, :8], ref["q"]) and torch.equal(qkv[:, :, 8:10], ref["k"]) and torch.equal(qkv[:, :, 10:], v)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(5, 0), (0, 3), (8, 0), (1, 0)])
+def test_norm_rope_of_queries_or_keys_alone(Hq, Hk):
+    x = torch.randn((3, 4, 8, 128), generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    pos, freqs = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4), sv.rope_frequencies(128)
+    both = sv.qk_norm_rope(x, x, pos, freqs)
+    r = sv.qk_norm_rope(x[:, :, :Hq], x[:, :, :Hk], pos, freqs)
+    assert torch.equal(r["q"], both["q"][:, :, :Hq]) and torch.equal(r["k"], both["k"][:, :, :Hk])
+
+
 def test_norm_of_zeros_and_nan_rows_stay_their_own():
     q = torch.randn((1, 2, 4, 64)).half().cuda()
     q[0, 0, 1] = 0
