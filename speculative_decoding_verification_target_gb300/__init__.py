@@ -137,6 +137,19 @@ def _need(t, name, dtype=None, shape=None):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+def _new(make, stream, *args, **kw):
+    """make(*args, **kw): a tensor that a call on `stream` makes for itself. It is made on that stream, so that it is
+    cleared before the call's kernels and its memory is nobody else's by then; it is the current stream's to read too."""
+    if stream is None:
+        return make(*args, **kw)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 def workspace_size(B, K, V, N=1) -> int:
     return int(load().spec_workspace_size(B, K, V, N))
 

@@ -13,6 +13,9 @@ refs int32 [pages]; the header states the format and every rule. One round of a 
     pages_commit(table, lengths, refs, accept_len)             keeps the accepted tokens, frees the rest
 
 and beside it pages_fork (a sequence that shares another's pages), pages_release, pages_compact and cache_read.
+
+A call runs on `stream`, or on the current one. Outputs and workspaces that are not given are made on that stream; what is given
+has to be ready on it. The status word is in the workspace (read_status): a caller that looks at it passes the workspace.
 """
 from __future__ import annotations
 
@@ -22,7 +25,7 @@ import math
 
 import torch
 
-from . import SPEC_OK, SpecError, _need, load as _load
+from . import SPEC_OK, SpecError, _need, _new, load as _load
 
 PAGE, GROUP = 64, 32
 WS_HEADER = 8192
@@ -199,12 +202,12 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     if k_weight is not None:
         _vector(k_weight, "k_weight", dt, (D,))
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _new(torch.empty_like, stream, q)
         qo = _own(q_out)
     else:
         qo = _heads(q_out, "q_out", (B, N, Hq, D), dt)
     if k_out is None:
-        k_out = torch.empty_like(k)
+        k_out = _new(torch.empty_like, stream, k)
         ko = _own(k_out)
     else:
         ko = _heads(k_out, "k_out", (B, N, Hk, D), dt)
@@ -224,7 +227,7 @@ def cache_append(pool, table, start, k, v, *, counts=None, workspace=None, strea
     if counts is not None:
         _ints(counts, "counts", (B,))
     if workspace is None:
-        workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
+        workspace = _new(torch.zeros, stream, WS_HEADER, dtype=torch.uint8, device=pool.device)
     _ok(_lib().spec_cache_append(_ptr(pool), P, _ptr(table), M, _ptr(start), _ptr(counts), _heads(k, "k", (B, N, H, D), k.dtype),
                                  _heads(v, "v", (B, N, H, D), k.dtype), code, B, N, H, D, _ptr(workspace), workspace.numel(),
                                  _on(pool, stream)))
@@ -240,18 +243,18 @@ def cache_read(pool, table, start, n, *, counts=None, dtype=torch.bfloat16, k=No
     if counts is not None:
         _ints(counts, "counts", (B,))
     if k is None:
-        k = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+        k = _new(torch.empty, stream, (B, n, H, D), dtype=dtype, device=pool.device)
         ki = _own(k)
     else:
         ki = _heads(k, "k", (B, n, H, D), dtype)
     if v is None:
-        v = torch.empty((B, n, H, D), dtype=dtype, device=pool.device)
+        v = _new(torch.empty, stream, (B, n, H, D), dtype=dtype, device=pool.device)
         vi = _own(v)
     else:
         vi = _heads(v, "v", (B, n, H, D), dtype)
     code = _code(k, "k")
     if workspace is None:
-        workspace = torch.zeros(WS_HEADER, dtype=torch.uint8, device=pool.device)
+        workspace = _new(torch.zeros, stream, WS_HEADER, dtype=torch.uint8, device=pool.device)
     _ok(_lib().spec_cache_read(pool.data_ptr(), P, table.data_ptr(), M, start.data_ptr(), _ptr(counts), ki, vi, code, B, n, H, D,
                                workspace.data_ptr(), workspace.numel(), _on(pool, stream)))
     return dict(k=k, v=v, workspace=workspace)
@@ -272,16 +275,16 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
         _ints(q_len, "q_len", (B,))
     qi = _heads(q, "q", (B, N, Hq, D), q.dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(torch.empty_like, stream, q)
         oi = _own(out)
     else:
         oi = _heads(out, "out", (B, N, Hq, D), q.dtype)
     if lse is not None:
         _vector(lse, "lse", torch.float32, (B, N, Hq))
     elif want_lse:
-        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+        lse = _new(torch.empty, stream, (B, N, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = new_attention_workspace(N, Hq, H, D, q.device)
+        workspace = _new(new_attention_workspace, stream, N, Hq, H, D, q.device)
     _ok(_lib().spec_cache_attention(qi, code, pool.data_ptr(), P, table.data_ptr(), M, kv_len.data_ptr(), _ptr(q_len), B, N,
                                     Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks, oi, _ptr(lse),
                                     workspace.data_ptr(), workspace.numel(), _on(q, stream)))
@@ -306,8 +309,8 @@ def _layers(pool, P):
     return (pool.shape[0] if pool.dim() == 4 else 1), pool.shape[-2] * pool.shape[-1]
 
 
-def _pages_ws(workspace, S, P, device):
-    return new_pages_workspace(S, P, device) if workspace is None else workspace
+def _pages_ws(workspace, S, P, device, stream):
+    return _new(new_pages_workspace, stream, S, P, device) if workspace is None else workspace
 
 
 def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
@@ -316,7 +319,7 @@ def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
     F = src.numel()
     _ints(src, "src", (F,))
     _ints(dst, "dst", (F,))
-    ws = _pages_ws(workspace, S, P, table.device)
+    ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_fork(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(src), _ptr(dst), F, _ptr(ws), ws.numel(),
                                _on(table, stream)))
     return ws
@@ -329,10 +332,10 @@ def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=N
     layers, page_bytes = _layers(pool, P)
     _ints(n_new, "n_new", (S,))
     if served is None:
-        served = torch.empty(S, dtype=torch.int32, device=table.device)
+        served = _new(torch.empty, stream, S, dtype=torch.int32, device=table.device)
     else:
         _ints(served, "served", (S,))
-    ws = _pages_ws(workspace, S, P, table.device)
+    ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_reserve(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(n_new),
                                   _ptr(served), _ptr(ws), ws.numel(), _on(pool, stream)))
     return served
@@ -343,7 +346,7 @@ def pages_commit(table, lengths, refs, advance, *, extra=1, window=0, sinks=0, w
     lengths, or with window > 0 out of every later query's view, are let go. Returns the workspace."""
     S, M, P = _books(table, lengths, refs)
     _ints(advance, "advance", (S,))
-    ws = _pages_ws(workspace, S, P, table.device)
+    ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_commit(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(advance), extra, window, sinks, _ptr(ws),
                                  ws.numel(), _on(table, stream)))
     return ws
@@ -354,7 +357,7 @@ def pages_release(table, lengths, refs, slots, *, workspace=None, stream=None):
     S, M, P = _books(table, lengths, refs)
     F = slots.numel()
     _ints(slots, "slots", (F,))
-    ws = _pages_ws(workspace, S, P, table.device)
+    ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_release(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(slots), F, _ptr(ws), ws.numel(),
                                   _on(table, stream)))
     return ws
@@ -366,10 +369,10 @@ def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
     S, M, P = _books(table, None, refs)
     layers, page_bytes = _layers(pool, P)
     if used is None:
-        used = torch.empty(1, dtype=torch.int32, device=table.device)
+        used = _new(torch.empty, stream, 1, dtype=torch.int32, device=table.device)
     else:
         _ints(used, "used", (1,))
-    ws = _pages_ws(workspace, S, P, table.device)
+    ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_compact(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(refs), S, M, P, _ptr(used), _ptr(ws), ws.numel(),
                                   _on(pool, stream)))
     return used

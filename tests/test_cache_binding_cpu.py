@@ -1,0 +1,86 @@
+"""CPU checks of what the cache's binding does around a launch, on stand-ins for CUDA tensors and streams (fake_cuda)."""
+import ctypes
+
+import pytest
+import torch
+
+import fake_cuda as fc
+import speculative_decoding_verification_target_gb300 as sv
+
+I32, BF16, U8 = torch.int32, torch.bfloat16, torch.uint8
+S, M, P, B, N, HQ, HK, D = 3, 4, 9, 3, 2, 8, 2, 64
+
+
+class Args:
+    """Arguments of every call, on one device."""
+
+    def __init__(self, index=0):
+        t = lambda shape, dtype=I32: fc.Tensor(shape, dtype, index)  # noqa: E731
+        self.q, self.k, self.v = t((B, N, HQ, D), BF16), t((B, N, HK, D), BF16), t((B, N, HK, D), BF16)
+        self.positions, self.freqs = t((B, N)), t((D // 2,), torch.int64)
+        self.pool, self.table, self.lengths, self.refs = t((P, HK, 68 * D), U8), t((S, M)), t((S,)), t((P,))
+        self.n, self.pairs, self.workspace = t((S,)), t((2,)), t((1 << 15,), U8)
+        self.q_weight, self.lse, self.served = t((D,), BF16), t((B, N, HQ), torch.float32), t((S,))
+
+
+CALLS = {
+    "qk_norm_rope": lambda a, **kw: sv.qk_norm_rope(a.q, a.k, a.positions, a.freqs, q_weight=a.q_weight, **kw),
+    "cache_append": lambda a, **kw: sv.cache_append(a.pool, a.table, a.lengths, a.k, a.v, counts=a.n, **kw),
+    "cache_read": lambda a, **kw: sv.cache_read(a.pool, a.table, a.lengths, 5, **kw),
+    "cache_attention": lambda a, **kw: sv.cache_attention(a.q, a.pool, a.table, a.lengths, q_len=a.n, want_lse=True, **kw),
+    "pages_fork": lambda a, **kw: sv.pages_fork(a.table, a.lengths, a.refs, a.pairs, a.pairs, **kw),
+    "pages_reserve": lambda a, **kw: sv.pages_reserve(a.pool, a.table, a.lengths, a.refs, a.n, **kw),
+    "pages_commit": lambda a, **kw: sv.pages_commit(a.table, a.lengths, a.refs, a.n, **kw),
+    "pages_release": lambda a, **kw: sv.pages_release(a.table, a.lengths, a.refs, a.pairs, **kw),
+    "pages_compact": lambda a, **kw: sv.pages_compact(a.pool, a.table, a.refs, **kw),
+}
+WITH_WORKSPACE = [n for n in CALLS if n != "qk_norm_rope"]
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    return fc.install(monkeypatch, sv)
+
+
+def launch_stream(lib):
+    """The stream of the last call: the C ABI's last argument."""
+    s = lib.calls[-1][1][-1]
+    return s.value if isinstance(s, ctypes.c_void_p) else s
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_what_a_call_makes_is_made_on_its_stream(fake, name):
+    """Outputs and the workspace are cleared and owned in the order of the stream that the kernel runs on; before the
+    allocator may give their memory away, it waits for the current stream too, where the caller may read them."""
+    t, lib = fake
+    here, s = t.cuda.now, fc.Stream("given")
+    CALLS[name](Args(), stream=s)
+    assert t.made and all(x.made_on is s for x in t.made)
+    assert all(x.used_on == [here] for x in t.made)
+    assert launch_stream(lib) == s.cuda_stream and t.cuda.now is here
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_without_a_stream_the_current_one_serves(fake, name):
+    t, lib = fake
+    CALLS[name](Args())
+    assert all(x.made_on is t.cuda.now and x.used_on == [] for x in t.made)
+    assert launch_stream(lib) == t.cuda.now.cuda_stream
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_current_stream_may_be_given(fake, name):
+    t, lib = fake
+    CALLS[name](Args(), stream=t.cuda.now)
+    assert all(x.made_on is t.cuda.now and x.used_on == [] for x in t.made)
+
+
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_a_workspace_made_for_a_call_is_clear_and_one_given_is_used(fake, name):
+    t, lib = fake
+    CALLS[name](Args())
+    made = [x for x in t.made if x.dtype is U8]
+    assert len(made) == 1 and made[0].clear
+    del t.made[:]
+    CALLS[name](Args(), workspace=fc.Tensor((1 << 16,), U8))
+    assert not [x for x in t.made if x.dtype is U8] and 1 << 16 in lib.calls[-1][1]
