@@ -8,6 +8,8 @@ when not given. There is no CPU path: if the library is missing, importing the c
     cactus_verify(target, draft, tokens, seeds, delta, temperature)  Cactus constrained acceptance
     counterfactual_gamma(target, drafters, temperature, selected, tokens, seeds)  HedgeSpec gamma
 
+A call runs on `stream`, or on the current one; what is not given is made on that stream, what is given has to be ready on it.
+
 The operators of the scoring step around a verification (head norms and rotation, a paged cache in 4 bits, attention
 over it, its pages) are in cache.py and exported here too.
 """
@@ -190,13 +192,13 @@ def last_plan() -> dict:
     return dict(stages=out[1], ctas=out[2], kernel=out[3], pieces=out[4])
 
 
-def _outputs(B, K, device, accept_len, out_tokens, diag, want_diag):
+def _outputs(B, K, device, accept_len, out_tokens, diag, want_diag, stream):
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=device)
+        accept_len = _new(torch.empty, stream, B, dtype=torch.int32, device=device)
     if out_tokens is None:
-        out_tokens = torch.empty((B, K + 1), dtype=torch.int32, device=device)
+        out_tokens = _new(torch.empty, stream, (B, K + 1), dtype=torch.int32, device=device)
     if diag is None and want_diag:
-        diag = torch.empty((B, K, 4), dtype=torch.float32, device=device)
+        diag = _new(torch.empty, stream, (B, K, 4), dtype=torch.float32, device=device)
     return accept_len, out_tokens, diag
 
 
@@ -210,8 +212,8 @@ def verify(target, draft, tokens, seeds, temperature=1.0, *, accept_len=None, ou
     _need(draft, "draft", target.dtype, (B, K, V))
     _need(tokens, "tokens", torch.int32, (B, K))
     _need(seeds, "seeds", None, (B,))
-    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag)
-    ws = workspace if workspace is not None else new_workspace(B, K, V, 1, target.device)
+    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
+    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
     _check(load().spec_verify(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V,
                               float(temperature), _p(accept_len), _p(out_tokens), _p(diag), _p(ws), ws.numel(),
                               _stream(stream)))
@@ -228,10 +230,10 @@ def cactus_verify(target, draft, tokens, seeds, delta, temperature=1.0, *, accep
     _need(draft, "draft", target.dtype, (B, K, V))
     _need(tokens, "tokens", torch.int32, (B, K))
     _need(seeds, "seeds", None, (B,))
-    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag)
+    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
     if gamma_star is None:
-        gamma_star = torch.empty((B, K), dtype=torch.float32, device=target.device)
-    ws = workspace if workspace is not None else new_workspace(B, K, V, 1, target.device)
+        gamma_star = _new(torch.empty, stream, (B, K), dtype=torch.float32, device=target.device)
+    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
     fn = load().spec_cactus_kl_verify if exact_kl else load().spec_cactus_verify
     _check(fn(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V, float(temperature),
               float(delta), _p(accept_len), _p(out_tokens), _p(diag), _p(gamma_star), _p(ws), ws.numel(),
@@ -246,8 +248,8 @@ def greedy_verify(target, tokens, *, accept_len=None, out_tokens=None, workspace
     K = K1 - 1
     _need(target, "target")
     _need(tokens, "tokens", torch.int32, (B, K))
-    accept_len, out_tokens, _ = _outputs(B, K, target.device, accept_len, out_tokens, None, False)
-    ws = workspace if workspace is not None else new_workspace(B, K, V, 1, target.device)
+    accept_len, out_tokens, _ = _outputs(B, K, target.device, accept_len, out_tokens, None, False, stream)
+    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
     _check(load().spec_greedy_verify(_p(target), _dtype_code(target), _p(tokens), B, K, V, _p(accept_len),
                                      _p(out_tokens), _p(ws), ws.numel(), _stream(stream)))
     return dict(accept_len=accept_len, out_tokens=out_tokens, workspace=ws)
@@ -258,9 +260,9 @@ def accept_length_estimate(gamma, *, est=None, loss=None, want_loss=True, stream
     N, B, K = gamma.shape
     _need(gamma, "gamma", torch.float32, (N, B, K))
     if est is None:
-        est = torch.empty((N, B), dtype=torch.float32, device=gamma.device)
+        est = _new(torch.empty, stream, (N, B), dtype=torch.float32, device=gamma.device)
     if loss is None and want_loss:
-        loss = torch.empty((N, B), dtype=torch.float32, device=gamma.device)
+        loss = _new(torch.empty, stream, (N, B), dtype=torch.float32, device=gamma.device)
     _check(load().spec_accept_length_estimate(_p(gamma), N, B, K, _p(est), _p(loss), _stream(stream)))
     return dict(est=est, loss=loss)
 
@@ -286,10 +288,12 @@ class HedgeFeedback:
         if n == 0 and B > 0:
             raise ValueError("unsupported sizes N=%d B=%d K=%d" % (N, B, K))
         dev = device or "cuda"
-        self.state = torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)
-        self.weights = torch.full((B, N), 1.0 / N, dtype=torch.float32, device=dev)
-        self.applied = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.state = _new(torch.zeros, stream, max(n, 16), dtype=torch.uint8, device=dev)
+        self.weights = _new(torch.full, stream, (B, N), 1.0 / N, dtype=torch.float32, device=dev)
+        self.applied = _new(torch.zeros, stream, B, dtype=torch.int32, device=dev)
         _check(lib.spec_hedge_feedback_init(_p(self.state), N, B, K, int(objective), _stream(stream)))
+        if stream is not None:      # the weights may be read on the current stream at once
+            torch.cuda.current_stream().wait_stream(stream)
 
     def push(self, gamma, accept_len, stream=None):
         _need(gamma, "gamma", torch.float32, (self.N, self.B, self.K))
@@ -314,11 +318,11 @@ def verify_filtered(target, draft, tokens, seeds, temperature=1.0, top_k=0, top_
     _need(draft, "draft", target.dtype, (B, K, V))
     _need(tokens, "tokens", torch.int32, (B, K))
     _need(seeds, "seeds", None, (B,))
-    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag)
+    accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
     lib = load()
     if workspace is None:
         n = lib.spec_filter_workspace_size(B, K, V, _dtype_code(target))
-        workspace = torch.zeros(n, dtype=torch.uint8, device=target.device)
+        workspace = _new(torch.zeros, stream, n, dtype=torch.uint8, device=target.device)
     _check(lib.spec_verify_filtered(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V,
                                     float(temperature), int(top_k), float(top_p), _p(accept_len), _p(out_tokens),
                                     _p(diag), _p(workspace), workspace.numel(), _stream(stream)))
@@ -337,16 +341,16 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
     _need(drafters, "drafters", target.dtype, (N, B, K, V))
     dev = target.device
     if gamma is None:
-        gamma = torch.empty((N, B, K), dtype=torch.float32, device=dev)
+        gamma = _new(torch.empty, stream, (N, B, K), dtype=torch.float32, device=dev)
     if loss is None and want_loss:
-        loss = torch.empty((N, B, K), dtype=torch.float32, device=dev)
+        loss = _new(torch.empty, stream, (N, B, K), dtype=torch.float32, device=dev)
     out = dict(gamma=gamma, loss=loss)
     if selected >= 0:
         _need(tokens, "tokens", torch.int32, (B, K))
         _need(seeds, "seeds", None, (B,))
-        accept_len, out_tokens, diag = _outputs(B, K, dev, accept_len, out_tokens, diag, want_diag)
+        accept_len, out_tokens, diag = _outputs(B, K, dev, accept_len, out_tokens, diag, want_diag, stream)
         out.update(accept_len=accept_len, out_tokens=out_tokens, diag=diag)
-    ws = workspace if workspace is not None else new_workspace(B, K, V, N, dev)
+    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, N, dev)
     _check(load().spec_counterfactual_gamma(_p(target), _p(drafters), _dtype_code(target), N, B, K, V,
                                             float(temperature), _p(gamma), _p(loss), int(selected), _p(tokens),
                                             _p(seeds), _p(out.get("accept_len")), _p(out.get("out_tokens")),

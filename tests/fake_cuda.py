@@ -16,7 +16,10 @@ class Device:
 
 class Stream:
     def __init__(self, name, index=0):
-        self.name, self.device, self.cuda_stream = name, Device(index), next(_address)
+        self.name, self.device, self.cuda_stream, self.waited_for = name, Device(index), next(_address), []
+
+    def wait_stream(self, stream):
+        self.waited_for.append(stream)
 
 
 class Tensor:

@@ -57,3 +57,21 @@ def test_calls_on_a_stream_beside_a_busy_one():
         got = calls(st)
         for name in want:
             assert torch.equal(got[name], want[name]), name
+
+
+def test_verification_on_a_stream_beside_a_busy_one():
+    g = torch.Generator().manual_seed(2)
+    target, draft = torch.randn((4, 4, 1000), generator=g).cuda(), torch.randn((4, 3, 1000), generator=g).cuda()
+    tokens, seeds = torch.randint(0, 1000, (4, 3), generator=g, dtype=torch.int32).cuda(), torch.arange(4, device="cuda")
+    want = [sv.verify(target, draft, tokens, seeds), sv.verify_filtered(target, draft, tokens, seeds, top_k=20),
+            sv.greedy_verify(target, tokens)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(200_000_000)
+    got = [sv.verify(target, draft, tokens, seeds, stream=st), sv.verify_filtered(target, draft, tokens, seeds, top_k=20, stream=st),
+           sv.greedy_verify(target, tokens, stream=st)]
+    st.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a["accept_len"], b["accept_len"])
+        for n, x, y in zip(a["accept_len"].tolist(), a["out_tokens"].tolist(), b["out_tokens"].tolist()):
+            assert x[:n + 1] == y[:n + 1]
