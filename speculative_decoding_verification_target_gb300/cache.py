@@ -14,7 +14,7 @@ refs int32 [pages]; the header states the format and every rule. One round of a 
 
 and beside it pages_fork (a sequence that shares another's pages), pages_release, pages_compact and cache_read.
 
-A call runs on `stream`, or on the current one. Outputs and workspaces that are not given are made on that stream; what is given
+Every tensor of a call is on the current device. A call runs on `stream`, or on the current one. Outputs and workspaces that are not given are made on that stream; what is given
 has to be ready on it. The status word is in the workspace (read_status): a caller that looks at it passes the workspace.
 """
 from __future__ import annotations
@@ -73,15 +73,34 @@ def _ok(code):
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 # The serving loop calls these once per layer and token, so the checks are written to cost little where they pass: one
 # condition, and the words for what is wrong only after it.
-def _on(t, stream):
-    """The stream's handle: the caller's, or the current one of t's device."""
+def _home(t, name, stream):
+    """The device of a call, t's: the current one, since the library launches there. Every other tensor has to be on it."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if d != _current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, d, _current_device()))
+    if stream is not None and stream.device.index != d:
+        raise ValueError("%s is on cuda:%d, the stream on cuda:%d" % (name, d, stream.device.index))
+    return d
+
+
+def _on(d, stream):
+    """The stream's handle: the caller's, or the current one of device d."""
     if stream is not None:
         return stream.cuda_stream
-    return _raw_stream(t.device.index) if _raw_stream is not None else torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(d) if _raw_stream is not None else torch.cuda.current_stream(d).cuda_stream
+
+
+def _wrong(t, name, dtype, shape, d):
+    """Says what keeps t from being a contiguous tensor of that type and shape (None: any) on device d."""
+    _need(t, name, dtype, shape)
+    raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, d, t.get_device()))
 
 
 def _ptr(t):
@@ -96,14 +115,16 @@ def _code(t, name, fp32=False):
     return code
 
 
-def _heads(t, name, shape, dtype):
+def _heads(t, name, shape, dtype, d):
     """[B, N, heads, D] with any strides but contiguous channels."""
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape):
+    if not (t.get_device() == d and t.dtype is dtype and t.shape == shape):
         if not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
         if t.dtype is not dtype:
             raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, d, t.get_device()))
     sb, sn, sh, sd = t.stride()
     if sd != 1:
         raise ValueError("%s must have contiguous channels" % name)
@@ -116,14 +137,14 @@ def _own(t):
     return Heads(t.data_ptr(), sb, sn, sh)
 
 
-def _vector(t, name, dtype, shape):
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        _need(t, name, dtype, shape)
+def _vector(t, name, dtype, shape, d):
+    if not (t.get_device() == d and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _wrong(t, name, dtype, shape, d)
 
 
-def _pool(pool, name="pool"):
-    if not (pool.is_cuda and pool.dtype is torch.uint8 and pool.is_contiguous()):
-        _need(pool, name, torch.uint8)
+def _pool(pool, d, name="pool"):
+    if not (pool.get_device() == d and pool.dtype is torch.uint8 and pool.is_contiguous()):
+        _wrong(pool, name, torch.uint8, None, d)
     if pool.dim() != 3:
         raise ValueError("%s must be [pages, Hk, 68 D], got %s" % (name, tuple(pool.shape)))
     P, H, n = pool.shape
@@ -132,17 +153,24 @@ def _pool(pool, name="pool"):
     return P, H, n // 68
 
 
-def _ints(t, name, shape):
-    if not (t.is_cuda and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
-        _need(t, name, torch.int32, shape)
+def _ints(t, name, shape, d):
+    if not (t.get_device() == d and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
+        _wrong(t, name, torch.int32, shape, d)
 
 
-def _table(table):
-    if not (table.is_cuda and table.dtype is torch.int32 and table.is_contiguous()):
-        _need(table, "table", torch.int32)
+def _table(table, d):
+    if not (table.get_device() == d and table.dtype is torch.int32 and table.is_contiguous()):
+        _wrong(table, "table", torch.int32, None, d)
     if table.dim() != 2:
         raise ValueError("table must be [sequences, max_pages], got %s" % (tuple(table.shape),))
     return table.shape
+
+
+def _workspace(ws, d):
+    """The caller's workspace as (address, bytes)."""
+    if not (ws.get_device() == d and ws.dtype is torch.uint8 and ws.is_contiguous()):
+        _wrong(ws, "workspace", torch.uint8, None, d)
+    return ws.data_ptr(), ws.numel()
 
 
 def new_pool(pages, kv_heads, head_dim, layers=None, device=None):
@@ -191,72 +219,75 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     Hk = k.shape[2]
     dt = q.dtype
     code = _code(q, "q", True)
-    qi, ki = _heads(q, "q", (B, N, Hq, D), dt), _heads(k, "k", (B, N, Hk, D), dt)
+    d = _home(q, "q", stream)
+    qi, ki = _heads(q, "q", (B, N, Hq, D), dt, d), _heads(k, "k", (B, N, Hk, D), dt, d)
     rotary, pos, fr = 0, None, None
     if freqs is not None:
-        _vector(freqs, "freqs", torch.int64, (freqs.numel(),))
-        _ints(positions, "positions", (B, N))
+        _vector(freqs, "freqs", torch.int64, (freqs.numel(),), d)
+        _ints(positions, "positions", (B, N), d)
         rotary, pos, fr = 2 * freqs.numel(), positions.data_ptr(), freqs.data_ptr()
     if q_weight is not None:
-        _vector(q_weight, "q_weight", dt, (D,))
+        _vector(q_weight, "q_weight", dt, (D,), d)
     if k_weight is not None:
-        _vector(k_weight, "k_weight", dt, (D,))
+        _vector(k_weight, "k_weight", dt, (D,), d)
     if q_out is None:
         q_out = _new(torch.empty_like, stream, q)
         qo = _own(q_out)
     else:
-        qo = _heads(q_out, "q_out", (B, N, Hq, D), dt)
+        qo = _heads(q_out, "q_out", (B, N, Hq, D), dt, d)
     if k_out is None:
         k_out = _new(torch.empty_like, stream, k)
         ko = _own(k_out)
     else:
-        ko = _heads(k_out, "k_out", (B, N, Hk, D), dt)
+        ko = _heads(k_out, "k_out", (B, N, Hk, D), dt, d)
     _ok(_lib().spec_qk_norm_rope(qi, ki, code, B, N, Hq, Hk, D, pos, fr, rotary, interleaved, _ptr(q_weight),
-                                 _ptr(k_weight), eps, qo, ko, _on(q, stream)))
+                                 _ptr(k_weight), eps, qo, ko, _on(d, stream)))
     return dict(q=q_out, k=k_out)
 
 
 def cache_append(pool, table, start, k, v, *, counts=None, workspace=None, stream=None):
     """Quantises k and v [B, N, Hk, D] (bf16 or fp16) into pool [pages, Hk, 68 D]: token i of sequence b to position
     start[b] + i, for i < counts[b] (None: N). Returns the workspace."""
-    P, H, D = _pool(pool)
-    B, M = _table(table)
+    d = _home(pool, "pool", stream)
+    P, H, D = _pool(pool, d)
+    B, M = _table(table, d)
     N = k.shape[1]
     code = _code(k, "k")
-    _ints(start, "start", (B,))
+    _ints(start, "start", (B,), d)
     if counts is not None:
-        _ints(counts, "counts", (B,))
+        _ints(counts, "counts", (B,), d)
     if workspace is None:
         workspace = _new(torch.zeros, stream, WS_HEADER, dtype=torch.uint8, device=pool.device)
-    _ok(_lib().spec_cache_append(_ptr(pool), P, _ptr(table), M, _ptr(start), _ptr(counts), _heads(k, "k", (B, N, H, D), k.dtype),
-                                 _heads(v, "v", (B, N, H, D), k.dtype), code, B, N, H, D, _ptr(workspace), workspace.numel(),
-                                 _on(pool, stream)))
+    _ok(_lib().spec_cache_append(pool.data_ptr(), P, table.data_ptr(), M, start.data_ptr(), _ptr(counts),
+                                 _heads(k, "k", (B, N, H, D), k.dtype, d), _heads(v, "v", (B, N, H, D), k.dtype, d), code, B, N,
+                                 H, D, *_workspace(workspace, d), _on(d, stream)))
     return workspace
 
 
 def cache_read(pool, table, start, n, *, counts=None, dtype=torch.bfloat16, k=None, v=None, workspace=None, stream=None):
     """The cached keys and values of positions start[b] .. start[b] + n - 1 as [B, n, Hk, D] in bf16 or fp16, exactly;
     zeros past counts[b] and where there is no page. Returns dict(k, v, workspace)."""
-    P, H, D = _pool(pool)
-    B, M = _table(table)
-    _ints(start, "start", (B,))
+    d = _home(pool, "pool", stream)
+    P, H, D = _pool(pool, d)
+    B, M = _table(table, d)
+    _ints(start, "start", (B,), d)
     if counts is not None:
-        _ints(counts, "counts", (B,))
+        _ints(counts, "counts", (B,), d)
     if k is None:
         k = _new(torch.empty, stream, (B, n, H, D), dtype=dtype, device=pool.device)
         ki = _own(k)
     else:
-        ki = _heads(k, "k", (B, n, H, D), dtype)
+        ki = _heads(k, "k", (B, n, H, D), dtype, d)
     if v is None:
         v = _new(torch.empty, stream, (B, n, H, D), dtype=dtype, device=pool.device)
         vi = _own(v)
     else:
-        vi = _heads(v, "v", (B, n, H, D), dtype)
+        vi = _heads(v, "v", (B, n, H, D), dtype, d)
     code = _code(k, "k")
     if workspace is None:
         workspace = _new(torch.zeros, stream, WS_HEADER, dtype=torch.uint8, device=pool.device)
     _ok(_lib().spec_cache_read(pool.data_ptr(), P, table.data_ptr(), M, start.data_ptr(), _ptr(counts), ki, vi, code, B, n, H, D,
-                               workspace.data_ptr(), workspace.numel(), _on(pool, stream)))
+                               *_workspace(workspace, d), _on(d, stream)))
     return dict(k=k, v=v, workspace=workspace)
 
 
@@ -266,44 +297,46 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     token, the new ones included; query i of sequence b stands at kv_len[b] - q_len[b] + i (q_len None: N). window > 0
     limits each query to the window last tokens and the first `sinks`. scale: 1 / sqrt(D) unless given. Returns
     dict(out, lse, workspace), lse [B, N, Hq] where wanted."""
-    P, H, D = _pool(pool)
-    B, M = _table(table)
+    d = _home(q, "q", stream)
+    P, H, D = _pool(pool, d)
+    B, M = _table(table, d)
     N, Hq = q.shape[1], q.shape[2]
     code = _code(q, "q")
-    _ints(kv_len, "kv_len", (B,))
+    _ints(kv_len, "kv_len", (B,), d)
     if q_len is not None:
-        _ints(q_len, "q_len", (B,))
-    qi = _heads(q, "q", (B, N, Hq, D), q.dtype)
+        _ints(q_len, "q_len", (B,), d)
+    qi = _heads(q, "q", (B, N, Hq, D), q.dtype, d)
     if out is None:
         out = _new(torch.empty_like, stream, q)
         oi = _own(out)
     else:
-        oi = _heads(out, "out", (B, N, Hq, D), q.dtype)
+        oi = _heads(out, "out", (B, N, Hq, D), q.dtype, d)
     if lse is not None:
-        _vector(lse, "lse", torch.float32, (B, N, Hq))
+        _vector(lse, "lse", torch.float32, (B, N, Hq), d)
     elif want_lse:
         lse = _new(torch.empty, stream, (B, N, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = _new(new_attention_workspace, stream, N, Hq, H, D, q.device)
     _ok(_lib().spec_cache_attention(qi, code, pool.data_ptr(), P, table.data_ptr(), M, kv_len.data_ptr(), _ptr(q_len), B, N,
                                     Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks, oi, _ptr(lse),
-                                    workspace.data_ptr(), workspace.numel(), _on(q, stream)))
+                                    *_workspace(workspace, d), _on(d, stream)))
     return dict(out=out, lse=lse, workspace=workspace)
 
 
-def _books(table, lengths, refs):
-    S, M = _table(table)
+def _books(table, lengths, refs, stream):
+    d = _home(table, "table", stream)
+    S, M = _table(table, d)
     if lengths is not None:
-        _ints(lengths, "lengths", (S,))
+        _ints(lengths, "lengths", (S,), d)
     P = refs.numel()
-    _ints(refs, "refs", (P,))
-    return S, M, P
+    _ints(refs, "refs", (P,), d)
+    return S, M, P, d
 
 
-def _layers(pool, P):
+def _layers(pool, P, d):
     """[pages, ...] or [layers, pages, ...] as (layers, bytes of a page)."""
-    if not (pool.is_cuda and pool.dtype is torch.uint8 and pool.is_contiguous()):
-        _need(pool, "pool", torch.uint8)
+    if not (pool.get_device() == d and pool.dtype is torch.uint8 and pool.is_contiguous()):
+        _wrong(pool, "pool", torch.uint8, None, d)
     if pool.dim() not in (3, 4) or pool.shape[-3] != P:
         raise ValueError("pool must be [%d, Hk, 68 D] or [layers, %d, Hk, 68 D], got %s" % (P, P, tuple(pool.shape)))
     return (pool.shape[0] if pool.dim() == 4 else 1), pool.shape[-2] * pool.shape[-1]
@@ -315,64 +348,64 @@ def _pages_ws(workspace, S, P, device, stream):
 
 def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
     """Sequence dst[f] becomes a copy of src[f] that shares its pages (int32 [F] each). Returns the workspace."""
-    S, M, P = _books(table, lengths, refs)
+    S, M, P, d = _books(table, lengths, refs, stream)
     F = src.numel()
-    _ints(src, "src", (F,))
-    _ints(dst, "dst", (F,))
+    _ints(src, "src", (F,), d)
+    _ints(dst, "dst", (F,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_fork(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(src), _ptr(dst), F, _ptr(ws), ws.numel(),
-                               _on(table, stream)))
+    _ok(_lib().spec_pages_fork(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(src), _ptr(dst), F, *_workspace(ws, d),
+                               _on(d, stream)))
     return ws
 
 
 def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=None, stream=None):
     """Pages of its own for each sequence's next n_new[s] tokens; a shared part-filled page is copied in every layer of
     pool. Returns served, int32 [sequences]: 0 where there was no room."""
-    S, M, P = _books(table, lengths, refs)
-    layers, page_bytes = _layers(pool, P)
-    _ints(n_new, "n_new", (S,))
+    S, M, P, d = _books(table, lengths, refs, stream)
+    layers, page_bytes = _layers(pool, P, d)
+    _ints(n_new, "n_new", (S,), d)
     if served is None:
         served = _new(torch.empty, stream, S, dtype=torch.int32, device=table.device)
     else:
-        _ints(served, "served", (S,))
+        _ints(served, "served", (S,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
     _ok(_lib().spec_pages_reserve(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(n_new),
-                                  _ptr(served), _ptr(ws), ws.numel(), _on(pool, stream)))
+                                  _ptr(served), *_workspace(ws, d), _on(d, stream)))
     return served
 
 
 def pages_commit(table, lengths, refs, advance, *, extra=1, window=0, sinks=0, workspace=None, stream=None):
     """lengths += advance + extra (a verification's accept_len and the token before the drafts); pages past the new
     lengths, or with window > 0 out of every later query's view, are let go. Returns the workspace."""
-    S, M, P = _books(table, lengths, refs)
-    _ints(advance, "advance", (S,))
+    S, M, P, d = _books(table, lengths, refs, stream)
+    _ints(advance, "advance", (S,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_commit(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(advance), extra, window, sinks, _ptr(ws),
-                                 ws.numel(), _on(table, stream)))
+    _ok(_lib().spec_pages_commit(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(advance), extra, window, sinks,
+                                 *_workspace(ws, d), _on(d, stream)))
     return ws
 
 
 def pages_release(table, lengths, refs, slots, *, workspace=None, stream=None):
     """Lets go of every page of the sequences slots (int32 [F]). Returns the workspace."""
-    S, M, P = _books(table, lengths, refs)
+    S, M, P, d = _books(table, lengths, refs, stream)
     F = slots.numel()
-    _ints(slots, "slots", (F,))
+    _ints(slots, "slots", (F,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_release(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(slots), F, _ptr(ws), ws.numel(),
-                                  _on(table, stream)))
+    _ok(_lib().spec_pages_release(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(slots), F, *_workspace(ws, d),
+                                  _on(d, stream)))
     return ws
 
 
 def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
     """Moves the pages in use to the front of the pool, in every layer; table and refs follow. Returns used, int32 [1]:
     how many there are."""
-    S, M, P = _books(table, None, refs)
-    layers, page_bytes = _layers(pool, P)
+    S, M, P, d = _books(table, None, refs, stream)
+    layers, page_bytes = _layers(pool, P, d)
     if used is None:
         used = _new(torch.empty, stream, 1, dtype=torch.int32, device=table.device)
     else:
-        _ints(used, "used", (1,))
+        _ints(used, "used", (1,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_compact(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(refs), S, M, P, _ptr(used), _ptr(ws), ws.numel(),
-                                  _on(pool, stream)))
+    _ok(_lib().spec_pages_compact(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(refs), S, M, P, _ptr(used), *_workspace(ws, d),
+                                  _on(d, stream)))
     return used

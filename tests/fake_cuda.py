@@ -129,4 +129,5 @@ def install(monkeypatch, sv, device=0):
     monkeypatch.setattr(cache, "torch", t)
     monkeypatch.setattr(cache, "_lib", lambda: lib)
     monkeypatch.setattr(cache, "_raw_stream", None)
+    monkeypatch.setattr(cache, "_current_device", t.cuda.current_device)
     return t, lib

@@ -84,3 +84,66 @@ def test_a_workspace_made_for_a_call_is_clear_and_one_given_is_used(fake, name):
     del t.made[:]
     CALLS[name](Args(), workspace=fc.Tensor((1 << 16,), U8))
     assert not [x for x in t.made if x.dtype is U8] and 1 << 16 in lib.calls[-1][1]
+
+
+# the arguments that each call looks at, beside its first one
+LOOKED_AT = {
+    "qk_norm_rope": "k positions freqs q_weight", "cache_append": "table lengths k v n", "cache_read": "table lengths",
+    "cache_attention": "pool table lengths n", "pages_fork": "lengths refs pairs", "pages_reserve": "pool lengths refs n",
+    "pages_commit": "lengths refs n", "pages_release": "lengths refs pairs", "pages_compact": "pool refs",
+}
+
+
+@pytest.mark.parametrize("where,words", [(1, "must be on cuda:0, got cuda:1"), (-1, "must be a CUDA tensor")])
+@pytest.mark.parametrize("name,which", [(n, w) for n, ws in LOOKED_AT.items() for w in ws.split()])
+def test_every_argument_is_on_the_call_s_device(fake, name, which, where, words):
+    _, lib = fake
+    a = Args()
+    getattr(a, which).index = where
+    with pytest.raises(ValueError, match=words):
+        CALLS[name](a)
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_of_another_device_than_the_current_one_are_refused(fake, name):
+    _, lib = fake
+    with pytest.raises(ValueError, match="is on cuda:1, the current device is cuda:0"):
+        CALLS[name](Args(1))
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_device_is_refused(fake, name):
+    _, lib = fake
+    with pytest.raises(ValueError, match="is on cuda:0, the stream on cuda:1"):
+        CALLS[name](Args(), stream=fc.Stream("far", 1))
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("workspace,error", [
+    (fc.Tensor((1 << 15,), U8, -1), ValueError), (fc.Tensor((1 << 15,), U8, 1), ValueError), (fc.Tensor((1 << 15,), I32), TypeError),
+    (fc.Tensor((1 << 14,), U8, strides=(2,)), ValueError),
+])
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_workspaces_that_are_not_device_bytes_are_refused(fake, name, workspace, error):
+    _, lib = fake
+    with pytest.raises(error):
+        CALLS[name](Args(), workspace=workspace)
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("name,given", [
+    ("qk_norm_rope", "q_out"), ("qk_norm_rope", "k_out"), ("cache_read", "k"), ("cache_read", "v"), ("cache_attention", "out"),
+    ("cache_attention", "lse"), ("pages_reserve", "served"), ("pages_compact", "used"),
+])
+@pytest.mark.parametrize("where", [-1, 1])
+def test_outputs_elsewhere_are_refused(fake, name, given, where):
+    _, lib = fake
+    t = {"q_out": ((B, N, HQ, D), BF16), "k_out": ((B, N, HK, D), BF16), "k": ((S, 5, HK, D), BF16), "v": ((S, 5, HK, D), BF16),
+         "out": ((B, N, HQ, D), BF16), "lse": ((B, N, HQ), torch.float32), "served": ((S,), I32), "used": ((1,), I32)}[given]
+    CALLS[name](Args(), **{given: fc.Tensor(*t)})
+    del lib.calls[:]
+    with pytest.raises(ValueError, match="CUDA tensor" if where < 0 else "must be on cuda:0, got cuda:1"):
+        CALLS[name](Args(), **{given: fc.Tensor(*t, where)})
+    assert lib.calls == []
