@@ -8,7 +8,7 @@ when not given. There is no CPU path: if the library is missing, importing the c
     cactus_verify(target, draft, tokens, seeds, delta, temperature)  Cactus constrained acceptance
     counterfactual_gamma(target, drafters, temperature, selected, tokens, seeds)  HedgeSpec gamma
 
-A call runs on `stream`, or on the current one; what is not given is made on that stream, what is given has to be ready on it.
+Every tensor of a call is on the current device. A call runs on `stream`, or on the current one; what is not given is made on that stream, what is given has to be ready on it.
 
 The operators of the scoring step around a verification (head norms and rotation, a paged cache in 4 bits, attention
 over it, its pages) are in cache.py and exported here too.
@@ -128,9 +128,14 @@ def _dtype_code(t):
     raise TypeError("logits must be bfloat16 or float32, got %s" % t.dtype)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _need(t, name, dtype=None, shape=None):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != _current_device():     # where the library launches
+        raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, _current_device(), t.get_device()))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     if dtype is not None and t.dtype != dtype:
@@ -192,14 +197,28 @@ def last_plan() -> dict:
     return dict(stages=out[1], ctas=out[2], kernel=out[3], pieces=out[4])
 
 
+def _given(t, name, dtype, shape, stream, device):
+    """The caller's output, or a new one."""
+    if t is None:
+        return _new(torch.empty, stream, shape, dtype=dtype, device=device)
+    _need(t, name)
+    return t
+
+
 def _outputs(B, K, device, accept_len, out_tokens, diag, want_diag, stream):
-    if accept_len is None:
-        accept_len = _new(torch.empty, stream, B, dtype=torch.int32, device=device)
-    if out_tokens is None:
-        out_tokens = _new(torch.empty, stream, (B, K + 1), dtype=torch.int32, device=device)
-    if diag is None and want_diag:
-        diag = _new(torch.empty, stream, (B, K, 4), dtype=torch.float32, device=device)
+    accept_len = _given(accept_len, "accept_len", torch.int32, B, stream, device)
+    out_tokens = _given(out_tokens, "out_tokens", torch.int32, (B, K + 1), stream, device)
+    if diag is not None or want_diag:
+        diag = _given(diag, "diag", torch.float32, (B, K, 4), stream, device)
     return accept_len, out_tokens, diag
+
+
+def _workspace(workspace, B, K, V, N, device, stream):
+    """The caller's workspace, or a new one."""
+    if workspace is None:
+        return _new(new_workspace, stream, B, K, V, N, device)
+    _need(workspace, "workspace")
+    return workspace
 
 
 def verify(target, draft, tokens, seeds, temperature=1.0, *, accept_len=None, out_tokens=None, diag=None,
@@ -213,7 +232,7 @@ def verify(target, draft, tokens, seeds, temperature=1.0, *, accept_len=None, ou
     _need(tokens, "tokens", torch.int32, (B, K))
     _need(seeds, "seeds", None, (B,))
     accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
-    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
+    ws = _workspace(workspace, B, K, V, 1, target.device, stream)
     _check(load().spec_verify(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V,
                               float(temperature), _p(accept_len), _p(out_tokens), _p(diag), _p(ws), ws.numel(),
                               _stream(stream)))
@@ -231,9 +250,8 @@ def cactus_verify(target, draft, tokens, seeds, delta, temperature=1.0, *, accep
     _need(tokens, "tokens", torch.int32, (B, K))
     _need(seeds, "seeds", None, (B,))
     accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
-    if gamma_star is None:
-        gamma_star = _new(torch.empty, stream, (B, K), dtype=torch.float32, device=target.device)
-    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
+    gamma_star = _given(gamma_star, "gamma_star", torch.float32, (B, K), stream, target.device)
+    ws = _workspace(workspace, B, K, V, 1, target.device, stream)
     fn = load().spec_cactus_kl_verify if exact_kl else load().spec_cactus_verify
     _check(fn(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V, float(temperature),
               float(delta), _p(accept_len), _p(out_tokens), _p(diag), _p(gamma_star), _p(ws), ws.numel(),
@@ -249,7 +267,7 @@ def greedy_verify(target, tokens, *, accept_len=None, out_tokens=None, workspace
     _need(target, "target")
     _need(tokens, "tokens", torch.int32, (B, K))
     accept_len, out_tokens, _ = _outputs(B, K, target.device, accept_len, out_tokens, None, False, stream)
-    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, 1, target.device)
+    ws = _workspace(workspace, B, K, V, 1, target.device, stream)
     _check(load().spec_greedy_verify(_p(target), _dtype_code(target), _p(tokens), B, K, V, _p(accept_len),
                                      _p(out_tokens), _p(ws), ws.numel(), _stream(stream)))
     return dict(accept_len=accept_len, out_tokens=out_tokens, workspace=ws)
@@ -259,10 +277,9 @@ def accept_length_estimate(gamma, *, est=None, loss=None, want_loss=True, stream
     """HedgeSpec accept-length estimate 1 + sum_k prod_{j<=k} gamma_j and loss K + 1 - est from gamma [N,B,K]."""
     N, B, K = gamma.shape
     _need(gamma, "gamma", torch.float32, (N, B, K))
-    if est is None:
-        est = _new(torch.empty, stream, (N, B), dtype=torch.float32, device=gamma.device)
-    if loss is None and want_loss:
-        loss = _new(torch.empty, stream, (N, B), dtype=torch.float32, device=gamma.device)
+    est = _given(est, "est", torch.float32, (N, B), stream, gamma.device)
+    if loss is not None or want_loss:
+        loss = _given(loss, "loss", torch.float32, (N, B), stream, gamma.device)
     _check(load().spec_accept_length_estimate(_p(gamma), N, B, K, _p(est), _p(loss), _stream(stream)))
     return dict(est=est, loss=loss)
 
@@ -323,6 +340,8 @@ def verify_filtered(target, draft, tokens, seeds, temperature=1.0, top_k=0, top_
     if workspace is None:
         n = lib.spec_filter_workspace_size(B, K, V, _dtype_code(target))
         workspace = _new(torch.zeros, stream, n, dtype=torch.uint8, device=target.device)
+    else:
+        _need(workspace, "workspace")
     _check(lib.spec_verify_filtered(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V,
                                     float(temperature), int(top_k), float(top_p), _p(accept_len), _p(out_tokens),
                                     _p(diag), _p(workspace), workspace.numel(), _stream(stream)))
@@ -340,17 +359,16 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
     _need(target, "target")
     _need(drafters, "drafters", target.dtype, (N, B, K, V))
     dev = target.device
-    if gamma is None:
-        gamma = _new(torch.empty, stream, (N, B, K), dtype=torch.float32, device=dev)
-    if loss is None and want_loss:
-        loss = _new(torch.empty, stream, (N, B, K), dtype=torch.float32, device=dev)
+    gamma = _given(gamma, "gamma", torch.float32, (N, B, K), stream, dev)
+    if loss is not None or want_loss:
+        loss = _given(loss, "loss", torch.float32, (N, B, K), stream, dev)
     out = dict(gamma=gamma, loss=loss)
     if selected >= 0:
         _need(tokens, "tokens", torch.int32, (B, K))
         _need(seeds, "seeds", None, (B,))
         accept_len, out_tokens, diag = _outputs(B, K, dev, accept_len, out_tokens, diag, want_diag, stream)
         out.update(accept_len=accept_len, out_tokens=out_tokens, diag=diag)
-    ws = workspace if workspace is not None else _new(new_workspace, stream, B, K, V, N, dev)
+    ws = _workspace(workspace, B, K, V, N, dev, stream)
     _check(load().spec_counterfactual_gamma(_p(target), _p(drafters), _dtype_code(target), N, B, K, V,
                                             float(temperature), _p(gamma), _p(loss), int(selected), _p(tokens),
                                             _p(seeds), _p(out.get("accept_len")), _p(out.get("out_tokens")),

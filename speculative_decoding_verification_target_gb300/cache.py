@@ -25,7 +25,7 @@ import math
 
 import torch
 
-from . import SPEC_OK, SpecError, _need, _new, load as _load
+from . import SPEC_OK, SpecError, _current_device, _need, _new, load as _load
 
 PAGE, GROUP = 64, 32
 WS_HEADER = 8192
@@ -73,7 +73,6 @@ def _ok(code):
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 # The serving loop calls these once per layer and token, so the checks are written to cost little where they pass: one
@@ -95,12 +94,6 @@ def _on(d, stream):
     if stream is not None:
         return stream.cuda_stream
     return _raw_stream(d) if _raw_stream is not None else torch.cuda.current_stream(d).cuda_stream
-
-
-def _wrong(t, name, dtype, shape, d):
-    """Says what keeps t from being a contiguous tensor of that type and shape (None: any) on device d."""
-    _need(t, name, dtype, shape)
-    raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, d, t.get_device()))
 
 
 def _ptr(t):
@@ -139,12 +132,12 @@ def _own(t):
 
 def _vector(t, name, dtype, shape, d):
     if not (t.get_device() == d and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        _wrong(t, name, dtype, shape, d)
+        _need(t, name, dtype, shape)
 
 
 def _pool(pool, d, name="pool"):
     if not (pool.get_device() == d and pool.dtype is torch.uint8 and pool.is_contiguous()):
-        _wrong(pool, name, torch.uint8, None, d)
+        _need(pool, name, torch.uint8)
     if pool.dim() != 3:
         raise ValueError("%s must be [pages, Hk, 68 D], got %s" % (name, tuple(pool.shape)))
     P, H, n = pool.shape
@@ -155,12 +148,12 @@ def _pool(pool, d, name="pool"):
 
 def _ints(t, name, shape, d):
     if not (t.get_device() == d and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
-        _wrong(t, name, torch.int32, shape, d)
+        _need(t, name, torch.int32, shape)
 
 
 def _table(table, d):
     if not (table.get_device() == d and table.dtype is torch.int32 and table.is_contiguous()):
-        _wrong(table, "table", torch.int32, None, d)
+        _need(table, "table", torch.int32)
     if table.dim() != 2:
         raise ValueError("table must be [sequences, max_pages], got %s" % (tuple(table.shape),))
     return table.shape
@@ -169,7 +162,7 @@ def _table(table, d):
 def _workspace(ws, d):
     """The caller's workspace as (address, bytes)."""
     if not (ws.get_device() == d and ws.dtype is torch.uint8 and ws.is_contiguous()):
-        _wrong(ws, "workspace", torch.uint8, None, d)
+        _need(ws, "workspace", torch.uint8)
     return ws.data_ptr(), ws.numel()
 
 
@@ -336,7 +329,7 @@ def _books(table, lengths, refs, stream):
 def _layers(pool, P, d):
     """[pages, ...] or [layers, pages, ...] as (layers, bytes of a page)."""
     if not (pool.get_device() == d and pool.dtype is torch.uint8 and pool.is_contiguous()):
-        _wrong(pool, "pool", torch.uint8, None, d)
+        _need(pool, "pool", torch.uint8)
     if pool.dim() not in (3, 4) or pool.shape[-3] != P:
         raise ValueError("pool must be [%d, Hk, 68 D] or [layers, %d, Hk, 68 D], got %s" % (P, P, tuple(pool.shape)))
     return (pool.shape[0] if pool.dim() == 4 else 1), pool.shape[-2] * pool.shape[-1]

@@ -129,5 +129,6 @@ def install(monkeypatch, sv, device=0):
     monkeypatch.setattr(cache, "torch", t)
     monkeypatch.setattr(cache, "_lib", lambda: lib)
     monkeypatch.setattr(cache, "_raw_stream", None)
-    monkeypatch.setattr(cache, "_current_device", t.cuda.current_device)
+    for module in (sv, cache):
+        monkeypatch.setattr(module, "_current_device", t.cuda.current_device)
     return t, lib
