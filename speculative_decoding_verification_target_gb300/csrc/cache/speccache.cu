@@ -347,7 +347,9 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
 
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D) {
     if (N < 1 || N > MAX_Q || Hk < 1 || Hq < Hk || Hq > MAX_HEADS || Hq % Hk || (D != 64 && D != 128)) return 0;
-    return att_layout(att_split(N * (Hq / Hk)), D).total;
+    size_t most = 0;      // fewer queries can take a wider kernel: 64 rows are one block of 64, 65 are two of 33 in 48 columns
+    for (int n = 1; n <= N; ++n) most = std::max(most, att_layout(att_split(n * (Hq / Hk)), D).total);
+    return most;
 }
 
 spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
@@ -365,7 +367,9 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     SPECC_TRY(check_heads(out, "out", dtype, B, N, Hq));
     SPECC_TRY(check_table(pool, pages, table, max_pages));
     if (!kv_len) return fail(SPEC_ERR_INVALID, "kv_len must not be NULL");
-    SPECC_TRY(check_workspace(workspace, workspace_bytes, spec_cache_attention_workspace_size(N, Hq, Hk, D)));
+    const AttSplit split = att_split(N * (Hq / Hk));
+    const AttLayout w = att_layout(split, D);
+    SPECC_TRY(check_workspace(workspace, workspace_bytes, w.total));
     AttnParams p = {};
     p.q = heads_of(q);
     p.out = heads_of(out);
@@ -385,12 +389,10 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     p.sinks = sinks;
     p.scale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.G = Hq / Hk;
-    const AttSplit split = att_split(N * p.G);
     p.RB = split.blocks;
     p.rpb = split.rows;
     p.width = split.wg * split.nw;
     p.fp16 = dtype == SPEC_FP16;
-    const AttLayout w = att_layout(split, D);
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
     p.desc = reinterpret_cast<int4*>(ws + w.desc);
     p.part_ml = reinterpret_cast<float2*>(ws + w.ml);

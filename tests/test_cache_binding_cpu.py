@@ -147,3 +147,12 @@ def test_outputs_elsewhere_are_refused(fake, name, given, where):
     with pytest.raises(ValueError, match="CUDA tensor" if where < 0 else "must be on cuda:0, got cuda:1"):
         CALLS[name](Args(), **{given: fc.Tensor(*t, where)})
     assert lib.calls == []
+
+
+@pytest.mark.parametrize("G,H", [(1, 1), (1, 8), (2, 4), (3, 2), (4, 8), (5, 1), (8, 8), (16, 2), (64, 1), (1024, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_attention_workspace_serves_fewer_tokens_too(G, H, D):
+    from speculative_decoding_verification_target_gb300 import _build, cache
+    _build.build()
+    sizes = [cache._lib().spec_cache_attention_workspace_size(n, G * H, H, D) for n in range(1, 1025)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))

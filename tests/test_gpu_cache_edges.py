@@ -75,3 +75,19 @@ def test_verification_on_a_stream_beside_a_busy_one():
         assert torch.equal(a["accept_len"], b["accept_len"])
         for n, x, y in zip(a["accept_len"].tolist(), a["out_tokens"].tolist(), b["out_tokens"].tolist()):
             assert x[:n + 1] == y[:n + 1]
+
+
+@pytest.mark.parametrize("Hq,H,D,most", [(64, 8, 128, 9), (32, 8, 128, 12), (8, 8, 64, 70)])
+def test_one_attention_workspace_for_every_number_of_tokens(Hq, H, D, most):
+    g = torch.Generator().manual_seed(most)
+    lens = torch.tensor([400, 90], **I32)
+    table, zero = torch.arange(14, **I32).view(2, 7), torch.zeros(2, **I32)
+    kv = torch.randn((2, 400, 2 * H, D), generator=g).half().cuda()
+    pool = sv.new_pool(14, H, D)
+    sv.cache_append(pool, table, zero, kv[:, :, :H], kv[:, :, H:])
+    ws = sv.new_attention_workspace(most, Hq, H, D)
+    for N in range(most, 0, -1):
+        q = torch.randn((2, N, Hq, D), generator=g).half().cuda()
+        got = sv.cache_attention(q, pool, table, lens, workspace=ws)["out"]
+        assert torch.equal(got, sv.cache_attention(q, pool, table, lens)["out"]), N
+    assert sv.read_status(ws) == 0
