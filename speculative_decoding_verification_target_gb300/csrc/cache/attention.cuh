@@ -20,9 +20,12 @@
 //     offsets beside them it took 195 us where it takes 182, since broadcasts cost shared memory by their bytes). Tokens that
 //     hold nothing have s = 0 there, so that whatever bits they have cannot reach O (0 times a NaN would).
 //   - The softmax works on S^T: a thread has one token and all queries. m_n is not the maximum but a reference that
-//     any value near it may serve as: it is moved, and O and l rescaled, only where a score exceeds it by more than 2^8,
+//     any value near it may serve as: it is moved, and O and l rescaled, only where a score exceeds it by more than 2^15,
 //     which the barrier before the second product detects at no cost. l_n is kept per thread and added up at the end.
-//     Probabilities are rounded to fp16 for the product, l is the sum of the unrounded ones.
+//     Probabilities are rounded to fp16 for the product, l is the sum of the unrounded ones. The reference is put 2^-7 of the
+//     maximum, so that they take a half's whole range: the largest are 2^7 .. 2^15, all down to 2^-21 of the largest keep their
+//     eleven bits, and what is lost of one below that is 2^-32 of the largest at most. (With the reference at the maximum it
+//     was 2^-25: beside a first token that takes nearly all the weight, 10^5 others with 2^-25 of it each came to nothing.)
 // A tile is 128 tokens, two pages, fetched as one bulk copy each, STAGES tiles ahead, by a warp that also issues the products:
 // with that in the computing warps, everyone waited for the one that did it. CTAs are small (four computing warps, four CTAs to
 // an SM, as many as the tensor memory has columns for; eight warps and two CTAs for over 32 queries) and hide each other's
@@ -45,7 +48,8 @@ constexpr int ATT_MAX_CTAS = 640;
 constexpr uint64_t ATT_WAIT_NS = 2000000000ull;      // after which a wait gives up
 constexpr int ATT_UNIT = 2;             // what beginning and ending a unit costs, in tiles
 constexpr float ATT_NONE = -1e30f;       // reference of a query that has seen nothing yet
-constexpr float ATT_SLACK = 8.f;         // how far (log2) a score may pass the reference: p <= 2^8 is well inside a half
+constexpr float ATT_BELOW = 7.f;         // how far (log2) below the maximum a reference is put
+constexpr float ATT_SLACK = 15.f;        // how far (log2) a score may pass the reference: p <= 2^15 is inside a half
 
 struct AttnParams {
     Heads q, out;
@@ -653,7 +657,8 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                 uint32_t u[NW];
                 tmem_load<NW>(tlane + C::COL_S + wg * NW, u);
                 if (move) {
-                    // the references move to the maxima seen so far; l and, unless this is the part's first tile, O follow
+                    // the references move to ATT_BELOW under the maxima seen so far; l and, unless this is the part's first tile,
+                    // O follow
                     float y[NW];
                     const uint32_t bits = here(seen);
 #pragma unroll
@@ -662,7 +667,8 @@ __global__ void __launch_bounds__(Att<D, WG, NW>::TH, Att<D, WG, NW>::CTAS)
                     bar_sync(BAR_COMPUTE, CT);
                     if (tid < NQ) {
                         const float old = -s_nm[tid];
-                        const float now = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), old);
+                        const float top = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
+                        const float now = fmaxf(top - ATT_BELOW, old);      // no token seen: -inf, and the old one stays
                         s_fac[tid] = specv::ex2(old - now);
                         s_nm[tid] = -now;
                     }

@@ -91,3 +91,63 @@ def test_one_attention_workspace_for_every_number_of_tokens(Hq, H, D, most):
         got = sv.cache_attention(q, pool, table, lens, workspace=ws)["out"]
         assert torch.equal(got, sv.cache_attention(q, pool, table, lens)["out"]), N
     assert sv.read_status(ws) == 0
+
+
+def sink_case(n, D, H, N, gap, dtype, dominant):
+    """n cached tokens with the same key and value 1 each, but for `dominant`, whose score is `gap` above and whose value is 0."""
+    k = torch.full((1, n, H, D), -1.0)
+    k[:, dominant] = 1.0
+    v = torch.ones((1, n, H, D))
+    v[:, dominant] = 0.0
+    M = (n + 63) // 64
+    pool, table = sv.new_pool(M, H, D), torch.randperm(M, generator=torch.Generator().manual_seed(n)).to(torch.int32).cuda().view(1, M)
+    sv.cache_append(pool, table, torch.zeros(1, **I32), k.to(dtype).cuda(), v.to(dtype).cuda())
+    held = sv.cache_read(pool, table, torch.zeros(1, **I32), n, dtype=torch.float16)
+    step = float(held["k"][0, dominant, 0, 0] - held["k"][0, 1 if dominant == 0 else 0, 0, 0])      # between the two keys
+    q = torch.full((1, N, 2 * H, D), gap / (step * D ** 0.5)).to(dtype).cuda()
+    return q, pool, table, held
+
+
+@pytest.mark.parametrize("gap", [6.0, 9.5, 12.0, 15.0, 17.0, 17.5, 18.0, 20.0])
+@pytest.mark.parametrize("n,D,H,N,dominant", [
+    (131072, 128, 1, 1, 0), (131072, 64, 2, 1, 0), (100001, 128, 1, 20, 0),     # a first token that takes the weight, parts joined
+    (3000, 128, 1, 3, 1500), (3000, 64, 1, 5, 2990), (130, 128, 4, 1, 129),     # one that comes later: the reference moves
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_small_probabilities_beside_a_dominant_one(gap, n, D, H, N, dominant, dtype):
+    """The rest's share, held by many tokens with less than 2^-14 of the largest probability each. A probability is off by 2^-11 of itself
+    or by 2^-32 of the largest: with the reference seven binary orders below the maximum or more, the largest is 2^7 or more in
+    the kernel's units and half a step of the smallest halves 2^-25. Else as in test_gpu_cache: scores within
+    delta = 2^-17 sum |q k| scale, the output rounded once."""
+    q, pool, table, held = sink_case(n, D, H, N, gap, dtype, dominant)
+    r = sv.cache_attention(q, pool, table, torch.tensor([n], **I32), want_lse=True)
+    k, v = held["k"][0].double().transpose(0, 1), held["v"][0].double().transpose(0, 1)           # [H, n, D]
+    x = q[0].double().view(N, H, 2, D).permute(1, 0, 2, 3).reshape(H, N * 2, D)
+    see = (torch.arange(n, device="cuda") <= (n - N + torch.arange(N, device="cuda"))[:, None]).repeat_interleave(2, 0)[None]
+    sc = (x @ k.transpose(1, 2) * D ** -0.5).masked_fill(~see, -torch.inf)
+    lse = sc.logsumexp(-1)
+    p = (sc - lse[..., None]).exp()
+    ref, mass, total = p @ v, p @ v.abs(), see.double().expand(H, -1, -1) @ v.abs()
+    delta = 2.0 ** -17 * (x.abs() @ k.abs().transpose(1, 2)).amax(-1) * D ** -0.5
+    tol = torch.finfo(dtype).eps / 2 * ref.abs() + (2.0 ** -11 + 2.0 ** -13 + 2 * delta[..., None]) * mass + 2.0 ** -32 * total
+    out = r["out"][0].double().view(N, H, 2, D).permute(1, 0, 2, 3).reshape(H, N * 2, D)
+    err = (out - ref).abs()
+    assert (err <= tol + torch.finfo(dtype).tiny).all(), float((err / tol).max())
+    got = r["lse"][0].double().view(N, H, 2).permute(1, 0, 2).reshape(H, N * 2)
+    assert ((got - lse).abs() <= delta + 2.0 ** -20 * (1 + lse.abs())).all()
+
+
+@pytest.mark.parametrize("gap", [12.0, 15.0, 17.0, 17.5, 18.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_probabilities_of_sequences_that_are_not_cut(gap, D):
+    """As above, with so many sequences (all of them the same pages) that a sequence's tokens are mostly one part's, beside its dominant one."""
+    n, S = 20000, 700
+    q, pool, table, held = sink_case(n, D, 1, 1, gap, torch.float16, 0)
+    out = sv.cache_attention(q.expand(S, 1, 2, D).contiguous(), pool, table.expand(S, -1).contiguous(), torch.full((S,), n, **I32))["out"]
+    k, v = held["k"][0, :, 0].double(), held["v"][0, :, 0].double()
+    sc = k @ q[0, 0, 0].double() * D ** -0.5
+    p = sc.softmax(-1)
+    ref = p @ v
+    delta = 2.0 ** -17 * float((k.abs() @ q[0, 0, 0].double().abs()).max()) * D ** -0.5
+    tol = (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -13 + 2 * delta) * ref + 2.0 ** -32 * n + 2.0 ** -25      # fp16 outputs: half a step, 2^-25 at least
+    assert ((out.double() - ref).abs() <= tol).all(), float(((out.double() - ref).abs() / tol).max())
