@@ -8,7 +8,8 @@ when not given. There is no CPU path: if the library is missing, importing the c
     cactus_verify(target, draft, tokens, seeds, delta, temperature)  Cactus constrained acceptance
     counterfactual_gamma(target, drafters, temperature, selected, tokens, seeds)  HedgeSpec gamma
 
-Every tensor of a call is on the current device. A call runs on `stream`, or on the current one; what is not given is made on that stream, what is given has to be ready on it.
+Every tensor of a call is on the current device. A call runs on `stream`, or on the current one; what is not given is made on
+that stream, what is given has to be ready on it.
 
 The operators of the scoring step around a verification (head norms and rotation, a paged cache in 4 bits, attention
 over it, its pages) are in cache.py and exported here too.
@@ -131,17 +132,24 @@ def _dtype_code(t):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _need(t, name, dtype=None, shape=None):
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.get_device() != _current_device():     # where the library launches
-        raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, _current_device(), t.get_device()))
+def _need(t, name, dtype=None, shape=None, device=None):
+    """Refuses t unless it is a contiguous tensor of that type and shape on `device`, or where that is None on the current one,
+    since the library launches there. Returns its device."""
+    d = t.get_device()
+    if d != device:
+        if d < 0:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if device is None:
+            device = _current_device()
+        if d != device:
+            raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, device, d))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return d
 
 
 def _new(make, stream, *args, **kw):
@@ -201,7 +209,7 @@ def _given(t, name, dtype, shape, stream, device):
     """The caller's output, or a new one."""
     if t is None:
         return _new(torch.empty, stream, shape, dtype=dtype, device=device)
-    _need(t, name)
+    _need(t, name, None, None, device.index)
     return t
 
 
@@ -217,7 +225,7 @@ def _workspace(workspace, B, K, V, N, device, stream):
     """The caller's workspace, or a new one."""
     if workspace is None:
         return _new(new_workspace, stream, B, K, V, N, device)
-    _need(workspace, "workspace")
+    _need(workspace, "workspace", None, None, device.index)
     return workspace
 
 
@@ -227,10 +235,10 @@ def verify(target, draft, tokens, seeds, temperature=1.0, *, accept_len=None, ou
     seeds int64/uint64 [B]. Returns dict(accept_len, out_tokens, diag)."""
     B, K1, V = target.shape
     K = K1 - 1
-    _need(target, "target")
-    _need(draft, "draft", target.dtype, (B, K, V))
-    _need(tokens, "tokens", torch.int32, (B, K))
-    _need(seeds, "seeds", None, (B,))
+    d = _need(target, "target")
+    _need(draft, "draft", target.dtype, (B, K, V), d)
+    _need(tokens, "tokens", torch.int32, (B, K), d)
+    _need(seeds, "seeds", None, (B,), d)
     accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
     ws = _workspace(workspace, B, K, V, 1, target.device, stream)
     _check(load().spec_verify(_p(target), _p(draft), _dtype_code(target), _p(tokens), _p(seeds), B, K, V,
@@ -245,10 +253,10 @@ def cactus_verify(target, draft, tokens, seeds, delta, temperature=1.0, *, accep
     gamma* as the root of the KL constraint (spec_cactus_kl_verify) instead of its Taylor closed form."""
     B, K1, V = target.shape
     K = K1 - 1
-    _need(target, "target")
-    _need(draft, "draft", target.dtype, (B, K, V))
-    _need(tokens, "tokens", torch.int32, (B, K))
-    _need(seeds, "seeds", None, (B,))
+    d = _need(target, "target")
+    _need(draft, "draft", target.dtype, (B, K, V), d)
+    _need(tokens, "tokens", torch.int32, (B, K), d)
+    _need(seeds, "seeds", None, (B,), d)
     accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
     gamma_star = _given(gamma_star, "gamma_star", torch.float32, (B, K), stream, target.device)
     ws = _workspace(workspace, B, K, V, 1, target.device, stream)
@@ -264,8 +272,8 @@ def greedy_verify(target, tokens, *, accept_len=None, out_tokens=None, workspace
     argmax of the first rejecting row (or of row K). target [B,K+1,V], tokens [B,K]."""
     B, K1, V = target.shape
     K = K1 - 1
-    _need(target, "target")
-    _need(tokens, "tokens", torch.int32, (B, K))
+    d = _need(target, "target")
+    _need(tokens, "tokens", torch.int32, (B, K), d)
     accept_len, out_tokens, _ = _outputs(B, K, target.device, accept_len, out_tokens, None, False, stream)
     ws = _workspace(workspace, B, K, V, 1, target.device, stream)
     _check(load().spec_greedy_verify(_p(target), _dtype_code(target), _p(tokens), B, K, V, _p(accept_len),
@@ -331,10 +339,10 @@ def verify_filtered(target, draft, tokens, seeds, temperature=1.0, top_k=0, top_
     draft row alike (ties at a threshold kept). Same layout and outputs as verify."""
     B, K1, V = target.shape
     K = K1 - 1
-    _need(target, "target")
-    _need(draft, "draft", target.dtype, (B, K, V))
-    _need(tokens, "tokens", torch.int32, (B, K))
-    _need(seeds, "seeds", None, (B,))
+    d = _need(target, "target")
+    _need(draft, "draft", target.dtype, (B, K, V), d)
+    _need(tokens, "tokens", torch.int32, (B, K), d)
+    _need(seeds, "seeds", None, (B,), d)
     accept_len, out_tokens, diag = _outputs(B, K, target.device, accept_len, out_tokens, diag, want_diag, stream)
     lib = load()
     if workspace is None:
@@ -356,16 +364,16 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
     B, K1, V = target.shape
     K = K1 - 1
     N = drafters.shape[0]
-    _need(target, "target")
-    _need(drafters, "drafters", target.dtype, (N, B, K, V))
+    d = _need(target, "target")
+    _need(drafters, "drafters", target.dtype, (N, B, K, V), d)
     dev = target.device
     gamma = _given(gamma, "gamma", torch.float32, (N, B, K), stream, dev)
     if loss is not None or want_loss:
         loss = _given(loss, "loss", torch.float32, (N, B, K), stream, dev)
     out = dict(gamma=gamma, loss=loss)
     if selected >= 0:
-        _need(tokens, "tokens", torch.int32, (B, K))
-        _need(seeds, "seeds", None, (B,))
+        _need(tokens, "tokens", torch.int32, (B, K), d)
+        _need(seeds, "seeds", None, (B,), d)
         accept_len, out_tokens, diag = _outputs(B, K, dev, accept_len, out_tokens, diag, want_diag, stream)
         out.update(accept_len=accept_len, out_tokens=out_tokens, diag=diag)
     ws = _workspace(workspace, B, K, V, N, dev, stream)

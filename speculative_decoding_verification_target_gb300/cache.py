@@ -14,8 +14,9 @@ refs int32 [pages]; the header states the format and every rule. One round of a 
 
 and beside it pages_fork (a sequence that shares another's pages), pages_release, pages_compact and cache_read.
 
-Every tensor of a call is on the current device. A call runs on `stream`, or on the current one. Outputs and workspaces that are not given are made on that stream; what is given
-has to be ready on it. The status word is in the workspace (read_status): a caller that looks at it passes the workspace.
+Every tensor of a call is on the current device. A call runs on `stream`, or on the current one. Outputs and workspaces that
+are not given are made on that stream; what is given has to be ready on it. The status word is in the workspace
+(read_status): a caller that looks at it passes the workspace.
 """
 from __future__ import annotations
 
@@ -108,8 +109,16 @@ def _code(t, name, fp32=False):
     return code
 
 
+def _rows(t, name):
+    """[B, N, heads, D] with any strides but contiguous channels, its type, shape and device known."""
+    sb, sn, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    return Heads(t.data_ptr(), sb, sn, sh)
+
+
 def _heads(t, name, shape, dtype, d):
-    """[B, N, heads, D] with any strides but contiguous channels."""
+    """The same, with those checked."""
     if not (t.get_device() == d and t.dtype is dtype and t.shape == shape):
         if not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
@@ -118,10 +127,7 @@ def _heads(t, name, shape, dtype, d):
         if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
         raise ValueError("%s must be on cuda:%d, got cuda:%d" % (name, d, t.get_device()))
-    sb, sn, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError("%s must have contiguous channels" % name)
-    return Heads(t.data_ptr(), sb, sn, sh)
+    return _rows(t, name)
 
 
 def _own(t):
@@ -213,7 +219,7 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     dt = q.dtype
     code = _code(q, "q", True)
     d = _home(q, "q", stream)
-    qi, ki = _heads(q, "q", (B, N, Hq, D), dt, d), _heads(k, "k", (B, N, Hk, D), dt, d)
+    qi, ki = _rows(q, "q"), _heads(k, "k", (B, N, Hk, D), dt, d)
     rotary, pos, fr = 0, None, None
     if freqs is not None:
         _vector(freqs, "freqs", torch.int64, (freqs.numel(),), d)
@@ -224,12 +230,12 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     if k_weight is not None:
         _vector(k_weight, "k_weight", dt, (D,), d)
     if q_out is None:
-        q_out = _new(torch.empty_like, stream, q)
+        q_out = torch.empty_like(q) if stream is None else _new(torch.empty_like, stream, q)
         qo = _own(q_out)
     else:
         qo = _heads(q_out, "q_out", (B, N, Hq, D), dt, d)
     if k_out is None:
-        k_out = _new(torch.empty_like, stream, k)
+        k_out = torch.empty_like(k) if stream is None else _new(torch.empty_like, stream, k)
         ko = _own(k_out)
     else:
         ko = _heads(k_out, "k_out", (B, N, Hk, D), dt, d)
@@ -293,14 +299,16 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     d = _home(q, "q", stream)
     P, H, D = _pool(pool, d)
     B, M = _table(table, d)
-    N, Hq = q.shape[1], q.shape[2]
+    Bq, N, Hq, Dq = q.shape
     code = _code(q, "q")
+    if Bq != B or Dq != D:
+        raise ValueError("q must have shape %s, got %s" % ((B, N, Hq, D), tuple(q.shape)))
     _ints(kv_len, "kv_len", (B,), d)
     if q_len is not None:
         _ints(q_len, "q_len", (B,), d)
-    qi = _heads(q, "q", (B, N, Hq, D), q.dtype, d)
+    qi = _rows(q, "q")
     if out is None:
-        out = _new(torch.empty_like, stream, q)
+        out = torch.empty_like(q) if stream is None else _new(torch.empty_like, stream, q)
         oi = _own(out)
     else:
         oi = _heads(out, "out", (B, N, Hq, D), q.dtype, d)
@@ -346,8 +354,8 @@ def pages_fork(table, lengths, refs, src, dst, *, workspace=None, stream=None):
     _ints(src, "src", (F,), d)
     _ints(dst, "dst", (F,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_fork(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(src), _ptr(dst), F, *_workspace(ws, d),
-                               _on(d, stream)))
+    _ok(_lib().spec_pages_fork(table.data_ptr(), _ptr(lengths), refs.data_ptr(), S, M, P, src.data_ptr(), dst.data_ptr(), F,
+                               *_workspace(ws, d), _on(d, stream)))
     return ws
 
 
@@ -362,8 +370,8 @@ def pages_reserve(pool, table, lengths, refs, n_new, *, served=None, workspace=N
     else:
         _ints(served, "served", (S,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_reserve(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(n_new),
-                                  _ptr(served), *_workspace(ws, d), _on(d, stream)))
+    _ok(_lib().spec_pages_reserve(pool.data_ptr(), layers, page_bytes, table.data_ptr(), _ptr(lengths), refs.data_ptr(), S, M, P,
+                                  n_new.data_ptr(), served.data_ptr(), *_workspace(ws, d), _on(d, stream)))
     return served
 
 
@@ -373,8 +381,8 @@ def pages_commit(table, lengths, refs, advance, *, extra=1, window=0, sinks=0, w
     S, M, P, d = _books(table, lengths, refs, stream)
     _ints(advance, "advance", (S,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_commit(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(advance), extra, window, sinks,
-                                 *_workspace(ws, d), _on(d, stream)))
+    _ok(_lib().spec_pages_commit(table.data_ptr(), _ptr(lengths), refs.data_ptr(), S, M, P, advance.data_ptr(), extra, window,
+                                 sinks, *_workspace(ws, d), _on(d, stream)))
     return ws
 
 
@@ -384,8 +392,8 @@ def pages_release(table, lengths, refs, slots, *, workspace=None, stream=None):
     F = slots.numel()
     _ints(slots, "slots", (F,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_release(_ptr(table), _ptr(lengths), _ptr(refs), S, M, P, _ptr(slots), F, *_workspace(ws, d),
-                                  _on(d, stream)))
+    _ok(_lib().spec_pages_release(table.data_ptr(), _ptr(lengths), refs.data_ptr(), S, M, P, slots.data_ptr(), F,
+                                  *_workspace(ws, d), _on(d, stream)))
     return ws
 
 
@@ -399,6 +407,6 @@ def pages_compact(pool, table, refs, *, used=None, workspace=None, stream=None):
     else:
         _ints(used, "used", (1,), d)
     ws = _pages_ws(workspace, S, P, table.device, stream)
-    _ok(_lib().spec_pages_compact(_ptr(pool), layers, page_bytes, _ptr(table), _ptr(refs), S, M, P, _ptr(used), *_workspace(ws, d),
-                                  _on(d, stream)))
+    _ok(_lib().spec_pages_compact(pool.data_ptr(), layers, page_bytes, table.data_ptr(), refs.data_ptr(), S, M, P, used.data_ptr(),
+                                  *_workspace(ws, d), _on(d, stream)))
     return used
