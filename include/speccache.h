@@ -40,7 +40,7 @@
  *
  * Activations are bf16, fp16 or, for the norm and rotation, fp32 (dtype: SPEC_BF16, SPEC_FP16, SPEC_FP32), as
  * [B, N, heads, D] with any strides over B, N and heads and contiguous channels; pointers and strides (of more than
- * one entry) are multiples of 16 bytes. D is 64 or 128 (the norm and rotation also 256).
+ * one entry) are multiples of 16 bytes; an output's rows must not overlap. D is 64 or 128 (the norm and rotation also 256).
  */
 #ifndef SPECCACHE_H
 #define SPECCACHE_H

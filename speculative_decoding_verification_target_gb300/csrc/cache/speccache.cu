@@ -43,6 +43,16 @@ spec_status check_heads(const spec_heads* t, const char* name, int dtype, int B,
     return SPEC_OK;
 }
 
+// An output: its rows must not share elements, as those of a stride below D do.
+spec_status check_out(const spec_heads* t, const char* name, int dtype, int B, int N, int heads, int D) {
+    const spec_status s = check_heads(t, name, dtype, B, N, heads);
+    if (s != SPEC_OK) return s;
+    auto apart = [&](int n, long long stride) { return n <= 1 || stride >= D || stride <= -D; };
+    if (!apart(B, t->stride_b) || !apart(N, t->stride_n) || !apart(heads, t->stride_h))
+        return fail(SPEC_ERR_INVALID, "%s: rows overlap: strides must be at least D = %d", name, D);
+    return SPEC_OK;
+}
+
 spec_status check_sizes(int B, int N, int heads, int max_n) {
     if (B < 0 || B > MAX_B) return fail(SPEC_ERR_INVALID, "B must be in [0, %d], got %d", MAX_B, B);
     if (N < 0 || N > max_n) return fail(SPEC_ERR_INVALID, "N must be in [0, %d], got %d", max_n, N);
@@ -271,11 +281,11 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
     if (B == 0 || N == 0) return SPEC_OK;
     if (Hq > 0) {
         SPECC_TRY(check_heads(q, "q", dtype, B, N, Hq));
-        SPECC_TRY(check_heads(q_out, "q_out", dtype, B, N, Hq));
+        SPECC_TRY(check_out(q_out, "q_out", dtype, B, N, Hq, D));
     }
     if (Hk > 0) {
         SPECC_TRY(check_heads(k, "k", dtype, B, N, Hk));
-        SPECC_TRY(check_heads(k_out, "k_out", dtype, B, N, Hk));
+        SPECC_TRY(check_out(k_out, "k_out", dtype, B, N, Hk, D));
     }
     if (rotary && (!positions || !freqs)) return fail(SPEC_ERR_INVALID, "positions and freqs must not be NULL");
     if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(SPEC_ERR_INVALID, "weights must be 16-byte aligned");
@@ -334,8 +344,8 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
     SPECC_TRY(check_tokens(pool, pages, table, max_pages, start, dtype, B, N, Hk, D, workspace, workspace_bytes));
     if (B == 0 || N == 0) return SPEC_OK;
     const bool has_k = k_out && k_out->data, has_v = v_out && v_out->data;
-    if (has_k) SPECC_TRY(check_heads(k_out, "k_out", dtype, B, N, Hk));
-    if (has_v) SPECC_TRY(check_heads(v_out, "v_out", dtype, B, N, Hk));
+    if (has_k) SPECC_TRY(check_out(k_out, "k_out", dtype, B, N, Hk, D));
+    if (has_v) SPECC_TRY(check_out(v_out, "v_out", dtype, B, N, Hk, D));
     if (!has_k && !has_v) return fail(SPEC_ERR_INVALID, "k_out and v_out must not both be NULL");
     const TokensParams p = tokens_params(pool, pages, table, max_pages, start, counts, has_k ? k_out : nullptr,
                                          has_v ? v_out : nullptr, B, N, Hk, workspace);
@@ -364,7 +374,7 @@ spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* poo
     if (window < 0 || sinks < 0) return fail(SPEC_ERR_INVALID, "window and sinks must not be negative");
     if (B == 0 || N == 0) return SPEC_OK;
     SPECC_TRY(check_heads(q, "q", dtype, B, N, Hq));
-    SPECC_TRY(check_heads(out, "out", dtype, B, N, Hq));
+    SPECC_TRY(check_out(out, "out", dtype, B, N, Hq, D));
     SPECC_TRY(check_table(pool, pages, table, max_pages));
     if (!kv_len) return fail(SPEC_ERR_INVALID, "kv_len must not be NULL");
     const AttSplit split = att_split(N * (Hq / Hk));

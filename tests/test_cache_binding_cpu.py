@@ -156,3 +156,16 @@ def test_an_attention_workspace_serves_fewer_tokens_too(G, H, D):
     _build.build()
     sizes = [cache._lib().spec_cache_attention_workspace_size(n, G * H, H, D) for n in range(1, 1025)]
     assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("kw", [dict(b=0), dict(n=0), dict(h=0), dict(b=64), dict(n=-64), dict(h=120)])
+def test_outputs_whose_rows_overlap_are_refused(kw):
+    """A stride below D = 128 over more than one entry: rows would overwrite one another. Inputs may repeat."""
+    import test_cache_cpu as ct
+    from speculative_decoding_verification_target_gb300 import _build, cache
+    _build.build()
+    lib = cache._lib()
+    bad = ct.H(**kw)
+    for call in (lambda: ct.norm(lib, qo=bad), lambda: ct.norm(lib, ko=bad), lambda: ct.tokens("spec_cache_read", lib, k=bad),
+                 lambda: ct.tokens("spec_cache_read", lib, v=bad), lambda: ct.attend(lib, out=bad)):
+        assert call() == 1 and b"rows overlap" in lib.spec_cache_last_error()
