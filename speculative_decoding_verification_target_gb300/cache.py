@@ -317,7 +317,7 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
     elif want_lse:
         lse = _new(torch.empty, stream, (B, N, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _new(new_attention_workspace, stream, N, Hq, H, D, q.device)
+        workspace = _new(new_attention_workspace, stream, max(N, 1), Hq, H, D, q.device)
     _ok(_lib().spec_cache_attention(qi, code, pool.data_ptr(), P, table.data_ptr(), M, kv_len.data_ptr(), _ptr(q_len), B, N,
                                     Hq, H, D, D ** -0.5 if scale is None else scale, window, sinks, oi, _ptr(lse),
                                     *_workspace(workspace, d), _on(d, stream)))

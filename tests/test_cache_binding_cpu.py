@@ -169,3 +169,17 @@ def test_outputs_whose_rows_overlap_are_refused(kw):
     for call in (lambda: ct.norm(lib, qo=bad), lambda: ct.norm(lib, ko=bad), lambda: ct.tokens("spec_cache_read", lib, k=bad),
                  lambda: ct.tokens("spec_cache_read", lib, v=bad), lambda: ct.attend(lib, out=bad)):
         assert call() == 1 and b"rows overlap" in lib.spec_cache_last_error()
+
+
+def test_attention_of_no_tokens_needs_no_workspace(fake):
+    """An empty call does nothing, whether a workspace is given or not."""
+    _, lib = fake
+    lib.spec_cache_attention_workspace_size = lambda N, *heads: (1 << 15) * (1 <= N <= 1024)
+    a = Args()
+    a.q = fc.Tensor((B, 0, HQ, D), BF16)
+    r = CALLS["cache_attention"](a)
+    assert r["out"].shape == (B, 0, HQ, D) and r["lse"].shape == (B, 0, HQ) and r["workspace"].numel() == 1 << 15
+    assert len(lib.calls) == 1
+    a.q = fc.Tensor((B, 1025, HQ, D), BF16)
+    with pytest.raises(ValueError, match="unsupported sizes N=1025"):
+        CALLS["cache_attention"](a)
