@@ -36,7 +36,8 @@
  * on the device is checked there: a bad page or length is never followed and ORs a bit into the status word, the
  * first word of the workspace (spec_read_status, spec_clear_status). A workspace's first SPEC_CACHE_WS_HEADER
  * bytes are zeroed once before its first use and kept by the calls; 16-byte aligned; calls that share one must
- * not overlap on the GPU. Empty calls (B, N or the number of pairs 0) do nothing.
+ * not overlap on the GPU. Empty calls (B, N, S or the number of pairs 0) do nothing, but for a compaction without
+ * sequences, which still moves the pages that are counted.
  *
  * Activations are bf16, fp16 or, for the norm and rotation, fp32 (dtype: SPEC_BF16, SPEC_FP16, SPEC_FP32), as
  * [B, N, heads, D] with any strides over B, N and heads and contiguous channels; pointers and strides (of more than
@@ -148,7 +149,8 @@ spec_status spec_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, 
                                const int32_t* slots, int F, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Moves the pages in use to the front of the pool: with n in use, the i-th used page at or past n goes to the
- * i-th free one below n, in every layer; table and refs follow. used: device int32 [1] or NULL, n. */
+ * i-th free one below n, in every layer; table and refs follow. used: device int32 [1] or NULL, n. Where a page went is
+ * in the table alone: a page that is to be found again needs an entry there. */
 spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int32_t* table, int32_t* refs, int S,
                                int max_pages, int pages, int32_t* used, void* workspace, size_t workspace_bytes,
                                void* stream);

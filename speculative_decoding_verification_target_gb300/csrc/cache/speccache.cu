@@ -207,11 +207,13 @@ spec_status attend(const AttnParams& p, const AttSplit& s, cudaStream_t st) {
 // ------------------------------------------------------------------------------------------------- pages
 size_t pages_scratch_ints(int S, int pages) { return 3 * static_cast<size_t>(S) + 3 * static_cast<size_t>(pages) + 16; }
 
+// EMPTY: a call on no sequences has something to do, on the counts alone.
+template <bool EMPTY = false>
 spec_status check_pages(const void* table, const void* refs, int S, int max_pages, int pages, void* ws, size_t ws_bytes,
                         size_t need) {
     if (S < 0 || S > (1 << 20)) return fail(SPEC_ERR_INVALID, "S must be in [0, %d], got %d", 1 << 20, S);
-    if (S == 0) return SPEC_OK;
-    if (!table || !refs) return fail(SPEC_ERR_INVALID, "table and refs must not be NULL");
+    if (S == 0 && !EMPTY) return SPEC_OK;
+    if ((S > 0 && !table) || !refs) return fail(SPEC_ERR_INVALID, "table and refs must not be NULL");
     if (pages < 1 || max_pages < 1) return fail(SPEC_ERR_INVALID, "pages and max_pages must be at least 1");
     if (static_cast<long long>(max_pages) * PAGE > 2147483647LL)
         return fail(SPEC_ERR_INVALID, "max_pages is limited to %d", 2147483647 / PAGE);
@@ -480,8 +482,7 @@ spec_status spec_pages_release(int32_t* table, int32_t* lengths, int32_t* refs, 
 spec_status spec_pages_compact(void* pool, int layers, long long page_bytes, int32_t* table, int32_t* refs, int S,
                                int max_pages, int pages, int32_t* used, void* workspace, size_t workspace_bytes,
                                void* stream) {
-    SPECC_TRY(check_pages(table, refs, S, max_pages, pages, workspace, workspace_bytes, spec_pages_workspace_size(S, pages)));
-    if (S == 0) return SPEC_OK;
+    SPECC_TRY(check_pages<true>(table, refs, S, max_pages, pages, workspace, workspace_bytes, spec_pages_workspace_size(S, pages)));
     SPECC_TRY(check_pool(pool, layers, page_bytes));
     const int sms = sm_count();
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");

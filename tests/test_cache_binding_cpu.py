@@ -183,3 +183,16 @@ def test_attention_of_no_tokens_needs_no_workspace(fake):
     a.q = fc.Tensor((B, 1025, HQ, D), BF16)
     with pytest.raises(ValueError, match="unsupported sizes N=1025"):
         CALLS["cache_attention"](a)
+
+
+def test_compaction_without_sequences_is_no_empty_call():
+    """The pages counted are still to be moved and counted, so the pool is looked at; the other page calls have nothing to do."""
+    from speculative_decoding_verification_target_gb300 import _build, cache
+    _build.build()
+    lib, p = cache._lib(), ctypes.c_void_p(1 << 20)
+    assert lib.spec_pages_compact(None, 1, 32, None, p, 0, 4, 8, p, p, 1 << 20, None) == 1
+    assert b"pool" in lib.spec_cache_last_error()
+    assert lib.spec_pages_compact(p, 1, 32, None, None, 0, 4, 8, p, p, 1 << 20, None) == 1
+    assert lib.spec_pages_compact(p, 1, 32, None, p, 0, 4, 8, p, p, 8192, None) == 1
+    assert lib.spec_pages_reserve(None, 1, 32, None, None, None, 0, 4, 8, None, None, p, 1 << 20, None) == 0
+    assert lib.spec_pages_commit(None, None, None, 0, 4, 8, None, 1, 0, 0, None, 0, None) == 0

@@ -151,3 +151,14 @@ def test_small_probabilities_of_sequences_that_are_not_cut(gap, D):
     delta = 2.0 ** -17 * float((k.abs() @ q[0, 0, 0].double().abs()).max()) * D ** -0.5
     tol = (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -13 + 2 * delta) * ref + 2.0 ** -32 * n + 2.0 ** -25      # fp16 outputs: half a step, 2^-25 at least
     assert ((out.double() - ref).abs() <= tol).all(), float(((out.double() - ref).abs() / tol).max())
+
+
+@pytest.mark.parametrize("P", [1, 7, 9000])
+def test_compaction_without_sequences(P):
+    rng = np.random.default_rng(P)
+    refs, pool = rng.integers(0, 2, P).astype(np.int32), rng.integers(0, 256, (2, P, 1, 32)).astype(np.uint8)
+    table = np.zeros((0, 3), np.int32)
+    gp, gr = torch.from_numpy(pool.copy()).cuda(), torch.from_numpy(refs.copy()).cuda()
+    used = sv.pages_compact(gp, torch.from_numpy(table).cuda(), gr)
+    assert int(used) == cu.compact(pool, table, refs)
+    assert np.array_equal(gp.cpu().numpy(), pool) and np.array_equal(gr.cpu().numpy(), refs)
