@@ -162,3 +162,32 @@ def test_compaction_without_sequences(P):
     used = sv.pages_compact(gp, torch.from_numpy(table).cuda(), gr)
     assert int(used) == cu.compact(pool, table, refs)
     assert np.array_equal(gp.cpu().numpy(), pool) and np.array_equal(gr.cpu().numpy(), refs)
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+@pytest.mark.parametrize("page_bytes", [32, 4096, 16384, 16400, 69632])
+def test_page_copies_of_every_size(page_bytes, layers):
+    """A copy's pieces are 16384 bytes: pages of less, of one, of one and a little, of 4.25 (8 heads of 128), byte for byte."""
+    rng = np.random.default_rng(page_bytes + layers)
+    S, M, P = 9, 4, 40
+    pool = rng.integers(0, 256, (layers, P, 1, page_bytes)).astype(np.uint8)
+    table, refs, lengths = np.full((S, M), -1, np.int32), np.zeros(P, np.int32), np.zeros(S, np.int32)
+    order = rng.permutation(P)
+    for s in range(4):
+        lengths[s] = [100, 63, 1, 129][s]
+        n = (lengths[s] + 63) // 64
+        table[s, :n], order = order[:n], order[n:]
+        refs[table[s, :n]] = 1
+    g = [torch.from_numpy(a.copy()).cuda() for a in (pool, table, lengths, refs)]
+    src, dst = np.array([0, 0, 1, 2, 3], np.int32), np.array([4, 5, 6, 7, 8], np.int32)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()  # noqa: E731
+    cu.fork(table, lengths, refs, src, dst)
+    sv.pages_fork(*g[1:], i32(src), i32(dst))
+    n_new = np.full(S, 3, np.int32)
+    served, _ = cu.reserve(pool, table, lengths, refs, n_new)      # every sequence's last page is shared: nine copies
+    assert served.all() and np.array_equal(sv.pages_reserve(*g, i32(n_new)).cpu().numpy(), served)
+    for t, a in zip(g, (pool, table, lengths, refs)):
+        assert np.array_equal(t.cpu().numpy(), a)
+    assert int(sv.pages_compact(g[0], g[1], g[3])) == cu.compact(pool, table, refs)
+    for t, a in zip(g, (pool, table, lengths, refs)):
+        assert np.array_equal(t.cpu().numpy(), a)
