@@ -136,6 +136,17 @@ def _own(t):
     return Heads(t.data_ptr(), sb, sn, sh)
 
 
+def _like(t, stream):
+    """An output in t's order of dimensions, and its rows. Contiguous where t repeats rows in a way that would leave the order
+    to a stride of 1 beside the channels'."""
+    o = torch.empty_like(t) if stream is None else _new(torch.empty_like, stream, t)
+    sb, sn, sh, sd = o.stride()
+    if sd != 1:
+        o = _new(torch.empty_like, stream, t, memory_format=torch.contiguous_format)
+        sb, sn, sh, sd = o.stride()
+    return o, Heads(o.data_ptr(), sb, sn, sh)
+
+
 def _vector(t, name, dtype, shape, d):
     if not (t.get_device() == d and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, shape)
@@ -230,13 +241,11 @@ def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e
     if k_weight is not None:
         _vector(k_weight, "k_weight", dt, (D,), d)
     if q_out is None:
-        q_out = torch.empty_like(q) if stream is None else _new(torch.empty_like, stream, q)
-        qo = _own(q_out)
+        q_out, qo = _like(q, stream)
     else:
         qo = _heads(q_out, "q_out", (B, N, Hq, D), dt, d)
     if k_out is None:
-        k_out = torch.empty_like(k) if stream is None else _new(torch.empty_like, stream, k)
-        ko = _own(k_out)
+        k_out, ko = _like(k, stream)
     else:
         ko = _heads(k_out, "k_out", (B, N, Hk, D), dt, d)
     _ok(_lib().spec_qk_norm_rope(qi, ki, code, B, N, Hq, Hk, D, pos, fr, rotary, interleaved, _ptr(q_weight),
@@ -308,8 +317,7 @@ def cache_attention(q, pool, table, kv_len, *, q_len=None, scale=None, window=0,
         _ints(q_len, "q_len", (B,), d)
     qi = _rows(q, "q")
     if out is None:
-        out = torch.empty_like(q) if stream is None else _new(torch.empty_like, stream, q)
-        oi = _own(out)
+        out, oi = _like(q, stream)
     else:
         oi = _heads(out, "out", (B, N, Hq, D), q.dtype, d)
     if lse is not None:

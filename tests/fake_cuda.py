@@ -100,8 +100,8 @@ class Torch:
     def full(self, shape, value, dtype=None, device=None):
         return self._make(shape, dtype, device, clear=True)
 
-    def empty_like(self, t):
-        real = torch.empty_like(torch.empty_strided(t.shape, t.strides, dtype=t.dtype))
+    def empty_like(self, t, memory_format=torch.preserve_format):
+        real = torch.empty_like(torch.empty_strided(t.shape, t.strides, dtype=t.dtype), memory_format=memory_format)
         return self._make(t.shape, t.dtype, t.device, real.stride())
 
 

@@ -196,3 +196,18 @@ def test_compaction_without_sequences_is_no_empty_call():
     assert lib.spec_pages_compact(p, 1, 32, None, p, 0, 4, 8, p, p, 8192, None) == 1
     assert lib.spec_pages_reserve(None, 1, 32, None, None, None, 0, 4, 8, None, None, p, 1 << 20, None) == 0
     assert lib.spec_pages_commit(None, None, None, 0, 4, 8, None, 1, 0, 0, None, 0, None) == 0
+
+
+@pytest.mark.parametrize("shape,strides", [
+    ((1, 2, 1, 64), (1, 0, 0)), ((2, 1, 3, 64), (64, 1, 0)), ((1, 3, 2, 64), (1, 128, 0)), ((2, 3, 4, 64), (0, 0, 0)),
+    ((1, 1, 2, 64), (128, 1, 0)), ((2, 3, 4, 64), (768, 0, 64)),
+])
+def test_outputs_of_broadcast_inputs_have_contiguous_channels(fake, shape, strides):
+    """Outputs follow the inputs' order of dimensions; where an input repeats rows and that order says nothing, they are contiguous."""
+    _, lib = fake
+    x = fc.Tensor(shape, BF16, strides=strides + (1,))
+    pos, freqs = fc.Tensor(shape[:2], I32), fc.Tensor((32,), torch.int64)
+    r = sv.qk_norm_rope(x, x, pos, freqs)
+    a = sv.cache_attention(x, fc.Tensor((P, 1, 68 * 64), U8), fc.Tensor((shape[0], M), I32), fc.Tensor((shape[0],), I32))
+    for t in (r["q"], r["k"], a["out"]):
+        assert t.strides[3] == 1 and all(n == 1 or s >= 64 for n, s in zip(shape[:3], t.strides))

@@ -191,3 +191,18 @@ def test_page_copies_of_every_size(page_bytes, layers):
     assert int(sv.pages_compact(g[0], g[1], g[3])) == cu.compact(pool, table, refs)
     for t, a in zip(g, (pool, table, lengths, refs)):
         assert np.array_equal(t.cpu().numpy(), a)
+
+
+def test_norm_and_attention_of_inputs_that_repeat_rows():
+    """One row for every head (stride 0), also with a single sequence whose stride says nothing."""
+    g = torch.Generator().manual_seed(4)
+    row = torch.randn((3, 64), generator=g).bfloat16().cuda()
+    q = row.as_strided((1, 3, 2, 64), (1, 64, 0, 1))
+    pos, freqs = torch.arange(3, **I32)[None], sv.rope_frequencies(64)
+    got, want = sv.qk_norm_rope(q, q, pos, freqs), sv.qk_norm_rope(q.contiguous(), q.contiguous(), pos, freqs)
+    assert torch.equal(got["q"], want["q"]) and torch.equal(got["k"], want["k"])
+    pool, table = sv.new_pool(2, 1, 64), torch.arange(2, **I32)[None]
+    kv = torch.randn((1, 90, 1, 64), generator=g).bfloat16().cuda()
+    sv.cache_append(pool, table, torch.zeros(1, **I32), kv, kv)
+    lens = torch.tensor([90], **I32)
+    assert torch.equal(sv.cache_attention(q, pool, table, lens)["out"], sv.cache_attention(q.contiguous(), pool, table, lens)["out"])
