@@ -26,7 +26,9 @@ constexpr int NORM_WARPS = 4;
 // are. 16384 tokens of 32 + 8 heads of 128 in bf16 take 58 us, 5.8 TB/s, 86% of the copy rate (70 us without the loads ahead,
 // 86 us with a head's eight channels side by side in a lane and shuffles for the rotation). Few tokens are split into parts;
 // there latency counts: 384 tokens 6.9 us.
-template <class T, int D, bool INTER>
+// WHOLE: every channel is rotated. Where some are not, their Q is 0, which an infinite mate would turn into a NaN: such rows
+// are looked for. (With that in the one kernel for both, the 16384 tokens take 57.0 us where they take 56.4.)
+template <class T, int D, bool INTER, bool WHOLE>
 __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_rope_kernel(const __grid_constant__ NormParams p) {
     constexpr int LPH = D / 8, RPW = 32 / LPH;   // lanes per head, heads per warp at a time
     constexpr int U = 4;                         // heads per lane in flight
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_
     const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
     const int c = lane % LPH, sub = lane / LPH;
     float2* const cs = s_cs[warp];
-    const bool rot = 8 * c < p.rotary;
+    const bool rot = WHOLE || 8 * c < p.rotary;
     const int oa = rot && !INTER ? 4 * c : 8 * c, ob = rot && !INTER ? p.rotary / 2 + 4 * c : 8 * c + 4;
     // The part's heads are part RPW + sub + m step, query and key heads in one count; queries first, then keys. A step's
     // heads can straddle the two: a group begins with the step that holds its first head.
@@ -126,6 +128,10 @@ __global__ void __launch_bounds__(NORM_WARPS * 32, sizeof(T) == 2 ? 5 : 4) norm_
                 float s = sp.x + sp.y;
 #pragma unroll
                 for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (!WHOLE && s == INFINITY && !rot) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m[i] = 0ull;
+                }
                 const float r = rsqrtf(fmaf(s, 1.f / D, p.eps));
                 const unsigned long long r2 = pack2(r, r);
 #pragma unroll

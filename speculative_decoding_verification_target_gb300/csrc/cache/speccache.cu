@@ -115,6 +115,19 @@ cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int thread
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
+// ------------------------------------------------------------------------------------- norm and rotation
+template <class T>
+auto norm_rope_as(int head, bool interleaved, bool whole) -> void (*)(const NormParams) {
+    static constexpr void (*fns[3][2][2])(const NormParams) = {
+        {{norm_rope_kernel<T, 64, false, false>, norm_rope_kernel<T, 64, false, true>},
+         {norm_rope_kernel<T, 64, true, false>, norm_rope_kernel<T, 64, true, true>}},
+        {{norm_rope_kernel<T, 128, false, false>, norm_rope_kernel<T, 128, false, true>},
+         {norm_rope_kernel<T, 128, true, false>, norm_rope_kernel<T, 128, true, true>}},
+        {{norm_rope_kernel<T, 256, false, false>, norm_rope_kernel<T, 256, false, true>},
+         {norm_rope_kernel<T, 256, true, false>, norm_rope_kernel<T, 256, true, true>}}};
+    return fns[head][interleaved ? 1 : 0][whole ? 1 : 0];
+}
+
 // ------------------------------------------------------------------------------------------------ tokens
 spec_status check_tokens(const void* pool, int pages, const int32_t* table, int max_pages, const int32_t* start, int dtype,
                          int B, int N, int Hk, int D, void* ws, size_t ws_bytes) {
@@ -311,18 +324,11 @@ spec_status spec_qk_norm_rope(const spec_heads* q, const spec_heads* k, int dtyp
     p.parts = static_cast<int>(std::max<long long>(1, std::min<long long>((Hq + Hk + rpw - 1) / rpw, 32LL * sms / p.tokens)));
     const long long units = p.tokens * p.parts, ctas = (units + NORM_WARPS - 1) / NORM_WARPS;
     if (ctas > 2147483647LL) return fail(SPEC_ERR_INVALID, "too many tokens: B N is limited to 2^31");
-    using Fn = void (*)(const NormParams);
-    static const Fn fns[3][3][2] = {
-        {{norm_rope_kernel<__nv_bfloat16, 64, false>, norm_rope_kernel<__nv_bfloat16, 64, true>},
-         {norm_rope_kernel<__nv_bfloat16, 128, false>, norm_rope_kernel<__nv_bfloat16, 128, true>},
-         {norm_rope_kernel<__nv_bfloat16, 256, false>, norm_rope_kernel<__nv_bfloat16, 256, true>}},
-        {{norm_rope_kernel<float, 64, false>, norm_rope_kernel<float, 64, true>},
-         {norm_rope_kernel<float, 128, false>, norm_rope_kernel<float, 128, true>},
-         {norm_rope_kernel<float, 256, false>, norm_rope_kernel<float, 256, true>}},
-        {{norm_rope_kernel<__half, 64, false>, norm_rope_kernel<__half, 64, true>},
-         {norm_rope_kernel<__half, 128, false>, norm_rope_kernel<__half, 128, true>},
-         {norm_rope_kernel<__half, 256, false>, norm_rope_kernel<__half, 256, true>}}};
-    const Fn fn = fns[dtype][D == 64 ? 0 : D == 128 ? 1 : 2][interleaved ? 1 : 0];
+    const int head = D == 64 ? 0 : D == 128 ? 1 : 2;
+    const bool whole = rotary == D;
+    void (*const fn)(const NormParams) = dtype == SPEC_BF16   ? norm_rope_as<__nv_bfloat16>(head, interleaved, whole)
+                                         : dtype == SPEC_FP16 ? norm_rope_as<__half>(head, interleaved, whole)
+                                                              : norm_rope_as<float>(head, interleaved, whole);
     return launched("norm and rotation", launch_behind(fn, p, dim3(static_cast<unsigned>(ctas)), NORM_WARPS * 32, static_cast<cudaStream_t>(stream)));
 }
 

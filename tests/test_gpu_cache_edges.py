@@ -206,3 +206,23 @@ def test_norm_and_attention_of_inputs_that_repeat_rows():
     sv.cache_append(pool, table, torch.zeros(1, **I32), kv, kv)
     lens = torch.tensor([90], **I32)
     assert torch.equal(sv.cache_attention(q, pool, table, lens)["out"], sv.cache_attention(q.contiguous(), pool, table, lens)["out"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("D,R", [(64, 32), (128, 64), (128, 128), (256, 16), (64, 0)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_norm_of_infinite_channels(dtype, D, R, inter):
+    """A row with an infinity has an infinite norm: its finite channels are 0, the infinite one is NaN, and so is what a rotation mixes it
+    with, but no other channel."""
+    H = D + 1
+    x = (torch.rand((1, 1, H, D), generator=torch.Generator().manual_seed(D)) + 0.5).to(dtype)
+    for h in range(D):
+        x[0, 0, h, h] = float("inf") if h % 2 else float("-inf")                  # the last head has none
+    freqs = sv.rope_frequencies(R) if R else None
+    q = sv.qk_norm_rope(x.cuda(), x[:, :, :1].cuda(), torch.full((1, 1), 5, **I32), freqs, interleaved=inter)["q"].cpu()[0, 0]
+    for h in range(D):
+        mate = h if h >= R else h ^ 1 if inter else (h + R // 2) % R
+        want = torch.zeros(D, dtype=dtype)
+        want[[h, mate]] = float("nan")
+        assert torch.equal(q[h].isnan(), want.isnan()) and (q[h][~want.isnan()] == 0).all(), h
+    assert torch.isfinite(q[D]).all() and (q[D] != 0).all()
