@@ -58,7 +58,8 @@ enum { SPEC_FP16 = 2 };   /* a further value of spec_dtype's int, for the calls 
 #define SPEC_CACHE_GROUP 32         /* channels that share a scale */
 #define SPEC_CACHE_WS_HEADER 8192   /* bytes of a workspace that are zeroed before its first use */
 
-/* Bits of the status word, beside specverify.h's. */
+/* Bits of the status word, beside specverify.h's. Of those, spec_cache_attention sets SPEC_STATUS_TIMEOUT: a wait within the
+ * kernel gave up after two seconds, and the outputs are invalid. */
 #define SPEC_STATUS_BAD_PAGE 4u     /* a page that was needed is missing or outside the pool */
 #define SPEC_STATUS_BAD_LENGTH 8u   /* a length outside the table, or a count outside [0, N] */
 #define SPEC_STATUS_NO_PAGES 16u    /* a reservation found too few free pages */

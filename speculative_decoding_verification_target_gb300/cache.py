@@ -16,7 +16,8 @@ and beside it pages_fork (a sequence that shares another's pages), pages_release
 
 Every tensor of a call is on the current device. A call runs on `stream`, or on the current one. Outputs and workspaces that
 are not given are made on that stream; what is given has to be ready on it. The status word is in the workspace
-(read_status): a caller that looks at it passes the workspace.
+(read_status, the STATUS_ bits): a caller that looks at it passes the workspace. No call records gradients: outputs are
+detached, also from inputs that require them.
 """
 from __future__ import annotations
 

@@ -211,3 +211,13 @@ def test_outputs_of_broadcast_inputs_have_contiguous_channels(fake, shape, strid
     a = sv.cache_attention(x, fc.Tensor((P, 1, 68 * 64), U8), fc.Tensor((shape[0], M), I32), fc.Tensor((shape[0],), I32))
     for t in (r["q"], r["k"], a["out"]):
         assert t.strides[3] == 1 and all(n == 1 or s >= 64 for n, s in zip(shape[:3], t.strides))
+
+
+def test_status_bits_are_the_headers_and_exported():
+    import os
+    import re
+    text = "".join(open(os.path.join(os.path.dirname(sv.__file__), os.pardir, "include", f)).read() for f in ("specverify.h", "speccache.h"))
+    bits = dict(re.findall(r"#define SPEC_(STATUS_\w+) (\d+)u?", text))
+    assert {"STATUS_BAD_TOKEN", "STATUS_TIMEOUT", "STATUS_BAD_PAGE", "STATUS_BAD_LENGTH", "STATUS_NO_PAGES", "STATUS_BAD_SLOT"} <= set(bits)
+    for name, value in bits.items():
+        assert getattr(sv, name) == int(value), name
