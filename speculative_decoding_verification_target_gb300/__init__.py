@@ -386,6 +386,6 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
 
 
 # the scoring step's operators (include/speccache.h); imported last, since the module uses the helpers above
-from .cache import (PAGE as CACHE_PAGE, STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_BAD_SLOT, STATUS_NO_PAGES, cache_append, cache_attention, cache_read, new_attention_workspace,  # noqa: E402
-                    new_pages_workspace, new_pool, pages_commit, pages_compact, pages_fork, pages_release,
-                    pages_reserve, qk_norm_rope, rope_frequencies)
+from .cache import (PAGE as CACHE_PAGE, STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_BAD_SLOT, STATUS_NO_PAGES,  # noqa: E402
+                    cache_append, cache_attention, cache_read, new_attention_workspace, new_pages_workspace, new_pool,
+                    pages_commit, pages_compact, pages_fork, pages_release, pages_reserve, qk_norm_rope, rope_frequencies)

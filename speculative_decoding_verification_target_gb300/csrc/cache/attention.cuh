@@ -27,17 +27,19 @@
 //     eleven bits, and what is lost of one below that is 2^-32 of the largest at most. (With the reference at the maximum it
 //     was 2^-25: beside a first token that takes nearly all the weight, 10^5 others with 2^-25 of it each came to nothing.)
 // A tile is 128 tokens, two pages, fetched as one bulk copy each, STAGES tiles ahead, by a warp that also issues the products:
-// with that in the computing warps, everyone waited for the one that did it. CTAs are small (four computing warps, four CTAs to
-// an SM, as many as the tensor memory has columns for; eight warps and two CTAs for over 32 queries) and hide each other's
-// waits.
+// with that in the computing warps, everyone waited for the one that did it. CTAs are small (four computing warps and four CTAs
+// to an SM, as many as the tensor memory has columns for; three CTAs for 25 to 32 queries, whose registers leave room for no
+// more; eight warps and two CTAs for over 32) and hide a part of each other's waits.
 // Work is split evenly whatever the lengths: the tiles of all (sequence, key head, query block) units form one line, with
 // ATT_UNIT places more for each unit's beginning and end, of which each CTA takes an equal run (places of 0, 1, 2, 3 and 4
 // tiles: 75, 64, 65, 66 and 67 us on 48 sequences of 130 to 8191 tokens, 74, 66, 63, 62 and 63 us on 96 windows). A unit that is
 // cut leaves partial (O, m, l) in the workspace, and a second kernel joins them in a fixed order.
 // Measured, 8 key heads of 128: 48 sequences, one query row of four heads each, 219 MB of cache: 61 us, 3.6 TB/s; 64 sequences,
-// 24 rows, 627 MB: 180 us, 3.5 TB/s, half of the copy rate. What bounds it: 3900 (24 rows) warp instructions a tile where
-// HBM delivers one in 765 cycles, issued at 64% of the slots by four warps a scheduler; integer pipe 49%, shared memory
-// 48%, tensor pipe 16%, DRAM 39%.
+// 24 rows, 627 MB: 180 us, 3.5 TB/s, half of the copy rate. What bounds it: waits within a tile. No unit is full (issue 64% of
+// the slots, integer pipe 49%, shared memory 48%, tensor pipe 16%, DRAM 39%): a tile is one chain of codes, product, softmax and
+// product in which a CTA's computing warps meet three times, and four warps a scheduler do not cover it (per issued
+// instruction fixed latencies 1.25 cycles, barriers 1.11). The 3900 (24 rows) instructions of a tile alone would take
+// 975 cycles of four full schedulers, where HBM delivers one in 765; the 3240 of single tokens 810.
 #pragma once
 #include "cache_format.cuh"
 #include "tmem.cuh"

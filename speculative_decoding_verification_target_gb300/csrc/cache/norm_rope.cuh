@@ -23,9 +23,9 @@ constexpr int NORM_WARPS = 4;
 // precision and no table is read. A lane's channels are the same in every head: y_i = r (x_i P_i + x_mate Q_i), where P
 // and Q hold the weights and the cosines and sines, once for the query heads and once for the key heads.
 // Bandwidth bounds many tokens: U heads a lane are on their way while U are worked on, the first of them before the angles
-// are. 16384 tokens of 32 + 8 heads of 128 in bf16 take 58 us, 5.8 TB/s, 86% of the copy rate (70 us without the loads ahead,
-// 86 us with a head's eight channels side by side in a lane and shuffles for the rotation). Few tokens are split into parts;
-// there latency counts: 384 tokens 6.9 us.
+// are. 16384 tokens of 32 + 8 heads of 128 in bf16 take 56.4 us, 5.9 TB/s, 89% of the copy rate (70 us
+// without the loads ahead, 86 us with a head's eight channels side by side in a lane and shuffles for the rotation); in fp32
+// 100.5 us, the copy rate. Few tokens are split into parts; there latency counts: 384 tokens 5.8 us.
 // WHOLE: every channel is rotated. Where some are not, their Q is 0, which an infinite mate would turn into a NaN: such rows
 // are looked for. (With that in the one kernel for both, the 16384 tokens take 57.0 us where they take 56.4.)
 template <class T, int D, bool INTER, bool WHOLE>

@@ -161,7 +161,10 @@ TokensParams tokens_params(const void* pool, int pages, const int32_t* table, in
 // --------------------------------------------------------------------------------------------- attention
 // The queries that read a key head, in equal blocks of at most 64 rows, each in the narrowest kernel that holds it: a block
 // costs the conversion of its tiles once, so one wide block is cheaper than two narrow ones (four sequences of 100001 to 131072
-// tokens, 8 key heads of 128: 64 rows 288 us as one block, 321 us as two of 32; 48 rows 228 and 288 us as two of 24).
+// tokens, 8 key heads of 128: 64 rows 266 us as one block, 304 us as two of 32; 48 rows 203 and 284 us as two of 24; 40 rows 203
+// and 284 us). The kernel of 49 to 64 rows spills, 232 bytes of stores and 268 of loads at heads of 128: nine warps leave a thread
+// 96 registers. 80 rows in one block, as two warpgroups of 40 columns, spilled 660 bytes under that limit and were as slow as two
+// blocks (438 and 433 us at the time), which says nothing of one pass with registers to hold it.
 struct AttSplit {
     int blocks, rows, wg, nw;
 };
@@ -254,7 +257,11 @@ PagesParams pages_params(int32_t* table, int32_t* lengths, int32_t* refs, int S,
 }
 
 // The bookkeeping kernels run as one cluster: two CTAs up to 8192 pages, where barriers cost more than the walk over the
-// counts (reserving over 8192: 15.5 us with two or four CTAs, 17.6 with eight), else eight (over 65536: 59.5, 28.6 and 20.5 us).
+// counts, else eight. A reservation for 64 sequences that need no page, and a compaction without moves, in us:
+//   pages          512          4096         8192         12288        16384        32768        65536        262144
+//   two CTAs       8.2   6.8    8.8   6.9    8.7   8.2    9.4   9.4    11.1  11.8   19.7  22.8   52.9  64.6   194   231
+//   four           8.5   6.9    9.1   6.9    8.7   7.6    9.3   7.7    9.9   8.1    13.6  12.4   24.3  23.2   122   120
+//   eight          9.8   7.6    10.3  7.6    9.7   8.0    10.3  7.8    10.6  7.7    11.2  9.0    14.9  13.1   67    66
 cudaError_t launch_cluster(void (*fn)(const PagesParams), const PagesParams& p, int ctas, cudaStream_t st) {
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
