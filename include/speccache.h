@@ -108,8 +108,9 @@ spec_status spec_cache_read(const void* pool, int pages, const int32_t* table, i
  * the sum of exponentials (device float [B, N, Hq] or NULL). kv_len, q_len: device int32 [B]. Pages that no query
  * sees may be -1. A visible page that is missing counts as unseen (SPEC_STATUS_BAD_PAGE). Queries and outputs
  * are bf16 or fp16; Hq is a multiple of Hk; window >= 0 (0: all), sinks >= 0; N at most 1024. Scores, softmax and
- * sums in fp32; probabilities are rounded to fp16 for the product with the values. The workspace size for N serves every
- * call with up to N new tokens a sequence and the same heads. */
+ * sums in fp32; probabilities are rounded to fp16 for the product with the values, those down to 2^-21 of the largest to
+ * its eleven bits and smaller ones by 2^-32 of the largest at most. The workspace size for N serves every call with up
+ * to N new tokens a sequence and the same heads. */
 size_t spec_cache_attention_workspace_size(int N, int Hq, int Hk, int D);
 spec_status spec_cache_attention(const spec_heads* q, int dtype, const void* pool, int pages, const int32_t* table,
                                  int max_pages, const int32_t* kv_len, const int32_t* q_len, int B, int N, int Hq,
