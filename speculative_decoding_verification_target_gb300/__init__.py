@@ -12,7 +12,8 @@ Every tensor of a call is on the current device. A call runs on `stream`, or on 
 that stream, what is given has to be ready on it.
 
 The operators of the scoring step around a verification (head norms and rotation, a paged cache in 4 bits, attention
-over it, its pages) are in cache.py and exported here too.
+over it, its pages) are in cache.py, those between its last layer and the verification (residual and norm, products in 8 bits,
+penalties and masks on the logits) in scoring.py; both are exported here too.
 """
 from __future__ import annotations
 
@@ -389,3 +390,4 @@ def counterfactual_gamma(target, drafters, temperature=1.0, selected=-1, tokens=
 from .cache import (PAGE as CACHE_PAGE, STATUS_BAD_LENGTH, STATUS_BAD_PAGE, STATUS_BAD_SLOT, STATUS_NO_PAGES,  # noqa: E402
                     cache_append, cache_attention, cache_read, new_attention_workspace, new_pages_workspace, new_pool,
                     pages_commit, pages_compact, pages_fork, pages_release, pages_reserve, qk_norm_rope, rope_frequencies)
+from .scoring import int8_matmul, new_matmul_workspace, process_logits, quantize_rows, residual_norm  # noqa: E402

@@ -9,10 +9,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
-CACHE = os.path.join(CSRC, "cache")
-SOURCES = [os.path.join(CSRC, "specverify.cu"), os.path.join(CACHE, "speccache.cu")]
-DEPS = SOURCES + [os.path.join(d, f) for d in (CSRC, CACHE) for f in os.listdir(d) if f.endswith((".cuh", ".h"))] + [
-    os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "speccache.h")]
+CACHE, SCORE = os.path.join(CSRC, "cache"), os.path.join(CSRC, "score")
+SOURCES = [os.path.join(CSRC, "specverify.cu"), os.path.join(CACHE, "speccache.cu"), os.path.join(SCORE, "specscore.cu")]
+DEPS = SOURCES + [os.path.join(d, f) for d in (CSRC, CACHE, SCORE) for f in os.listdir(d) if f.endswith((".cuh", ".h"))] + [
+    os.path.join(INCLUDE, f) for f in ("specverify.h", "speccache.h", "specscore.h")]
 
 
 def nvcc_path() -> str:

@@ -1,0 +1,269 @@
+// Host side of the C ABI declared in include/specscore.h: argument checks and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "specscore.h"
+#include "logits.cuh"
+#include "matmul.cuh"
+#include "norm.cuh"
+
+namespace specs {
+namespace {
+
+thread_local char g_err[512] = "";
+
+spec_status fail(spec_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+spec_status launched(const char* what, cudaError_t e) {
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
+}
+
+#define SPECS_TRY(expr)                        \
+    do {                                       \
+        const spec_status try_s = (expr);      \
+        if (try_s != SPEC_OK) return try_s;    \
+    } while (0)
+
+constexpr int MAX_B = 65535, MAX_N = 1 << 20, MAX_V = 262144, MAX_C = 1 << 20;
+constexpr long long MAX_TOKENS = 1 << 22;      // B N
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+spec_status check_tokens(int B, int N) {
+    if (B < 0 || B > MAX_B) return fail(SPEC_ERR_INVALID, "B must be in [0, %d], got %d", MAX_B, B);
+    if (N < 0 || N > MAX_N) return fail(SPEC_ERR_INVALID, "N must be in [0, %d], got %d", MAX_N, N);
+    if (static_cast<long long>(B) * N > MAX_TOKENS)
+        return fail(SPEC_ERR_INVALID, "B N must be at most %lld, got %lld", MAX_TOKENS, static_cast<long long>(B) * N);
+    return SPEC_OK;
+}
+
+// Rows [B, N] of values of `bytes` each: present, and the pointer on a value of its type.
+spec_status check_rows(const spec_rows* t, const char* name, size_t bytes) {
+    if (!t || !t->data) return fail(SPEC_ERR_INVALID, "%s must not be NULL", name);
+    if (reinterpret_cast<uintptr_t>(t->data) % bytes) return fail(SPEC_ERR_INVALID, "%s: the pointer must be a multiple of %zu bytes", name, bytes);
+    return SPEC_OK;
+}
+
+// An output: two of its rows must not share elements. Rows of one index lie `width` or more apart; where both have several, one
+// index's steps must pass the whole reach of the other.
+spec_status check_out(const spec_rows* t, const char* name, size_t bytes, int B, int N, long long width) {
+    SPECS_TRY(check_rows(t, name, bytes));
+    const long long sb = B > 1 ? std::llabs(t->stride_b) : 0, sn = N > 1 ? std::llabs(t->stride_n) : 0;
+    const bool ok = (B <= 1 || sb >= width) && (N <= 1 || sn >= width) &&
+                    (B <= 1 || N <= 1 || sb >= sn * (N - 1) + width || sn >= sb * (B - 1) + width);
+    return ok ? SPEC_OK : fail(SPEC_ERR_INVALID, "%s: rows overlap: strides must keep rows of %lld values apart", name, width);
+}
+
+// An output in an input's place: row for row.
+spec_status check_same(const spec_rows* out, const char* name, const spec_rows* x, const spec_rows* y, int B, int N) {
+    for (const spec_rows* in : {x, y})
+        if (in && in->data == out->data && ((B > 1 && in->stride_b != out->stride_b) || (N > 1 && in->stride_n != out->stride_n)))
+            return fail(SPEC_ERR_INVALID, "%s in an input's place must have its strides", name);
+    return SPEC_OK;
+}
+
+size_t type_bytes(int dtype) { return dtype == SPEC_INT8 ? 1 : dtype == SPEC_FP32 ? 4 : 2; }
+
+spec_status check_type(int dtype) {
+    return dtype == SPEC_BF16 || dtype == SPEC_FP16 || dtype == SPEC_FP32
+               ? SPEC_OK
+               : fail(SPEC_ERR_UNSUPPORTED, "dtype must be bf16, fp16 or fp32, got %d", dtype);
+}
+
+Rows rows_of(const spec_rows* t) { return t ? Rows{t->data, t->stride_b, t->stride_n} : Rows{nullptr, 0, 0}; }
+
+// A launch whose CTAs may take their places while the kernel before still runs; each waits for that kernel's end by itself.
+template <class P>
+cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st, size_t smem = 0) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+// ---------------------------------------------------------------------------------------- norm and codes
+template <class T>
+spec_status norm_as(const NormParams& p, bool codes, cudaStream_t st) {
+    return launched("norm", launch_behind(codes ? norm_kernel<T, true> : norm_kernel<T, false>, p,
+                                          dim3(static_cast<unsigned>(p.rows)), 256, st));
+}
+
+spec_status norm(const NormParams& p, int dtype, bool codes, cudaStream_t st) {
+    return dtype == SPEC_BF16 ? norm_as<__nv_bfloat16>(p, codes, st)
+           : dtype == SPEC_FP16 ? norm_as<__half>(p, codes, st) : norm_as<float>(p, codes, st);
+}
+
+spec_status check_norm(int dtype, int B, int N, int D) {
+    SPECS_TRY(check_type(dtype));
+    SPECS_TRY(check_tokens(B, N));
+    if (D < 1 || D > SPEC_SCORE_MAX_D)
+        return fail(SPEC_ERR_UNSUPPORTED, "D must be in [1, %d], got %d", SPEC_SCORE_MAX_D, D);
+    return SPEC_OK;
+}
+
+// --------------------------------------------------------------------------------------------- product
+size_t matmul_bytes(int, int, int) { return SPEC_SCORE_WS_HEADER; }
+
+}  // namespace
+}  // namespace specs
+
+using namespace specs;
+
+extern "C" {
+
+const char* spec_score_last_error(void) { return g_err; }
+
+spec_status spec_residual_norm(const spec_rows* x, const spec_rows* residual, int dtype, int B, int N, int D,
+                               const void* weight, float eps, const spec_rows* residual_out, const spec_rows* out,
+                               int out_type, float* scale, void* stream) {
+    SPECS_TRY(check_norm(dtype, B, N, D));
+    if (out_type != SPEC_INT8 && out_type != dtype)
+        return fail(SPEC_ERR_UNSUPPORTED, "out_type must be dtype or SPEC_INT8, got %d", out_type);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SPEC_ERR_INVALID, "eps must be finite and not negative");
+    if (!residual != !residual_out) return fail(SPEC_ERR_INVALID, "residual and residual_out come together");
+    if (B == 0 || N == 0) return SPEC_OK;
+    const size_t e = type_bytes(dtype);
+    SPECS_TRY(check_rows(x, "x", e));
+    if (residual) {
+        SPECS_TRY(check_rows(residual, "residual", e));
+        SPECS_TRY(check_out(residual_out, "residual_out", e, B, N, D));
+    }
+    SPECS_TRY(check_out(out, "out", type_bytes(out_type), B, N, D));
+    if (residual && residual_out->data == out->data) return fail(SPEC_ERR_INVALID, "out must not be residual_out");
+    if (residual) SPECS_TRY(check_same(residual_out, "residual_out", x, residual, B, N));
+    if (out_type != SPEC_INT8) SPECS_TRY(check_same(out, "out", x, residual, B, N));
+    else if (out->data == x->data || (residual && out->data == residual->data))
+        return fail(SPEC_ERR_INVALID, "out in 8 bits must not be an input");
+    if (out_type == SPEC_INT8 && !scale) return fail(SPEC_ERR_INVALID, "scale must not be NULL");
+    if (reinterpret_cast<uintptr_t>(weight) % e) return fail(SPEC_ERR_INVALID, "weight: the pointer must be a multiple of %zu bytes", e);
+    NormParams p = {};
+    p.x = rows_of(x);
+    p.res = rows_of(residual);
+    p.res_out = rows_of(residual_out);
+    p.out = rows_of(out);
+    p.weight = weight;
+    p.scale = scale;
+    p.rows = static_cast<long long>(B) * N;
+    p.N = N;
+    p.D = D;
+    p.eps = eps;
+    p.norm = 1;
+    return norm(p, dtype, out_type == SPEC_INT8, static_cast<cudaStream_t>(stream));
+}
+
+spec_status spec_quantize_rows(const spec_rows* x, int dtype, int B, int N, int D, const spec_rows* out, float* scale,
+                               void* stream) {
+    SPECS_TRY(check_norm(dtype, B, N, D));
+    if (B == 0 || N == 0) return SPEC_OK;
+    SPECS_TRY(check_rows(x, "x", type_bytes(dtype)));
+    SPECS_TRY(check_out(out, "out", 1, B, N, D));
+    if (out->data == x->data) return fail(SPEC_ERR_INVALID, "out in 8 bits must not be an input");
+    if (!scale) return fail(SPEC_ERR_INVALID, "scale must not be NULL");
+    NormParams p = {};
+    p.x = rows_of(x);
+    p.out = rows_of(out);
+    p.scale = scale;
+    p.rows = static_cast<long long>(B) * N;
+    p.N = N;
+    p.D = D;
+    return norm(p, dtype, true, static_cast<cudaStream_t>(stream));
+}
+
+size_t spec_int8_matmul_workspace_size(int tokens, int C, int K) {
+    if (tokens < 0 || tokens > MAX_TOKENS || C < 0 || C > MAX_C || K < 1 || K > SPEC_SCORE_MAX_K) return 0;
+    return matmul_bytes(tokens, C, K);
+}
+
+spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const void* w, long long w_stride,
+                             const float* w_scale, const float* bias, int B, int N, int C, int K, const spec_rows* out,
+                             int out_type, void* workspace, size_t workspace_bytes, void* stream) {
+    SPECS_TRY(check_type(out_type));
+    SPECS_TRY(check_tokens(B, N));
+    if (C < 0 || C > MAX_C) return fail(SPEC_ERR_INVALID, "C must be in [0, %d], got %d", MAX_C, C);
+    if (K < 1 || K > SPEC_SCORE_MAX_K) return fail(SPEC_ERR_UNSUPPORTED, "K must be in [1, %d], got %d", SPEC_SCORE_MAX_K, K);
+    if (B == 0 || N == 0 || C == 0) return SPEC_OK;
+    SPECS_TRY(check_rows(a, "a", 1));
+    SPECS_TRY(check_out(out, "out", type_bytes(out_type), B, N, C));
+    if (!w || !a_scale || !w_scale) return fail(SPEC_ERR_INVALID, "w, a_scale and w_scale must not be NULL");
+    if (C > 1 && w_stride < 0) return fail(SPEC_ERR_INVALID, "w_stride must not be negative");
+    if (!workspace || !aligned16(workspace)) return fail(SPEC_ERR_INVALID, "workspace must be 16-byte aligned device memory");
+    const size_t need = matmul_bytes(B * N, C, K);
+    if (workspace_bytes < need) return fail(SPEC_ERR_INVALID, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    MatmulParams p = {};
+    p.a = rows_of(a);
+    p.out = rows_of(out);
+    p.w = static_cast<const signed char*>(w);
+    p.a_scale = a_scale;
+    p.w_scale = w_scale;
+    p.bias = bias;
+    p.w_stride = w_stride;
+    p.tokens = B * N;
+    p.N = N;
+    p.C = C;
+    p.K = K;
+    p.status = static_cast<unsigned*>(workspace);
+    void (*const fn)(const MatmulParams) = out_type == SPEC_BF16   ? matmul_kernel<__nv_bfloat16>
+                                           : out_type == SPEC_FP16 ? matmul_kernel<__half> : matmul_kernel<float>;
+    return launched("product", launch_behind(fn, p, dim3((C + MT - 1) / MT, (p.tokens + MT - 1) / MT), 256, static_cast<cudaStream_t>(stream)));
+}
+
+spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R, int V, const int32_t* tokens, int T,
+                                const int32_t* history, const int32_t* lengths, const int32_t* prompt, int L,
+                                const float* repetition, const float* frequency, const float* presence,
+                                const int32_t* bias_tokens, const float* bias, int biases, const uint32_t* mask,
+                                long long mask_stride_b, long long mask_stride_r, const spec_rows* out, void* stream) {
+    if (dtype != SPEC_BF16 && dtype != SPEC_FP32) return fail(SPEC_ERR_UNSUPPORTED, "dtype must be bf16 or fp32, got %d", dtype);
+    if (B < 0 || B > MAX_B) return fail(SPEC_ERR_INVALID, "B must be in [0, %d], got %d", MAX_B, B);
+    if (R < 0 || R > SPEC_SCORE_MAX_ROWS) return fail(SPEC_ERR_INVALID, "R must be in [0, %d], got %d", SPEC_SCORE_MAX_ROWS, R);
+    if (V < 1 || V > MAX_V) return fail(SPEC_ERR_INVALID, "V must be in [1, %d], got %d", MAX_V, V);
+    if (L < 0 || L > SPEC_SCORE_MAX_HISTORY) return fail(SPEC_ERR_INVALID, "L must be in [0, %d], got %d", SPEC_SCORE_MAX_HISTORY, L);
+    if (biases < 0 || biases > SPEC_SCORE_MAX_BIASES)
+        return fail(SPEC_ERR_INVALID, "biases must be in [0, %d], got %d", SPEC_SCORE_MAX_BIASES, biases);
+    if (B == 0 || R == 0) return SPEC_OK;
+    const size_t e = type_bytes(dtype);
+    SPECS_TRY(check_rows(logits, "logits", e));
+    SPECS_TRY(check_out(out, "out", e, B, R, V));
+    SPECS_TRY(check_same(out, "out", logits, nullptr, B, R));
+    if (tokens && T < R - 1) return fail(SPEC_ERR_INVALID, "tokens must have at least R - 1 = %d a sequence, got %d", R - 1, T);
+    if (history && L > 0 && !lengths) return fail(SPEC_ERR_INVALID, "lengths must not be NULL");
+    if (bias_tokens && biases > 0 && !bias) return fail(SPEC_ERR_INVALID, "bias must not be NULL");
+    LogitsParams p = {};
+    p.in = rows_of(logits);
+    p.out = rows_of(out);
+    p.tokens = tokens;
+    p.history = L > 0 ? history : nullptr;
+    p.lengths = lengths;
+    p.prompt = prompt;
+    p.bias_tokens = biases > 0 ? bias_tokens : nullptr;
+    p.repetition = repetition;
+    p.frequency = frequency;
+    p.presence = presence;
+    p.bias = bias;
+    p.mask = mask;
+    p.mask_sb = mask_stride_b;
+    p.mask_sr = mask_stride_r;
+    p.R = R;
+    p.V = V;
+    p.T = T;
+    p.L = L;
+    p.biases = biases;
+    return launched("logits", launch_behind(dtype == SPEC_BF16 ? logits_kernel<__nv_bfloat16> : logits_kernel<float>, p,
+                                            dim3((V + SEG - 1) / SEG, B), 256, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
