@@ -1,4 +1,4 @@
-// The product of 8-bit integers with scales for each token and each channel.
+// The product of 8-bit integers for few tokens, and for rows that the copies of product.cuh cannot take.
 #pragma once
 #include "rows.cuh"
 
@@ -10,48 +10,83 @@ struct MatmulParams {
     const float *a_scale, *w_scale, *bias;
     long long w_stride;
     int tokens, N, C, K;
-    unsigned* status;
+    int first;        // token of the launch's first row
+    int k_warps;      // of a CTA's eight: 1, 2, 4 or 8
 };
 
-// A CTA takes 64 tokens by 64 channels, a thread 4 by 4 of them; 64 of K at a time in shared memory, four to a word.
-constexpr int MT = 64, MK = 64, MPAD = MK / 4 + 1;
+constexpr int MV_WARPS = 8, MV_CH = 4;
 
-template <class T>
-__global__ void __launch_bounds__(256) matmul_kernel(const __grid_constant__ MatmulParams p) {
-    __shared__ int sa[MT * MPAD], sw[MT * MPAD];
-    after_previous();
-    const int t0 = blockIdx.y * MT, c0 = blockIdx.x * MT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += MK) {
-        for (int i = threadIdx.x; i < MT * MK; i += 256) {
-            const int r = i / MK, k = k0 + i % MK;
-            signed char va = 0, vw = 0;
-            if (k < p.K && t0 + r < p.tokens) va = row_of<signed char>(p.a, (t0 + r) / p.N, (t0 + r) % p.N)[k];
-            if (k < p.K && c0 + r < p.C) vw = p.w[static_cast<long long>(c0 + r) * p.w_stride + k];
-            reinterpret_cast<signed char*>(sa)[r * MPAD * 4 + i % MK] = va;
-            reinterpret_cast<signed char*>(sw)[r * MPAD * 4 + i % MK] = vw;
+// 16 codes at p, of which `valid` are there; the others are 0. Without alignment only words that hold a valid code are read.
+template <bool ALIGNED>
+__device__ __forceinline__ void load16(const signed char* p, int valid, int (&x)[4]) {
+    if constexpr (ALIGNED) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+        const int by = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+        const unsigned* const w = reinterpret_cast<const unsigned*>(p - by);
+        unsigned v[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = 4 * i < by + valid ? __ldg(w + i) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned y = __funnelshift_r(v[i], v[i + 1], 8 * by);
+            const int left = valid - 4 * i;
+            x[i] = static_cast<int>(left >= 4 ? y : left <= 0 ? 0u : y & ((1u << (8 * left)) - 1u));
         }
-        __syncthreads();
-#pragma unroll 4
-        for (int k = 0; k < MK / 4; ++k) {
-            int a[4], w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sa[(ty + 16 * i) * MPAD + k], w[i] = sw[(tx + 16 * i) * MPAD + k];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(a[i], w[j], acc[i][j]);
-        }
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int t = t0 + ty + 16 * i, c = c0 + tx + 16 * j;
-            if (t >= p.tokens || c >= p.C) continue;
-            float y = static_cast<float>(acc[i][j]) * (p.a_scale[t] * p.w_scale[c]);
-            if (p.bias) y += p.bias[c];
-            row_of<T>(p.out, t / p.N, t % p.N)[c] = from_float<T>(y);
+}
+
+// A warp takes four channels and up to TOKENS tokens, its lanes 16 of K each; k_warps of a CTA's warps share their K. Integer
+// products four at a time (dp4a, 64 lanes a cycle and SM: 37 T products a second), whole sums in 32 bits, so their order does
+// not matter.
+template <class T, int TOKENS, bool ALIGNED>
+__global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_constant__ MatmulParams p) {
+    __shared__ int s_sum[MV_WARPS][MV_CH * TOKENS];
+    after_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp % p.k_warps, groups = MV_WARPS / p.k_warps;
+    const int c0 = (blockIdx.x * groups + warp / p.k_warps) * MV_CH, t0 = p.first + blockIdx.y * TOKENS;
+    const signed char *w[MV_CH], *a[TOKENS];
+#pragma unroll
+    for (int i = 0; i < MV_CH; ++i) w[i] = p.w + min(c0 + i, p.C - 1) * p.w_stride;      // past the end the last one once more
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+        const int t = min(t0 + j, p.tokens - 1), b = t / p.N;
+        a[j] = row_of<signed char>(p.a, b, t - b * p.N);
+    }
+    int acc[MV_CH][TOKENS] = {};
+    for (int k = (kw * 32 + lane) * 16; k < p.K; k += p.k_warps * 512) {
+        int x[MV_CH][4];
+#pragma unroll
+        for (int i = 0; i < MV_CH; ++i) load16<ALIGNED>(w[i] + k, p.K - k, x[i]);
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            int y[4];
+            load16<ALIGNED>(a[j] + k, p.K - k, y);
+#pragma unroll
+            for (int i = 0; i < MV_CH; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j] = __dp4a(x[i][q], y[q], acc[i][j]);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < MV_CH; ++i)
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            const int s = __reduce_add_sync(0xffffffffu, acc[i][j]);
+            if (lane == 0) s_sum[warp][j * MV_CH + i] = s;
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < groups * MV_CH * TOKENS; e += MV_WARPS * 32) {
+        const int g = e / (MV_CH * TOKENS), i = e % MV_CH, j = e % (MV_CH * TOKENS) / MV_CH;
+        const int c = (blockIdx.x * groups + g) * MV_CH + i, t = t0 + j;
+        if (c >= p.C || t >= p.tokens) continue;
+        int sum = 0;
+        for (int q = 0; q < p.k_warps; ++q) sum += s_sum[g * p.k_warps + q][j * MV_CH + i];
+        float y = static_cast<float>(sum) * (p.a_scale[t] * p.w_scale[c]);
+        if (p.bias) y += p.bias[c];
+        row_of<T>(p.out, t / p.N, t % p.N)[c] = from_float<T>(y);
+    }
 }
 
 }  // namespace specs

@@ -1,0 +1,425 @@
+// The product of 8-bit integers on the tensor cores, which take no 8-bit integers on this card: as halves, exactly.
+#pragma once
+#include <cuda.h>
+
+#include "../cache/tmem.cuh"
+#include "rows.cuh"
+
+namespace specs {
+
+using specv::smem_addr;
+
+// A step is 128 of K: 128 channels' codes as they are (16 KB) and the tokens' halves.
+constexpr int PR_K = 128, PR_CH = 128, PR_TOKENS = 192, PR_THREADS = 512, PR_STAGES = 11;
+// Warps that turn step g's codes wait for its copies when they have written step g - 2, so when the products of step g - 4 are
+// done: the stage's barrier is then in the phase that they mean only if its last use was no later than that.
+constexpr int PR_MIN_STAGES = 4, PR_TOKENS_ALONE = 128;      // a CTA without a pair has room for four stages up to 144 tokens
+constexpr int PR_W_BYTES = PR_CH * PR_K;
+constexpr int PR_SMEM = 224 * 1024;                    // of it up to 1 KB is lost to alignment
+constexpr uint32_t PR_COL_A = 2 * PR_TOKENS;           // tensor memory: two accumulators, two steps of channels
+constexpr uint64_t PR_WAIT_NS = 2000000000ull;
+// The sum of two steps is at most 256 x 2^14 = 2^22 in magnitude, so exact in fp32 as are its parts. Added to 1.5 x 2^23, whose last
+// place is 1, it stands in the last bits of the sum (2^22 itself carries into the exponent, and the bits still count on).
+constexpr int PR_CHUNK = 2;
+constexpr float PR_MAGIC = 12582912.f;
+constexpr uint32_t PR_MAGIC_BITS = 0x4B400000u;
+
+struct ProductParams {
+    CUtensorMap w;       // 64-byte aligned, as its type says
+    Rows out;
+    const unsigned char* tokens16;
+    const float *a_scale, *w_scale, *bias;
+    int tokens, N, C;
+    int n, token_tiles, channel_tiles, steps, stages, split;
+    int stream_w;        // the codes are read once: they need not stay in L2
+    unsigned* status;
+};
+
+struct HalvesParams {
+    Rows a;
+    unsigned char* out;
+    int tokens, N, K, n, steps;
+    long long groups;    // of 16 codes
+};
+
+// ------------------------------------------------------------------------------------ tokens to halves
+// The tokens' codes as halves, in the blocks that the product reads: for each tile of n tokens and 64 of K, n rows of 128 bytes
+// whose 16-byte pieces are exchanged as 128-byte swizzling wants it (piece c of row r at c ^ (r & 7)). Rows and columns past the
+// ends are 0. One pass of a few MB from and to L2: 384 tokens of 4096 take 2 us.
+__device__ __forceinline__ void halves_of(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    // a byte b behind 0x64 is the half 1024 + b; with b = code + 128 that is the code and 1152
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    x ^= 0x80808080u;
+    const uint32_t l = __byte_perm(x, 0x64646464u, 0x4140), h = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), off), b = __hsub2(*reinterpret_cast<const __half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__global__ void __launch_bounds__(256) halves_kernel(const __grid_constant__ HalvesParams p) {
+    after_previous();
+    const long long g = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    if (g >= p.groups) return;
+    const int per_row = p.steps * (PR_K / 16);
+    const int row = static_cast<int>(g / per_row), k = static_cast<int>(g - static_cast<long long>(row) * per_row) * 16;
+    uint32_t x[4] = {0u, 0u, 0u, 0u};
+    if (row < p.tokens && k < p.K) {
+        const signed char* const src = row_of<signed char>(p.a, row / p.N, row % p.N) + k;
+        if (k + 16 <= p.K && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (k + i < p.K) x[i / 4] |= static_cast<uint32_t>(static_cast<unsigned char>(src[i])) << (8 * (i % 4));
+        }
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) halves_of(x[i], h[2 * i], h[2 * i + 1]);
+    const int tile = row / p.n, r = row - tile * p.n, c = k % 64 / 8;
+    unsigned char* const dst = p.out + (static_cast<long long>(tile) * p.steps * 2 + k / 64) * p.n * 128 + r * 128;
+    *reinterpret_cast<uint4*>(dst + ((c ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + (((c + 1) ^ (r & 7)) * 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// ------------------------------------------------------------------------------------------- the product
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits, as a warp, for a phase of `bar`. Where it gives up it sets the status bit and clears `alive`, so that later waits end at
+// once: the results are invalid, but every barrier behind is still met.
+__device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, bool& alive, unsigned* status) {
+    uint64_t since = 0;
+    for (int i = 1; !__all_sync(0xffffffffu, phase_done(bar, parity)) && alive; ++i) {
+        if (i % 256 == 0) {
+            const uint64_t now = specv::global_timer_ns();
+            if (since == 0) since = now;
+            if (!__all_sync(0xffffffffu, now - since < PR_WAIT_NS)) {
+                atomicOr(status, SPEC_STATUS_TIMEOUT);
+                alive = false;
+            }
+        }
+    }
+}
+
+// Arrives at the barrier of the pair's first CTA (its own one where there is no pair).
+template <bool PAIR>
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+            "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+            : "memory");
+    else
+        specv::mbar_arrive(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {      // of both CTAs of a pair
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+            "h"(static_cast<unsigned short>(3))
+            : "memory");
+    else
+        specc::umma_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+            "r"(static_cast<uint32_t>(add))
+            : "memory");
+    else
+        specc::umma_ts(d, a, b, idesc, add);
+}
+
+__device__ __forceinline__ void load_codes(void* dst, const CUtensorMap* map, int k, int channel, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(k), "r"(channel), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Tokens' halves in shared memory: rows of 128 bytes, swizzled, eight rows to 1024 bytes.
+__device__ __forceinline__ uint64_t tokens_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <int REGS, bool MORE>
+__device__ __forceinline__ void set_registers() {
+    if (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// The units of a CTA (a pair): tiles of channels times tiles of tokens. Tiles of tokens come in groups of eight, within which the
+// units of neighbouring CTAs share their channels' codes.
+struct Unit {
+    int channel, tile;
+    __device__ Unit(const ProductParams& p, long long u) {
+        const long long per = 8LL * p.channel_tiles;
+        const int group = static_cast<int>(u / per), wide = min(8, p.token_tiles - 8 * group);
+        const int in = static_cast<int>(u - group * per);
+        channel = in / wide;
+        tile = 8 * group + in % wide;
+    }
+};
+
+// Channels stand on the tensor cores' long side, tokens on the other. Four parts work beside one another:
+//   warp 0         copies: the channels' codes as they are in memory, the tokens' halves
+//   warp 1         products: D[channel, token] += A[channel, k] B[k, token], A in tensor memory, 16 of K at a time
+//   warps 4 .. 11  codes to halves, exactly, from shared to tensor memory; two halves of the warps take the steps in turn
+//   warps 12 .. 15 sums of 256 products out of the tensor memory into integers in registers, and at the end to the output
+// PAIR: two CTAs share a tile of 256 channels; each holds its channels and half of the tokens, the first one issues.
+// split > 1: the CTAs of a cluster share a tile's K, and add their integers through one another's shared memory.
+template <class T, bool PAIR>
+__global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
+    extern __shared__ unsigned char dynamic[];
+    __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[2], s_a_empty[2], s_acc_full[2], s_acc_empty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ float s_scale[PR_TOKENS];
+    __shared__ long long s_row[PR_TOKENS];
+    unsigned char* const smem = dynamic + ((1024u - (smem_addr(dynamic) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    constexpr int CTAS = PAIR ? 2 : 1;
+    const int rank = PAIR || p.split > 1 ? static_cast<int>(specv::cluster_ctarank()) : 0;
+    const int own_n = p.n / CTAS, half_bytes = own_n * 128, stage_bytes = PR_W_BYTES + 2 * half_bytes;
+    const int group = PAIR ? 2 : p.split;
+    const long long units = static_cast<long long>(p.channel_tiles) * p.token_tiles, first = blockIdx.x / group, by = gridDim.x / group;
+    const int k_from = PAIR ? 0 : static_cast<int>(static_cast<long long>(p.steps) * rank / p.split);
+    const int k_to = PAIR ? p.steps : static_cast<int>(static_cast<long long>(p.steps) * (rank + 1) / p.split);
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) specv::mbar_init(&s_full[i], 1), specv::mbar_init(&s_empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            specv::mbar_init(&s_ready[i], 4 * CTAS), specv::mbar_init(&s_a_empty[i], 1);
+            specv::mbar_init(&s_acc_full[i], 1), specv::mbar_init(&s_acc_empty[i], 4 * CTAS);
+        }
+        specv::fence_mbarrier_init_cluster();
+    }
+    if (warp == 2) {
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s_tmem)) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            specc::tmem_alloc(&s_tmem, 512);
+        }
+        specc::tmem_fence_before();
+    }
+    __syncthreads();
+    if (PAIR) specv::cluster_sync_all();
+    specc::tmem_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool alive = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, alive, p.status); };
+
+    if (warp < 4) {
+        set_registers<40, false>();
+        if (warp == 0) {
+            // ================ copies
+            const uint64_t keep = specv::policy_evict_last(), w_policy = p.stream_w ? specv::policy_evict_first() : specv::policy_evict_normal();
+            auto codes = [&](int st, const Unit& u, int k) {
+                if (lane == 0) {
+                    specv::mbar_arrive_expect_tx(&s_full[st], stage_bytes);
+                    load_codes(smem + st * stage_bytes, &p.w, k * PR_K, (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH, &s_full[st], w_policy);
+                }
+            };
+            auto tokens = [&](int st, const Unit& u, int k) {
+                if (lane < 2) {
+                    const unsigned char* src = p.tokens16 + ((static_cast<long long>(u.tile) * p.steps + k) * 2 + lane) * p.n * 128 + (PAIR ? rank * half_bytes : 0);
+                    specv::bulk_load(smem + st * stage_bytes + PR_W_BYTES + lane * half_bytes, src, half_bytes, &s_full[st], keep);
+                }
+            };
+            // The first copies of codes are on their way before the kernel in front, which makes the tokens' halves, has ended: what
+            // it waited for before it let this one in holds the codes.
+            int ahead = 0;
+            if (first < units) {
+                const Unit u(p, first);
+                for (; ahead < p.stages && k_from + ahead < k_to; ++ahead) codes(ahead, u, k_from + ahead);
+            }
+            asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+            int g = 0;
+            for (long long i = first; i < units; i += by) {
+                const Unit u(p, i);
+                for (int k = k_from; k < k_to; ++k, ++g) {
+                    const int st = g % p.stages, round = g / p.stages;
+                    if (g >= ahead) {
+                        if (round > 0) wait(&s_empty[st], (round - 1) & 1);
+                        if (!alive) break;
+                        codes(st, u, k);
+                    }
+                    __syncwarp();
+                    tokens(st, u, k);
+                }
+                if (!alive) break;
+            }
+            // this CTA's copies have landed, and the products' arrivals are in, before it ends
+            for (int i = max(0, g - p.stages); i < g; ++i) {
+                bool once = true;
+                wait_phase(&s_full[i % p.stages], (i / p.stages) & 1, once, p.status);
+                wait(&s_empty[i % p.stages], (i / p.stages) & 1);
+            }
+        } else if (warp == 1 && (!PAIR || rank == 0)) {
+            // ================ products
+            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) | (static_cast<uint32_t>(PR_CH * CTAS >> 4) << 24);
+            int g = 0, chunk = 0;
+            for (long long i = first; i < units; i += by) {
+                for (int k = k_from; k < k_to; ++k, ++g) {
+                    const int st = g % p.stages, at = (k - k_from) % PR_CHUNK;
+                    const uint32_t d = tmem + (chunk & 1) * PR_TOKENS, a = tmem + PR_COL_A + (g & 1) * 64;
+                    if (at == 0 && chunk >= 2) wait(&s_acc_empty[chunk & 1], ((chunk >> 1) - 1) & 1);
+                    wait(&s_ready[g & 1], (g >> 1) & 1);
+                    specc::tmem_fence_after();
+                    const bool last = at == PR_CHUNK - 1 || k + 1 == k_to;
+                    if (alive && specc::elect_one()) {
+                        const uint32_t b = smem_addr(smem + st * stage_bytes + PR_W_BYTES);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma<PAIR>(d, a + 8 * j, tokens_desc(b + (j / 4) * half_bytes + (j % 4) * 32), idesc, at > 0 || j > 0);
+                        commit<PAIR>(&s_empty[st]);
+                        commit<PAIR>(&s_a_empty[g & 1]);
+                        if (last) commit<PAIR>(&s_acc_full[chunk & 1]);
+                    }
+                    __syncwarp();
+                    if (last) ++chunk;
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ================ codes to halves
+        set_registers<104, false>();
+        const int mine = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t to = tmem + PR_COL_A + mine * 64 + (static_cast<uint32_t>(warp & 3) << 21);
+        int g = 0, last = -1;
+        for (long long i = first; i < units; i += by)
+            for (int k = k_from; k < k_to; ++k, ++g) {
+                if ((g & 1) != mine) continue;
+                last = g;
+                const int st = g % p.stages;
+                wait(&s_full[st], (g / p.stages) & 1);
+                const unsigned char* const src = smem + st * stage_bytes + row * 128;
+                uint4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) * 16));
+                if (g >= 2) wait(&s_a_empty[mine], ((g >> 1) - 1) & 1);
+                specc::tmem_fence_after();
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    uint32_t h[16];
+                    halves_of(v[j].x, h[0], h[1]), halves_of(v[j].y, h[2], h[3]);
+                    halves_of(v[j].z, h[4], h[5]), halves_of(v[j].w, h[6], h[7]);
+                    halves_of(v[j + 1].x, h[8], h[9]), halves_of(v[j + 1].y, h[10], h[11]);
+                    halves_of(v[j + 1].z, h[12], h[13]), halves_of(v[j + 1].w, h[14], h[15]);
+                    specc::tmem_st16(to + 8 * j, h);
+                }
+                specc::tmem_wait_st();
+                specc::tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first<PAIR>(&s_ready[mine]);
+            }
+        if (last >= 0) wait(&s_a_empty[mine], (last >> 1) & 1);      // no arrival comes in behind the CTA's end
+    } else {
+        // ================ sums, and the output
+        set_registers<232, true>();
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const uint32_t from = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const int in_tile = (warp & 3) * 32 + lane;
+        int chunk = 0;
+        for (long long i = first; i < units; i += by) {
+            const Unit u(p, i);
+            const int t0 = u.tile * p.n, nt = min(p.n, p.tokens - t0);
+            __syncwarp();      // these barriers are for whole warps
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            for (int j = tid - 384; j < nt; j += 128) {
+                const int t = t0 + j, b = t / p.N;
+                s_scale[j] = p.a_scale[t];
+                s_row[j] = b * p.out.sb + (t - b * p.N) * p.out.sn;
+            }
+            __syncwarp();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int c = (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH + in_tile;
+            uint32_t acc[PR_TOKENS];
+#pragma unroll
+            for (int j = 0; j < PR_TOKENS; ++j) acc[j] = 0u;
+            const int chunks = (k_to - k_from + PR_CHUNK - 1) / PR_CHUNK;
+            for (int q = 0; q < chunks; ++q, ++chunk) {
+                wait(&s_acc_full[chunk & 1], (chunk >> 1) & 1);
+                specc::tmem_fence_after();
+#pragma unroll
+                for (int j = 0; j < PR_TOKENS; j += 32)
+                    if (j < p.n) {
+                        uint32_t v[32];
+                        specc::tmem_ld(from + (chunk & 1) * PR_TOKENS + j, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) acc[j + e] += __float_as_uint(__uint_as_float(v[e]) + PR_MAGIC);
+                    }
+                specc::tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_first<PAIR>(&s_acc_empty[chunk & 1]);
+            }
+            const uint32_t off = static_cast<uint32_t>(chunks) * PR_MAGIC_BITS;
+            const float ws = c < p.C ? p.w_scale[c] : 0.f, bias = p.bias && c < p.C ? p.bias[c] : 0.f;
+            T* const out = static_cast<T*>(p.out.p) + c;
+            auto put = [&](int j, int sum) {
+                float y = static_cast<float>(sum) * (s_scale[j] * ws);
+                if (p.bias) y += bias;
+                if (c < p.C) out[s_row[j]] = from_float<T>(y);
+            };
+            if (!PAIR && p.split > 1) {
+                // one tile a cluster: its CTAs add their sums, each for every split-th token
+                int* const part = reinterpret_cast<int*>(smem) + in_tile;
+#pragma unroll
+                for (int j = 0; j < PR_TOKENS; j += 32)
+                    if (j < nt) {
+#pragma unroll
+                        for (int e = j; e < j + 32; ++e)
+                            if (e < nt) part[e * PR_CH] = static_cast<int>(acc[e] - off);
+                    }
+                __syncwarp();
+                specv::cluster_sync_all();
+                for (int j = rank; j < nt; j += p.split) {
+                    int sum = 0;
+                    for (int r = 0; r < p.split; ++r)
+                        sum += __float_as_int(specv::ld_cluster_f32(specv::map_to_rank(smem_addr(part + j * PR_CH), r)));
+                    put(j, sum);
+                }
+                __syncwarp();
+                specv::cluster_sync_all();
+            } else {
+#pragma unroll
+                for (int j = 0; j < PR_TOKENS; j += 32)
+                    if (j < nt) {
+#pragma unroll
+                        for (int e = j; e < j + 32; ++e)
+                            if (e < nt) put(e, static_cast<int>(acc[e] - off));
+                    }
+            }
+        }
+    }
+    // What follows is run by warps with 40 and with 232 registers: it needs a few.
+    __syncwarp();
+    if (!PAIR && p.split > 1 && warp < 12) {      // the barriers around the sums' exchange above
+        specv::cluster_sync_all();
+        specv::cluster_sync_all();
+    }
+    specc::tmem_fence_before();
+    __syncthreads();
+    if (PAIR) specv::cluster_sync_all();
+    if (warp == 2) {
+        specc::tmem_fence_after();
+        if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        else specc::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace specs

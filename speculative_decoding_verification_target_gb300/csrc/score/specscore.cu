@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/specscore.h: argument checks and launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -8,6 +9,7 @@
 #include "logits.cuh"
 #include "matmul.cuh"
 #include "norm.cuh"
+#include "product.cuh"
 
 namespace specs {
 namespace {
@@ -82,17 +84,19 @@ Rows rows_of(const spec_rows* t) { return t ? Rows{t->data, t->stride_b, t->stri
 
 // A launch whose CTAs may take their places while the kernel before still runs; each waits for that kernel's end by itself.
 template <class P>
-cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st, size_t smem = 0) {
-    cudaLaunchAttribute at[1];
+cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int threads, cudaStream_t st, size_t smem = 0, int cluster = 1) {
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
@@ -117,7 +121,126 @@ spec_status check_norm(int dtype, int B, int N, int D) {
 }
 
 // --------------------------------------------------------------------------------------------- product
-size_t matmul_bytes(int, int, int) { return SPEC_SCORE_WS_HEADER; }
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+// Workspace: header, and the tokens' halves in tiles of equal width, a multiple of 32.
+size_t matmul_bytes(int tokens, int, int K) {
+    const size_t tiles = (static_cast<size_t>(tokens) + PR_TOKENS - 1) / PR_TOKENS;
+    return SPEC_SCORE_WS_HEADER + ((static_cast<size_t>(tokens) + 31) / 32 * 32 + 32 * tiles) * ((static_cast<size_t>(K) + PR_K - 1) / PR_K * PR_K) * 2;
+}
+
+template <class T, bool ALIGNED>
+spec_status matvec_as(MatmulParams p, cudaStream_t st) {
+    p.k_warps = p.K > 2048 ? 8 : p.K > 1024 ? 4 : p.K > 512 ? 2 : 1;
+    const int per = MV_WARPS / p.k_warps * MV_CH;
+    const int width = p.tokens > 4 ? 8 : p.tokens > 2 ? 4 : p.tokens;
+    void (*const fn)(const MatmulParams) = width == 8 ? matvec_kernel<T, 8, ALIGNED> : width == 4 ? matvec_kernel<T, 4, ALIGNED>
+                                           : width == 2 ? matvec_kernel<T, 2, ALIGNED> : matvec_kernel<T, 1, ALIGNED>;
+    const long long rows = (static_cast<long long>(p.tokens) + width - 1) / width;
+    for (long long from = 0; from < rows; from += 65535) {      // the grid's second side ends there
+        MatmulParams q = p;
+        q.first = static_cast<int>(from * width);
+        SPECS_TRY(launched("product", launch_behind(fn, q, dim3((p.C + per - 1) / per, static_cast<unsigned>(std::min(rows - from, 65535LL))),
+                                                    MV_WARPS * 32, st)));
+    }
+    return SPEC_OK;
+}
+
+template <class T>
+spec_status matvec(const MatmulParams& p, bool aligned, cudaStream_t st) {
+    return aligned ? matvec_as<T, true>(p, st) : matvec_as<T, false>(p, st);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static std::atomic<void*> found{nullptr};
+    void* f = found.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult how;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+            how != cudaDriverEntryPointSuccess)
+            return nullptr;
+        found.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+template <class T, bool PAIR>
+spec_status product_as(const ProductParams& p, int grid, cudaStream_t st) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
+    static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
+    const unsigned bit = dev < 32 ? 1u << dev : 0u;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(product_kernel<T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, PR_SMEM);
+        if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "product kernel attribute failed: %s", cudaGetErrorString(e));
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    return launched("product", launch_behind(product_kernel<T, PAIR>, p, dim3(grid), PR_THREADS, st, PR_SMEM, PAIR ? 2 : p.split));
+}
+
+spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not to be had");
+    ProductParams p = {};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.K), static_cast<cuuint64_t>(m.C)};
+    const cuuint64_t strides[1] = {m.C > 1 ? static_cast<cuuint64_t>(m.w_stride) : static_cast<cuuint64_t>((m.K + 15) / 16 * 16)};
+    const cuuint32_t box[2] = {PR_K, PR_CH}, one[2] = {1, 1};
+    if (encode(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<signed char*>(m.w), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return fail(SPEC_ERR_CUDA, "no tensor map for w");
+    p.out = m.out;
+    p.tokens16 = ws + SPEC_SCORE_WS_HEADER;
+    p.a_scale = m.a_scale;
+    p.w_scale = m.w_scale;
+    p.bias = m.bias;
+    p.tokens = m.tokens;
+    p.N = m.N;
+    p.C = m.C;
+    p.steps = (m.K + PR_K - 1) / PR_K;
+    p.status = reinterpret_cast<unsigned*>(ws);
+    p.token_tiles = (m.tokens + PR_TOKENS - 1) / PR_TOKENS;
+    const bool pair = m.tokens > 64 && static_cast<long long>((m.C + 2 * PR_CH - 1) / (2 * PR_CH)) * p.token_tiles >= sms / 4;
+    if (!pair) p.token_tiles = (m.tokens + PR_TOKENS_ALONE - 1) / PR_TOKENS_ALONE;
+    const int per = (m.tokens + p.token_tiles - 1) / p.token_tiles;
+    p.n = pair ? (per + 31) / 32 * 32 : (per + 15) / 16 * 16;
+    p.channel_tiles = (m.C + PR_CH * (pair ? 2 : 1) - 1) / (PR_CH * (pair ? 2 : 1));
+    const long long units = static_cast<long long>(p.channel_tiles) * p.token_tiles;
+    p.split = 1;
+    if (!pair)
+        while (p.split < 8 && units * p.split * 2 <= sms && p.split * 2 <= p.steps) p.split *= 2;
+    p.stages = std::min(PR_STAGES, (PR_SMEM - 1024) / (PR_W_BYTES + 2 * 128 * (pair ? p.n / 2 : p.n)));
+    if (p.stages < PR_MIN_STAGES) return fail(SPEC_ERR_CUDA, "no room for %d stages", PR_MIN_STAGES);
+    p.stream_w = p.token_tiles <= 8;
+    HalvesParams h = {};
+    h.a = m.a;
+    h.out = ws + SPEC_SCORE_WS_HEADER;
+    h.tokens = m.tokens;
+    h.N = m.N;
+    h.K = m.K;
+    h.n = p.n;
+    h.steps = p.steps;
+    h.groups = static_cast<long long>(p.token_tiles) * p.n * p.steps * (PR_K / 16);
+    SPECS_TRY(launched("product's halves", launch_behind(halves_kernel, h, dim3(static_cast<unsigned>((h.groups + 255) / 256)), 256, st)));
+    if (pair) {
+        const int grid = static_cast<int>(std::min<long long>(units, sms / 2)) * 2;
+        return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, true>(p, grid, st)
+               : out_type == SPEC_FP16 ? product_as<__half, true>(p, grid, st) : product_as<float, true>(p, grid, st);
+    }
+    const int grid = p.split > 1 ? static_cast<int>(units) * p.split : static_cast<int>(std::min<long long>(units, sms));
+    return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false>(p, grid, st)
+           : out_type == SPEC_FP16 ? product_as<__half, false>(p, grid, st) : product_as<float, false>(p, grid, st);
+}
 
 }  // namespace
 }  // namespace specs
@@ -216,10 +339,12 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     p.N = N;
     p.C = C;
     p.K = K;
-    p.status = static_cast<unsigned*>(workspace);
-    void (*const fn)(const MatmulParams) = out_type == SPEC_BF16   ? matmul_kernel<__nv_bfloat16>
-                                           : out_type == SPEC_FP16 ? matmul_kernel<__half> : matmul_kernel<float>;
-    return launched("product", launch_behind(fn, p, dim3((C + MT - 1) / MT, (p.tokens + MT - 1) / MT), 256, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool codes16 = aligned16(w) && (C == 1 || w_stride % 16 == 0);
+    if (p.tokens > 8 && codes16) return product(p, out_type, static_cast<unsigned char*>(workspace), st);
+    const bool aligned = codes16 && K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
+    return out_type == SPEC_BF16   ? matvec<__nv_bfloat16>(p, aligned, st)
+           : out_type == SPEC_FP16 ? matvec<__half>(p, aligned, st) : matvec<float>(p, aligned, st);
 }
 
 spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R, int V, const int32_t* tokens, int T,

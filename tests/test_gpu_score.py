@@ -183,7 +183,8 @@ def check_product(a, w, seed=0, dtype=BF16, bias=False, **kw):
 SHAPES = [(1, 1, 1), (1, 1, 16), (1, 128, 64), (2, 3, 4), (1, 4096, 4096), (3, 129, 512), (7, 127, 1000), (8, 256, 528), (16, 128, 128),
           (17, 300, 144), (33, 1000, 2064), (64, 512, 513), (65, 64, 4096), (96, 640, 1024), (129, 257, 112), (192, 256, 1536),
           (193, 384, 640), (200, 130, 48), (256, 1024, 4096), (384, 2000, 1040), (385, 515, 16), (1000, 768, 272), (1, 70, 16400),
-          (5, 40, 131071), (2, 16, 131056), (640, 33, 2048)]
+          (5, 40, 131071), (2, 16, 131056), (640, 33, 2048), (65, 9800, 272), (70, 38900, 144), (193, 6000, 400), (250, 5001, 2064),
+          (1000, 2100, 640), (2500, 1300, 128), (9, 20000, 64), (40, 5000, 16400)]
 
 
 @pytest.mark.parametrize("M,C,K", SHAPES)
@@ -464,6 +465,19 @@ def test_two_products_at_once_on_two_streams():
     for row in outs:
         for got, job in zip(row, jobs):
             assert torch.equal(got, job[-1])
+
+
+@pytest.mark.parametrize("M,C,K", [(1100, 11, 2048), (4265, 11, 13648), (300, 40, 1024), (12, 700, 4096), (384, 9999, 512)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_products_in_a_row(M, C, K, dtype):
+    """Calls that nothing waits between, few and many channels to many and few tokens."""
+    a, w = ints(M, K, 40).cuda(), ints(C, K, 41).cuda()
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    sa, sw, ws = one(M), one(C), sv.new_matmul_workspace(M, C, K)
+    want = (a.double() @ w.double().t()).float().to(dtype)
+    outs = [sv.int8_matmul(a, sa, w, sw, dtype=dtype, workspace=ws)["out"] for _ in range(30)]
+    torch.cuda.synchronize()
+    assert sv.read_status(ws) == 0 and all(torch.equal(o, want) for o in outs)
 
 
 def test_empty_calls():
