@@ -10,7 +10,7 @@ namespace specs {
 using specv::smem_addr;
 
 // A step is 128 of K: 128 channels' codes as they are (16 KB) and the tokens' halves.
-constexpr int PR_K = 128, PR_CH = 128, PR_TOKENS = 192, PR_THREADS = 512, PR_STAGES = 11;
+constexpr int PR_K = 128, PR_CH = 128, PR_TOKENS = 192, PR_THREADS = 640, PR_STAGES = 11;
 // Warps that turn step g's codes wait for its copies when they have written step g - 2, so when the products of step g - 4 are
 // done: the stage's barrier is then in the phase that they mean only if its last use was no later than that.
 constexpr int PR_MIN_STAGES = 4, PR_TOKENS_ALONE = 128;      // a CTA without a pair has room for four stages up to 144 tokens
@@ -18,11 +18,8 @@ constexpr int PR_W_BYTES = PR_CH * PR_K;
 constexpr int PR_SMEM = 224 * 1024;                    // of it up to 1 KB is lost to alignment
 constexpr uint32_t PR_COL_A = 2 * PR_TOKENS;           // tensor memory: two accumulators, two steps of channels
 constexpr uint64_t PR_WAIT_NS = 2000000000ull;
-// The sum of two steps is at most 256 x 2^14 = 2^22 in magnitude, so exact in fp32 as are its parts. Added to 1.5 x 2^23, whose last
-// place is 1, it stands in the last bits of the sum (2^22 itself carries into the exponent, and the bits still count on).
-constexpr int PR_CHUNK = 2;
-constexpr float PR_MAGIC = 12582912.f;
-constexpr uint32_t PR_MAGIC_BITS = 0x4B400000u;
+// The sum of four steps is at most 512 x 2^14 = 2^23 in magnitude, so exact in fp32 as are its parts.
+constexpr int PR_CHUNK = 4;
 
 struct ProductParams {
     CUtensorMap w;       // 64-byte aligned, as its type says
@@ -87,26 +84,38 @@ __global__ void __launch_bounds__(256) halves_kernel(const __grid_constant__ Hal
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
     return ok != 0;
 }
-// Waits, as a warp, for a phase of `bar`. Where it gives up it sets the status bit and clears `alive`, so that later waits end at
-// once: the results are invalid, but every barrier behind is still met.
+// Waits, as a warp, for a phase of `bar`. A lane that gives up sets the status bit and clears its `alive`, so that its later waits end
+// at once: the results are invalid, but every barrier behind is still met.
 __device__ __forceinline__ void wait_phase(uint64_t* bar, uint32_t parity, bool& alive, unsigned* status) {
     uint64_t since = 0;
-    for (int i = 1; !__all_sync(0xffffffffu, phase_done(bar, parity)) && alive; ++i) {
+    for (int i = 1; !phase_done(bar, parity) && alive; ++i) {
         if (i % 256 == 0) {
             const uint64_t now = specv::global_timer_ns();
             if (since == 0) since = now;
-            if (!__all_sync(0xffffffffu, now - since < PR_WAIT_NS)) {
+            if (now - since >= PR_WAIT_NS) {
                 atomicOr(status, SPEC_STATUS_TIMEOUT);
                 alive = false;
             }
         }
     }
+    __syncwarp();
+}
+
+// Whether the phase is over, without a wait.
+__device__ __forceinline__ bool phase_over(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Arrives at the barrier of the pair's first CTA (its own one where there is no pair).
@@ -115,33 +124,42 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
     if (PAIR)
         asm volatile(
             "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-            "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
+            "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar))
             : "memory");
     else
         specv::mbar_arrive(bar);
 }
 
+// Of the lane with `lead`, in converged code: so the operands stay where the warp's common values are.
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t* bar) {      // of both CTAs of a pair
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {      // at both CTAs of a pair
     if (PAIR)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-            "h"(static_cast<unsigned short>(3))
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+            "h"(static_cast<unsigned short>(3)), "r"(lead)
             : "memory");
     else
-        specc::umma_commit(bar);
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(lead)
+            : "memory");
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
     if (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-            "r"(static_cast<uint32_t>(add))
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+            "r"(static_cast<uint32_t>(add)), "r"(lead)
             : "memory");
     else
-        specc::umma_ts(d, a, b, idesc, add);
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+            "r"(static_cast<uint32_t>(add)), "r"(lead)
+            : "memory");
 }
 
 __device__ __forceinline__ void load_codes(void* dst, const CUtensorMap* map, int k, int channel, uint64_t* bar, uint64_t policy) {
@@ -152,9 +170,9 @@ __device__ __forceinline__ void load_codes(void* dst, const CUtensorMap* map, in
         : "memory");
 }
 
-// Tokens' halves in shared memory: rows of 128 bytes, swizzled, eight rows to 1024 bytes.
+// Tokens' halves in shared memory: rows of 128 bytes, swizzled, eight rows to 1024 bytes; `addr` in 16 bytes.
 __device__ __forceinline__ uint64_t tokens_desc(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return static_cast<uint64_t>(addr & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
 template <int REGS, bool MORE>
@@ -180,13 +198,14 @@ struct Unit {
 //   warp 0         copies: the channels' codes as they are in memory, the tokens' halves
 //   warp 1         products: D[channel, token] += A[channel, k] B[k, token], A in tensor memory, 16 of K at a time
 //   warps 4 .. 11  codes to halves, exactly, from shared to tensor memory; two halves of the warps take the steps in turn
-//   warps 12 .. 15 sums of 256 products out of the tensor memory into integers in registers, and at the end to the output
+//   warps 12 .. 19 sums of 512 products out of the tensor memory into integers in registers, and at the end to the output; each half
+//                  of the warps takes half of the tokens
 // PAIR: two CTAs share a tile of 256 channels; each holds its channels and half of the tokens, the first one issues.
 // split > 1: the CTAs of a cluster share a tile's K, and add their integers through one another's shared memory.
 template <class T, bool PAIR>
 __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char dynamic[];
-    __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[2], s_a_empty[2], s_acc_full[2], s_acc_empty[2];
+    __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[4], s_half_empty[2], s_acc_full[2], s_acc_empty[2];
     __shared__ uint32_t s_tmem;
     __shared__ float s_scale[PR_TOKENS];
     __shared__ long long s_row[PR_TOKENS];
@@ -201,10 +220,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
     const int k_to = PAIR ? p.steps : static_cast<int>(static_cast<long long>(p.steps) * (rank + 1) / p.split);
     if (tid == 0) {
         for (int i = 0; i < p.stages; ++i) specv::mbar_init(&s_full[i], 1), specv::mbar_init(&s_empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            specv::mbar_init(&s_ready[i], 4 * CTAS), specv::mbar_init(&s_a_empty[i], 1);
-            specv::mbar_init(&s_acc_full[i], 1), specv::mbar_init(&s_acc_empty[i], 4 * CTAS);
-        }
+        for (int i = 0; i < 4; ++i) specv::mbar_init(&s_ready[i], 4 * CTAS);
+        for (int i = 0; i < 2; ++i) specv::mbar_init(&s_half_empty[i], 1), specv::mbar_init(&s_acc_full[i], 1), specv::mbar_init(&s_acc_empty[i], 8 * CTAS);
         specv::fence_mbarrier_init_cluster();
     }
     if (warp == 2) {
@@ -224,7 +241,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
     auto wait = [&](uint64_t* bar, uint32_t parity) { wait_phase(bar, parity, alive, p.status); };
 
     if (warp < 4) {
-        set_registers<40, false>();
+        set_registers<48, false>();
         if (warp == 0) {
             // ================ copies
             const uint64_t keep = specv::policy_evict_last(), w_policy = p.stream_w ? specv::policy_evict_first() : specv::policy_evict_normal();
@@ -248,126 +265,133 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                 for (; ahead < p.stages && k_from + ahead < k_to; ++ahead) codes(ahead, u, k_from + ahead);
             }
             asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
-            int g = 0;
+            int g = 0, st = 0;
+            uint32_t round = 0;      // of the stages' uses
             for (long long i = first; i < units; i += by) {
                 const Unit u(p, i);
-                for (int k = k_from; k < k_to; ++k, ++g) {
-                    const int st = g % p.stages, round = g / p.stages;
+                for (int k = k_from; k < k_to; ++k) {
                     if (g >= ahead) {
                         if (round > 0) wait(&s_empty[st], (round - 1) & 1);
-                        if (!alive) break;
-                        codes(st, u, k);
+                        if (alive) codes(st, u, k);
                     }
                     __syncwarp();
-                    tokens(st, u, k);
+                    if (alive) tokens(st, u, k);
+                    ++g;
+                    if (++st == p.stages) st = 0, ++round;
                 }
-                if (!alive) break;
             }
             // this CTA's copies have landed, and the products' arrivals are in, before it ends
             for (int i = max(0, g - p.stages); i < g; ++i) {
-                bool once = true;
+                bool once = alive;
                 wait_phase(&s_full[i % p.stages], (i / p.stages) & 1, once, p.status);
                 wait(&s_empty[i % p.stages], (i / p.stages) & 1);
             }
         } else if (warp == 1 && (!PAIR || rank == 0)) {
-            // ================ products
+            // ================ products, issued by one lane
+            const uint32_t lead = specc::elect_one();
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) | (static_cast<uint32_t>(PR_CH * CTAS >> 4) << 24);
-            int g = 0, chunk = 0;
-            for (long long i = first; i < units; i += by) {
-                for (int k = k_from; k < k_to; ++k, ++g) {
-                    const int st = g % p.stages, at = (k - k_from) % PR_CHUNK;
-                    const uint32_t d = tmem + (chunk & 1) * PR_TOKENS, a = tmem + PR_COL_A + (g & 1) * 64;
-                    if (at == 0 && chunk >= 2) wait(&s_acc_empty[chunk & 1], ((chunk >> 1) - 1) & 1);
-                    wait(&s_ready[g & 1], (g >> 1) & 1);
-                    specc::tmem_fence_after();
-                    const bool last = at == PR_CHUNK - 1 || k + 1 == k_to;
-                    if (alive && specc::elect_one()) {
-                        const uint32_t b = smem_addr(smem + st * stage_bytes + PR_W_BYTES);
+            const uint32_t base = smem_addr(smem + PR_W_BYTES) >> 4, half = half_bytes >> 4;
+            int st = 0, chunk = 0;
+            uint32_t at = 0;                                         // half steps
+            bool over = phase_over(&s_ready[0], 0);                  // looked at one half step ahead
+            for (long long i = first; i < units; i += by)
+                for (int k = k_from; k < k_to; ++k) {
+                    const bool starts = (k - k_from) % PR_CHUNK == 0, ends = (k - k_from) % PR_CHUNK == PR_CHUNK - 1 || k + 1 == k_to;
+                    const uint32_t d = tmem + (chunk & 1) * PR_TOKENS, b = base + st * (stage_bytes >> 4);
+                    if (starts && chunk >= 2) wait(&s_acc_empty[chunk & 1], ((chunk >> 1) - 1) & 1);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mma<PAIR>(d, a + 8 * j, tokens_desc(b + (j / 4) * half_bytes + (j % 4) * 32), idesc, at > 0 || j > 0);
-                        commit<PAIR>(&s_empty[st]);
-                        commit<PAIR>(&s_a_empty[g & 1]);
-                        if (last) commit<PAIR>(&s_acc_full[chunk & 1]);
+                    for (int h = 0; h < 2; ++h, ++at) {
+                        if (!__all_sync(0xffffffffu, over)) wait(&s_ready[at & 3], (at >> 2) & 1);
+                        specc::tmem_fence_after();
+                        over = phase_over(&s_ready[(at + 1) & 3], ((at + 1) >> 2) & 1);
+                        const uint32_t a = tmem + PR_COL_A + (at & 3) * 32, go = alive ? lead : 0u;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma<PAIR>(d, a + 8 * j, tokens_desc(b + h * half + j * 2), idesc, !starts || h > 0 || j > 0, go);
+                        commit<PAIR>(h ? &s_empty[st] : &s_half_empty[(at >> 1) & 1], go);
+                        if (h && ends) commit<PAIR>(&s_acc_full[chunk & 1], go);
                     }
-                    __syncwarp();
-                    if (last) ++chunk;
+                    if (ends) ++chunk;
+                    if (++st == p.stages) st = 0;
                 }
-            }
         }
     } else if (warp < 12) {
         // ================ codes to halves
-        set_registers<104, false>();
+        set_registers<80, false>();
         const int mine = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t to = tmem + PR_COL_A + mine * 64 + (static_cast<uint32_t>(warp & 3) << 21);
-        int g = 0, last = -1;
+        int g = 0, st = -1, used = -1;      // step, its stage, the stage of this buffer's last step
+        uint32_t round = 0, used_round = 0;
         for (long long i = first; i < units; i += by)
             for (int k = k_from; k < k_to; ++k, ++g) {
+                if (++st == p.stages) st = 0, ++round;
                 if ((g & 1) != mine) continue;
-                last = g;
-                const int st = g % p.stages;
-                wait(&s_full[st], (g / p.stages) & 1);
+                wait(&s_full[st], round & 1);
                 const unsigned char* const src = smem + st * stage_bytes + row * 128;
                 uint4 v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) * 16));
-                if (g >= 2) wait(&s_a_empty[mine], ((g >> 1) - 1) & 1);
-                specc::tmem_fence_after();
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    uint32_t h[16];
-                    halves_of(v[j].x, h[0], h[1]), halves_of(v[j].y, h[2], h[3]);
-                    halves_of(v[j].z, h[4], h[5]), halves_of(v[j].w, h[6], h[7]);
-                    halves_of(v[j + 1].x, h[8], h[9]), halves_of(v[j + 1].y, h[10], h[11]);
-                    halves_of(v[j + 1].z, h[12], h[13]), halves_of(v[j + 1].w, h[14], h[15]);
-                    specc::tmem_st16(to + 8 * j, h);
+                for (int half = 0; half < 2; ++half) {
+                    // the buffer's half is free when the products of step g - 2 have read it; of the second half that is when they are done
+                    if (g >= 2) half ? wait(&s_empty[used], used_round & 1) : wait(&s_half_empty[mine], ((g >> 1) - 1) & 1);
+                    specc::tmem_fence_after();
+#pragma unroll
+                    for (int j = 4 * half; j < 4 * half + 4; j += 2) {
+                        uint32_t h[16];
+                        halves_of(v[j].x, h[0], h[1]), halves_of(v[j].y, h[2], h[3]);
+                        halves_of(v[j].z, h[4], h[5]), halves_of(v[j].w, h[6], h[7]);
+                        halves_of(v[j + 1].x, h[8], h[9]), halves_of(v[j + 1].y, h[10], h[11]);
+                        halves_of(v[j + 1].z, h[12], h[13]), halves_of(v[j + 1].w, h[14], h[15]);
+                        specc::tmem_st16(to + 8 * j, h);
+                    }
+                    specc::tmem_wait_st();
+                    specc::tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_first<PAIR>(&s_ready[2 * mine + half]);
                 }
-                specc::tmem_wait_st();
-                specc::tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first<PAIR>(&s_ready[mine]);
+                used = st, used_round = round;
             }
-        if (last >= 0) wait(&s_a_empty[mine], (last >> 1) & 1);      // no arrival comes in behind the CTA's end
+        if (used >= 0) wait(&s_half_empty[mine], ((g - 1 - ((g - 1) & 1 ^ mine)) >> 1) & 1);      // no arrival comes in behind the CTA's end
     } else {
         // ================ sums, and the output
-        set_registers<232, true>();
+        set_registers<136, true>();
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const uint32_t from = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const int in_tile = (warp & 3) * 32 + lane;
+        const int low = (warp - 12) >> 2 ? (p.n / 2 + 15) / 16 * 16 : 0, high = (warp - 12) >> 2 ? p.n : (p.n / 2 + 15) / 16 * 16;
         int chunk = 0;
         for (long long i = first; i < units; i += by) {
             const Unit u(p, i);
-            const int t0 = u.tile * p.n, nt = min(p.n, p.tokens - t0);
+            const int t0 = u.tile * p.n, nt = min(p.n, p.tokens - t0), mine = min(high, nt) - low;      // tokens; this warp's
             __syncwarp();      // these barriers are for whole warps
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            for (int j = tid - 384; j < nt; j += 128) {
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            for (int j = tid - 384; j < nt; j += 256) {
                 const int t = t0 + j, b = t / p.N;
                 s_scale[j] = p.a_scale[t];
                 s_row[j] = b * p.out.sb + (t - b * p.N) * p.out.sn;
             }
             __syncwarp();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
             const int c = (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH + in_tile;
-            uint32_t acc[PR_TOKENS];
+            int acc[PR_TOKENS / 2];
 #pragma unroll
-            for (int j = 0; j < PR_TOKENS; ++j) acc[j] = 0u;
+            for (int j = 0; j < PR_TOKENS / 2; ++j) acc[j] = 0;
             const int chunks = (k_to - k_from + PR_CHUNK - 1) / PR_CHUNK;
             for (int q = 0; q < chunks; ++q, ++chunk) {
                 wait(&s_acc_full[chunk & 1], (chunk >> 1) & 1);
                 specc::tmem_fence_after();
 #pragma unroll
-                for (int j = 0; j < PR_TOKENS; j += 32)
-                    if (j < p.n) {
-                        uint32_t v[32];
-                        specc::tmem_ld(from + (chunk & 1) * PR_TOKENS + j, v);
+                for (int j = 0; j < PR_TOKENS / 2; j += 16)
+                    if (low + j < high) {
+                        uint32_t v[16];
+                        specc::tmem_ld(from + (chunk & 1) * PR_TOKENS + low + j, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[j + e] += __float_as_uint(__uint_as_float(v[e]) + PR_MAGIC);
+                        for (int e = 0; e < 16; ++e) acc[j + e] += __float2int_rn(__uint_as_float(v[e]));
                     }
                 specc::tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_first<PAIR>(&s_acc_empty[chunk & 1]);
             }
-            const uint32_t off = static_cast<uint32_t>(chunks) * PR_MAGIC_BITS;
             const float ws = c < p.C ? p.w_scale[c] : 0.f, bias = p.bias && c < p.C ? p.bias[c] : 0.f;
             T* const out = static_cast<T*>(p.out.p) + c;
             auto put = [&](int j, int sum) {
@@ -379,15 +403,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                 // one tile a cluster: its CTAs add their sums, each for every split-th token
                 int* const part = reinterpret_cast<int*>(smem) + in_tile;
 #pragma unroll
-                for (int j = 0; j < PR_TOKENS; j += 32)
-                    if (j < nt) {
+                for (int j = 0; j < PR_TOKENS / 2; j += 16)
+                    if (j < mine) {
 #pragma unroll
-                        for (int e = j; e < j + 32; ++e)
-                            if (e < nt) part[e * PR_CH] = static_cast<int>(acc[e] - off);
+                        for (int e = j; e < j + 16; ++e)
+                            if (e < mine) part[(low + e) * PR_CH] = acc[e];
                     }
                 __syncwarp();
                 specv::cluster_sync_all();
-                for (int j = rank; j < nt; j += p.split) {
+                for (int j = rank + ((warp - 12) >> 2) * p.split; j < nt; j += 2 * p.split) {
                     int sum = 0;
                     for (int r = 0; r < p.split; ++r)
                         sum += __float_as_int(specv::ld_cluster_f32(specv::map_to_rank(smem_addr(part + j * PR_CH), r)));
@@ -397,16 +421,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                 specv::cluster_sync_all();
             } else {
 #pragma unroll
-                for (int j = 0; j < PR_TOKENS; j += 32)
-                    if (j < nt) {
+                for (int j = 0; j < PR_TOKENS / 2; j += 16)
+                    if (j < mine) {
 #pragma unroll
-                        for (int e = j; e < j + 32; ++e)
-                            if (e < nt) put(e, static_cast<int>(acc[e] - off));
+                        for (int e = j; e < j + 16; ++e)
+                            if (e < mine) put(low + e, acc[e]);
                     }
             }
         }
     }
-    // What follows is run by warps with 40 and with 232 registers: it needs a few.
+    // What follows is run by warps with 48 and with 136 registers: it needs a few.
     __syncwarp();
     if (!PAIR && p.split > 1 && warp < 12) {      // the barriers around the sums' exchange above
         specv::cluster_sync_all();
