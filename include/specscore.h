@@ -33,7 +33,7 @@ enum { SPEC_INT8 = 3 };   /* a further value of the type arguments of this heade
 #define SPEC_SCORE_MAX_D 32768          /* values of a row of spec_residual_norm and spec_quantize_rows */
 #define SPEC_SCORE_MAX_K 131071         /* products of a sum: the longest that 32 bits always hold */
 #define SPEC_SCORE_MAX_ROWS 65          /* logits rows of a sequence */
-#define SPEC_SCORE_MAX_HISTORY 1000000  /* tokens of a history */
+#define SPEC_SCORE_MAX_HISTORY 500000   /* tokens of a history */
 #define SPEC_SCORE_MAX_BIASES 1024      /* biases of a sequence */
 #define SPEC_SCORE_WS_HEADER 256        /* bytes of a workspace that are zeroed before its first use */
 

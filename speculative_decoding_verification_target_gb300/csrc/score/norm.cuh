@@ -10,20 +10,204 @@ struct NormParams {
     float* scale;
     long long rows;
     int N, D;
+    int tpr;       // threads of a row: a multiple of 32
     float eps;
     int norm;      // 0: codes of x as it is
 };
 
-// The integer nearest to 127 p / m, even on ties. p and m hold at most 24 significant bits, so the quotient in 64 bits is on
-// the side of a half-integer that the exact one is on, and equal to it where that is.
-__device__ __forceinline__ int code_exact(float p, float m) {
-    return __double2int_rn(127.0 * static_cast<double>(p) / static_cast<double>(m));
+// The larger magnitude; a NaN stays.
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
+// 127 p / m is rounded to the nearest integer, ties to even, as if it were exact. In fp32, p times the rounded 127 / m is off by
+// 127 x 2^-23 at most, so the integer next to it is the right one unless it lies that near to the middle of two. There the
+// exact products decide: with k the integer below, 254 p against (2 k + 1) m, each as a float and its rounding error.
+struct Codes {
+    float m, by, scale;      // the row's largest magnitude, 127 / m, and the power of two that brings m into range for the exact step
+    bool all;                // every code by the exact step
+    __device__ explicit Codes(float top) : m(top) {
+        scale = top < 8.6736174e-19f ? 1.8446744e19f : top > 1.1529215e18f ? 5.4210109e-20f : 1.f;      // 2^-60: 2^64, 2^60: 2^-64
+        all = scale != 1.f;
+        by = top > 0.f ? 127.f / top : 0.f;
+    }
+    __device__ int exact(float p) const {
+        if (m == 0.f) return 0;
+        float ps = p * scale, ms = m * scale;
+        if (ms < 8.6736174e-19f) ps *= 1.8446744e19f, ms *= 1.8446744e19f;      // the smallest subnormal numbers
+        const float k = floorf(ps * (127.f / ms)), h = 2.f * k + 1.f;
+        const float a = 254.f * ps, b = h * ms;
+        const float d = (a - b) + (fmaf(254.f, ps, -a) - fmaf(h, ms, -b));
+        const bool up = d > 0.f || (d == 0.f && (static_cast<int>(k) & 1));
+        return static_cast<int>(k) + (up ? 1 : 0);
+    }
+    // Codes of n values; the low byte of each float's bits in c.
+    template <int n>
+    __device__ void of(const float (&p)[n], uint32_t (&c)[n]) const {
+        float off = all ? 1.f : 0.f;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float q = p[i] * by, f = q + 12582912.f;      // its last place is 1
+            off = fmaxf(off, fabsf(q - (f - 12582912.f)));
+            c[i] = __float_as_uint(f);
+        }
+        if (off > 0.49998f) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) c[i] = static_cast<uint32_t>(exact(p[i]));
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// A piece of a row: 16 bytes of values where the rows allow it, else one value.
+template <class T, bool VEC>
+struct Piece {
+    static constexpr int E = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
+    using Raw = std::conditional_t<VEC, uint4, T>;
+    static __device__ void get(const Raw& r, float (&v)[E]) {
+        if constexpr (!VEC) v[0] = to_float(r);
+        else if constexpr (std::is_same_v<T, float>) {
+            v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+        } else {
+            specc::Eight<T> e;
+            e.r = r;
+            e.get(v);
+        }
+    }
+    static __device__ Raw put(const float (&v)[E]) {
+        if constexpr (!VEC) return from_float<T>(v[0]);
+        else if constexpr (std::is_same_v<T, float>)
+            return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else {
+            specc::Eight<T> e;
+            e.set(v);
+            return e.r;
+        }
+    }
+    static __device__ void codes(signed char* to, const uint32_t (&c)[E]) {
+        if constexpr (E == 1) *to = static_cast<signed char>(c[0]);
+        else if constexpr (E == 4) *reinterpret_cast<uint32_t*>(to) = pack4(c[0], c[1], c[2], c[3]);
+        else *reinterpret_cast<uint2*>(to) = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+    }
+};
+
+// The sum and the largest magnitude over a row's `warps` warps, the first of which is `from`; `turn` alternates.
+__device__ __forceinline__ void join_row(float& sum, float& top, int from, int warps, int turn, float2 (*s_part)[32]) {
+    sum = specv::warp_sum(sum);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));      // not negative; a NaN is the largest
+    if (warps == 1) return;
+    if ((threadIdx.x & 31) == 0) s_part[turn][threadIdx.x >> 5] = make_float2(sum, top);
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const float2 v = lane < warps ? s_part[turn][from + lane] : make_float2(0.f, 0.f);
+    sum = specv::warp_sum(v.x);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v.y)));
+}
+
+// A row is in the registers of tpr threads, SLOTS pieces each, between its one read and its one write; the next row of these
+// threads is on its way meanwhile, and the weights stay. Bandwidth bounds many rows, latency few: there a row has more threads.
+template <class T, bool CODES, int SLOTS, bool VEC>
+__global__ void __launch_bounds__(512) norm_rows_kernel(const __grid_constant__ NormParams p) {
+    using P = Piece<T, VEC>;
+    using Raw = typename P::Raw;
+    constexpr int E = P::E;
+    __shared__ float2 s_part[2][32];
+    after_previous();
+    const int per = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, c = threadIdx.x - sub * p.tpr, pieces = (p.D + E - 1) / E;
+    const bool with = p.res.p != nullptr;
+    Raw x[SLOTS], y[SLOTS], w[SLOTS];
+    auto place = [&](const Rows& t, long long row) {
+        const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<long long>(b) * p.N);
+        return b * t.sb + n * t.sn;
+    };
+    auto fetch = [&](long long row) {
+        if (row >= p.rows) return;
+        const T* const px = static_cast<const T*>(p.x.p) + place(p.x, row);
+        const T* const py = with ? static_cast<const T*>(p.res.p) + place(p.res, row) : px;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (c + s * p.tpr < pieces) {
+                x[s] = *reinterpret_cast<const Raw*>(px + (c + s * p.tpr) * E);
+                if (with) y[s] = *reinterpret_cast<const Raw*>(py + (c + s * p.tpr) * E);
+            }
+    };
+    long long row = static_cast<long long>(blockIdx.x) * per + sub;
+    fetch(row);
+    if (p.weight) {
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (c + s * p.tpr < pieces) w[s] = *reinterpret_cast<const Raw*>(static_cast<const T*>(p.weight) + (c + s * p.tpr) * E);
+    }
+    const long long step = static_cast<long long>(gridDim.x) * per;
+    int turn = 0;
+    for (long long base = row - sub; base < p.rows; base += step, row += step, turn ^= 1) {
+        float r[SLOTS][E];
+        float sum = 0.f, top = 0.f;
+        T* const res_out = with && row < p.rows ? static_cast<T*>(p.res_out.p) + place(p.res_out, row) : nullptr;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            if (row >= p.rows || c + s * p.tpr >= pieces) continue;
+            P::get(x[s], r[s]);
+            if (with) {
+                float add[E];
+                P::get(y[s], add);
+#pragma unroll
+                for (int i = 0; i < E; ++i) r[s][i] += add[i];
+                const Raw rounded = P::put(r[s]);
+                *reinterpret_cast<Raw*>(res_out + (c + s * p.tpr) * E) = rounded;
+                P::get(rounded, r[s]);
+            }
+            float g[E];
+            if (p.weight) P::get(w[s], g);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                sum = fmaf(r[s][i], r[s][i], sum);
+                if (p.weight) r[s][i] *= g[i];
+                if (CODES) top = larger(top, r[s][i]);
+            }
+        }
+        fetch(row + step);
+        join_row(sum, top, threadIdx.x / 32 - c / 32, p.tpr / 32, turn, s_part);
+        if (row >= p.rows) continue;
+        const float inv = p.norm ? rsqrtf(sum / p.D + p.eps) : 1.f;
+        if constexpr (CODES) {
+            const bool bad = !(top < INFINITY);
+            const Codes codes(bad ? 0.f : top);
+            signed char* const out = static_cast<signed char*>(p.out.p) + place(p.out, row);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                if (c + s * p.tpr >= pieces) continue;
+                uint32_t q[E];
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) r[s][i] = 0.f;
+                }
+                codes.of(r[s], q);
+                P::codes(out + (c + s * p.tpr) * E, q);
+            }
+            if (c == 0) p.scale[row] = bad ? NAN : top / 127.f * inv;
+        } else {
+            T* const out = static_cast<T*>(p.out.p) + place(p.out, row);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                if (c + s * p.tpr >= pieces) continue;
+#pragma unroll
+                for (int i = 0; i < E; ++i) r[s][i] *= inv;
+                *reinterpret_cast<Raw*>(out + (c + s * p.tpr) * E) = P::put(r[s]);
+            }
+        }
+    }
+}
+
+// Rows that do not fit in registers: read twice, the second time from the caches.
 template <class T, bool CODES>
-__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float s_sum[8];
-    __shared__ unsigned s_max[8];
+__global__ void __launch_bounds__(512) norm_long_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float2 s_part[2][32];
     after_previous();
     const long long t = blockIdx.x;
     const int b = static_cast<int>(t / p.N), n = static_cast<int>(t - static_cast<long long>(b) * p.N);
@@ -34,28 +218,28 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormP
         const T v = x[i];
         return res ? to_float(from_float<T>(to_float(v) + to_float(res[i]))) : to_float(v);
     };
-    float sum = 0.f;
-    unsigned top = 0u;
-    for (int i = threadIdx.x; i < p.D; i += 256) {
-        const float r = value(i), q = w ? r * to_float(w[i]) : r;
+    float sum = 0.f, top = 0.f;
+    for (int i = threadIdx.x; i < p.D; i += 512) {
+        const float r = value(i);
         sum = fmaf(r, r, sum);
-        top = max(top, __float_as_uint(q) & 0x7FFFFFFFu);
+        top = larger(top, w ? r * to_float(w[i]) : r);
     }
-    sum = specv::warp_sum(sum);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum, s_max[threadIdx.x >> 5] = top;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < 8; ++i) sum += s_sum[i], top = max(top, s_max[i]);
-    const float inv = p.norm ? rsqrtf(sum / p.D + p.eps) : 1.f, m = __uint_as_float(top);
-    const bool bad = !(m < INFINITY);
-    for (int i = threadIdx.x; i < p.D; i += 256) {
-        const float r = value(i), q = w ? r * to_float(w[i]) : r;
+    join_row(sum, top, 0, 16, 0, s_part);
+    const float inv = p.norm ? rsqrtf(sum / p.D + p.eps) : 1.f;
+    const bool bad = !(top < INFINITY);
+    const Codes codes(bad ? 0.f : top);
+    for (int i = threadIdx.x; i < p.D; i += 512) {
+        const float r = value(i), q[1] = {w ? r * to_float(w[i]) : r};
         if (res) row_of<T>(p.res_out, b, n)[i] = from_float<T>(r);
-        if (CODES) row_of<signed char>(p.out, b, n)[i] = static_cast<signed char>(bad || m == 0.f ? 0 : code_exact(q, m));
-        else row_of<T>(p.out, b, n)[i] = from_float<T>(q * inv);
+        if (CODES) {
+            uint32_t c[1] = {0u};
+            if (!bad) codes.of(q, c);
+            row_of<signed char>(p.out, b, n)[i] = static_cast<signed char>(c[0]);
+        } else {
+            row_of<T>(p.out, b, n)[i] = from_float<T>(q[0] * inv);
+        }
     }
-    if (CODES && threadIdx.x == 0) p.scale[t] = bad ? NAN : m / 127.f * inv;
+    if (CODES && threadIdx.x == 0) p.scale[t] = bad ? NAN : top / 127.f * inv;
 }
 
 }  // namespace specs

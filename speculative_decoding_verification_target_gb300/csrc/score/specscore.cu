@@ -100,16 +100,57 @@ cudaError_t launch_behind(void (*fn)(const P), const P& p, dim3 grid, int thread
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
-// ---------------------------------------------------------------------------------------- norm and codes
-template <class T>
-spec_status norm_as(const NormParams& p, bool codes, cudaStream_t st) {
-    return launched("norm", launch_behind(codes ? norm_kernel<T, true> : norm_kernel<T, false>, p,
-                                          dim3(static_cast<unsigned>(p.rows)), 256, st));
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
 }
 
-spec_status norm(const NormParams& p, int dtype, bool codes, cudaStream_t st) {
-    return dtype == SPEC_BF16 ? norm_as<__nv_bfloat16>(p, codes, st)
-           : dtype == SPEC_FP16 ? norm_as<__half>(p, codes, st) : norm_as<float>(p, codes, st);
+// ---------------------------------------------------------------------------------------- norm and codes
+// Rows of one value short of 16 bytes anywhere go value by value.
+bool whole_pieces(const NormParams& p, size_t e, bool codes, int B) {
+    const int per = 16 / static_cast<int>(e);
+    auto fits = [&](const Rows& t, size_t bytes) {
+        return !t.p || (reinterpret_cast<uintptr_t>(t.p) % bytes == 0 && (B <= 1 || t.sb % per == 0) && (p.N <= 1 || t.sn % per == 0));
+    };
+    return p.D % per == 0 && fits(p.x, 16) && fits(p.res, 16) && fits(p.res_out, 16) && fits(p.out, codes ? per : 16) && aligned16(p.weight);
+}
+
+template <class T, bool CODES, bool VEC>
+auto norm_of(int slots) -> void (*)(const NormParams) {
+    if constexpr (VEC) return slots == 1 ? norm_rows_kernel<T, CODES, 1, VEC> : slots == 2 ? norm_rows_kernel<T, CODES, 2, VEC>
+                                                                                          : norm_rows_kernel<T, CODES, 4, VEC>;
+    else return slots <= 4 ? norm_rows_kernel<T, CODES, 4, VEC> : norm_rows_kernel<T, CODES, 16, VEC>;
+}
+
+template <class T, bool CODES>
+spec_status norm_as(NormParams p, bool vec, int sms, cudaStream_t st) {
+    const int pieces = vec ? p.D / (16 / static_cast<int>(sizeof(T))) : p.D, most = vec ? 4 : 16;
+    if (pieces > 512 * most)
+        return launched("norm", launch_behind(norm_long_kernel<T, CODES>, p, dim3(static_cast<unsigned>(p.rows)), 512, st));
+    // many rows: threads with four pieces, so that much is on its way; few: as many threads as there are pieces
+    const bool few = p.rows < 4LL * sms;
+    int slots = vec ? (few ? 1 : pieces >= 128 ? 4 : pieces >= 64 ? 2 : 1) : (few ? 4 : 16);
+    while ((pieces + slots - 1) / slots > 512) slots *= vec ? 2 : 4;
+    p.tpr = ((pieces + slots - 1) / slots + 31) / 32 * 32;
+    const int per = few ? 1 : std::max(1, 128 / p.tpr), threads = per * p.tpr;
+    const long long ctas = std::min((p.rows + per - 1) / per, static_cast<long long>(sms) * std::max(1, 512 / threads));
+    return launched("norm", launch_behind(vec ? norm_of<T, CODES, true>(slots) : norm_of<T, CODES, false>(slots), p,
+                                          dim3(static_cast<unsigned>(ctas)), threads, st));
+}
+
+template <class T>
+spec_status norm_as(const NormParams& p, bool codes, int B, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    const bool vec = whole_pieces(p, sizeof(T), codes, B);
+    return codes ? norm_as<T, true>(p, vec, sms, st) : norm_as<T, false>(p, vec, sms, st);
+}
+
+spec_status norm(const NormParams& p, int dtype, bool codes, int B, cudaStream_t st) {
+    return dtype == SPEC_BF16 ? norm_as<__nv_bfloat16>(p, codes, B, st)
+           : dtype == SPEC_FP16 ? norm_as<__half>(p, codes, B, st) : norm_as<float>(p, codes, B, st);
 }
 
 spec_status check_norm(int dtype, int B, int N, int D) {
@@ -121,13 +162,6 @@ spec_status check_norm(int dtype, int B, int N, int D) {
 }
 
 // --------------------------------------------------------------------------------------------- product
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 // Workspace: header, and the tokens' halves in tiles of equal width, a multiple of 32.
 size_t matmul_bytes(int tokens, int, int K) {
     const size_t tiles = (static_cast<size_t>(tokens) + PR_TOKENS - 1) / PR_TOKENS;
@@ -286,7 +320,7 @@ spec_status spec_residual_norm(const spec_rows* x, const spec_rows* residual, in
     p.D = D;
     p.eps = eps;
     p.norm = 1;
-    return norm(p, dtype, out_type == SPEC_INT8, static_cast<cudaStream_t>(stream));
+    return norm(p, dtype, out_type == SPEC_INT8, B, static_cast<cudaStream_t>(stream));
 }
 
 spec_status spec_quantize_rows(const spec_rows* x, int dtype, int B, int N, int D, const spec_rows* out, float* scale,
@@ -304,7 +338,7 @@ spec_status spec_quantize_rows(const spec_rows* x, int dtype, int B, int N, int 
     p.rows = static_cast<long long>(B) * N;
     p.N = N;
     p.D = D;
-    return norm(p, dtype, true, static_cast<cudaStream_t>(stream));
+    return norm(p, dtype, true, B, static_cast<cudaStream_t>(stream));
 }
 
 size_t spec_int8_matmul_workspace_size(int tokens, int C, int K) {
@@ -387,8 +421,18 @@ spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R
     p.T = T;
     p.L = L;
     p.biases = biases;
+    const int sms = sm_count();
+    if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
+    // as large a part of the vocabulary as still gives the card four CTAs an SM: each reads the whole history
+    p.seg = 8192;
+    while (p.seg > 1024 && static_cast<long long>((V + p.seg - 1) / p.seg) * B < 4LL * sms) p.seg /= 2;
+    auto alike = [&](long long x, long long y) { return (x - y) * static_cast<long long>(e) % 16 == 0; };
+    p.pieces = (reinterpret_cast<uintptr_t>(logits->data) - reinterpret_cast<uintptr_t>(out->data)) % 16 == 0 &&
+               (B == 1 || alike(logits->stride_b, out->stride_b)) && (R == 1 || alike(logits->stride_n, out->stride_n));
+    p.stream = out->data != logits->data || mask;
     return launched("logits", launch_behind(dtype == SPEC_BF16 ? logits_kernel<__nv_bfloat16> : logits_kernel<float>, p,
-                                            dim3((V + SEG - 1) / SEG, B), 256, static_cast<cudaStream_t>(stream)));
+                                            dim3((V + p.seg - 1) / p.seg, B), LG_THREADS, static_cast<cudaStream_t>(stream),
+                                            static_cast<size_t>(p.seg) * 4));
 }
 
 }  // extern "C"
