@@ -19,7 +19,10 @@ struct LogitsParams {
 // What the history, the drafts and the biases say of a token, in a word: bit 31 in the prompt, bit 30 among the drafts, bits
 // 11 .. 29 the times among the output, bits 0 .. 10 the number of its bias's entry + 1.
 constexpr unsigned W_PROMPT = 1u << 31, W_DRAFT = 1u << 30, W_ONE = 1u << 11, W_BIAS = W_ONE - 1, W_COUNT = W_DRAFT - W_ONE;
-constexpr int LG_THREADS = 256;
+constexpr int LG_SEG = 16384, LG_THREADS = 512;      // at most
+// Once all is counted, a word is the number that is taken off the logit: 0 for a token that nothing is said of, -0 where nothing is
+// taken off but the repetition counts. Tokens with a bias or among the drafts are kept in a list, and their words are 0.
+constexpr int LG_LIST = SPEC_SCORE_MAX_BIASES + SPEC_SCORE_MAX_ROWS;
 
 // The mask's bits of the `n` <= 8 tokens from v on; `last` is its last word.
 __device__ __forceinline__ unsigned mask_bits(const unsigned* mask, int v, int last, int n) {
@@ -45,84 +48,171 @@ __device__ __forceinline__ uint4 masked(uint4 x, unsigned bits) {
     return x;
 }
 
-// A CTA takes one sequence and `seg` tokens of the vocabulary, for all rows. It first copies the rows, 16 bytes at a time, with the
-// mask: bandwidth bounds that. What the sequence's tokens say comes from a table in shared memory, one word a token; the few
-// logits that it changes are then worked out once more, each by itself.
+// `n` <= 8 bits of the table's flags from v on; a word behind the last is there.
+__device__ __forceinline__ unsigned flag_bits(const unsigned* flags, int v, int n) {
+    return __funnelshift_r(flags[v >> 5], flags[(v >> 5) + 1], v & 31) & ((1u << n) - 1u);
+}
+
+// Where token v's word stands. 16-bit logits take eight words a piece: the first and the second four of them in parts of their own,
+// so that neighbouring lanes read neighbouring 16 bytes.
+template <int E>
+__device__ __forceinline__ int word_at(int v, int seg) {
+    return E == 4 ? v : ((v >> 3) + (v >> 2 & 1) * (seg / 8 + 1)) * 4 + (v & 3);
+}
+
+// The words of tokens v .. v + E - 1, v - from a multiple of four, `from` the same for every lane.
+template <int E>
+__device__ __forceinline__ void words_of(const unsigned* s_word, int v, int from, int seg, uint32_t (&w)[E]) {
+    uint32_t t[E + 4];
+#pragma unroll
+    for (int i = 0; i < E + 4; i += 4) {
+        if (i == E && from == 0) break;
+        const uint4 q = *reinterpret_cast<const uint4*>(s_word + word_at<E>(v - from + i, seg));
+        t[i] = q.x, t[i + 1] = q.y, t[i + 2] = q.z, t[i + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = from == 0 ? t[i] : from == 1 ? t[i + 1] : from == 2 ? t[i + 2] : t[i + 3];
+}
+
+// A CTA takes one sequence and `seg` tokens of the vocabulary, for all rows. What the sequence's tokens say comes first, from a
+// pass over its history, into a table in shared memory: a word for each token, and a bit for each that is not 0. Then the rows
+// go by, 16 bytes at a time: bandwidth bounds that. A piece without a bit is copied, with the mask; in the others every value goes
+// through the one formula, which leaves those that nothing is said of as they are. Listed tokens come last, each by itself.
 template <class T>
 __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constant__ LogitsParams p) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T));
-    extern __shared__ unsigned s_word[];
-    __shared__ unsigned s_draft[SPEC_SCORE_MAX_ROWS];
+    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 2;
+    extern __shared__ unsigned s_word[];                     // [seg + 8], then the bits [seg / 32 + 1]
+    __shared__ unsigned s_draft[SPEC_SCORE_MAX_ROWS], s_list[LG_LIST], s_listed;
+    __shared__ unsigned short s_token[LG_LIST];
     after_previous();
-    const int b = blockIdx.y, tid = threadIdx.x, last_word = (p.V - 1) / 32;
+    const int b = blockIdx.y, tid = threadIdx.x, threads = blockDim.x, last_word = (p.V - 1) / 32;
     const int v0 = blockIdx.x * p.seg, n = min(p.seg, p.V - v0);
-    for (int i = tid; i < p.seg / 4; i += LG_THREADS) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0u, 0u, 0u, 0u);
+    unsigned* const s_flag = s_word + p.seg + 8;
+    if (tid == 0) s_listed = 0u;
+    auto at = [&](int v) { return word_at<E>(v, p.seg); };
+    for (int i = tid; i < p.seg / 4 + 2; i += threads) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i <= p.seg / 32; i += threads) s_flag[i] = 0u;
     // drafts before a row: an id outside this part of the vocabulary is n or more, below 0 too
-    for (int j = tid; j < p.R; j += LG_THREADS)
+    for (int j = tid; j < p.R; j += threads)
         s_draft[j] = p.tokens && j < p.R - 1 ? static_cast<unsigned>(p.tokens[static_cast<long long>(b) * p.T + j]) - v0 : ~0u;
-    if (p.stream) {
-        for (int j = 0; j < p.R; ++j) {
-            const T* const in = row_of<T>(p.in, b, j) + v0;
-            T* const out = row_of<T>(p.out, b, j) + v0;
-            const unsigned* const mask = p.mask ? p.mask + b * p.mask_sb + j * p.mask_sr : nullptr;
-            int head = 0, whole = 0;
-            if (p.pieces) {
-                head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
-                whole = (n - head) / E;
-            }
-            const uint4* const from = reinterpret_cast<const uint4*>(in + head);
-            uint4* const to = reinterpret_cast<uint4*>(out + head);
-#pragma unroll 4
-            for (int i = tid; i < whole; i += LG_THREADS) {
-                uint4 x = from[i];
-                if (mask) x = masked<T>(x, mask_bits(mask, v0 + head + i * E, last_word, E));
-                to[i] = x;
-            }
-            for (int i = tid; i < n - whole * E; i += LG_THREADS) {      // the rest, one by one
-                const int at = i < head ? i : i + whole * E;
-                out[at] = !mask || mask_bits(mask, v0 + at, last_word, 1) ? in[at] : from_float<T>(-INFINITY);
-            }
-        }
-    }
     __syncthreads();
     if (p.bias_tokens) {
-        for (int i = tid; i < p.biases; i += LG_THREADS) {
+        for (int i = tid; i < p.biases; i += threads) {
             const unsigned v = static_cast<unsigned>(p.bias_tokens[static_cast<long long>(b) * p.biases + i]) - v0;
-            if (v < static_cast<unsigned>(n)) atomicMax(&s_word[v], static_cast<unsigned>(i + 1));
+            if (v < static_cast<unsigned>(n)) atomicMax(&s_word[at(v)], static_cast<unsigned>(i + 1));
         }
         __syncthreads();
     }
     if (p.history) {
         const int len = min(max(p.lengths[b], 0), p.L), pr = p.prompt ? p.prompt[b] : 0;
         const int* const h = p.history + static_cast<long long>(b) * p.L;
-#pragma unroll 4
-        for (int i = tid; i < len; i += LG_THREADS) {
-            const unsigned v = static_cast<unsigned>(__ldg(h + i)) - v0;
-            if (v >= static_cast<unsigned>(n)) continue;
-            if (i < pr) atomicOr(&s_word[v], W_PROMPT);
-            else atomicAdd(&s_word[v], W_ONE);
+        auto count = [&](int id, int i) {
+            const unsigned v = static_cast<unsigned>(id) - v0;
+            if (v >= static_cast<unsigned>(n)) return;
+            if (i < pr) atomicOr(&s_word[at(v)], W_PROMPT);
+            else atomicAdd(&s_word[at(v)], W_ONE);
+        };
+        const int fours = (reinterpret_cast<uintptr_t>(h) & 15u) == 0 ? len / 4 : 0;
+#pragma unroll 2
+        for (int i = tid; i < fours; i += threads) {
+            const int4 t = __ldg(reinterpret_cast<const int4*>(h) + i);
+            count(t.x, 4 * i), count(t.y, 4 * i + 1), count(t.z, 4 * i + 2), count(t.w, 4 * i + 3);
         }
+#pragma unroll 4
+        for (int i = 4 * fours + tid; i < len; i += threads) count(__ldg(h + i), i);
     }
-    for (int j = tid; j < p.R; j += LG_THREADS)
-        if (s_draft[j] < static_cast<unsigned>(n)) atomicOr(&s_word[s_draft[j]], W_DRAFT);
+    for (int j = tid; j < p.R; j += threads)
+        if (s_draft[j] < static_cast<unsigned>(n)) atomicOr(&s_word[at(s_draft[j])], W_DRAFT);
     __syncthreads();
     const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f,
-                pres = p.presence ? p.presence[b] : 0.f;
-    for (int v = tid; v < n; v += LG_THREADS) {
-        const unsigned w = s_word[v];
-        if (!w) continue;
-        const float add = w & W_BIAS ? p.bias[static_cast<long long>(b) * p.biases + (w & W_BIAS) - 1] : 0.f;
-        unsigned count = (w & W_COUNT) / W_ONE;
-#pragma unroll 4
-        for (int j = 0; j < p.R; ++j) {
-            if (j && s_draft[j - 1] == static_cast<unsigned>(v)) ++count;
-            if (!(w & (W_PROMPT | W_BIAS)) && !count) continue;
-            if (p.mask && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) continue;
-            float y = to_float(row_of<T>(p.in, b, j)[v0 + v]) + add;
-            if (count || w & W_PROMPT) y = y > 0.f ? y / rep : y * rep;
-            if (count) y = y - freq * static_cast<float>(count) - pres;
-            row_of<T>(p.out, b, j)[v0 + v] = from_float<T>(y);
+                pres = p.presence ? p.presence[b] : 0.f, per_rep = 1.f / rep;
+    // what n > 0 times among the output take off; n as a float without a conversion
+    auto taken = [&](unsigned n) { return n ? fmaf(freq, __uint_as_float(n | 0x4B000000u) - 8388608.f, pres) : 0.f; };
+    for (int i = tid; i < p.seg; i += threads) {             // whole warps: seg is a multiple of 32, and so are the threads
+        unsigned& word = s_word[at(i)];
+        const unsigned w = word;
+        const bool list = w & (W_BIAS | W_DRAFT);
+        const unsigned any = __ballot_sync(0xffffffffu, w != 0u && !list);
+        if (i % 32 == 0) s_flag[i / 32] = any;
+        if (list) {
+            const unsigned to = atomicAdd(&s_listed, 1u);
+            s_list[to] = w;
+            s_token[to] = static_cast<unsigned short>(i);
+            word = 0u;
+        } else if (w) {
+            const unsigned off = __float_as_uint(taken((w & W_COUNT) / W_ONE));
+            word = off ? off : 0x80000000u;
         }
+    }
+    __syncthreads();
+    auto simple = [&](float x, unsigned w) { return fmaf(x, w ? (x > 0.f ? per_rep : rep) : 1.f, -__uint_as_float(w)); };
+    for (int j = 0; j < p.R; ++j) {
+        const T* const in = row_of<T>(p.in, b, j) + v0;
+        T* const out = row_of<T>(p.out, b, j) + v0;
+        const unsigned* const mask = p.mask ? p.mask + b * p.mask_sb + j * p.mask_sr : nullptr;
+        int head = 0, whole = 0;
+        if (p.pieces) {
+            head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
+            whole = (n - head) / E;
+        }
+        const uint4* const from = reinterpret_cast<const uint4*>(in + head);
+        uint4* const to = reinterpret_cast<uint4*>(out + head);
+        // U pieces of a thread at once: their loads are on their way together
+        for (int i = tid; i < whole; i += U * threads) {
+            uint4 x[U];
+            unsigned flags[U], bits[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int q = i + k * threads;
+                flags[k] = q < whole ? flag_bits(s_flag, head + q * E, E) : 0u;
+                bits[k] = ~0u;
+                if (q >= whole || !(p.stream || flags[k])) continue;
+                x[k] = from[q];
+                if (mask) bits[k] = mask_bits(mask, v0 + head + q * E, last_word, E);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int q = i + k * threads, v = head + q * E;
+                if (q >= whole || !(p.stream || flags[k])) continue;
+                if (flags[k]) {
+                    uint32_t w[E];
+                    words_of<E>(s_word, v, v & 3, p.seg, w);
+                    if constexpr (E == 4) {
+                        x[k].x = __float_as_uint(simple(__uint_as_float(x[k].x), w[0])), x[k].y = __float_as_uint(simple(__uint_as_float(x[k].y), w[1]));
+                        x[k].z = __float_as_uint(simple(__uint_as_float(x[k].z), w[2])), x[k].w = __float_as_uint(simple(__uint_as_float(x[k].w), w[3]));
+                    } else {
+                        auto two = [&](uint32_t u, unsigned a, unsigned c) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(simple(__uint_as_float(u << 16), a), simple(__uint_as_float(u & 0xFFFF0000u), c));
+                            return *reinterpret_cast<const uint32_t*>(&h);
+                        };
+                        x[k] = make_uint4(two(x[k].x, w[0], w[1]), two(x[k].y, w[2], w[3]), two(x[k].z, w[4], w[5]), two(x[k].w, w[6], w[7]));
+                    }
+                }
+                to[q] = mask ? masked<T>(x[k], bits[k]) : x[k];
+            }
+        }
+        for (int i = tid; i < n - whole * E; i += threads) {      // the rest, one by one
+            const int v = i < head ? i : i + whole * E;
+            const unsigned w = s_word[at(v)];
+            if (mask && !mask_bits(mask, v0 + v, last_word, 1)) out[v] = from_float<T>(-INFINITY);
+            else if (w) out[v] = from_float<T>(simple(to_float(in[v]), w));
+            else if (p.stream) out[v] = in[v];
+        }
+    }
+    __syncthreads();      // the rows are written: listed tokens' logits as they were
+    const int listed = static_cast<int>(s_listed);
+    for (int i = tid; i < listed * p.R; i += threads) {
+        const int j = i / listed, v = s_token[i - j * listed];
+        const unsigned w = s_list[i - j * listed];
+        if (p.mask && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) continue;
+        float x = to_float(row_of<T>(p.in, b, j)[v0 + v]);
+        unsigned count = (w & W_COUNT) / W_ONE;
+        if (w & W_DRAFT)
+            for (int k = 0; k < j; ++k) count += s_draft[k] == static_cast<unsigned>(v);
+        if (w & W_BIAS) x += p.bias[static_cast<long long>(b) * p.biases + (w & W_BIAS) - 1];
+        if (!count && !(w & (W_PROMPT | W_BIAS))) continue;
+        if (count || w & W_PROMPT) x = x * (x > 0.f ? per_rep : rep) - taken(count);
+        row_of<T>(p.out, b, j)[v0 + v] = from_float<T>(x);
     }
 }
 
