@@ -13,13 +13,14 @@ struct LogitsParams {
     int R, V, T, L, biases;
     int seg;        // tokens of the vocabulary that a CTA takes
     int pieces;     // every row and its output begin alike within 16 bytes
+    int together;   // every row of a sequence begins alike within 16 bytes
     int stream;     // 0: the output is the input, and no mask changes it
 };
 
 // What the history, the drafts and the biases say of a token, in a word: bit 31 in the prompt, bit 30 among the drafts, bits
 // 11 .. 29 the times among the output, bits 0 .. 10 the number of its bias's entry + 1.
 constexpr unsigned W_PROMPT = 1u << 31, W_DRAFT = 1u << 30, W_ONE = 1u << 11, W_BIAS = W_ONE - 1, W_COUNT = W_DRAFT - W_ONE;
-constexpr int LG_SEG = 16384, LG_THREADS = 512;      // at most
+constexpr int LG_SEG = 8192, LG_THREADS = 256, LG_CTAS = 4;      // at most; CTAs of an SM
 // Once all is counted, a word is the number that is taken off the logit: 0 for a token that nothing is said of, -0 where nothing is
 // taken off but the repetition counts. Tokens with a bias or among the drafts are kept in a list, and their words are 0.
 constexpr int LG_LIST = SPEC_SCORE_MAX_BIASES + SPEC_SCORE_MAX_ROWS;
@@ -39,18 +40,19 @@ __device__ __forceinline__ uint4 masked(uint4 x, unsigned bits) {
         x.x = bits & 1u ? x.x : 0xFF800000u, x.y = bits & 2u ? x.y : 0xFF800000u;
         x.z = bits & 4u ? x.z : 0xFF800000u, x.w = bits & 8u ? x.w : 0xFF800000u;
     } else {
-        auto two = [](uint32_t v, unsigned b) {
-            const uint32_t keep = (b & 1u) * 0xFFFFu | (b >> 1 & 1u) * 0xFFFF0000u;
-            return (v & keep) | (0xFF80FF80u & ~keep);
-        };
-        x.x = two(x.x, bits), x.y = two(x.y, bits >> 2), x.z = two(x.z, bits >> 4), x.w = two(x.w, bits >> 6);
+        // four bits to the bytes of a word, each byte to 0 or 255, and twice for a half
+        const uint32_t lo = ((bits & 15u) * 0x00204081u & 0x01010101u) * 255u, hi = ((bits >> 4) * 0x00204081u & 0x01010101u) * 255u;
+        auto two = [](uint32_t v, uint32_t keep) { return (v & keep) | (0xFF80FF80u & ~keep); };
+        x.x = two(x.x, __byte_perm(lo, 0, 0x1100)), x.y = two(x.y, __byte_perm(lo, 0, 0x3322));
+        x.z = two(x.z, __byte_perm(hi, 0, 0x1100)), x.w = two(x.w, __byte_perm(hi, 0, 0x3322));
     }
     return x;
 }
 
 // `n` <= 8 bits of the table's flags from v on; a word behind the last is there.
 __device__ __forceinline__ unsigned flag_bits(const unsigned* flags, int v, int n) {
-    return __funnelshift_r(flags[v >> 5], flags[(v >> 5) + 1], v & 31) & ((1u << n) - 1u);
+    const unsigned low = flags[v >> 5] >> (v & 31);
+    return ((v & 31) + n > 32 ? low | flags[(v >> 5) + 1] << (32 - (v & 31)) : low) & ((1u << n) - 1u);
 }
 
 // Where token v's word stands. 16-bit logits take eight words a piece: the first and the second four of them in parts of their own,
@@ -63,24 +65,32 @@ __device__ __forceinline__ int word_at(int v, int seg) {
 // The words of tokens v .. v + E - 1, v - from a multiple of four, `from` the same for every lane.
 template <int E>
 __device__ __forceinline__ void words_of(const unsigned* s_word, int v, int from, int seg, uint32_t (&w)[E]) {
+    if (from == 0) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(s_word + word_at<E>(v + i, seg));
+            w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+        }
+        return;
+    }
     uint32_t t[E + 4];
 #pragma unroll
     for (int i = 0; i < E + 4; i += 4) {
-        if (i == E && from == 0) break;
         const uint4 q = *reinterpret_cast<const uint4*>(s_word + word_at<E>(v - from + i, seg));
         t[i] = q.x, t[i + 1] = q.y, t[i + 2] = q.z, t[i + 3] = q.w;
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) w[i] = from == 0 ? t[i] : from == 1 ? t[i + 1] : from == 2 ? t[i + 2] : t[i + 3];
+    for (int i = 0; i < E; ++i) w[i] = from == 1 ? t[i + 1] : from == 2 ? t[i + 2] : t[i + 3];
 }
 
 // A CTA takes one sequence and `seg` tokens of the vocabulary, for all rows. What the sequence's tokens say comes first, from a
 // pass over its history, into a table in shared memory: a word for each token, and a bit for each that is not 0. Then the rows
-// go by, 16 bytes at a time: bandwidth bounds that. A piece without a bit is copied, with the mask; in the others every value goes
-// through the one formula, which leaves those that nothing is said of as they are. Listed tokens come last, each by itself.
-template <class T>
-__global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constant__ LogitsParams p) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 2;
+// go by, 16 bytes of a row at a time, and all rows at a place one behind the other, since the table says the same to them: bandwidth
+// bounds that. A piece without a bit is copied, with the mask; in the others every value goes through the one formula, which leaves
+// those that nothing is said of as they are. Listed tokens come last, each by itself.
+template <class T, bool MASK>
+__global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __grid_constant__ LogitsParams p) {
+    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 6;
     extern __shared__ unsigned s_word[];                     // [seg + 8], then the bits [seg / 32 + 1]
     __shared__ unsigned s_draft[SPEC_SCORE_MAX_ROWS], s_list[LG_LIST], s_listed;
     __shared__ unsigned short s_token[LG_LIST];
@@ -96,10 +106,11 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
     for (int j = tid; j < p.R; j += threads)
         s_draft[j] = p.tokens && j < p.R - 1 ? static_cast<unsigned>(p.tokens[static_cast<long long>(b) * p.T + j]) - v0 : ~0u;
     __syncthreads();
+    auto mark = [&](unsigned v) { atomicOr(&s_flag[v / 32], 1u << (v % 32)); };
     if (p.bias_tokens) {
         for (int i = tid; i < p.biases; i += threads) {
             const unsigned v = static_cast<unsigned>(p.bias_tokens[static_cast<long long>(b) * p.biases + i]) - v0;
-            if (v < static_cast<unsigned>(n)) atomicMax(&s_word[at(v)], static_cast<unsigned>(i + 1));
+            if (v < static_cast<unsigned>(n)) atomicMax(&s_word[at(v)], static_cast<unsigned>(i + 1)), mark(v);
         }
         __syncthreads();
     }
@@ -109,8 +120,10 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
         auto count = [&](int id, int i) {
             const unsigned v = static_cast<unsigned>(id) - v0;
             if (v >= static_cast<unsigned>(n)) return;
-            if (i < pr) atomicOr(&s_word[at(v)], W_PROMPT);
-            else atomicAdd(&s_word[at(v)], W_ONE);
+            unsigned* const word = &s_word[at(v)];
+            if (i < pr) atomicOr(word, W_PROMPT);
+            else atomicAdd(word, W_ONE);
+            mark(v);
         };
         const int fours = (reinterpret_cast<uintptr_t>(h) & 15u) == 0 ? len / 4 : 0;
 #pragma unroll 2
@@ -122,89 +135,100 @@ __global__ void __launch_bounds__(LG_THREADS) logits_kernel(const __grid_constan
         for (int i = 4 * fours + tid; i < len; i += threads) count(__ldg(h + i), i);
     }
     for (int j = tid; j < p.R; j += threads)
-        if (s_draft[j] < static_cast<unsigned>(n)) atomicOr(&s_word[at(s_draft[j])], W_DRAFT);
+        if (s_draft[j] < static_cast<unsigned>(n)) atomicOr(&s_word[at(s_draft[j])], W_DRAFT), mark(s_draft[j]);
     __syncthreads();
     const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f,
                 pres = p.presence ? p.presence[b] : 0.f, per_rep = 1.f / rep;
     // what n > 0 times among the output take off; n as a float without a conversion
     auto taken = [&](unsigned n) { return n ? fmaf(freq, __uint_as_float(n | 0x4B000000u) - 8388608.f, pres) : 0.f; };
-    for (int i = tid; i < p.seg; i += threads) {             // whole warps: seg is a multiple of 32, and so are the threads
-        unsigned& word = s_word[at(i)];
-        const unsigned w = word;
-        const bool list = w & (W_BIAS | W_DRAFT);
-        const unsigned any = __ballot_sync(0xffffffffu, w != 0u && !list);
-        if (i % 32 == 0) s_flag[i / 32] = any;
-        if (list) {
-            const unsigned to = atomicAdd(&s_listed, 1u);
-            s_list[to] = w;
-            s_token[to] = static_cast<unsigned short>(i);
-            word = 0u;
-        } else if (w) {
-            const unsigned off = __float_as_uint(taken((w & W_COUNT) / W_ONE));
-            word = off ? off : 0x80000000u;
+    for (int i = tid; i < p.seg / 4; i += threads)
+        for (unsigned rest = s_flag[i / 8] >> 4 * (i % 8) & 15u; rest; rest &= rest - 1) {
+            const int v = 4 * i + __ffs(rest) - 1;
+            unsigned& word = s_word[at(v)];
+            const unsigned w = word;
+            if (w & (W_BIAS | W_DRAFT)) {
+                const unsigned to = atomicAdd(&s_listed, 1u);
+                s_list[to] = w;
+                s_token[to] = static_cast<unsigned short>(v);
+                word = 0u;
+            } else {
+                const unsigned off = __float_as_uint(taken((w & W_COUNT) / W_ONE));
+                word = off ? off : 0x80000000u;
+            }
         }
-    }
     __syncthreads();
     auto simple = [&](float x, unsigned w) { return fmaf(x, w ? (x > 0.f ? per_rep : rep) : 1.f, -__uint_as_float(w)); };
-    for (int j = 0; j < p.R; ++j) {
-        const T* const in = row_of<T>(p.in, b, j) + v0;
-        T* const out = row_of<T>(p.out, b, j) + v0;
-        const unsigned* const mask = p.mask ? p.mask + b * p.mask_sb + j * p.mask_sr : nullptr;
+    const int together = p.together ? p.R : 1;
+    for (int first = 0; first < p.R; first += together) {
+        const int past = min(first + together, p.R);
+        const T* const in = row_of<T>(p.in, b, first) + v0;
+        T* const out = row_of<T>(p.out, b, first) + v0;
+        const unsigned* const mask = MASK ? p.mask + b * p.mask_sb + first * p.mask_sr : nullptr;
         int head = 0, whole = 0;
         if (p.pieces) {
             head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
             whole = (n - head) / E;
         }
-        const uint4* const from = reinterpret_cast<const uint4*>(in + head);
-        uint4* const to = reinterpret_cast<uint4*>(out + head);
-        // U pieces of a thread at once: their loads are on their way together
-        for (int i = tid; i < whole; i += U * threads) {
-            uint4 x[U];
-            unsigned flags[U], bits[U];
+        for (int i = tid; i < whole; i += threads) {
+            const int v = head + i * E;
+            const unsigned flags = flag_bits(s_flag, v, E);
+            if (!p.stream && !flags) continue;
+            uint32_t w[E];                                   // what the table says, once for all rows
+            if (flags) words_of<E>(s_word, v, v & 3, p.seg, w);
+            const T* from = in + v;
+            T* to = out + v;
+            const unsigned* bits_from = mask;
+            for (int j = first; j < past; j += U) {      // the loads of U rows are on their way together
+                uint4 x[U];
+                unsigned bits[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int q = i + k * threads;
-                flags[k] = q < whole ? flag_bits(s_flag, head + q * E, E) : 0u;
-                bits[k] = ~0u;
-                if (q >= whole || !(p.stream || flags[k])) continue;
-                x[k] = from[q];
-                if (mask) bits[k] = mask_bits(mask, v0 + head + q * E, last_word, E);
-            }
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int q = i + k * threads, v = head + q * E;
-                if (q >= whole || !(p.stream || flags[k])) continue;
-                if (flags[k]) {
-                    uint32_t w[E];
-                    words_of<E>(s_word, v, v & 3, p.seg, w);
-                    if constexpr (E == 4) {
-                        x[k].x = __float_as_uint(simple(__uint_as_float(x[k].x), w[0])), x[k].y = __float_as_uint(simple(__uint_as_float(x[k].y), w[1]));
-                        x[k].z = __float_as_uint(simple(__uint_as_float(x[k].z), w[2])), x[k].w = __float_as_uint(simple(__uint_as_float(x[k].w), w[3]));
-                    } else {
-                        auto two = [&](uint32_t u, unsigned a, unsigned c) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(simple(__uint_as_float(u << 16), a), simple(__uint_as_float(u & 0xFFFF0000u), c));
-                            return *reinterpret_cast<const uint32_t*>(&h);
-                        };
-                        x[k] = make_uint4(two(x[k].x, w[0], w[1]), two(x[k].y, w[2], w[3]), two(x[k].z, w[4], w[5]), two(x[k].w, w[6], w[7]));
-                    }
+                for (int k = 0; k < U; ++k) {
+                    if (j + k >= past) break;
+                    x[k] = *reinterpret_cast<const uint4*>(from + k * p.in.sn);
+                    if (MASK) bits[k] = mask_bits(bits_from + k * p.mask_sr, v0 + v, last_word, E);
                 }
-                to[q] = mask ? masked<T>(x[k], bits[k]) : x[k];
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    if (j + k >= past) break;
+                    if (flags) {
+                        uint4 y = x[k];
+                        if constexpr (E == 4) {
+                            y.x = __float_as_uint(simple(__uint_as_float(y.x), w[0])), y.y = __float_as_uint(simple(__uint_as_float(y.y), w[1]));
+                            y.z = __float_as_uint(simple(__uint_as_float(y.z), w[2])), y.w = __float_as_uint(simple(__uint_as_float(y.w), w[3]));
+                        } else {
+                            auto two = [&](uint32_t u, uint32_t a, uint32_t c) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(simple(__uint_as_float(u << 16), a),
+                                                                               simple(__uint_as_float(u & 0xFFFF0000u), c));
+                                return *reinterpret_cast<const uint32_t*>(&h);
+                            };
+                            y = make_uint4(two(y.x, w[0], w[1]), two(y.y, w[2], w[3]), two(y.z, w[4], w[5]), two(y.w, w[6], w[7]));
+                        }
+                        x[k] = y;
+                    }
+                    *reinterpret_cast<uint4*>(to + k * p.out.sn) = MASK ? masked<T>(x[k], bits[k]) : x[k];
+                }
+                from += U * p.in.sn;
+                to += U * p.out.sn;
+                bits_from += MASK ? U * p.mask_sr : 0;
             }
         }
-        for (int i = tid; i < n - whole * E; i += threads) {      // the rest, one by one
-            const int v = i < head ? i : i + whole * E;
-            const unsigned w = s_word[at(v)];
-            if (mask && !mask_bits(mask, v0 + v, last_word, 1)) out[v] = from_float<T>(-INFINITY);
-            else if (w) out[v] = from_float<T>(simple(to_float(in[v]), w));
-            else if (p.stream) out[v] = in[v];
-        }
+        for (int j = first; j < past; ++j)
+            for (int i = tid; i < n - whole * E; i += threads) {      // the rest, one by one
+                const int v = i < head ? i : i + whole * E;
+                const unsigned w = s_word[at(v)];
+                T* const to = row_of<T>(p.out, b, j) + v0 + v;
+                const T x = row_of<T>(p.in, b, j)[v0 + v];
+                if (MASK && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) *to = from_float<T>(-INFINITY);
+                else if (w) *to = from_float<T>(simple(to_float(x), w));
+                else if (p.stream) *to = x;
+            }
     }
     __syncthreads();      // the rows are written: listed tokens' logits as they were
     const int listed = static_cast<int>(s_listed);
     for (int i = tid; i < listed * p.R; i += threads) {
         const int j = i / listed, v = s_token[i - j * listed];
         const unsigned w = s_list[i - j * listed];
-        if (p.mask && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) continue;
+        if (MASK && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) continue;
         float x = to_float(row_of<T>(p.in, b, j)[v0 + v]);
         unsigned count = (w & W_COUNT) / W_ONE;
         if (w & W_DRAFT)

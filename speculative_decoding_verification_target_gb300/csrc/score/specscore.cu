@@ -277,22 +277,11 @@ spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cuda
 }
 
 // ---------------------------------------------------------------------------------------------- logits
-template <class T>
-spec_status logits_as(const LogitsParams& p, int B, int threads, cudaStream_t st) {
+template <class T, bool MASK>
+spec_status logits_as(const LogitsParams& p, int B, cudaStream_t st) {
     const size_t smem = (static_cast<size_t>(p.seg) + p.seg / 32 + 16) * 4;
-    if (smem > 48 * 1024) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
-        static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
-        const unsigned bit = dev < 32 ? 1u << dev : 0u;
-        if (!(ready.load(std::memory_order_acquire) & bit)) {
-            const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (LG_SEG + LG_SEG / 32 + 16) * 4);
-            if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "logits kernel attribute failed: %s", cudaGetErrorString(e));
-            ready.fetch_or(bit, std::memory_order_release);
-        }
-    }
-    return launched("logits", launch_behind(logits_kernel<T>, p, dim3((p.V + p.seg - 1) / p.seg, B), threads, st, smem));
+    static_assert((LG_SEG + LG_SEG / 32 + 16) * 4 <= 40 * 1024, "within what every kernel may have");
+    return launched("logits", launch_behind(logits_kernel<T, MASK>, p, dim3((p.V + p.seg - 1) / p.seg, B), LG_THREADS, st, smem));
 }
 
 }  // namespace
@@ -445,13 +434,14 @@ spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R
     // as large a part of the vocabulary as still gives the card four CTAs an SM: each reads the whole history
     p.seg = LG_SEG;
     while (p.seg > 1024 && static_cast<long long>((V + p.seg - 1) / p.seg) * B < 4LL * sms) p.seg /= 2;
-    const int threads = p.seg >= 8192 ? LG_THREADS : 256;
     auto alike = [&](long long x, long long y) { return (x - y) * static_cast<long long>(e) % 16 == 0; };
     p.pieces = (reinterpret_cast<uintptr_t>(logits->data) - reinterpret_cast<uintptr_t>(out->data)) % 16 == 0 &&
                (B == 1 || alike(logits->stride_b, out->stride_b)) && (R == 1 || alike(logits->stride_n, out->stride_n));
+    p.together = p.pieces && (R == 1 || alike(logits->stride_n, 0));
     p.stream = out->data != logits->data || mask;
-    return dtype == SPEC_BF16 ? logits_as<__nv_bfloat16>(p, B, threads, static_cast<cudaStream_t>(stream))
-                              : logits_as<float>(p, B, threads, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (mask) return dtype == SPEC_BF16 ? logits_as<__nv_bfloat16, true>(p, B, st) : logits_as<float, true>(p, B, st);
+    return dtype == SPEC_BF16 ? logits_as<__nv_bfloat16, false>(p, B, st) : logits_as<float, false>(p, B, st);
 }
 
 }  // extern "C"
