@@ -117,11 +117,11 @@ bool whole_pieces(const NormParams& p, size_t e, bool codes, int B) {
     return p.D % per == 0 && fits(p.x, 16) && fits(p.res, 16) && fits(p.res_out, 16) && fits(p.out, codes ? per : 16) && aligned16(p.weight);
 }
 
-template <class T, bool CODES, bool VEC>
+template <class T, bool CODES, bool VEC, bool FULL>
 auto norm_of(int slots) -> void (*)(const NormParams) {
-    if constexpr (VEC) return slots == 1 ? norm_rows_kernel<T, CODES, 1, VEC> : slots == 2 ? norm_rows_kernel<T, CODES, 2, VEC>
-                                                                                          : norm_rows_kernel<T, CODES, 4, VEC>;
-    else return slots <= 4 ? norm_rows_kernel<T, CODES, 4, VEC> : norm_rows_kernel<T, CODES, 16, VEC>;
+    if constexpr (VEC) return slots == 1 ? norm_rows_kernel<T, CODES, 1, VEC, FULL> : slots == 2 ? norm_rows_kernel<T, CODES, 2, VEC, FULL>
+                                                                                          : norm_rows_kernel<T, CODES, 4, VEC, FULL>;
+    else return slots <= 4 ? norm_rows_kernel<T, CODES, 4, VEC, FULL> : norm_rows_kernel<T, CODES, 16, VEC, FULL>;
 }
 
 template <class T, bool CODES>
@@ -129,15 +129,18 @@ spec_status norm_as(NormParams p, bool vec, int sms, cudaStream_t st) {
     const int pieces = vec ? p.D / (16 / static_cast<int>(sizeof(T))) : p.D, most = vec ? 4 : 16;
     if (pieces > 512 * most)
         return launched("norm", launch_behind(norm_long_kernel<T, CODES>, p, dim3(static_cast<unsigned>(p.rows)), 512, st));
-    // many rows: threads with four pieces, so that much is on its way; few: as many threads as there are pieces
-    const bool few = p.rows < 4LL * sms;
-    int slots = vec ? (few ? 1 : pieces >= 128 ? 4 : pieces >= 64 ? 2 : 1) : (few ? 4 : 16);
-    while ((pieces + slots - 1) / slots > 512) slots *= vec ? 2 : 4;
+    const bool full = p.norm || p.weight || p.res.p;
+    // many rows: threads with four pieces, so that much is on its way; few: threads with as few as leave room for every row at once
+    int slots = vec ? 4 : 16;
+    const long long room = full ? 512 : 1024;      // threads of an SM, by registers
+    while (slots > 1 && p.rows * ((pieces + slots / 2 - 1) / (slots / 2) + 31) / 32 * 32 <= room * sms && 2 * pieces <= 512 * slots) slots /= 2;
+    if (!vec && slots < 16) slots = slots < 4 ? 4 : slots == 8 ? 16 : slots;      // there are kernels of 4 and of 16
     p.tpr = ((pieces + slots - 1) / slots + 31) / 32 * 32;
-    const int per = few ? 1 : std::max(1, 128 / p.tpr), threads = per * p.tpr;
-    const long long ctas = std::min((p.rows + per - 1) / per, static_cast<long long>(sms) * std::max(1, 512 / threads));
-    return launched("norm", launch_behind(vec ? norm_of<T, CODES, true>(slots) : norm_of<T, CODES, false>(slots), p,
-                                          dim3(static_cast<unsigned>(ctas)), threads, st));
+    const int per = std::max(1, (p.rows > 4LL * sms ? 128 : 32) / p.tpr), threads = per * p.tpr;
+    const long long ctas = std::min((p.rows + per - 1) / per, static_cast<long long>(sms) * std::max<long long>(1, room / threads));
+    void (*const fn)(const NormParams) = !full && CODES ? (vec ? norm_of<T, true, true, false>(slots) : norm_of<T, true, false, false>(slots))
+                                                        : (vec ? norm_of<T, CODES, true, true>(slots) : norm_of<T, CODES, false, true>(slots));
+    return launched("norm", launch_behind(fn, p, dim3(static_cast<unsigned>(ctas)), threads, st));
 }
 
 template <class T>
