@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
     extern __shared__ unsigned char dynamic[];
     __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[4], s_half_empty[2], s_acc_full[2], s_acc_empty[2];
     __shared__ uint32_t s_tmem;
-    __shared__ float s_scale[PR_TOKENS];
-    __shared__ long long s_row[PR_TOKENS];
+    __shared__ alignas(16) float s_scale[PR_TOKENS];
+    __shared__ alignas(16) long long s_row[PR_TOKENS];
     unsigned char* const smem = dynamic + ((1024u - (smem_addr(dynamic) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int CTAS = PAIR ? 2 : 1;
@@ -394,10 +394,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             }
             const float ws = c < p.C ? p.w_scale[c] : 0.f, bias = p.bias && c < p.C ? p.bias[c] : 0.f;
             T* const out = static_cast<T*>(p.out.p) + c;
-            auto put = [&](int j, int sum) {
-                float y = static_cast<float>(sum) * (s_scale[j] * ws);
-                if (p.bias) y += bias;
-                if (c < p.C) out[s_row[j]] = from_float<T>(y);
+            auto scaled = [&](int j, int sum) {
+                const float y = static_cast<float>(sum) * (s_scale[j] * ws);
+                return from_float<T>(p.bias ? y + bias : y);
             };
             if (!PAIR && p.split > 1) {
                 // one tile a cluster: its CTAs add their sums, each for every split-th token
@@ -415,17 +414,27 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                     int sum = 0;
                     for (int r = 0; r < p.split; ++r)
                         sum += __float_as_int(specv::ld_cluster_f32(specv::map_to_rank(smem_addr(part + j * PR_CH), r)));
-                    put(j, sum);
+                    const T y = scaled(j, sum);
+                    if (c < p.C) out[s_row[j]] = y;
                 }
                 __syncwarp();
                 specv::cluster_sync_all();
             } else {
+                // sixteen tokens at a time, their values before their stores, which need not wait for one another
 #pragma unroll
                 for (int j = 0; j < PR_TOKENS / 2; j += 16)
                     if (j < mine) {
+                        T y[16];
 #pragma unroll
-                        for (int e = j; e < j + 16; ++e)
-                            if (e < mine) put(low + e, acc[e]);
+                        for (int e = 0; e < 16; ++e) y[e] = scaled(low + j + e, acc[j + e]);
+                        if (j + 16 <= mine && c < p.C) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) out[s_row[low + j + e]] = y[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (j + e < mine && c < p.C) out[s_row[low + j + e]] = y[e];
+                        }
                     }
             }
         }
