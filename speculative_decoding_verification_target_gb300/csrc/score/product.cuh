@@ -15,7 +15,7 @@ constexpr int PR_K = 128, PR_CH = 128, PR_TOKENS = 192, PR_THREADS = 640, PR_STA
 // done: the stage's barrier is then in the phase that they mean only if its last use was no later than that.
 constexpr int PR_MIN_STAGES = 4, PR_TOKENS_ALONE = 128;      // a CTA without a pair has room for four stages up to 144 tokens
 constexpr int PR_W_BYTES = PR_CH * PR_K;
-constexpr int PR_SMEM = 224 * 1024;                    // of it up to 1 KB is lost to alignment
+constexpr int PR_SMEM = 222 * 1024;                    // of it up to 1 KB is lost to alignment
 constexpr uint32_t PR_COL_A = 2 * PR_TOKENS;           // tensor memory: two accumulators, two steps of channels
 constexpr uint64_t PR_WAIT_NS = 2000000000ull;
 // The sum of four steps is at most 512 x 2^14 = 2^23 in magnitude, so exact in fp32 as are its parts.
@@ -185,10 +185,8 @@ __device__ __forceinline__ void set_registers() {
 // units of neighbouring CTAs share their channels' codes.
 struct Unit {
     int channel, tile;
-    __device__ Unit(const ProductParams& p, long long u) {
-        const long long per = 8LL * p.channel_tiles;
-        const int group = static_cast<int>(u / per), wide = min(8, p.token_tiles - 8 * group);
-        const int in = static_cast<int>(u - group * per);
+    __device__ Unit(const ProductParams& p, int u) {
+        const int per = 8 * p.channel_tiles, group = u / per, wide = min(8, p.token_tiles - 8 * group), in = u - group * per;
         channel = in / wide;
         tile = 8 * group + in % wide;
     }
@@ -207,15 +205,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
     extern __shared__ unsigned char dynamic[];
     __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[4], s_half_empty[2], s_acc_full[2], s_acc_empty[2];
     __shared__ uint32_t s_tmem;
-    __shared__ alignas(16) float s_scale[PR_TOKENS];
-    __shared__ alignas(16) long long s_row[PR_TOKENS];
+    __shared__ alignas(16) float s_scales[2][PR_TOKENS];
+    __shared__ alignas(16) long long s_rows[2][PR_TOKENS];      // of this tile and the next
     unsigned char* const smem = dynamic + ((1024u - (smem_addr(dynamic) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     constexpr int CTAS = PAIR ? 2 : 1;
     const int rank = PAIR || p.split > 1 ? static_cast<int>(specv::cluster_ctarank()) : 0;
     const int own_n = p.n / CTAS, half_bytes = own_n * 128, stage_bytes = PR_W_BYTES + 2 * half_bytes;
     const int group = PAIR ? 2 : p.split;
-    const long long units = static_cast<long long>(p.channel_tiles) * p.token_tiles, first = blockIdx.x / group, by = gridDim.x / group;
+    const int units = p.channel_tiles * p.token_tiles, first = blockIdx.x / group, by = gridDim.x / group;      // the host keeps units small
     const int k_from = PAIR ? 0 : static_cast<int>(static_cast<long long>(p.steps) * rank / p.split);
     const int k_to = PAIR ? p.steps : static_cast<int>(static_cast<long long>(p.steps) * (rank + 1) / p.split);
     if (tid == 0) {
@@ -267,7 +265,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
             int g = 0, st = 0;
             uint32_t round = 0;      // of the stages' uses
-            for (long long i = first; i < units; i += by) {
+            for (int i = first; i < units; i += by) {
                 const Unit u(p, i);
                 for (int k = k_from; k < k_to; ++k) {
                     if (g >= ahead) {
@@ -294,7 +292,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             int st = 0, chunk = 0;
             uint32_t at = 0;                                         // half steps
             bool over = phase_over(&s_ready[0], 0);                  // looked at one half step ahead
-            for (long long i = first; i < units; i += by)
+            for (int i = first; i < units; i += by)
                 for (int k = k_from; k < k_to; ++k) {
                     const bool starts = (k - k_from) % PR_CHUNK == 0, ends = (k - k_from) % PR_CHUNK == PR_CHUNK - 1 || k + 1 == k_to;
                     const uint32_t d = tmem + (chunk & 1) * PR_TOKENS, b = base + st * (stage_bytes >> 4);
@@ -321,7 +319,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
         const uint32_t to = tmem + PR_COL_A + mine * 64 + (static_cast<uint32_t>(warp & 3) << 21);
         int g = 0, st = -1, used = -1;      // step, its stage, the stage of this buffer's last step
         uint32_t round = 0, used_round = 0;
-        for (long long i = first; i < units; i += by)
+        for (int i = first; i < units; i += by)
             for (int k = k_from; k < k_to; ++k, ++g) {
                 if (++st == p.stages) st = 0, ++round;
                 if ((g & 1) != mine) continue;
@@ -359,25 +357,33 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
         const uint32_t from = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const int in_tile = (warp & 3) * 32 + lane;
         const int low = (warp - 12) >> 2 ? (p.n / 2 + 15) / 16 * 16 : 0, high = (warp - 12) >> 2 ? p.n : (p.n / 2 + 15) / 16 * 16;
-        int chunk = 0;
-        for (long long i = first; i < units; i += by) {
+        auto look_up = [&](int i, int to) {      // the scales and the places of a tile's tokens
+            if (i >= units) return;
             const Unit u(p, i);
-            const int t0 = u.tile * p.n, nt = min(p.n, p.tokens - t0), mine = min(high, nt) - low;      // tokens; this warp's
-            __syncwarp();      // these barriers are for whole warps
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            for (int j = tid - 384; j < nt; j += 256) {
-                const int t = t0 + j, b = t / p.N;
-                s_scale[j] = p.a_scale[t];
-                s_row[j] = b * p.out.sb + (t - b * p.N) * p.out.sn;
+            for (int j = tid - 384; j < p.n && u.tile * p.n + j < p.tokens; j += 256) {
+                const int t = u.tile * p.n + j, b = t / p.N;
+                s_scales[to][j] = p.a_scale[t];
+                s_rows[to][j] = b * p.out.sb + (t - b * p.N) * p.out.sn;
             }
             __syncwarp();
+        };
+        look_up(first, 0);
+        int chunk = 0, turn = 0;
+        for (int i = first; i < units; i += by, turn ^= 1) {
+            const Unit u(p, i);
+            const int t0 = u.tile * p.n, nt = min(p.n, p.tokens - t0), mine = min(high, nt) - low;      // tokens; this warp's
+            const float* const s_scale = s_scales[turn];
+            const long long* const s_row = s_rows[turn];
+            __syncwarp();      // this barrier is for whole warps
             asm volatile("bar.sync 1, 256;" ::: "memory");
             const int c = (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH + in_tile;
+            const float ws = c < p.C ? p.w_scale[c] : 0.f, bias = p.bias && c < p.C ? p.bias[c] : 0.f;
             int acc[PR_TOKENS / 2];
 #pragma unroll
             for (int j = 0; j < PR_TOKENS / 2; ++j) acc[j] = 0;
             const int chunks = (k_to - k_from + PR_CHUNK - 1) / PR_CHUNK;
             for (int q = 0; q < chunks; ++q, ++chunk) {
+                if (q == min(2, chunks - 1)) look_up(i + by, turn ^ 1);      // where there is time
                 wait(&s_acc_full[chunk & 1], (chunk >> 1) & 1);
                 specc::tmem_fence_after();
 #pragma unroll
@@ -385,14 +391,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                     if (low + j < high) {
                         uint32_t v[16];
                         specc::tmem_ld(from + (chunk & 1) * PR_TOKENS + low + j, v);
+                        if (low + j + 16 >= high) {      // the last of them are out of the accumulator
+                            specc::tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_first<PAIR>(&s_acc_empty[chunk & 1]);
+                            __syncwarp();
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) acc[j + e] += __float2int_rn(__uint_as_float(v[e]));
                     }
-                specc::tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_first<PAIR>(&s_acc_empty[chunk & 1]);
+                if (low >= high && lane == 0) arrive_first<PAIR>(&s_acc_empty[chunk & 1]);      // a narrow tile's other half
             }
-            const float ws = c < p.C ? p.w_scale[c] : 0.f, bias = p.bias && c < p.C ? p.bias[c] : 0.f;
             T* const out = static_cast<T*>(p.out.p) + c;
             auto scaled = [&](int j, int sum) {
                 const float y = static_cast<float>(sum) * (s_scale[j] * ws);

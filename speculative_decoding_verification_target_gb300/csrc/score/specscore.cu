@@ -253,6 +253,7 @@ spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cuda
     p.n = pair ? (per + 31) / 32 * 32 : (per + 15) / 16 * 16;
     p.channel_tiles = (m.C + PR_CH * (pair ? 2 : 1) - 1) / (PR_CH * (pair ? 2 : 1));
     const long long units = static_cast<long long>(p.channel_tiles) * p.token_tiles;
+    if (units > (1LL << 30)) return fail(SPEC_ERR_UNSUPPORTED, "too many tokens and channels: %lld tiles", units);
     p.split = 1;
     if (!pair)
         while (p.split < 8 && units * p.split * 2 <= sms && p.split * 2 <= p.steps) p.split *= 2;
