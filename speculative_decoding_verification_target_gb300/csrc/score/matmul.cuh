@@ -1,4 +1,4 @@
-// The product of 8-bit integers for few tokens, and for rows that the copies of product.cuh cannot take.
+// The product of 8-bit integers for few tokens.
 #pragma once
 #include "rows.cuh"
 
@@ -14,7 +14,7 @@ struct MatmulParams {
     int k_warps;      // of a CTA's eight: 1, 2, 4 or 8
 };
 
-constexpr int MV_WARPS = 8, MV_CH = 4;
+constexpr int MV_WARPS = 8, MV_CH = 4, MV_SMS = 152;
 
 // 16 codes at p, of which `valid` are there; the others are 0. Without alignment only words that hold a valid code are read.
 template <bool ALIGNED>
@@ -38,8 +38,9 @@ __device__ __forceinline__ void load16(const signed char* p, int valid, int (&x)
 }
 
 // A warp takes four channels and up to TOKENS tokens, its lanes 16 of K each; k_warps of a CTA's warps share their K. Integer
-// products four at a time (dp4a, 64 lanes a cycle and SM: 37 T products a second), whole sums in 32 bits, so their order does
-// not matter.
+// products four at a time (dp4a, 64 lanes a cycle and SM; the tensor cores' own integer products are no faster here), whole sums in 32
+// bits, so their order does not matter. The weights' bytes bound one token (128256 channels of 4096 in 78.4 us, the copy rate), the
+// products eight.
 template <class T, int TOKENS, bool ALIGNED>
 __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_constant__ MatmulParams p) {
     __shared__ int s_sum[MV_WARPS][MV_CH * TOKENS];
@@ -55,6 +56,8 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_cons
         a[j] = row_of<signed char>(p.a, b, t - b * p.N);
     }
     int acc[MV_CH][TOKENS] = {};
+    constexpr int AHEAD = TOKENS == 1 ? 4 : TOKENS == 8 ? 1 : 2;      // turns whose loads are on their way together
+#pragma unroll AHEAD
     for (int k = (kw * 32 + lane) * 16; k < p.K; k += p.k_warps * 512) {
         int x[MV_CH][4];
 #pragma unroll

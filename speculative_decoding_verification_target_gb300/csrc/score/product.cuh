@@ -3,7 +3,7 @@
 #include <cuda.h>
 
 #include "../cache/tmem.cuh"
-#include "rows.cuh"
+#include "matmul.cuh"
 
 namespace specs {
 
@@ -26,7 +26,9 @@ struct ProductParams {
     Rows out;
     const unsigned char* tokens16;
     const float *a_scale, *w_scale, *bias;
-    int tokens, N, C;
+    const signed char* codes;      // w, for rows that no tensor map can hold
+    long long w_stride;
+    int tokens, N, C, K;
     int n, token_tiles, channel_tiles, steps, stages, split;
     int stream_w;        // the codes are read once: they need not stay in L2
     unsigned* status;
@@ -199,8 +201,9 @@ struct Unit {
 //   warps 12 .. 19 sums of 512 products out of the tensor memory into integers in registers, and at the end to the output; each half
 //                  of the warps takes half of the tokens
 // PAIR: two CTAs share a tile of 256 channels; each holds its channels and half of the tokens, the first one issues.
+// MAP: the codes' rows are on 16 bytes, and copies bring them; else the warps that turn them fetch them themselves, 16 bytes a lane.
 // split > 1: the CTAs of a cluster share a tile's K, and add their integers through one another's shared memory.
-template <class T, bool PAIR>
+template <class T, bool PAIR, bool MAP>
 __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char dynamic[];
     __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[4], s_half_empty[2], s_acc_full[2], s_acc_empty[2];
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             const uint64_t keep = specv::policy_evict_last(), w_policy = p.stream_w ? specv::policy_evict_first() : specv::policy_evict_normal();
             auto codes = [&](int st, const Unit& u, int k) {
                 if (lane == 0) {
-                    specv::mbar_arrive_expect_tx(&s_full[st], stage_bytes);
-                    load_codes(smem + st * stage_bytes, &p.w, k * PR_K, (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH, &s_full[st], w_policy);
+                    specv::mbar_arrive_expect_tx(&s_full[st], MAP ? stage_bytes : 2 * half_bytes);
+                    if (MAP) load_codes(smem + st * stage_bytes, &p.w, k * PR_K, (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH, &s_full[st], w_policy);
                 }
             };
             auto tokens = [&](int st, const Unit& u, int k) {
@@ -323,7 +326,28 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             for (int k = k_from; k < k_to; ++k, ++g) {
                 if (++st == p.stages) st = 0, ++round;
                 if ((g & 1) != mine) continue;
-                wait(&s_full[st], round & 1);
+                if constexpr (!MAP) {
+                    // eight lanes to a row's 128 codes; the place in shared memory is free when the step's other copies may begin
+                    unsigned char* const to_row = smem + st * stage_bytes;
+                    const int t = tid & 127, piece = t & 7, at = k * PR_K + piece * 16;
+                    const Unit u(p, i);
+                    int x[8][4];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int c = u.channel * PR_CH + r * 16 + (t >> 3);
+                        x[r][0] = x[r][1] = x[r][2] = x[r][3] = 0;
+                        if (c < p.C && at < p.K) load16<false>(p.codes + c * p.w_stride + at, p.K - at, x[r]);
+                    }
+                    wait(&s_full[st], round & 1);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int c = r * 16 + (t >> 3);
+                        *reinterpret_cast<int4*>(to_row + c * 128 + ((piece ^ (c & 7)) * 16)) = make_int4(x[r][0], x[r][1], x[r][2], x[r][3]);
+                    }
+                    asm volatile("bar.sync %0, 128;" ::"r"(2 + mine) : "memory");
+                } else {
+                    wait(&s_full[st], round & 1);
+                }
                 const unsigned char* const src = smem + st * stage_bytes + row * 128;
                 uint4 v[8];
 #pragma unroll

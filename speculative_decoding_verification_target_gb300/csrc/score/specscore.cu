@@ -173,7 +173,9 @@ size_t matmul_bytes(int tokens, int, int K) {
 
 template <class T, bool ALIGNED>
 spec_status matvec_as(MatmulParams p, cudaStream_t st) {
-    p.k_warps = p.K > 2048 ? 8 : p.K > 1024 ? 4 : p.K > 512 ? 2 : 1;
+    // as few warps to a channel's K as still give every SM its 64: then each has more loads on their way and fewer sums to join
+    p.k_warps = 1;
+    while (p.k_warps < 8 && p.K > 512 * p.k_warps && static_cast<long long>((p.C + MV_CH - 1) / MV_CH) * p.k_warps < 48LL * MV_SMS) p.k_warps *= 2;
     const int per = MV_WARPS / p.k_warps * MV_CH;
     const int width = p.tokens > 4 ? 8 : p.tokens > 2 ? 4 : p.tokens;
     void (*const fn)(const MatmulParams) = width == 8 ? matvec_kernel<T, 8, ALIGNED> : width == 4 ? matvec_kernel<T, 4, ALIGNED>
@@ -209,33 +211,38 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-template <class T, bool PAIR>
+template <class T, bool PAIR, bool MAP>
 spec_status product_as(const ProductParams& p, int grid, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
     static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
     const unsigned bit = dev < 32 ? 1u << dev : 0u;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(product_kernel<T, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, PR_SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(product_kernel<T, PAIR, MAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, PR_SMEM);
         if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "product kernel attribute failed: %s", cudaGetErrorString(e));
         ready.fetch_or(bit, std::memory_order_release);
     }
-    return launched("product", launch_behind(product_kernel<T, PAIR>, p, dim3(grid), PR_THREADS, st, PR_SMEM, PAIR ? 2 : p.split));
+    return launched("product", launch_behind(product_kernel<T, PAIR, MAP>, p, dim3(grid), PR_THREADS, st, PR_SMEM, PAIR ? 2 : p.split));
 }
 
-spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cudaStream_t st) {
+spec_status product(const MatmulParams& m, bool map, int out_type, unsigned char* ws, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not to be had");
     ProductParams p = {};
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.K), static_cast<cuuint64_t>(m.C)};
-    const cuuint64_t strides[1] = {m.C > 1 ? static_cast<cuuint64_t>(m.w_stride) : static_cast<cuuint64_t>((m.K + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {PR_K, PR_CH}, one[2] = {1, 1};
-    if (encode(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<signed char*>(m.w), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return fail(SPEC_ERR_CUDA, "no tensor map for w");
+    if (map) {
+        const EncodeTiled encode = encode_tiled();
+        if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not to be had");
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(m.K), static_cast<cuuint64_t>(m.C)};
+        const cuuint64_t strides[1] = {m.C > 1 ? static_cast<cuuint64_t>(m.w_stride) : static_cast<cuuint64_t>((m.K + 15) / 16 * 16)};
+        const cuuint32_t box[2] = {PR_K, PR_CH}, one[2] = {1, 1};
+        if (encode(&p.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<signed char*>(m.w), dims, strides, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return fail(SPEC_ERR_CUDA, "no tensor map for w");
+    }
+    p.codes = m.w;
+    p.w_stride = m.w_stride;
+    p.K = m.K;
     p.out = m.out;
     p.tokens16 = ws + SPEC_SCORE_WS_HEADER;
     p.a_scale = m.a_scale;
@@ -247,7 +254,7 @@ spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cuda
     p.steps = (m.K + PR_K - 1) / PR_K;
     p.status = reinterpret_cast<unsigned*>(ws);
     p.token_tiles = (m.tokens + PR_TOKENS - 1) / PR_TOKENS;
-    const bool pair = m.tokens > 64 && static_cast<long long>((m.C + 2 * PR_CH - 1) / (2 * PR_CH)) * p.token_tiles >= sms / 4;
+    const bool pair = map && m.tokens > 64 && static_cast<long long>((m.C + 2 * PR_CH - 1) / (2 * PR_CH)) * p.token_tiles >= sms / 4;
     if (!pair) p.token_tiles = (m.tokens + PR_TOKENS_ALONE - 1) / PR_TOKENS_ALONE;
     const int per = (m.tokens + p.token_tiles - 1) / p.token_tiles;
     p.n = pair ? (per + 31) / 32 * 32 : (per + 15) / 16 * 16;
@@ -272,12 +279,15 @@ spec_status product(const MatmulParams& m, int out_type, unsigned char* ws, cuda
     SPECS_TRY(launched("product's halves", launch_behind(halves_kernel, h, dim3(static_cast<unsigned>((h.groups + 255) / 256)), 256, st)));
     if (pair) {
         const int grid = static_cast<int>(std::min<long long>(units, sms / 2)) * 2;
-        return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, true>(p, grid, st)
-               : out_type == SPEC_FP16 ? product_as<__half, true>(p, grid, st) : product_as<float, true>(p, grid, st);
+        return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, true, true>(p, grid, st)
+               : out_type == SPEC_FP16 ? product_as<__half, true, true>(p, grid, st) : product_as<float, true, true>(p, grid, st);
     }
     const int grid = p.split > 1 ? static_cast<int>(units) * p.split : static_cast<int>(std::min<long long>(units, sms));
-    return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false>(p, grid, st)
-           : out_type == SPEC_FP16 ? product_as<__half, false>(p, grid, st) : product_as<float, false>(p, grid, st);
+    if (map)
+        return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false, true>(p, grid, st)
+               : out_type == SPEC_FP16 ? product_as<__half, false, true>(p, grid, st) : product_as<float, false, true>(p, grid, st);
+    return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false, false>(p, grid, st)
+           : out_type == SPEC_FP16 ? product_as<__half, false, false>(p, grid, st) : product_as<float, false, false>(p, grid, st);
 }
 
 // ---------------------------------------------------------------------------------------------- logits
@@ -387,7 +397,17 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     p.K = K;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool codes16 = aligned16(w) && (C == 1 || w_stride % 16 == 0);
-    if (p.tokens > 8 && codes16) return product(p, out_type, static_cast<unsigned char*>(workspace), st);
+    // Up to eight tokens of not too many weights go without the tensor cores, whose two kernels take 6 us before they are under way. In
+    // us, this way / with tensor cores (C x K):
+    //   tokens  1024 x 4096   4096 x 4096   14336 x 4096   8192 x 8192   128256 x 4096
+    //   1       2.3  7.1      4.0  9.5      12.3  18.2     12.6  19.3    78.4   96.8
+    //   2       2.1  7.1      4.2  9.6      13.1  18.2     13.5  19.4    82.7   96.9
+    //   4       3.0  7.2      5.8  9.5      18.1  18.2     22.3  19.4    99.9   96.4
+    //   8       3.4  7.3      9.7  9.6      24.5  18.2     22.4  19.9    124.7  96.6
+    const long long weights = static_cast<long long>(C) * K;
+    // Rows off 16 bytes: 8 tokens, 14336 x 4099: 62 and 104; 64 tokens, 2000 x 4097: 77 and 27.
+    const bool few = p.tokens <= 2 || (p.tokens <= 8 && (!codes16 || weights <= (p.tokens <= 4 ? 50000000LL : 16000000LL)));
+    if (!few) return product(p, codes16, out_type, static_cast<unsigned char*>(workspace), st);
     const bool aligned = codes16 && K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
     return out_type == SPEC_BF16   ? matvec<__nv_bfloat16>(p, aligned, st)
            : out_type == SPEC_FP16 ? matvec<__half>(p, aligned, st) : matvec<float>(p, aligned, st);
