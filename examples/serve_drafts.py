@@ -23,7 +23,7 @@ import speculative_decoding_verification_target_gb300 as sv  # noqa: E402
 class Target:
     """Embedding, one attention layer over the cache, a gated feed-forward part and the vocabulary's logits."""
 
-    def __init__(self, vocab=2048, width=512, q_heads=8, kv_heads=2, head_dim=64, seed=0, window=0, sinks=4):
+    def __init__(self, vocab=2048, width=512, q_heads=8, kv_heads=2, head_dim=64, seed=0, window=0, sinks=4, int8=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.Hq, self.Hk, self.D, self.window, self.sinks = q_heads, kv_heads, head_dim, window, sinks
 
@@ -35,6 +35,17 @@ class Target:
         self.up, self.down, self.head = w(width, 4 * width), w(2 * width, width), 4 * w(width, vocab)
         self.q_weight = self.k_weight = torch.ones(head_dim, dtype=torch.bfloat16, device="cuda")
         self.freqs = sv.rope_frequencies(head_dim, 10000.0)
+        # a row of 8-bit weights is an output channel
+        self.int8 = {k: sv.quantize_rows(getattr(self, k).t().contiguous()) for k in ("up", "down", "head")} if int8 else None
+        self._product_ws = {}
+
+    def product(self, name, codes):
+        """Tokens in 8 bits (out, scale) times one of the weights in 8 bits."""
+        a, w = codes["out"], self.int8[name]
+        size = (a.shape[0] * a.shape[1], w["out"].shape[0], a.shape[2])
+        if size not in self._product_ws:
+            self._product_ws[size] = sv.new_matmul_workspace(*size)
+        return sv.int8_matmul(a, codes["scale"], w["out"], w["scale"], workspace=self._product_ws[size])["out"]
 
     def project(self, tokens, positions):
         """The new tokens' residual stream, rotated queries and keys, and values."""
@@ -46,6 +57,12 @@ class Target:
         return x, r["q"], r["k"], qkv[:, :, self.Hq + self.Hk:]
 
     def finish(self, x, attended):
+        if self.int8:
+            r = sv.residual_norm(attended.flatten(2) @ self.o, x, quantize=True)
+            a, b = self.product("up", r).chunk(2, -1)
+            inner = sv.quantize_rows(torch.nn.functional.silu(a) * b)
+            r = sv.residual_norm(self.product("down", inner), r["residual"], quantize=True)
+            return self.product("head", r)
         x = x + attended.flatten(2) @ self.o
         a, b = (x @ self.up).chunk(2, -1)
         return (x + (torch.nn.functional.silu(a) * b) @ self.down) @ self.head
@@ -100,9 +117,22 @@ def draft(bigram, last, K, temperature, gen):
     return torch.stack(tokens, 1), torch.stack(logits, 1).contiguous()
 
 
-def serve(rounds=24, K=4, prompts=(37, 64, 5, 130), window=0, seed=0, temperature=1.0):
-    """Returns the cache, the target, every slot's tokens, and the accepted lengths [rounds, slots]."""
-    target = Target(seed=seed, window=window)
+def process(logits, text, prompts, proposed, penalties, allowed):
+    """The target's logits with the penalties over each slot's text and the drafts before a row, and with the mask."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    longest = max(1, max(map(len, text)))
+    history = torch.tensor([t + [-1] * (longest - len(t)) for t in text], **i32)
+    lengths = torch.tensor([len(t) for t in text], **i32)
+    rates = {k: torch.full((len(text),), float(v), device="cuda") for k, v in (penalties or {}).items()}
+    mask = None if allowed is None else allowed.expand(logits.shape[0], logits.shape[1], -1)
+    return sv.process_logits(logits, tokens=proposed, history=history, lengths=lengths, prompt=torch.tensor(prompts, **i32),
+                             mask=mask, out=logits, **rates)["out"]
+
+
+def serve(rounds=24, K=4, prompts=(37, 64, 5, 130), window=0, seed=0, temperature=1.0, int8=False, penalties=None, allowed=None):
+    """Returns the cache, the target, every slot's tokens, and the accepted lengths [rounds, slots]. penalties: dict(repetition,
+    frequency, presence), any of them; allowed: a mask int32 [vocab / 32] of the tokens that may come."""
+    target = Target(seed=seed, window=window, int8=int8)
     slots, S = len(prompts) + 1, len(prompts)
     cache = Cache(target, slots, pages=64, max_pages=8)
     gen = torch.Generator(device="cuda").manual_seed(seed + 1)
@@ -130,8 +160,10 @@ def serve(rounds=24, K=4, prompts=(37, 64, 5, 130), window=0, seed=0, temperatur
         counts = torch.where(live, K + 1, 0).to(torch.int32)
         served = cache.reserve(counts)
         assert bool(served.all())
-        logits = target.score(cache, torch.cat([last[:, None], proposed], 1), counts)
-        v = sv.verify(logits.contiguous(), draft_logits, proposed, seeds + r * slots, temperature, want_diag=False)
+        logits = target.score(cache, torch.cat([last[:, None], proposed], 1), counts).contiguous()
+        if penalties or allowed is not None:      # the drafts keep the distribution that they were drawn from
+            logits = process(logits, text, list(prompts) + [prompts[0]], proposed, penalties, allowed)
+        v = sv.verify(logits, draft_logits, proposed, seeds + r * slots, temperature, want_diag=False)
         # a free slot stays empty: its advance takes the one token back that every live sequence gains
         cache.commit(torch.where(live, v["accept_len"], -1).to(torch.int32))
         accepted.append(v["accept_len"].tolist())
@@ -145,8 +177,11 @@ def main():
     a = argparse.ArgumentParser()
     a.add_argument("--rounds", type=int, default=24)
     a.add_argument("--window", type=int, default=0)
+    a.add_argument("--int8", action="store_true")
+    a.add_argument("--penalties", action="store_true")
     o = a.parse_args()
-    cache, target, text, accepted = serve(o.rounds, window=o.window)
+    rates = dict(repetition=1.2, frequency=0.3, presence=0.2) if o.penalties else None
+    cache, target, text, accepted = serve(o.rounds, window=o.window, int8=o.int8, penalties=rates)
     used = sv.pages_compact(cache.pool, cache.table, cache.refs, workspace=cache.pages_ws)
     print("mean accepted drafts a round: %.2f" % (sum(map(sum, accepted)) / sum(map(len, accepted))))
     print("tokens per slot: %s, cached: %s" % ([len(t) for t in text], cache.lengths.tolist()))

@@ -396,7 +396,8 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     p.C = C;
     p.K = K;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool codes16 = aligned16(w) && (C == 1 || w_stride % 16 == 0);
+    // what a tensor map can hold: rows on 16 bytes that do not overlap
+    const bool codes16 = aligned16(w) && (C == 1 || (w_stride % 16 == 0 && w_stride >= K && w_stride < (1LL << 40)));
     // Up to eight tokens of not too many weights go without the tensor cores, whose two kernels take 6 us before they are under way. In
     // us, this way / with tensor cores (C x K):
     //   tokens  1024 x 4096   4096 x 4096   14336 x 4096   8192 x 8192   128256 x 4096
@@ -408,7 +409,7 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     // Rows off 16 bytes: 8 tokens, 14336 x 4099: 62 and 104; 64 tokens, 2000 x 4097: 77 and 27.
     const bool few = p.tokens <= 2 || (p.tokens <= 8 && (!codes16 || weights <= (p.tokens <= 4 ? 50000000LL : 16000000LL)));
     if (!few) return product(p, codes16, out_type, static_cast<unsigned char*>(workspace), st);
-    const bool aligned = codes16 && K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
+    const bool aligned = aligned16(w) && (C == 1 || w_stride % 16 == 0) && K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
     return out_type == SPEC_BF16   ? matvec<__nv_bfloat16>(p, aligned, st)
            : out_type == SPEC_FP16 ? matvec<__half>(p, aligned, st) : matvec<float>(p, aligned, st);
 }

@@ -146,7 +146,11 @@ def new_matmul_workspace(tokens, C, K, device=None):
     n = int(_lib().spec_int8_matmul_workspace_size(tokens, C, K))
     if n == 0:
         raise ValueError("unsupported sizes tokens=%d C=%d K=%d" % (tokens, C, K))
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    if n <= 1 << 16:
+        return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws[:WS_HEADER].zero_()
+    return ws
 
 
 def int8_matmul(a, a_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out=None, workspace=None, stream=None):

@@ -113,6 +113,21 @@ def test_norm_of_zeros():
     assert (got["out"] == 0).all() and (got["scale"] == 0).all()
 
 
+@pytest.mark.parametrize("D", [1024, 20000])
+def test_norm_in_both_inputs_places(D):
+    """out in x's place and the residual in its own, and the other way round; a weight that does not begin on 16 bytes; repeated rows."""
+    x, res, buf = values(40, D, BF16, 70).cuda(), values(40, D, BF16, 71, 3.0).cuda(), torch.rand(D + 3, generator=gen(72)).bfloat16().cuda()
+    w = buf[3:]
+    want = sv.residual_norm(x, res, w)
+    check_norm(x.cpu(), res.cpu(), w.cpu(), 1e-6, False)
+    for swap in (False, True):
+        a, b = x.clone(), res.clone()
+        sv.residual_norm(a, b, w, out=b if swap else a, residual_out=a if swap else b)
+        assert torch.equal(b if swap else a, want["out"]) and torch.equal(a if swap else b, want["residual"])
+    got = sv.residual_norm(x[:1].expand(7, D), res[:1].expand(7, D), w)
+    assert torch.equal(got["out"], want["out"][:1].expand(7, D)) and torch.equal(got["residual"], want["residual"][:1].expand(7, D))
+
+
 @pytest.mark.parametrize("quantize", [False, True])
 @pytest.mark.parametrize("D", [512, 520, 509])
 def test_norm_strides_places_and_shapes(D, quantize):
@@ -226,6 +241,27 @@ def test_product_strides_and_rims():
         got = sv.int8_matmul(av, sa.cuda().view(B, N), wv, sw.cuda(), out=buf[:, :, 4:4 + C])["out"]
         assert torch.equal(got.reshape(B * N, C), plain)
         assert (buf[:, :, :4] == 5).all() and (buf[:, :, 4 + C:] == 5).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_product_of_rows_that_repeat_or_overlap(M):
+    """Inputs may: one token's codes for all, one channel's for all, and channels that begin 16 or 5 codes after one another."""
+    K, C = 320, 70
+    one, long = ints(1, K, 50).cuda(), ints(1, K + 16 * C, 51, "any").cuda()[0]
+    sa, sw = torch.ones(M, device="cuda"), torch.ones(C, device="cuda")
+    for a in (ints(M, K, 52).cuda(), one.expand(M, K)):
+        for w in (one.expand(C, K), long.as_strided((C, K), (16, 1)), long.as_strided((C, K), (5, 1), 3)):
+            got = sv.int8_matmul(a, sa, w, sw, dtype=F32)["out"]
+            assert torch.equal(got.double(), a.double() @ w.double().t())
+
+
+def test_a_workspace_that_is_not_given_is_ready():
+    """Also one so large that only its header is cleared."""
+    a, w = ints(600, 1024, 53).cuda(), ints(300, 1024, 54).cuda()
+    torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")      # what the allocator may hand out
+    r = sv.int8_matmul(a, torch.ones(600, device="cuda"), w, torch.ones(300, device="cuda"), dtype=F32)
+    assert r["workspace"].numel() > 1 << 16 and sv.read_status(r["workspace"]) == 0
+    assert torch.equal(r["out"].double(), a.double() @ w.double().t())
 
 
 def test_a_scale_of_nan_stays_in_its_row():
@@ -342,6 +378,23 @@ def test_lengths_and_prompts_outside_the_history():
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
     run_logits(dict(x=x, history=h, lengths=i32(-5, 0, 21, 2 ** 31 - 1), prompt=i32(-1, 5, 100, -2 ** 31), frequency=torch.ones(4),
                     repetition=torch.full((4,), 1.5)))
+
+
+def test_untouched_logits_keep_their_values():
+    """Next to penalised tokens: infinities, NaN, zeros of both signs and subnormal numbers, in place too."""
+    for dtype in (BF16, F32):
+        x = torch.randn(1, 2, 64, generator=gen(60)).to(dtype)
+        x[0, :, 1:8] = torch.tensor([float("inf"), float("-inf"), float("nan"), -0.0, 0.0, 1e-40, -1e-39]).to(dtype)
+        h = torch.arange(0, 64, 8, dtype=torch.int32)[None].cuda()
+        a = dict(history=h, lengths=torch.tensor([8], dtype=torch.int32).cuda(), repetition=torch.tensor([1.5]).cuda(),
+                 frequency=torch.tensor([0.5]).cuda(), bias_tokens=torch.tensor([[9]], dtype=torch.int32).cuda(), bias=torch.tensor([[2.0]]).cuda())
+        y = x.cuda()
+        for got in (sv.process_logits(x.cuda(), **a)["out"], sv.process_logits(y, out=y, **a)["out"]):
+            for i in list(range(1, 8)) + list(range(10, 16)):
+                p, q = got[0, :, i].cpu(), x[0, :, i]
+                assert torch.equal(torch.isnan(p), torch.isnan(q)) and torch.equal(torch.signbit(p[~torch.isnan(p)]), torch.signbit(q[~torch.isnan(q)]))
+                assert torch.equal(p[~torch.isnan(p)], q[~torch.isnan(q)])
+            assert torch.equal(got[0, :, 9].cpu(), (x[0, :, 9].float() + 2).to(dtype))
 
 
 def test_repeated_entries():
