@@ -22,15 +22,15 @@ __device__ __forceinline__ float larger(float a, float b) {
     return r;
 }
 
-// 127 p / m is rounded to the nearest integer, ties to even, as if it were exact. In fp32, p times the rounded 127 / m is off by
-// 127 x 2^-23 at most, so the integer next to it is the right one unless it lies that near to the middle of two. There the
+// 127 p / m is rounded to the nearest integer, ties to even, as if it were exact. The exact product of p and the rounded 127 / m is
+// off by 127 x 2^-24 at most, so the integer next to it is the right one unless it lies that near to the middle of two. There the
 // exact products decide: with k the integer below, 254 p against (2 k + 1) m, each as a float and its rounding error.
 struct Codes {
     float m, by, scale;      // the row's largest magnitude, 127 / m, and the power of two that brings m into range for the exact step
     bool all;                // every code by the exact step
     __device__ explicit Codes(float top) : m(top) {
         scale = top < 8.6736174e-19f ? 1.8446744e19f : top > 1.1529215e18f ? 5.4210109e-20f : 1.f;      // 2^-60: 2^64, 2^60: 2^-64
-        all = scale != 1.f;
+        all = scale != 1.f && top > 0.f;
         by = top > 0.f ? 127.f / top : 0.f;
     }
     __device__ int exact(float p) const {
@@ -44,18 +44,41 @@ struct Codes {
         return static_cast<int>(k) + (up ? 1 : 0);
     }
     // Codes of n values; the low byte of each float's bits in c.
+    static constexpr float DOUBT = 0.49999f;
     template <int n>
     __device__ void of(const float (&p)[n], uint32_t (&c)[n]) const {
         float off = all ? 1.f : 0.f;
+        if constexpr (n % 2 == 0) {
+            const unsigned long long by2 = specc::pack2(by, by), magic = specc::pack2(12582912.f, 12582912.f), minus = specc::pack2(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float q = p[i] * by, f = q + 12582912.f;      // its last place is 1
-            off = fmaxf(off, fabsf(q - (f - 12582912.f)));
-            c[i] = __float_as_uint(f);
+            for (int i = 0; i < n; i += 2) {
+                const unsigned long long v = specc::pack2(p[i], p[i + 1]), f = specc::fma2(v, by2, magic);      // its last place is 1
+                const float2 d = specc::unpack2(specc::fma2(v, by2, specc::fma2(f, minus, magic))), c2 = specc::unpack2(f);
+                off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+                c[i] = __float_as_uint(c2.x), c[i + 1] = __float_as_uint(c2.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float f = fmaf(p[i], by, 12582912.f);
+                off = fmaxf(off, fabsf(fmaf(p[i], by, 12582912.f - f)));
+                c[i] = __float_as_uint(f);
+            }
         }
-        if (off > 0.49998f) {
+        if (off > DOUBT) {      // one after the other, by choosing among the registers: a copy of the step for each made it no faster
+            unsigned left = 0u;
 #pragma unroll
-            for (int i = 0; i < n; ++i) c[i] = static_cast<uint32_t>(exact(p[i]));
+            for (int i = 0; i < n; ++i)
+                left |= (all || fabsf(fmaf(p[i], by, 12582912.f - __uint_as_float(c[i]))) > DOUBT ? 1u : 0u) << i;
+            for (; left; left &= left - 1) {
+                const int at = __ffs(left) - 1;
+                float v = p[0];
+#pragma unroll
+                for (int i = 1; i < n; ++i) v = i == at ? p[i] : v;
+                const uint32_t e = static_cast<uint32_t>(exact(v));
+#pragma unroll
+                for (int i = 0; i < n; ++i) c[i] = i == at ? e : c[i];
+            }
         }
     }
 };
@@ -95,6 +118,12 @@ struct Piece {
         else *reinterpret_cast<uint2*>(to) = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
     }
 };
+
+// The larger magnitudes of pairs of 16-bit values, as integers: a NaN is above all.
+__device__ __forceinline__ uint32_t larger2(uint32_t a, const uint4& x) {
+    a = __vmaxu2(a, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu));
+    return __vmaxu2(a, __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+}
 
 // The sum and the largest magnitude over a row's `warps` warps, the first of which is `from`; `turn` alternates.
 __device__ __forceinline__ void join_row(float& sum, float& top, int from, int warps, int turn, float2 (*s_part)[32]) {
@@ -148,12 +177,19 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __gr
     const long long step = static_cast<long long>(gridDim.x) * per;
     int turn = 0;
     for (long long base = row - sub; base < p.rows; base += step, row += step, turn ^= 1) {
-        float r[SLOTS][E];
+        constexpr bool AS_IS = !FULL && VEC && sizeof(T) == 2;      // kept as they were read
+        std::conditional_t<AS_IS, Raw, float[E]> r[SLOTS];
         float sum = 0.f, top = 0.f;
+        uint32_t pairs = 0u;
         T* const res_out = with && row < p.rows ? static_cast<T*>(p.res_out.p) + place(p.res_out, row) : nullptr;
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
             if (row >= p.rows || c + s * p.tpr >= pieces) continue;
+            if constexpr (AS_IS) {
+                r[s] = x[s];
+                pairs = larger2(pairs, x[s]);
+                continue;
+            } else {
             P::get(x[s], r[s]);
             if (with) {
                 float add[E];
@@ -172,6 +208,12 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __gr
                 if (weighted) r[s][i] *= g[i];
                 if (CODES) top = larger(top, r[s][i]);
             }
+            }
+        }
+        if constexpr (AS_IS) {
+            const unsigned short m = static_cast<unsigned short>(max(pairs & 0xFFFFu, pairs >> 16));
+            if constexpr (std::is_same_v<T, __half>) top = __half2float(__ushort_as_half(m));
+            else top = __uint_as_float(static_cast<uint32_t>(m) << 16);
         }
         fetch(row + step);
         join_row(sum, top, threadIdx.x / 32 - c / 32, p.tpr / 32, turn, s_part);
@@ -185,15 +227,21 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __gr
             for (int s = 0; s < SLOTS; ++s) {
                 if (c + s * p.tpr >= pieces) continue;
                 uint32_t q[E];
+                float v[E];
+                if constexpr (AS_IS) P::get(r[s], v);
+                else {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) v[i] = r[s][i];
+                }
                 if (bad) {
 #pragma unroll
-                    for (int i = 0; i < E; ++i) r[s][i] = 0.f;
+                    for (int i = 0; i < E; ++i) v[i] = 0.f;
                 }
-                codes.of(r[s], q);
+                codes.of(v, q);
                 P::codes(out + (c + s * p.tpr) * E, q);
             }
             if (c == 0) p.scale[row] = bad ? NAN : top / 127.f * inv;
-        } else {
+        } else if constexpr (!AS_IS) {
             T* const out = static_cast<T*>(p.out.p) + place(p.out, row);
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s) {
