@@ -141,7 +141,7 @@ __device__ __forceinline__ void join_row(float& sum, float& top, int from, int w
 // A row is in the registers of tpr threads, SLOTS pieces each, between its one read and its one write; the next row of these
 // threads is on its way meanwhile, and the weights stay. Bandwidth bounds many rows, latency few: there a row has more threads.
 // FULL: with a residual, a weight or a norm; else codes of the rows as they are, with half the registers. 16384 rows of 4096 in bf16,
-// with all of it, take 78.8 us (89% of the copy rate), 8192 rows of 14336 as they are 87.9 us (60%; 101.8 us with one CTA an SM).
+// with all of it, take 78.4 us (90% of the copy rate), 8192 rows of 14336 as they are 79.3 us (66%; instruction issue and the row's barrier).
 template <class T, bool CODES, int SLOTS, bool VEC, bool FULL>
 __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __grid_constant__ NormParams p) {
     using P = Piece<T, VEC>;
@@ -250,6 +250,152 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __gr
                 for (int i = 0; i < E; ++i) r[s][i] *= inv;
                 *reinterpret_cast<Raw*>(out + (c + s * p.tpr) * E) = P::put(r[s]);
             }
+        }
+    }
+}
+
+// 16-bit rows of which each begins elsewhere within 16 bytes, but all of a token's alike, as those of an odd width do: pieces of 16
+// bytes from the row's first such place on, and up to seven single values at either end, one a thread. The weights come from shared
+// memory, shifted by the row's place. 5001 rows of 2051 in fp16 take 22.6 us (value by value 27.6).
+template <class T, bool CODES, int SLOTS>
+__global__ void __launch_bounds__(512) norm_peel_kernel(const __grid_constant__ NormParams p) {
+    using P = Piece<T, true>;
+    constexpr int E = P::E;
+    extern __shared__ uint4 s_weight[];      // up to the second piece behind the last value
+    __shared__ float2 s_part[2][32];
+    after_previous();
+    const int per = blockDim.x / p.tpr, sub = threadIdx.x / p.tpr, c = threadIdx.x - sub * p.tpr;
+    const bool with = p.res.p != nullptr;
+    uint4 x[SLOTS], y[SLOTS];
+    T x1 = from_float<T>(0.f), y1 = from_float<T>(0.f);
+    auto place = [&](const Rows& t, long long row) {
+        const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<long long>(b) * p.N);
+        return static_cast<T*>(t.p) + b * t.sb + n * t.sn;
+    };
+    // a row's first value on 16 bytes, its pieces, and the single value that is this thread's or -1
+    struct Cut {
+        int head, whole, single;
+        __device__ Cut(const T* row, int D, int c, int tpr) {
+            head = min(D, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
+            whole = (D - head) / E;
+            const int tail = D - head - whole * E, back = tpr - 1 - c;
+            single = c < head ? c : back < tail ? D - 1 - back : -1;
+        }
+    };
+    auto fetch = [&](long long row) {
+        if (row >= p.rows) return;
+        const T *const px = place(p.x, row), *const py = with ? place(p.res, row) : px;
+        const Cut cut(px, p.D, c, p.tpr);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (c + s * p.tpr < cut.whole) {
+                x[s] = *reinterpret_cast<const uint4*>(px + cut.head + (c + s * p.tpr) * E);
+                if (with) y[s] = *reinterpret_cast<const uint4*>(py + cut.head + (c + s * p.tpr) * E);
+            }
+        if (cut.single >= 0) {
+            x1 = px[cut.single];
+            if (with) y1 = py[cut.single];
+        }
+    };
+    long long row = static_cast<long long>(blockIdx.x) * per + sub;
+    fetch(row);
+    const T* const w = static_cast<const T*>(p.weight);
+    T* const sw = reinterpret_cast<T*>(s_weight);
+    if (w) {
+        for (int i = threadIdx.x; i < (p.D + 7) / 8 * 8 + 8; i += blockDim.x) sw[i] = i < p.D ? w[i] : from_float<T>(0.f);
+        __syncthreads();
+    }
+    const long long step = static_cast<long long>(gridDim.x) * per;
+    int turn = 0;
+    for (long long base = row - sub; base < p.rows; base += step, row += step, turn ^= 1) {
+        const bool real = row < p.rows;
+        const Cut cut(real ? place(p.x, row) : nullptr, p.D, c, p.tpr);
+        T* const res_out = with && real ? place(p.res_out, row) : nullptr;
+        float r[SLOTS][E], r1 = 0.f, sum = 0.f, top = 0.f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const int q = c + s * p.tpr;
+            if (!real || q >= cut.whole) continue;
+            P::get(x[s], r[s]);
+            if (with) {
+                float add[E];
+                P::get(y[s], add);
+#pragma unroll
+                for (int i = 0; i < E; ++i) r[s][i] += add[i];
+                const uint4 rounded = P::put(r[s]);
+                *reinterpret_cast<uint4*>(res_out + cut.head + q * E) = rounded;
+                P::get(rounded, r[s]);
+            }
+            float g[E];
+            if (w) {
+                const uint4 a = s_weight[q], b = s_weight[q + 1];
+                const uint32_t t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                const int by = cut.head >> 1;
+                uint32_t m[5], u[4];
+#pragma unroll
+                for (int i = 0; i < 5; ++i) m[i] = by == 0 ? t[i] : by == 1 ? t[i + 1] : by == 2 ? t[i + 2] : t[i + 3];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = cut.head & 1 ? __byte_perm(m[i], m[i + 1], 0x5432) : m[i];
+                P::get(make_uint4(u[0], u[1], u[2], u[3]), g);
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                sum = fmaf(r[s][i], r[s][i], sum);
+                if (w) r[s][i] *= g[i];
+                if (CODES) top = larger(top, r[s][i]);
+            }
+        }
+        if (real && cut.single >= 0) {
+            r1 = to_float(x1);
+            if (with) {
+                const T rounded = from_float<T>(r1 + to_float(y1));
+                res_out[cut.single] = rounded;
+                r1 = to_float(rounded);
+            }
+            sum = fmaf(r1, r1, sum);
+            if (w) r1 *= to_float(sw[cut.single]);
+            if (CODES) top = larger(top, r1);
+        }
+        fetch(row + step);
+        join_row(sum, top, threadIdx.x / 32 - c / 32, p.tpr / 32, turn, s_part);
+        if (!real) continue;
+        const float inv = p.norm ? rsqrtf(sum / p.D + p.eps) : 1.f;
+        if constexpr (CODES) {
+            const bool bad = !(top < INFINITY);
+            const Codes codes(bad ? 0.f : top);
+            const int b = static_cast<int>(row / p.N), n = static_cast<int>(row - static_cast<long long>(b) * p.N);
+            signed char* const out = row_of<signed char>(p.out, b, n);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                const int q = c + s * p.tpr;
+                if (q >= cut.whole) continue;
+                uint32_t k[E];
+                if (bad) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) r[s][i] = 0.f;
+                }
+                codes.of(r[s], k);
+#pragma unroll
+                for (int i = 0; i < E; ++i) out[cut.head + q * E + i] = static_cast<signed char>(k[i]);
+            }
+            if (cut.single >= 0) {
+                const float one[1] = {bad ? 0.f : r1};
+                uint32_t k[1];
+                codes.of(one, k);
+                out[cut.single] = static_cast<signed char>(k[0]);
+            }
+            if (c == 0) p.scale[row] = bad ? NAN : top / 127.f * inv;
+        } else {
+            T* const out = place(p.out, row);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s) {
+                const int q = c + s * p.tpr;
+                if (q >= cut.whole) continue;
+#pragma unroll
+                for (int i = 0; i < E; ++i) r[s][i] *= inv;
+                *reinterpret_cast<uint4*>(out + cut.head + q * E) = P::put(r[s]);
+            }
+            if (cut.single >= 0) out[cut.single] = from_float<T>(r1 * inv);
         }
     }
 }

@@ -117,6 +117,15 @@ bool whole_pieces(const NormParams& p, size_t e, bool codes, int B) {
     return p.D % per == 0 && fits(p.x, 16) && fits(p.res, 16) && fits(p.res_out, 16) && fits(p.out, codes ? per : 16) && aligned16(p.weight);
 }
 
+// Rows that begin alike within 16 bytes, one token's of x, residual and 16-bit outputs.
+bool alike_rows(const NormParams& p, size_t e, bool codes, int B) {
+    auto as_x = [&](const Rows& t) {
+        return !t.p || ((reinterpret_cast<uintptr_t>(t.p) - reinterpret_cast<uintptr_t>(p.x.p)) % 16 == 0 &&
+                        (B <= 1 || (t.sb - p.x.sb) * static_cast<long long>(e) % 16 == 0) && (p.N <= 1 || (t.sn - p.x.sn) * static_cast<long long>(e) % 16 == 0));
+    };
+    return as_x(p.res) && as_x(p.res_out) && (codes || as_x(p.out));
+}
+
 template <class T, bool CODES, bool VEC, bool FULL>
 auto norm_of(int slots) -> void (*)(const NormParams) {
     if constexpr (VEC) return slots == 1 ? norm_rows_kernel<T, CODES, 1, VEC, FULL> : slots == 2 ? norm_rows_kernel<T, CODES, 2, VEC, FULL>
@@ -125,7 +134,18 @@ auto norm_of(int slots) -> void (*)(const NormParams) {
 }
 
 template <class T, bool CODES>
-spec_status norm_as(NormParams p, bool vec, int sms, cudaStream_t st) {
+spec_status norm_as(NormParams p, bool vec, bool peel, int sms, cudaStream_t st) {
+    if constexpr (sizeof(T) == 2) {
+        if (peel && p.D >= 256 && p.D <= 16384) {
+            const int slots = p.D > 4096 || p.rows > 4LL * sms ? 4 : 2;
+            p.tpr = ((p.D / 8 + slots - 1) / slots + 31) / 32 * 32;
+            const int per = std::max(1, 128 / p.tpr), threads = per * p.tpr;
+            const long long ctas = std::min((p.rows + per - 1) / per, static_cast<long long>(sms) * std::max(1, 512 / threads));
+            const size_t smem = p.weight ? ((static_cast<size_t>(p.D) + 7) / 8 * 8 + 8) * 2 : 0;
+            return launched("norm", launch_behind(slots == 4 ? norm_peel_kernel<T, CODES, 4> : norm_peel_kernel<T, CODES, 2>, p,
+                                                  dim3(static_cast<unsigned>(ctas)), threads, st, smem));
+        }
+    }
     const int pieces = vec ? p.D / (16 / static_cast<int>(sizeof(T))) : p.D, most = vec ? 4 : 16;
     if (pieces > 512 * most)
         return launched("norm", launch_behind(norm_long_kernel<T, CODES>, p, dim3(static_cast<unsigned>(p.rows)), 512, st));
@@ -148,7 +168,8 @@ spec_status norm_as(const NormParams& p, bool codes, int B, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
     const bool vec = whole_pieces(p, sizeof(T), codes, B);
-    return codes ? norm_as<T, true>(p, vec, sms, st) : norm_as<T, false>(p, vec, sms, st);
+    const bool peel = !vec && alike_rows(p, sizeof(T), codes, B);
+    return codes ? norm_as<T, true>(p, vec, peel, sms, st) : norm_as<T, false>(p, vec, peel, sms, st);
 }
 
 spec_status norm(const NormParams& p, int dtype, bool codes, int B, cudaStream_t st) {

@@ -38,7 +38,7 @@ def check_norm(x, residual, weight, eps, quantize, **kw):
         assert ((got["out"].cpu().double() - v).abs() <= tol).all()
 
 
-WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 127, 128, 255, 256, 257, 1000, 1024, 2051, 4096, 4104, 8192, 10007, 16384, 32760, 32768]
+WIDTHS = [1, 2, 7, 8, 31, 32, 33, 64, 127, 128, 255, 256, 257, 261, 263, 511, 1000, 1024, 2050, 2051, 4095, 4096, 4097, 4104, 8192, 10007, 16383, 16384, 16385, 32760, 32768]
 
 
 @pytest.mark.parametrize("quantize", [False, True])
@@ -50,7 +50,7 @@ def test_norm(D, dtype, quantize):
                    (1 + 0.2 * torch.randn(D, generator=gen(seed + 20))).to(dtype) if weight else None, 1e-6, quantize)
 
 
-@pytest.mark.parametrize("rows,D", [(1, 4096), (6, 4096), (151, 512), (1217, 96), (700, 2048), (3001, 264), (400, 8192)])
+@pytest.mark.parametrize("rows,D", [(1, 4096), (6, 4096), (151, 512), (1217, 96), (700, 2048), (3001, 264), (400, 8192), (1500, 2051), (700, 4099), (2000, 301)])
 def test_norm_of_many_rows(rows, D):
     x, res, w = values(rows, D, BF16, 5), values(rows, D, BF16, 6, 3.0), (1 + 0.2 * torch.randn(D, generator=gen(7))).bfloat16()
     for quantize in (False, True):
