@@ -44,7 +44,7 @@ struct HalvesParams {
 // ------------------------------------------------------------------------------------ tokens to halves
 // The tokens' codes as halves, in the blocks that the product reads: for each tile of n tokens and 64 of K, n rows of 128 bytes
 // whose 16-byte pieces are exchanged as 128-byte swizzling wants it (piece c of row r at c ^ (r & 7)). Rows and columns past the
-// ends are 0. One pass of a few MB from and to L2: 384 tokens of 4096 take 2 us.
+// ends are 0. A few MB from and to L2; the product's first copies of codes are on their way meanwhile.
 __device__ __forceinline__ void halves_of(uint32_t x, uint32_t& lo, uint32_t& hi) {
     // a byte b behind 0x64 is the half 1024 + b; with b = code + 128 that is the code and 1152
     const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
