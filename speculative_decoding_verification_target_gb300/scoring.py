@@ -20,8 +20,8 @@ import functools
 
 import torch
 
-from . import SPEC_OK, SpecError, _need, _new, load as _load
-from .cache import _DTYPES, _code, _home, _on, _ptr, _vector, _workspace
+from . import SPEC_OK, SpecError, _current_device, _need, _new, load as _load
+from .cache import _DTYPES, _code, _home, _on, _raw_stream, _vector, _workspace
 
 WS_HEADER = 256
 INT8 = 3
@@ -56,15 +56,20 @@ def _ok(code):
         raise SpecError(code, _lib().spec_score_last_error().decode())
 
 
+# A serving loop makes these calls for every few tokens, where the host takes longer than the device: what passes is looked at in one
+# condition, and functions are called for what does not.
 def _rows(t, name):
     """[rows, values] or [B, N, values] as (B, N, values) and its rows; type and device known."""
-    if t.dim() == 2:
-        (N, D), (sn, sd) = t.shape, t.stride()
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2:
+        N, D = shape
+        sn, sd = strides
         B, sb = 1, 0
-    elif t.dim() == 3:
-        (B, N, D), (sb, sn, sd) = t.shape, t.stride()
+    elif len(shape) == 3:
+        B, N, D = shape
+        sb, sn, sd = strides
     else:
-        raise ValueError("%s must be [rows, values] or [B, N, values], got %s" % (name, tuple(t.shape)))
+        raise ValueError("%s must be [rows, values] or [B, N, values], got %s" % (name, tuple(shape)))
     if sd != 1 and D > 1:
         raise ValueError("%s must have contiguous values" % name)
     return B, N, D, Rows(t.data_ptr(), sb, sn)
@@ -83,23 +88,30 @@ def _rows_like(t, name, shape, dtype, d):
     return _rows(t, name)[3]
 
 
-def _output(t, name, shape, dtype, d, device, stream):
-    """The caller's output or a new one, with its rows."""
-    if t is not None:
-        return t, _rows_like(t, name, shape, dtype, d)
-    if stream is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-    else:
-        t = _new(torch.empty, stream, shape, dtype=dtype, device=device)
+def _make(shape, dtype, device, stream):
+    """A new output, and its rows."""
+    t = torch.empty(shape, dtype=dtype, device=device) if stream is None else _new(torch.empty, stream, shape, dtype=dtype, device=device)
     n = shape[-1]
     return t, Rows(t.data_ptr(), n * shape[-2], n)
 
 
 def _scales(t, shape, d, device, stream):
-    if t is None:
-        return _new(torch.empty, stream, shape, dtype=torch.float32, device=device)
-    _vector(t, "scale", torch.float32, shape, d)
-    return t
+    if t is not None:
+        _vector(t, "scale", torch.float32, shape, d)
+        return t
+    if stream is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    return _new(torch.empty, stream, shape, dtype=torch.float32, device=device)
+
+
+def _device_of(t, name, stream):
+    """The device of a call: the current one, where t is and the stream."""
+    d = t.get_device()
+    return d if stream is None and d >= 0 and d == _current_device() else _home(t, name, stream)
+
+
+def _handle(d, stream):
+    return _raw_stream(d) if stream is None and _raw_stream is not None else _on(d, stream)
 
 
 def residual_norm(x, residual=None, weight=None, eps=1e-6, *, quantize=False, out=None, scale=None, residual_out=None,
@@ -107,25 +119,32 @@ def residual_norm(x, residual=None, weight=None, eps=1e-6, *, quantize=False, ou
     """r = x + residual and its root-mean-square norm times a weight [D], in x's type (bf16, fp16 or fp32) or, with quantize, in
     8 bits with a scale per token. residual_out may be x or residual, out (not in 8 bits) may be the other one. Returns dict(out,
     scale, residual); scale is None without quantize, residual without a residual."""
-    code = _code(x, "x", True)
-    d = _home(x, "x", stream)
-    B, N, D, xi = _rows(x, "x")
     shape, dt = x.shape, x.dtype
-    ri = ro = None
+    code = _code(x, "x", True)
+    d = _device_of(x, "x", stream)
+    B, N, D, xi = _rows(x, "x")
+    ri = ro = w = sp = None
     if residual is not None:
         ri = _rows_like(residual, "residual", shape, dt, d)
-        residual_out, ro = _output(residual_out, "residual_out", shape, dt, d, x.device, stream)
+        if residual_out is None:
+            residual_out, ro = _make(shape, dt, x.device, stream)
+        else:
+            ro = _rows_like(residual_out, "residual_out", shape, dt, d)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if weight is not None:
         _vector(weight, "weight", dt, (D,), d)
+        w = weight.data_ptr()
     if quantize:
         scale = _scales(scale, shape[:-1], d, x.device, stream)
+        sp = scale.data_ptr()
     elif scale is not None:
         raise ValueError("scale needs quantize")
-    out, oi = _output(out, "out", shape, torch.int8 if quantize else dt, d, x.device, stream)
-    _ok(_lib().spec_residual_norm(xi, ri, code, B, N, D, _ptr(weight), eps, ro, oi, INT8 if quantize else code, _ptr(scale),
-                                  _on(d, stream)))
+    if out is None:
+        out, oi = _make(shape, torch.int8 if quantize else dt, x.device, stream)
+    else:
+        oi = _rows_like(out, "out", shape, torch.int8 if quantize else dt, d)
+    _ok(_lib().spec_residual_norm(xi, ri, code, B, N, D, w, eps, ro, oi, INT8 if quantize else code, sp, _handle(d, stream)))
     return dict(out=out, scale=scale, residual=residual_out)
 
 
@@ -133,11 +152,15 @@ def quantize_rows(x, *, out=None, scale=None, stream=None):
     """Each row of x (bf16, fp16 or fp32) in 8 bits: code = the integer nearest to 127 x / m, scale = m / 127, m the row's largest
     magnitude. For weights [C, K] once, for activations each time. Returns dict(out, scale)."""
     code = _code(x, "x", True)
-    d = _home(x, "x", stream)
+    d = _device_of(x, "x", stream)
     B, N, D, xi = _rows(x, "x")
-    scale = _scales(scale, x.shape[:-1], d, x.device, stream)
-    out, oi = _output(out, "out", x.shape, torch.int8, d, x.device, stream)
-    _ok(_lib().spec_quantize_rows(xi, code, B, N, D, oi, scale.data_ptr(), _on(d, stream)))
+    shape = x.shape
+    scale = _scales(scale, shape[:-1], d, x.device, stream)
+    if out is None:
+        out, oi = _make(shape, torch.int8, x.device, stream)
+    else:
+        oi = _rows_like(out, "out", shape, torch.int8, d)
+    _ok(_lib().spec_quantize_rows(xi, code, B, N, D, oi, scale.data_ptr(), _handle(d, stream)))
     return dict(out=out, scale=scale)
 
 
@@ -158,26 +181,33 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out=
     [C]: the sum in integers, exactly, then scaled and rounded to dtype (bf16, fp16 or fp32). Returns dict(out, workspace)."""
     if a.dtype is not torch.int8:
         raise TypeError("a must be torch.int8, got %s" % a.dtype)
-    d = _home(a, "a", stream)
+    d = _device_of(a, "a", stream)
     B, N, K, ai = _rows(a, "a")
     if w.dim() != 2:
         raise ValueError("w must be [C, K], got %s" % (tuple(w.shape),))
     C = w.shape[0]
     wi = _rows_like(w, "w", (C, K), torch.int8, d)
-    _vector(a_scale, "a_scale", torch.float32, a.shape[:-1], d)
+    tokens = a.shape[:-1]
+    _vector(a_scale, "a_scale", torch.float32, tokens, d)
     _vector(w_scale, "w_scale", torch.float32, (C,), d)
+    bp = None
     if bias is not None:
         _vector(bias, "bias", torch.float32, (C,), d)
+        bp = bias.data_ptr()
     if out is not None:
         dtype = out.dtype
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError("out must be bfloat16, float16 or float32, got %s" % dtype)
-    out, oi = _output(out, "out", a.shape[:-1] + (C,), dtype, d, a.device, stream)
+    if out is None:
+        out, oi = _make(tokens + (C,), dtype, a.device, stream)
+    else:
+        oi = _rows_like(out, "out", tokens + (C,), dtype, d)
     if workspace is None:
         workspace = _new(new_matmul_workspace, stream, max(B * N, 1), C, K, a.device)
-    _ok(_lib().spec_int8_matmul(ai, a_scale.data_ptr(), w.data_ptr(), wi.stride_n, w_scale.data_ptr(), _ptr(bias), B, N, C, K,
-                                oi, code, *_workspace(workspace, d), _on(d, stream)))
+    wp, size = _workspace(workspace, d)
+    _ok(_lib().spec_int8_matmul(ai, a_scale.data_ptr(), wi.data, wi.stride_n, w_scale.data_ptr(), bp, B, N, C, K, oi, code, wp, size,
+                                _handle(d, stream)))
     return dict(out=out, workspace=workspace)
 
 
@@ -196,7 +226,7 @@ def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=No
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V], got %s" % (tuple(logits.shape),))
     code = _code(logits, "logits", True)
-    d = _home(logits, "logits", stream)
+    d = _device_of(logits, "logits", stream)
     B, R, V, xi = _rows(logits, "logits")
     T = L = n = 0
     tp = hp = lp = pp = bt = bp = mp = None
@@ -211,9 +241,11 @@ def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=No
             raise ValueError("history needs lengths")
         lp = _ints(lengths, "lengths", (B,), d)
         pp = None if prompt is None else _ints(prompt, "prompt", (B,), d)
+    rates = []
     for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence")):
         if t is not None:
             _vector(t, name, torch.float32, (B,), d)
+        rates.append(None if t is None else t.data_ptr())
     if bias_tokens is not None:
         n = bias_tokens.shape[-1]
         bt = _ints(bias_tokens, "bias_tokens", (B, n), d)
@@ -224,7 +256,9 @@ def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=No
     if mask is not None:
         mi = _rows_like(mask, "mask", (B, R, (V + 31) // 32), torch.int32, d)
         mp, sb, sr = mi.data, mi.stride_b, mi.stride_n
-    out, oi = _output(out, "out", logits.shape, logits.dtype, d, logits.device, stream)
-    _ok(_lib().spec_process_logits(xi, code, B, R, V, tp, T, hp, lp, pp, L, _ptr(repetition), _ptr(frequency), _ptr(presence),
-                                   bt, bp, n, mp, sb, sr, oi, _on(d, stream)))
+    if out is None:
+        out, oi = _make(logits.shape, logits.dtype, logits.device, stream)
+    else:
+        oi = _rows_like(out, "out", logits.shape, logits.dtype, d)
+    _ok(_lib().spec_process_logits(xi, code, B, R, V, tp, T, hp, lp, pp, L, *rates, bt, bp, n, mp, sb, sr, oi, _handle(d, stream)))
     return dict(out=out)

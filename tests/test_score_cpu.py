@@ -164,6 +164,8 @@ def fake(monkeypatch):
     t, lib = fc.install(monkeypatch, sv)
     monkeypatch.setattr(scoring, "torch", t)
     monkeypatch.setattr(scoring, "_lib", lambda: lib)
+    monkeypatch.setattr(scoring, "_raw_stream", None)
+    monkeypatch.setattr(scoring, "_current_device", t.cuda.current_device)
     return t, lib
 
 
