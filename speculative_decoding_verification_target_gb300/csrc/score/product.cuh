@@ -26,6 +26,7 @@ struct ProductParams {
     Rows out;
     const unsigned char* tokens16;
     const float *a_scale, *w_scale, *bias;
+    Rows a;                        // the tokens' codes, where they become halves here
     const signed char* codes;      // w, for rows that no tensor map can hold
     long long w_stride;
     int tokens, N, C, K;
@@ -202,10 +203,11 @@ struct Unit {
 //                  of the warps takes half of the tokens
 // PAIR: two CTAs share a tile of 256 channels; each holds its channels and half of the tokens, the first one issues.
 // MAP: the codes' rows are on 16 bytes, and copies bring them; else the warps that turn them fetch them themselves, 16 bytes a lane.
+// HERE: up to 32 tokens, one tile of them, whose codes the same warps fetch and turn, a step of theirs ahead: one launch.
 // split > 1: the CTAs of a cluster share a tile's K, and add their integers through one another's shared memory.
 // 384 tokens, 128256 channels of 4096 take 240 us, 1.68 P operations a second, 86% of what a library product in bf16 reaches; 8192
 // tokens, 14336 channels of 4096 561 us, 88%.
-template <class T, bool PAIR, bool MAP>
+template <class T, bool PAIR, bool MAP, bool HERE>
 __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char dynamic[];
     __shared__ alignas(8) uint64_t s_full[PR_STAGES], s_empty[PR_STAGES], s_ready[4], s_half_empty[2], s_acc_full[2], s_acc_empty[2];
@@ -250,12 +252,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             const uint64_t keep = specv::policy_evict_last(), w_policy = p.stream_w ? specv::policy_evict_first() : specv::policy_evict_normal();
             auto codes = [&](int st, const Unit& u, int k) {
                 if (lane == 0) {
-                    specv::mbar_arrive_expect_tx(&s_full[st], MAP ? stage_bytes : 2 * half_bytes);
+                    specv::mbar_arrive_expect_tx(&s_full[st], (MAP ? PR_W_BYTES : 0) + (HERE ? 0 : 2 * half_bytes));
                     if (MAP) load_codes(smem + st * stage_bytes, &p.w, k * PR_K, (u.channel * CTAS + (PAIR ? rank : 0)) * PR_CH, &s_full[st], w_policy);
                 }
             };
             auto tokens = [&](int st, const Unit& u, int k) {
-                if (lane < 2) {
+                if (!HERE && lane < 2) {
                     const unsigned char* src = p.tokens16 + ((static_cast<long long>(u.tile) * p.steps + k) * 2 + lane) * p.n * 128 + (PAIR ? rank * half_bytes : 0);
                     specv::bulk_load(smem + st * stage_bytes + PR_W_BYTES + lane * half_bytes, src, half_bytes, &s_full[st], keep);
                 }
@@ -263,11 +265,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             // The first copies of codes are on their way before the kernel in front, which makes the tokens' halves, has ended: what
             // it waited for before it let this one in holds the codes.
             int ahead = 0;
+            if (HERE) asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");      // no kernel in front
             if (first < units) {
                 const Unit u(p, first);
                 for (; ahead < p.stages && k_from + ahead < k_to; ++ahead) codes(ahead, u, k_from + ahead);
             }
-            asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+            if (!HERE) asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
             int g = 0, st = 0;
             uint32_t round = 0;      // of the stages' uses
             for (int i = first; i < units; i += by) {
@@ -322,6 +325,26 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
         set_registers<80, false>();
         const int mine = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t to = tmem + PR_COL_A + mine * 64 + (static_cast<uint32_t>(warp & 3) << 21);
+        // HERE: the lane's tokens, eight lanes to a row's 16 bytes each, and their codes for this buffer's next step
+        const int t = tid & 127, piece = t & 7;
+        const signed char* token[2] = {nullptr, nullptr};
+        uint4 codes[2];
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                codes[r] = make_uint4(0u, 0u, 0u, 0u);
+                if (token[r] && k * PR_K + piece * 16 < p.K) codes[r] = __ldg(reinterpret_cast<const uint4*>(token[r] + k * PR_K + piece * 16));
+            }
+        };
+        if (HERE) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int n = r * 16 + (t >> 3), b = n / p.N;
+                if (n < p.tokens) token[r] = row_of<const signed char>(p.a, b, n - b * p.N);
+            }
+            fetch(k_from + mine % (k_to - k_from));
+        }
         int g = 0, st = -1, used = -1;      // step, its stage, the stage of this buffer's last step
         uint32_t round = 0, used_round = 0;
         for (int i = first; i < units; i += by)
@@ -331,7 +354,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                 if constexpr (!MAP) {
                     // eight lanes to a row's 128 codes; the place in shared memory is free when the step's other copies may begin
                     unsigned char* const to_row = smem + st * stage_bytes;
-                    const int t = tid & 127, piece = t & 7, at = k * PR_K + piece * 16;
+                    const int at = k * PR_K + piece * 16;
                     const Unit u(p, i);
                     int x[8][4];
 #pragma unroll
@@ -349,6 +372,21 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
                     asm volatile("bar.sync %0, 128;" ::"r"(2 + mine) : "memory");
                 } else {
                     wait(&s_full[st], round & 1);
+                }
+                if constexpr (HERE) {
+                    unsigned char* const to_row = smem + st * stage_bytes + PR_W_BYTES + (piece >> 2) * half_bytes;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int n = r * 16 + (t >> 3), c = (piece & 3) * 2;
+                        if (n >= p.n) break;
+                        uint32_t h[8];
+                        halves_of(codes[r].x, h[0], h[1]), halves_of(codes[r].y, h[2], h[3]);
+                        halves_of(codes[r].z, h[4], h[5]), halves_of(codes[r].w, h[6], h[7]);
+                        *reinterpret_cast<uint4*>(to_row + n * 128 + ((c ^ (n & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(to_row + n * 128 + (((c + 1) ^ (n & 7)) * 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    specv::fence_proxy_async_shared();
+                    fetch(k_from + (k - k_from + 2) % (k_to - k_from));
                 }
                 const unsigned char* const src = smem + st * stage_bytes + row * 128;
                 uint4 v[8];

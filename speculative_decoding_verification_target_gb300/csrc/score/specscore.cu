@@ -232,21 +232,21 @@ EncodeTiled encode_tiled() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-template <class T, bool PAIR, bool MAP>
+template <class T, bool PAIR, bool MAP, bool HERE = false>
 spec_status product_as(const ProductParams& p, int grid, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return fail(SPEC_ERR_CUDA, "device query failed");
     static std::atomic<unsigned> ready{0};       // devices whose limit of dynamic shared memory is raised
     const unsigned bit = dev < 32 ? 1u << dev : 0u;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(product_kernel<T, PAIR, MAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, PR_SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(product_kernel<T, PAIR, MAP, HERE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PR_SMEM);
         if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "product kernel attribute failed: %s", cudaGetErrorString(e));
         ready.fetch_or(bit, std::memory_order_release);
     }
-    return launched("product", launch_behind(product_kernel<T, PAIR, MAP>, p, dim3(grid), PR_THREADS, st, PR_SMEM, PAIR ? 2 : p.split));
+    return launched("product", launch_behind(product_kernel<T, PAIR, MAP, HERE>, p, dim3(grid), PR_THREADS, st, PR_SMEM, PAIR ? 2 : p.split));
 }
 
-spec_status product(const MatmulParams& m, bool map, int out_type, unsigned char* ws, cudaStream_t st) {
+spec_status product(const MatmulParams& m, bool map, bool a16, int out_type, unsigned char* ws, cudaStream_t st) {
     const int sms = sm_count();
     if (sms < 1) return fail(SPEC_ERR_CUDA, "device query failed");
     ProductParams p = {};
@@ -288,6 +288,11 @@ spec_status product(const MatmulParams& m, bool map, int out_type, unsigned char
     p.stages = std::min(PR_STAGES, (PR_SMEM - 1024) / (PR_W_BYTES + 2 * 128 * (pair ? p.n / 2 : p.n)));
     if (p.stages < PR_MIN_STAGES) return fail(SPEC_ERR_CUDA, "no room for %d stages", PR_MIN_STAGES);
     p.stream_w = p.token_tiles <= 8;
+    // Up to 32 tokens of few weights become halves where they are used: a CTA does that for each of its channel tiles, but there is
+    // one launch less. In us, so / in a kernel of their own: 16 tokens over 1024 x 1024 5.1 and 6.7, 4096 x 4096 8.9 and 10.2, 14336 x
+    // 4096 18.8 and 18.4, 128256 x 4096 109 and 96; 32 tokens over 4096 x 4096 10.0 and 11.1, 14336 x 4096 19.5 and 18.5.
+    const bool here = map && a16 && m.tokens <= 32 && static_cast<long long>(m.C) * m.K <= 32000000LL;
+    p.a = m.a;
     HalvesParams h = {};
     h.a = m.a;
     h.out = ws + SPEC_SCORE_WS_HEADER;
@@ -297,13 +302,16 @@ spec_status product(const MatmulParams& m, bool map, int out_type, unsigned char
     h.n = p.n;
     h.steps = p.steps;
     h.groups = static_cast<long long>(p.token_tiles) * p.n * p.steps * (PR_K / 16);
-    SPECS_TRY(launched("product's halves", launch_behind(halves_kernel, h, dim3(static_cast<unsigned>((h.groups + 255) / 256)), 256, st)));
+    if (!here) SPECS_TRY(launched("product's halves", launch_behind(halves_kernel, h, dim3(static_cast<unsigned>((h.groups + 255) / 256)), 256, st)));
     if (pair) {
         const int grid = static_cast<int>(std::min<long long>(units, sms / 2)) * 2;
         return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, true, true>(p, grid, st)
                : out_type == SPEC_FP16 ? product_as<__half, true, true>(p, grid, st) : product_as<float, true, true>(p, grid, st);
     }
     const int grid = p.split > 1 ? static_cast<int>(units) * p.split : static_cast<int>(std::min<long long>(units, sms));
+    if (here)
+        return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false, true, true>(p, grid, st)
+               : out_type == SPEC_FP16 ? product_as<__half, false, true, true>(p, grid, st) : product_as<float, false, true, true>(p, grid, st);
     if (map)
         return out_type == SPEC_BF16 ? product_as<__nv_bfloat16, false, true>(p, grid, st)
                : out_type == SPEC_FP16 ? product_as<__half, false, true>(p, grid, st) : product_as<float, false, true>(p, grid, st);
@@ -429,8 +437,9 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     const long long weights = static_cast<long long>(C) * K;
     // Rows off 16 bytes: 8 tokens, 14336 x 4099: 62 and 104; 64 tokens, 2000 x 4097: 77 and 27.
     const bool few = p.tokens <= 2 || (p.tokens <= 8 && (!codes16 || weights <= (p.tokens <= 4 ? 50000000LL : 16000000LL)));
-    if (!few) return product(p, codes16, out_type, static_cast<unsigned char*>(workspace), st);
-    const bool aligned = aligned16(w) && (C == 1 || w_stride % 16 == 0) && K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
+    const bool a16 = K % 16 == 0 && aligned16(a->data) && (B == 1 || a->stride_b % 16 == 0) && (N == 1 || a->stride_n % 16 == 0);
+    if (!few) return product(p, codes16, a16, out_type, static_cast<unsigned char*>(workspace), st);
+    const bool aligned = a16 && aligned16(w) && (C == 1 || w_stride % 16 == 0);
     return out_type == SPEC_BF16   ? matvec<__nv_bfloat16>(p, aligned, st)
            : out_type == SPEC_FP16 ? matvec<__half>(p, aligned, st) : matvec<float>(p, aligned, st);
 }

@@ -200,7 +200,8 @@ SHAPES = [(1, 1, 1), (1, 1, 16), (1, 128, 64), (2, 3, 4), (1, 4096, 4096), (3, 1
           (193, 384, 640), (200, 130, 48), (256, 1024, 4096), (384, 2000, 1040), (385, 515, 16), (1000, 768, 272), (1, 70, 16400),
           (5, 40, 131071), (2, 16, 131056), (640, 33, 2048), (65, 9800, 272), (70, 38900, 144), (193, 6000, 400), (250, 5001, 2064),
           (1000, 2100, 640), (2500, 1300, 128), (9, 20000, 64), (40, 5000, 16400), (100, 300, 4097), (40, 129, 16399), (513, 1000, 1001), (130, 5, 5000), (4, 20000, 4096),
-          (3, 12000, 4096), (4, 16, 1000), (300, 9999, 130)]
+          (3, 12000, 4096), (4, 16, 1000), (300, 9999, 130), (9, 5000, 128), (31, 30000, 384), (32, 129, 4112), (17, 40000, 640),
+          (24, 1000, 96)]
 
 
 @pytest.mark.parametrize("M,C,K", SHAPES)
@@ -521,7 +522,7 @@ def test_two_products_at_once_on_two_streams():
             assert torch.equal(got, job[-1])
 
 
-@pytest.mark.parametrize("M,C,K", [(1100, 11, 2048), (4265, 11, 13648), (300, 40, 1024), (12, 700, 4096), (384, 9999, 512), (200, 900, 3999)])
+@pytest.mark.parametrize("M,C,K", [(1100, 11, 2048), (4265, 11, 13648), (300, 40, 1024), (12, 700, 4096), (384, 9999, 512), (200, 900, 3999), (30, 25000, 1152), (20, 400, 2064)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_products_in_a_row(M, C, K, dtype):
     """Calls that nothing waits between, few and many channels to many and few tokens."""
