@@ -1,4 +1,4 @@
-// The product of 8-bit integers for few tokens.
+// The product of 8-bit integers for up to eight tokens.
 #pragma once
 #include "rows.cuh"
 
@@ -10,7 +10,6 @@ struct MatmulParams {
     const float *a_scale, *w_scale, *bias;
     long long w_stride;
     int tokens, N, C, K;
-    int first;        // token of the launch's first row
     int k_warps;      // of a CTA's eight: 1, 2, 4 or 8
 };
 
@@ -46,13 +45,13 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_cons
     __shared__ int s_sum[MV_WARPS][MV_CH * TOKENS];
     after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp % p.k_warps, groups = MV_WARPS / p.k_warps;
-    const int c0 = (blockIdx.x * groups + warp / p.k_warps) * MV_CH, t0 = p.first + blockIdx.y * TOKENS;
+    const int c0 = (blockIdx.x * groups + warp / p.k_warps) * MV_CH;
     const signed char *w[MV_CH], *a[TOKENS];
 #pragma unroll
     for (int i = 0; i < MV_CH; ++i) w[i] = p.w + min(c0 + i, p.C - 1) * p.w_stride;      // past the end the last one once more
 #pragma unroll
     for (int j = 0; j < TOKENS; ++j) {
-        const int t = min(t0 + j, p.tokens - 1), b = t / p.N;
+        const int t = min(j, p.tokens - 1), b = t / p.N;
         a[j] = row_of<signed char>(p.a, b, t - b * p.N);
     }
     int acc[MV_CH][TOKENS] = {};
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_cons
     __syncthreads();
     for (int e = threadIdx.x; e < groups * MV_CH * TOKENS; e += MV_WARPS * 32) {
         const int g = e / (MV_CH * TOKENS), i = e % MV_CH, j = e % (MV_CH * TOKENS) / MV_CH;
-        const int c = (blockIdx.x * groups + g) * MV_CH + i, t = t0 + j;
+        const int c = (blockIdx.x * groups + g) * MV_CH + i, t = j;
         if (c >= p.C || t >= p.tokens) continue;
         int sum = 0;
         for (int q = 0; q < p.k_warps; ++q) sum += s_sum[g * p.k_warps + q][j * MV_CH + i];

@@ -201,14 +201,7 @@ spec_status matvec_as(MatmulParams p, cudaStream_t st) {
     const int width = p.tokens > 4 ? 8 : p.tokens > 2 ? 4 : p.tokens;
     void (*const fn)(const MatmulParams) = width == 8 ? matvec_kernel<T, 8, ALIGNED> : width == 4 ? matvec_kernel<T, 4, ALIGNED>
                                            : width == 2 ? matvec_kernel<T, 2, ALIGNED> : matvec_kernel<T, 1, ALIGNED>;
-    const long long rows = (static_cast<long long>(p.tokens) + width - 1) / width;
-    for (long long from = 0; from < rows; from += 65535) {      // the grid's second side ends there
-        MatmulParams q = p;
-        q.first = static_cast<int>(from * width);
-        SPECS_TRY(launched("product", launch_behind(fn, q, dim3((p.C + per - 1) / per, static_cast<unsigned>(std::min(rows - from, 65535LL))),
-                                                    MV_WARPS * 32, st)));
-    }
-    return SPEC_OK;
+    return launched("product", launch_behind(fn, p, dim3((p.C + per - 1) / per), MV_WARPS * 32, st));
 }
 
 template <class T>
