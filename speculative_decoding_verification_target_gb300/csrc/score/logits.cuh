@@ -33,20 +33,24 @@ __device__ __forceinline__ unsigned mask_bits(const unsigned* mask, int v, int l
     return bits & ((1u << n) - 1u);
 }
 
-// -inf where a bit is 0.
+// -inf where a bit is 0. For 16-bit values `keep` holds the words' bits to be kept for each of the 256 bytes of a mask: an entry is a
+// read of 16 bytes where working it out takes as many instructions.
 template <class T>
-__device__ __forceinline__ uint4 masked(uint4 x, unsigned bits) {
+__device__ __forceinline__ uint4 masked(uint4 x, unsigned bits, const uint4* keep) {
     if constexpr (std::is_same_v<T, float>) {
         x.x = bits & 1u ? x.x : 0xFF800000u, x.y = bits & 2u ? x.y : 0xFF800000u;
         x.z = bits & 4u ? x.z : 0xFF800000u, x.w = bits & 8u ? x.w : 0xFF800000u;
     } else {
-        // four bits to the bytes of a word, each byte to 0 or 255, and twice for a half
-        const uint32_t lo = ((bits & 15u) * 0x00204081u & 0x01010101u) * 255u, hi = ((bits >> 4) * 0x00204081u & 0x01010101u) * 255u;
-        auto two = [](uint32_t v, uint32_t keep) { return (v & keep) | (0xFF80FF80u & ~keep); };
-        x.x = two(x.x, __byte_perm(lo, 0, 0x1100)), x.y = two(x.y, __byte_perm(lo, 0, 0x3322));
-        x.z = two(x.z, __byte_perm(hi, 0, 0x1100)), x.w = two(x.w, __byte_perm(hi, 0, 0x3322));
+        const uint4 k = keep[bits];
+        auto two = [](uint32_t v, uint32_t m) { return (v & m) | (0xFF80FF80u & ~m); };
+        x.x = two(x.x, k.x), x.y = two(x.y, k.y), x.z = two(x.z, k.z), x.w = two(x.w, k.w);
     }
     return x;
+}
+__device__ __forceinline__ uint4 kept_bits(unsigned bits) {
+    // four bits to the bytes of a word, each byte to 0 or 255, and twice for a half
+    const uint32_t lo = ((bits & 15u) * 0x00204081u & 0x01010101u) * 255u, hi = ((bits >> 4) * 0x00204081u & 0x01010101u) * 255u;
+    return make_uint4(__byte_perm(lo, 0, 0x1100), __byte_perm(lo, 0, 0x3322), __byte_perm(hi, 0, 0x1100), __byte_perm(hi, 0, 0x3322));
 }
 
 // `n` <= 8 bits of the table's flags from v on; a word behind the last is there.
@@ -88,19 +92,22 @@ __device__ __forceinline__ void words_of(const unsigned* s_word, int v, int from
 // go by, 16 bytes of a row at a time, and all rows at a place one behind the other, since the table says the same to them: bandwidth
 // bounds that. A piece without a bit is copied, with the mask; in the others every value goes through the one formula, which leaves
 // those that nothing is said of as they are. Listed tokens come last, each by itself. 128 sequences of 21 rows of 151936 in bf16 with
-// histories of up to 32768 tokens take 291 us, 84% of the copy rate; 64 of 6 rows of 128256 with masks and biases 65.6 us (47%), where
+// histories of up to 32768 tokens take 291 us, 84% of the copy rate; 64 of 6 rows of 128256 with masks and biases 62.3 us (49%), where
 // the table, made once for six rows, and the masks count for more.
 template <class T, bool MASK>
 __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __grid_constant__ LogitsParams p) {
-    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 6;
+    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = MASK ? 3 : 6;
     extern __shared__ unsigned s_word[];                     // [seg + 8], then the bits [seg / 32 + 1]
     __shared__ unsigned s_draft[SPEC_SCORE_MAX_ROWS], s_list[LG_LIST], s_listed;
     __shared__ unsigned short s_token[LG_LIST];
+    __shared__ uint4 s_keep[MASK && E == 8 ? 256 : 1];
     after_previous();
     const int b = blockIdx.y, tid = threadIdx.x, threads = blockDim.x, last_word = (p.V - 1) / 32;
     const int v0 = blockIdx.x * p.seg, n = min(p.seg, p.V - v0);
     unsigned* const s_flag = s_word + p.seg + 8;
     if (tid == 0) s_listed = 0u;
+    if (MASK && E == 8)
+        for (int i = tid; i < 256; i += threads) s_keep[i] = kept_bits(i);
     auto at = [&](int v) { return word_at<E>(v, p.seg); };
     for (int i = tid; i < p.seg / 4 + 2; i += threads) reinterpret_cast<uint4*>(s_word)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i <= p.seg / 32; i += threads) s_flag[i] = 0u;
@@ -171,6 +178,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
             head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
             whole = (n - head) / E;
         }
+        const bool even = E == 8 && head % 8 == 0;           // a piece's bits are a byte of the mask
         for (int i = tid; i < whole; i += threads) {
             const int v = head + i * E;
             const unsigned flags = flag_bits(s_flag, v, E);
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
                 for (int k = 0; k < U; ++k) {
                     if (j + k >= past) break;
                     x[k] = *reinterpret_cast<const uint4*>(from + k * p.in.sn);
-                    if (MASK) bits[k] = mask_bits(bits_from + k * p.mask_sr, v0 + v, last_word, E);
+                    if (MASK) bits[k] = even ? __ldg(reinterpret_cast<const unsigned char*>(bits_from + k * p.mask_sr) + (v0 + v) / 8) : mask_bits(bits_from + k * p.mask_sr, v0 + v, last_word, E);
                 }
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
                         }
                         x[k] = y;
                     }
-                    *reinterpret_cast<uint4*>(to + k * p.out.sn) = MASK ? masked<T>(x[k], bits[k]) : x[k];
+                    *reinterpret_cast<uint4*>(to + k * p.out.sn) = MASK ? masked<T>(x[k], bits[k], s_keep) : x[k];
                 }
                 from += U * p.in.sn;
                 to += U * p.out.sn;
