@@ -183,10 +183,12 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out=
         raise TypeError("a must be torch.int8, got %s" % a.dtype)
     d = _device_of(a, "a", stream)
     B, N, K, ai = _rows(a, "a")
-    if w.dim() != 2:
-        raise ValueError("w must be [C, K], got %s" % (tuple(w.shape),))
-    C = w.shape[0]
-    wi = _rows_like(w, "w", (C, K), torch.int8, d)
+    size, strides = w.shape, w.stride()
+    if len(size) != 2:
+        raise ValueError("w must be [C, K], got %s" % (tuple(size),))
+    C = size[0]
+    if not (size[1] == K and w.dtype is torch.int8 and w.get_device() == d and (strides[1] == 1 or K == 1)):
+        _rows_like(w, "w", (C, K), torch.int8, d)
     tokens = a.shape[:-1]
     _vector(a_scale, "a_scale", torch.float32, tokens, d)
     _vector(w_scale, "w_scale", torch.float32, (C,), d)
@@ -205,8 +207,8 @@ def int8_matmul(a, a_scale, w, w_scale, *, bias=None, dtype=torch.bfloat16, out=
         oi = _rows_like(out, "out", tokens + (C,), dtype, d)
     if workspace is None:
         workspace = _new(new_matmul_workspace, stream, max(B * N, 1), C, K, a.device)
-    wp, size = _workspace(workspace, d)
-    _ok(_lib().spec_int8_matmul(ai, a_scale.data_ptr(), wi.data, wi.stride_n, w_scale.data_ptr(), bp, B, N, C, K, oi, code, wp, size,
+    wp, held = _workspace(workspace, d)
+    _ok(_lib().spec_int8_matmul(ai, a_scale.data_ptr(), w.data_ptr(), strides[0], w_scale.data_ptr(), bp, B, N, C, K, oi, code, wp, held,
                                 _handle(d, stream)))
     return dict(out=out, workspace=workspace)
 
