@@ -78,7 +78,8 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
  *   y = y > 0 ? y / repetition[b] : y repetition[b]     where the token is in the prompt or the output,
  *   y = y - frequency[b] n - (n > 0 ? presence[b] : 0),
  *   y = -inf                                            where bit (token % 32) of mask[b, j, token / 32] is 0,
- * in fp32, rounded once. Each part is left out where its pointer is NULL. history: device int32 [B, L] with lengths [B] and prompt
+ * in fp32, rounded once; the quotient of bf16 logits is y times the rounded 1 / repetition[b]. Each part is left out where its
+ * pointer is NULL. history: device int32 [B, L] with lengths [B] and prompt
  * [B] (NULL: all output); a length is taken as at least 0 and at most L. tokens: device int32 [B, T], T >= R - 1. Tokens outside
  * [0, V) are passed over, so -1 pads. bias_tokens: device int32 [B, biases], bias: device float of the same shape; of entries with
  * the same token the last counts. repetition (> 0), frequency, presence: device float [B]. mask: device 32-bit words, the

@@ -148,8 +148,11 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
     __syncthreads();
     const float rep = p.repetition ? p.repetition[b] : 1.f, freq = p.frequency ? p.frequency[b] : 0.f,
                 pres = p.presence ? p.presence[b] : 0.f, per_rep = 1.f / rep;
-    // what n > 0 times among the output take off; n as a float without a conversion
-    auto taken = [&](unsigned n) { return n ? fmaf(freq, __uint_as_float(n | 0x4B000000u) - 8388608.f, pres) : 0.f; };
+    // the word of a token of the text, n times among the output; n as a float without a conversion
+    auto said = [&](unsigned n) {
+        const unsigned off = n ? __float_as_uint(fmaf(freq, __uint_as_float(n | 0x4B000000u) - 8388608.f, pres)) : 0u;
+        return off ? off : 0x80000000u;
+    };
     for (int i = tid; i < p.seg / 4; i += threads)
         for (unsigned rest = s_flag[i / 8] >> 4 * (i % 8) & 15u; rest; rest &= rest - 1) {
             const int v = 4 * i + __ffs(rest) - 1;
@@ -161,12 +164,26 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
                 s_token[to] = static_cast<unsigned short>(v);
                 word = 0u;
             } else {
-                const unsigned off = __float_as_uint(taken((w & W_COUNT) / W_ONE));
-                word = off ? off : 0x80000000u;
+                word = said((w & W_COUNT) / W_ONE);
             }
         }
     __syncthreads();
-    auto simple = [&](float x, unsigned w) { return fmaf(x, w ? (x > 0.f ? per_rep : rep) : 1.f, -__uint_as_float(w)); };
+    // A quotient by a divisor known in advance (Brisebarre, Muller and Raina, IEEE Transactions on Computers 53, 2004): x times the
+    // rounded reciprocal and times what that lacks, joined by one rounding. Before bf16's rounding the reciprocal alone does: its half
+    // step of fp32 is a 2^16th of the half step behind it, and the second product costs 5% to 9% of a call. Repetitions near either end of
+    // fp32's range, whose reciprocals are not whole, divide, value by value.
+    const float rest = fmaf(-rep, per_rep, 1.f) / rep;
+    const bool known = rep >= 5.4210109e-20f && rep <= 1.8446744e19f;      // 2^-64, 2^64
+    auto simple = [&](float x, unsigned w) {
+        const float off = __uint_as_float(w);
+        if constexpr (E == 8) {
+            return fmaf(x, w ? (x > 0.f ? per_rep : rep) : 1.f, -off);
+        } else {
+            const bool up = w && __float_as_uint(x) - 1u < 0x7F7FFFFFu;      // 0 < x < infinity
+            return fmaf(x, up ? per_rep : w ? rep : 1.f, up ? fmaf(x, rest, -off) : -off);
+        }
+    };
+    auto one = [&](float x, unsigned w) { return known || !w || !(x > 0.f) ? simple(x, w) : x / rep - __uint_as_float(w); };
     const int together = p.together ? p.R : 1;
     for (int first = 0; first < p.R; first += together) {
         const int past = min(first + together, p.R);
@@ -174,7 +191,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
         T* const out = row_of<T>(p.out, b, first) + v0;
         const unsigned* const mask = MASK ? p.mask + b * p.mask_sb + first * p.mask_sr : nullptr;
         int head = 0, whole = 0;
-        if (p.pieces) {
+        if (p.pieces && known) {
             head = min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
             whole = (n - head) / E;
         }
@@ -229,7 +246,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
                 T* const to = row_of<T>(p.out, b, j) + v0 + v;
                 const T x = row_of<T>(p.in, b, j)[v0 + v];
                 if (MASK && !mask_bits(p.mask + b * p.mask_sb + j * p.mask_sr, v0 + v, last_word, 1)) *to = from_float<T>(-INFINITY);
-                else if (w) *to = from_float<T>(simple(to_float(x), w));
+                else if (w) *to = from_float<T>(one(to_float(x), w));
                 else if (p.stream) *to = x;
             }
     }
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
             for (int k = 0; k < j; ++k) count += s_draft[k] == static_cast<unsigned>(v);
         if (w & W_BIAS) x += p.bias[static_cast<long long>(b) * p.biases + (w & W_BIAS) - 1];
         if (!count && !(w & (W_PROMPT | W_BIAS))) continue;
-        if (count || w & W_PROMPT) x = x * (x > 0.f ? per_rep : rep) - taken(count);
+        if (count || w & W_PROMPT) x = one(x, said(count));
         row_of<T>(p.out, b, j)[v0 + v] = from_float<T>(x);
     }
 }
