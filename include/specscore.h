@@ -61,8 +61,8 @@ spec_status spec_quantize_rows(const spec_rows* x, int dtype, int B, int N, int 
                                void* stream);
 
 /* out[b, n, c] = (sum_k a[b, n, k] w[c, k]) a_scale[b, n] w_scale[c] + bias[c], a and w 8-bit integers in -128..127.
- * The sum is exact (integers of 32 bits); it and the scales' product are rounded to fp32, multiplied and, with a
- * bias, added to it in fp32, and rounded once to out_type (SPEC_BF16, SPEC_FP16, SPEC_FP32). a: rows [B, N] of K; w: rows [C] of
+ * The sum is exact (integers of 32 bits); it, the scales' product, the product of both and, with a bias, its sum with that are
+ * rounded to fp32 each, and the result to out_type (SPEC_BF16, SPEC_FP16, SPEC_FP32). a: rows [B, N] of K; w: rows [C] of
  * K, w_stride apart; scales and bias (or NULL) device float, contiguous. 1 <= K <= SPEC_SCORE_MAX_K. The workspace, 16-byte aligned,
  * has its first SPEC_SCORE_WS_HEADER bytes zeroed once before its first use; its first word is the status word (SPEC_STATUS_TIMEOUT: a
  * wait within the kernel gave up after two seconds and the outputs are invalid). The size for T tokens, C channels and K serves

@@ -36,6 +36,13 @@ __device__ __forceinline__ void load16(const signed char* p, int valid, int (&x)
     }
 }
 
+// A sum times its scales' product, and with a bias: each step is rounded by itself, in every kernel, so that a token's outputs do not
+// depend on how many others are with it.
+__device__ __forceinline__ float scaled_sum(int sum, float scale, bool biased, float bias) {
+    const float y = __fmul_rn(static_cast<float>(sum), scale);
+    return biased ? __fadd_rn(y, bias) : y;
+}
+
 // A warp takes four channels and up to TOKENS tokens, its lanes 16 of K each; k_warps of a CTA's warps share their K. Integer
 // products four at a time (dp4a, 64 lanes a cycle and SM; the tensor cores' own integer products are no faster here), whole sums in 32
 // bits, so their order does not matter. The weights' bytes bound one token (128256 channels of 4096 in 78.4 us, the copy rate), the
@@ -85,9 +92,8 @@ __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_cons
         if (c >= p.C || t >= p.tokens) continue;
         int sum = 0;
         for (int q = 0; q < p.k_warps; ++q) sum += s_sum[g * p.k_warps + q][j * MV_CH + i];
-        float y = static_cast<float>(sum) * (p.a_scale[t] * p.w_scale[c]);
-        if (p.bias) y += p.bias[c];
-        row_of<T>(p.out, t / p.N, t % p.N)[c] = from_float<T>(y);
+        const float bias = p.bias ? p.bias[c] : 0.f;
+        row_of<T>(p.out, t / p.N, t % p.N)[c] = from_float<T>(scaled_sum(sum, p.a_scale[t] * p.w_scale[c], p.bias != nullptr, bias));
     }
 }
 

@@ -468,8 +468,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             }
             T* const out = static_cast<T*>(p.out.p) + c;
             auto scaled = [&](int j, int sum) {
-                const float y = static_cast<float>(sum) * (s_scale[j] * ws);
-                return from_float<T>(p.bias ? y + bias : y);
+                return from_float<T>(scaled_sum(sum, s_scale[j] * ws, p.bias != nullptr, bias));
             };
             if (!PAIR && p.split > 1) {
                 // one tile a cluster: its CTAs add their sums, each for every split-th token

@@ -12,6 +12,24 @@ def gen(seed=0):
     return torch.Generator().manual_seed(seed)
 
 
+# ----------------------------------------------------------------------------------------------------- product
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("C,K", [(257, 512), (300, 4096), (200, 301)])
+def test_a_bias_is_added_to_the_rounded_product_whatever_the_tokens(C, K, dtype):
+    """Bit for bit, and the same for a token alone, among few and among many."""
+    g = gen(9)
+    M = 150
+    a = (32 * torch.randn(M, K, generator=g)).round().clamp(-127, 127).to(torch.int8)
+    w = torch.randint(-128, 128, (C, K), generator=g).to(torch.int8)
+    sa, sw = 0.01 + torch.rand(M, generator=g), 0.01 + torch.rand(C, generator=g)
+    total = (a.double() @ w.double().t()).float()
+    bias = total[3] * sa[3] * sw * (torch.rand(C, generator=g) - 1.2)      # much of what they are added to is taken off again
+    want = (total * (sa[:, None] * sw) + bias).to(dtype)
+    for n in (1, 2, 4, 7, 8, 9, 20, 33, 70, M):
+        got = sv.int8_matmul(a[:n].cuda(), sa[:n].cuda(), w.cuda(), sw.cuda(), bias=bias.cuda(), dtype=dtype)["out"]
+        assert torch.equal(got.cpu(), want[:n]), n
+
+
 # ------------------------------------------------------------------------------------------------------ logits
 @pytest.mark.parametrize("V", [1000, 1003])
 @pytest.mark.parametrize("dtype", [BF16, F32])
