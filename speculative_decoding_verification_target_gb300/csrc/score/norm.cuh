@@ -38,8 +38,9 @@ struct Codes {
         float ps = p * scale, ms = m * scale;
         if (ms < 8.6736174e-19f) ps *= 1.8446744e19f, ms *= 1.8446744e19f;      // the smallest subnormal numbers
         const float k = floorf(ps * (127.f / ms)), h = 2.f * k + 1.f;
-        const float a = 254.f * ps, b = h * ms;
-        const float d = (a - b) + (fmaf(254.f, ps, -a) - fmaf(h, ms, -b));
+        // rounded by themselves: joined with the difference, a product would count its rounding error twice
+        const float a = __fmul_rn(254.f, ps), b = __fmul_rn(h, ms);
+        const float d = __fadd_rn(__fsub_rn(a, b), __fsub_rn(fmaf(254.f, ps, -a), fmaf(h, ms, -b)));
         const bool up = d > 0.f || (d == 0.f && (static_cast<int>(k) & 1));
         return static_cast<int>(k) + (up ? 1 : 0);
     }

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import score_util as su
 import speculative_decoding_verification_target_gb300 as sv
 
 pytestmark = pytest.mark.gpu
@@ -10,6 +11,59 @@ BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 def gen(seed=0):
     return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------------------------------------------- codes
+def rows_of_codes(p):
+    """Codes of fp32 values as they are and behind a norm, which takes the same ones."""
+    got = sv.quantize_rows(p.cuda())["out"].cpu()
+    assert torch.equal(sv.residual_norm(p.cuda(), quantize=True)["out"].cpu(), got)
+    return got
+
+
+@pytest.mark.parametrize("D", [768, 765, 9000])
+def test_codes_next_to_the_middle_of_two(D):
+    """m with all 24 bits, and the three values next to each (2 k + 1) m / 254: products that fp32 rounds decide. Rows of 16 bytes, value
+    by value, and read twice."""
+    odd = torch.arange(-253, 254, 2, dtype=torch.float64)
+    rows = []
+    for i, m in enumerate((1 + torch.rand(24, generator=gen(1))).tolist()):
+        m = torch.tensor(m * 2.0 ** (i % 5 * 7 - 14), dtype=F32)
+        p = (odd * m.double() / 254).float()
+        near = torch.cat([p, torch.nextafter(p, m.expand(254)), torch.nextafter(p, -m.expand(254))])
+        rows.append(torch.cat([m[None], near[:D - 1], torch.zeros(max(0, D - 1 - near.numel()))]))
+    x = torch.stack(rows)
+    codes, _ = su.exact_codes(x)
+    assert torch.equal(rows_of_codes(x), codes)
+
+
+@pytest.mark.parametrize("D", [256, 255, 8200])
+def test_codes_on_the_middle_of_two(D):
+    """m = 254 x and p = (2 k + 1) x, x of 16 bits: both 254 p and (2 k + 1) m are rounded, and equal all the same."""
+    odd = torch.arange(-253, 254, 2, dtype=torch.float64)
+    rows = []
+    for x in (32769 + 2 * torch.randint(0, 16383, (24,), generator=gen(2))).tolist():
+        row = torch.cat([torch.tensor([254.0], dtype=torch.float64), odd])[:D] * x
+        assert torch.equal(row.float().double(), row)
+        rows.append(torch.cat([row.float(), torch.zeros(max(0, D - 255))]))
+    x = torch.stack(rows)
+    codes, _ = su.exact_codes(x)
+    assert torch.equal(rows_of_codes(x), codes)
+    assert torch.equal(codes[0, 1:255] % 2, torch.zeros(min(D, 255) - 1, dtype=torch.int8))      # all ties go to the even one
+
+
+@pytest.mark.parametrize("D", [256, 261, 16392, 16389])
+def test_weighted_codes_on_the_middle_of_two(D):
+    """fp16 rows times weights of 11 bits: p has 22 bits, and its ties are rounded products too. Rows of 16 bytes, rows that begin
+    elsewhere, and rows that are read twice."""
+    odd = torch.arange(-253, 254, 2, dtype=torch.float64)
+    values = torch.cat([torch.tensor([254.0], dtype=torch.float64), odd])
+    x = torch.stack([torch.cat([torch.zeros(s, dtype=torch.float64), values, torch.zeros(D, dtype=torch.float64)])[:D] * k for s, k in ((0, 5), (1, 7), (0, 3))])
+    x = x.half()
+    w = torch.full((D,), 2047 / 1024, dtype=F16)
+    got = sv.residual_norm(x.cuda(), None, w.cuda(), quantize=True)["out"].cpu()
+    codes, _ = su.exact_codes(x.float() * w.float())
+    assert torch.equal(got, codes)
 
 
 # ----------------------------------------------------------------------------------------------------- product
