@@ -243,6 +243,8 @@ def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=No
             raise ValueError("history needs lengths")
         lp = _ints(lengths, "lengths", (B,), d)
         pp = None if prompt is None else _ints(prompt, "prompt", (B,), d)
+    elif lengths is not None or prompt is not None:
+        raise ValueError("%s needs history" % ("prompt" if lengths is None else "lengths"))
     rates = []
     for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence")):
         if t is not None:
@@ -255,6 +257,8 @@ def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=No
             raise ValueError("bias_tokens needs bias")
         _vector(bias, "bias", torch.float32, (B, n), d)
         bp = bias.data_ptr()
+    elif bias is not None:
+        raise ValueError("bias needs bias_tokens")
     if mask is not None:
         mi = _rows_like(mask, "mask", (B, R, (V + 31) // 32), torch.int32, d)
         mp, sb, sr = mi.data, mi.stride_b, mi.stride_n

@@ -246,6 +246,15 @@ def test_binding_refusals(fake, call, error, words):
     assert fake[1].calls == []
 
 
+@pytest.mark.parametrize("alone,partner", [("bias", "bias_tokens"), ("lengths", "history"), ("prompt", "history")])
+def test_what_says_nothing_without_its_partner_is_refused(fake, alone, partner):
+    a = Args()
+    given = dict(bias=a.biases, lengths=a.lengths, prompt=a.prompt)
+    with pytest.raises(ValueError, match="%s needs %s" % (alone, partner)):
+        sv.process_logits(a.logits, tokens=a.tokens, **{alone: given[alone]})
+    assert fake[1].calls == []
+
+
 def test_a_mask_may_be_expanded(fake):
     sv.process_logits(Args().logits, mask=fc.Tensor((B, N, 4), I32, strides=(0, 0, 1)))
     assert fake[1].calls[-1][1][-5:-2] == (fake[1].calls[-1][1][-5], 0, 0)
