@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "specscore.h"
 #include "logits.cuh"
@@ -51,6 +52,17 @@ spec_status check_tokens(int B, int N) {
 spec_status check_rows(const spec_rows* t, const char* name, size_t bytes) {
     if (!t || !t->data) return fail(SPEC_ERR_INVALID, "%s must not be NULL", name);
     if (reinterpret_cast<uintptr_t>(t->data) % bytes) return fail(SPEC_ERR_INVALID, "%s: the pointer must be a multiple of %zu bytes", name, bytes);
+    return SPEC_OK;
+}
+
+// Arrays of 32-bit words, or NULL.
+struct Words {
+    const void* p;
+    const char* name;
+};
+spec_status check_words(std::initializer_list<Words> all) {
+    for (const Words& w : all)
+        if (reinterpret_cast<uintptr_t>(w.p) % 4) return fail(SPEC_ERR_INVALID, "%s: the pointer must be a multiple of 4 bytes", w.name);
     return SPEC_OK;
 }
 
@@ -351,6 +363,7 @@ spec_status spec_residual_norm(const spec_rows* x, const spec_rows* residual, in
     else if (out->data == x->data || (residual && out->data == residual->data))
         return fail(SPEC_ERR_INVALID, "out in 8 bits must not be an input");
     if (out_type == SPEC_INT8 && !scale) return fail(SPEC_ERR_INVALID, "scale must not be NULL");
+    SPECS_TRY(check_words({{scale, "scale"}}));
     if (reinterpret_cast<uintptr_t>(weight) % e) return fail(SPEC_ERR_INVALID, "weight: the pointer must be a multiple of %zu bytes", e);
     NormParams p = {};
     p.x = rows_of(x);
@@ -375,6 +388,7 @@ spec_status spec_quantize_rows(const spec_rows* x, int dtype, int B, int N, int 
     SPECS_TRY(check_out(out, "out", 1, B, N, D));
     if (out->data == x->data) return fail(SPEC_ERR_INVALID, "out in 8 bits must not be an input");
     if (!scale) return fail(SPEC_ERR_INVALID, "scale must not be NULL");
+    SPECS_TRY(check_words({{scale, "scale"}}));
     NormParams p = {};
     p.x = rows_of(x);
     p.out = rows_of(out);
@@ -401,6 +415,7 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
     SPECS_TRY(check_rows(a, "a", 1));
     SPECS_TRY(check_out(out, "out", type_bytes(out_type), B, N, C));
     if (!w || !a_scale || !w_scale) return fail(SPEC_ERR_INVALID, "w, a_scale and w_scale must not be NULL");
+    SPECS_TRY(check_words({{a_scale, "a_scale"}, {w_scale, "w_scale"}, {bias, "bias"}}));
     if (C > 1 && w_stride < 0) return fail(SPEC_ERR_INVALID, "w_stride must not be negative");
     if (!workspace || !aligned16(workspace)) return fail(SPEC_ERR_INVALID, "workspace must be 16-byte aligned device memory");
     const size_t need = matmul_bytes(B * N, C, K);
@@ -457,6 +472,8 @@ spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R
     if (tokens && T < R - 1) return fail(SPEC_ERR_INVALID, "tokens must have at least R - 1 = %d a sequence, got %d", R - 1, T);
     if (history && L > 0 && !lengths) return fail(SPEC_ERR_INVALID, "lengths must not be NULL");
     if (bias_tokens && biases > 0 && !bias) return fail(SPEC_ERR_INVALID, "bias must not be NULL");
+    SPECS_TRY(check_words({{tokens, "tokens"}, {history, "history"}, {lengths, "lengths"}, {prompt, "prompt"}, {repetition, "repetition"},
+                           {frequency, "frequency"}, {presence, "presence"}, {bias_tokens, "bias_tokens"}, {bias, "bias"}, {mask, "mask"}}));
     LogitsParams p = {};
     p.in = rows_of(logits);
     p.out = rows_of(out);

@@ -133,6 +133,12 @@ def test_logits_refusals(lib, kw, code, words):
     assert logits(lib, **kw) == code and words in lib.spec_score_last_error().decode()
 
 
+@pytest.mark.parametrize("call,name,off", [(norm, "scale", 2), (quantize, "scale", 1), (product, "sa", 3), (product, "sw", 2), (product, "bias", 2)]
+                         + [(logits, n, 2) for n in ("tokens", "history", "lengths", "prompt", "rep", "freq", "pres", "bt", "bias", "mask")])
+def test_pointers_off_their_words_are_refused(lib, call, name, off):
+    assert call(lib, **{name: (1 << 27) + off}) == INVALID and "multiple of 4 bytes" in lib.spec_score_last_error().decode()
+
+
 # ------------------------------------------------------------------------------------ the binding, on stand-ins
 B, N, D, C, V, L = 3, 2, 64, 40, 100, 7
 
