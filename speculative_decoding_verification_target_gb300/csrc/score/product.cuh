@@ -294,6 +294,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_con
             }
         } else if (warp == 1 && (!PAIR || rank == 0)) {
             // ================ products, issued by one lane
+            // a kernel in front that lasts does not count as this one's wait
+            if (HERE) asm volatile("griddepcontrol.wait;" ::: "memory");
             const uint32_t lead = specc::elect_one();
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.n >> 3) << 17) | (static_cast<uint32_t>(PR_CH * CTAS >> 4) << 24);
             const uint32_t base = smem_addr(smem + PR_W_BYTES) >> 4, half = half_bytes >> 4;

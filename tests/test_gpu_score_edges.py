@@ -1,9 +1,13 @@
 """Borders of the operators between the last layer and a verification, on the GPU."""
+import ctypes
+import subprocess
+
 import pytest
 import torch
 
 import score_util as su
 import speculative_decoding_verification_target_gb300 as sv
+from speculative_decoding_verification_target_gb300 import _build
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -82,6 +86,53 @@ def test_a_bias_is_added_to_the_rounded_product_whatever_the_tokens(C, K, dtype)
     for n in (1, 2, 4, 7, 8, 9, 20, 33, 70, M):
         got = sv.int8_matmul(a[:n].cuda(), sa[:n].cuda(), w.cuda(), sw.cuda(), bias=bias.cuda(), dtype=dtype)["out"]
         assert torch.equal(got.cpu(), want[:n]), n
+
+
+LASTING = r"""
+// lets the next kernel of its stream in and ends 2.5 s later, after 3000 naps at most
+__global__ void lasting() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    unsigned long long from, now;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(from));
+    for (int i = 0; i < 3000; ++i) {
+        __nanosleep(1000000);
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+        if (now - from > 2500000000ull) break;
+    }
+}
+extern "C" int last(void* stream) {
+    lasting<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
+    return cudaGetLastError();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def lasting(tmp_path_factory):
+    d = tmp_path_factory.mktemp("lasting")
+    (d / "lasting.cu").write_text(LASTING)
+    subprocess.run([_build.nvcc_path(), "-gencode", "arch=compute_103a,code=sm_103a", "-Xcompiler", "-fPIC", "-shared", "-o", str(d / "lasting.so"),
+                    str(d / "lasting.cu")], check=True)
+    fn = ctypes.CDLL(str(d / "lasting.so")).last
+    fn.argtypes = [ctypes.c_void_p]
+    return fn
+
+
+@pytest.mark.parametrize("M", [3, 16, 40, 300])
+def test_a_kernel_in_front_may_last(M, lasting):
+    """Longer than the two seconds after which a wait within the product gives up: those begin where that kernel ends."""
+    g = gen(15)
+    a, w = (torch.randint(-128, 128, (n, 1024), generator=g).to(torch.int8).cuda() for n in (M, 1024))
+    sa, sw, ws = torch.ones(M, device="cuda"), torch.ones(1024, device="cuda"), sv.new_matmul_workspace(M, 1024, 1024)
+    want = (a.double() @ w.double().t()).float()
+    out = torch.empty(M, 1024, device="cuda")
+    sv.int8_matmul(a, sa, w, sw, out=out, workspace=ws)      # loaded
+    out.zero_()
+    torch.cuda.synchronize()
+    assert lasting(torch.cuda.current_stream().cuda_stream) == 0
+    sv.int8_matmul(a, sa, w, sw, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert sv.read_status(ws) == 0 and torch.equal(out, want)
 
 
 # ------------------------------------------------------------------------------------------------------ logits
