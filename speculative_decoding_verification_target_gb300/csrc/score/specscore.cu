@@ -10,6 +10,7 @@
 #include "logits.cuh"
 #include "matmul.cuh"
 #include "norm.cuh"
+#include "norm_threads.h"
 #include "product.cuh"
 
 namespace specs {
@@ -162,14 +163,10 @@ spec_status norm_as(NormParams p, bool vec, bool peel, int sms, cudaStream_t st)
     if (pieces > 512 * most)
         return launched("norm", launch_behind(norm_long_kernel<T, CODES>, p, dim3(static_cast<unsigned>(p.rows)), 512, st));
     const bool full = p.norm || p.weight || p.res.p;
-    // many rows: threads with four pieces, so that much is on its way; few: threads with as few as leave room for every row at once
-    int slots = vec ? 4 : 16;
-    const long long room = full ? 512 : 1024;      // threads of an SM, by registers
-    while (slots > 1 && p.rows * ((pieces + slots / 2 - 1) / (slots / 2) + 31) / 32 * 32 <= room * sms && 2 * pieces <= 512 * slots) slots /= 2;
-    if (!vec && slots < 16) slots = slots < 4 ? 4 : slots == 8 ? 16 : slots;      // there are kernels of 4 and of 16
-    p.tpr = ((pieces + slots - 1) / slots + 31) / 32 * 32;
-    const int per = std::max(1, (p.rows > 4LL * sms ? 128 : 32) / p.tpr), threads = per * p.tpr;
-    const long long ctas = std::min((p.rows + per - 1) / per, static_cast<long long>(sms) * std::max<long long>(1, room / threads));
+    const NormThreads t = norm_threads(p.rows, pieces, vec, CODES, full, sms);
+    p.tpr = t.tpr;
+    const int slots = t.slots, threads = t.per * t.tpr;
+    const long long ctas = std::min((p.rows + t.per - 1) / t.per, static_cast<long long>(sms) * std::max<long long>(1, t.room / threads));
     void (*const fn)(const NormParams) = !full && CODES ? (vec ? norm_of<T, true, true, false>(slots) : norm_of<T, true, false, false>(slots))
                                                         : (vec ? norm_of<T, CODES, true, true>(slots) : norm_of<T, CODES, false, true>(slots));
     return launched("norm", launch_behind(fn, p, dim3(static_cast<unsigned>(ctas)), threads, st));

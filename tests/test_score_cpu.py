@@ -3,6 +3,7 @@ binding around a launch on stand-ins (fake_cuda), and the plain forms of score_u
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -137,6 +138,52 @@ def test_logits_refusals(lib, kw, code, words):
                          + [(logits, n, 2) for n in ("tokens", "history", "lengths", "prompt", "rep", "freq", "pres", "bt", "bias", "mask")])
 def test_pointers_off_their_words_are_refused(lib, call, name, off):
     assert call(lib, **{name: (1 << 27) + off}) == INVALID and "multiple of 4 bytes" in lib.spec_score_last_error().decode()
+
+
+THREADS = r"""
+#include "norm_threads.h"
+extern "C" void threads(long long rows, int pieces, int vec, int codes, int full, int sms, int* out) {
+    const specs::NormThreads t = specs::norm_threads(rows, pieces, vec, codes, full, sms);
+    out[0] = t.slots, out[1] = t.tpr, out[2] = t.per, out[3] = static_cast<int>(t.room);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def threads(tmp_path_factory):
+    d = tmp_path_factory.mktemp("threads")
+    (d / "threads.cpp").write_text(THREADS)
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", _build.SCORE, "-o", str(d / "threads.so"), str(d / "threads.cpp")], check=True)
+    fn = ctypes.CDLL(str(d / "threads.so")).threads
+    fn.argtypes, fn.restype = [ctypes.c_longlong] + [ctypes.c_int] * 5 + [ctypes.POINTER(ctypes.c_int)], None
+
+    def call(*a):
+        out = (ctypes.c_int * 4)()
+        fn(*a, out)
+        return tuple(out)
+    return call
+
+
+@pytest.mark.parametrize("sms", [152, 148])
+def test_threads_of_a_row(threads, sms):
+    """Each choice is one that a kernel stands behind; rows for codes whose places of two pieces a thread fit side by side have those."""
+    for full, room in ((1, 512), (0, 1024)):
+        for pieces in (1, 2, 31, 32, 33, 64, 100, 128, 255, 256, 257, 511, 512, 513, 1000, 1024, 1025, 2048):
+            row = ((pieces + 1) // 2 + 31) // 32 * 32
+            most = room * sms // row
+            for rows in {1, 2, most // 2 + 1, most - 1, most, most + 1, 4 * sms, 4 * sms + 1, 10 * most + 7}:
+                for codes in (0, 1):
+                    slots, tpr, per, got = threads(max(rows, 1), pieces, 1, codes, full, sms)
+                    assert slots in (1, 2, 4) and tpr % 32 == 0 and slots * tpr >= pieces and tpr * per <= 512 and got == room
+                    assert slots * (tpr - 32) < pieces
+                    if codes and pieces <= 1024 and rows <= most:
+                        assert slots <= 2, (rows, pieces)
+                    if rows > most:
+                        assert slots == 4 or pieces <= 32 or rows * tpr <= room * sms
+        for pieces in (1, 33, 261, 512, 2048, 2049, 4097, 8192):
+            for rows in (1, 100, 5000):
+                slots, tpr, per, _ = threads(rows, pieces, 0, 1, full, sms)
+                assert slots in (4, 16) and tpr % 32 == 0 and slots * tpr >= pieces and tpr * per <= 512
 
 
 # ------------------------------------------------------------------------------------ the binding, on stand-ins
