@@ -42,10 +42,12 @@ class Target:
     def product(self, name, codes):
         """Tokens in 8 bits (out, scale) times one of the weights in 8 bits."""
         a, w = codes["out"], self.int8[name]
-        size = (a.shape[0] * a.shape[1], w["out"].shape[0], a.shape[2])
-        if size not in self._product_ws:
-            self._product_ws[size] = sv.new_matmul_workspace(*size)
-        return sv.int8_matmul(a, codes["scale"], w["out"], w["scale"], workspace=self._product_ws[size])["out"]
+        tokens = a.shape[0] * a.shape[1]
+        if tokens > max(self._product_ws, default=0):      # the one for the most tokens serves every call with fewer
+            weights = [m["out"].shape for m in self.int8.values()]
+            self._product_ws = {tokens: sv.new_matmul_workspace(tokens, max(C for C, _ in weights), max(K for _, K in weights))}
+        workspace, = self._product_ws.values()
+        return sv.int8_matmul(a, codes["scale"], w["out"], w["scale"], workspace=workspace)["out"]
 
     def project(self, tokens, positions):
         """The new tokens' residual stream, rotated queries and keys, and values."""

@@ -73,3 +73,19 @@ def test_process_is_the_plain_form_over_the_text():
     want, tol, _ = su.logits(logits, tokens=proposed, history=i32([t + [-1] * (L - len(t)) for t in text]), lengths=i32([len(t) for t in text]),
                              prompt=i32(prompts), **{k: torch.full((4,), v) for k, v in rates.items()})
     assert ((got - want).abs() <= tol + su.half_step(want, torch.bfloat16) * 1.01).all()
+
+
+def test_one_product_workspace_serves_every_call():
+    """Prompts, drafts and a table of the whole vocabulary, three weights: the one for the most tokens and the longest sums."""
+    import serve_drafts as ex
+    cache, target, text, _ = ex.serve(rounds=4, prompts=[9, 4, 17, 6], int8=True)
+    assert len(target._product_ws) == 1 and all(sv.read_status(w) == 0 for w in target._product_ws.values())
+    g = torch.Generator().manual_seed(5)
+    ws, = target._product_ws.values()
+    for tokens in (2048, 3, 700):
+        x = torch.randn(1, tokens, 1024, generator=g).bfloat16().cuda()
+        want = sv.int8_matmul(*sv.quantize_rows(x).values(), *target.int8["down"].values())["out"]
+        assert torch.equal(target.product("down", sv.quantize_rows(x)), want)
+    assert list(target._product_ws.values())[0] is ws
+    target.product("up", sv.quantize_rows(torch.randn(1, 3000, 512, generator=g).bfloat16().cuda()))      # more than there were
+    assert len(target._product_ws) == 1 and list(target._product_ws.values())[0].numel() > ws.numel()
