@@ -172,7 +172,7 @@ def workspace_size(B, K, V, N=1) -> int:
 
 def new_workspace(B, K, V, N=1, device=None):
     """Device workspace for calls up to these sizes, with its status word cleared."""
-    ws = torch.zeros(workspace_size(B, K, V, N), dtype=torch.uint8, device=device or "cuda")
+    ws = torch.zeros(workspace_size(B, K, V, N), dtype=torch.uint8, device="cuda" if device is None else device)
     return ws
 
 
@@ -313,7 +313,7 @@ class HedgeFeedback:
         n = int(lib.spec_hedge_feedback_state_size(N, B, K))
         if n == 0 and B > 0:
             raise ValueError("unsupported sizes N=%d B=%d K=%d" % (N, B, K))
-        dev = device or "cuda"
+        dev = "cuda" if device is None else device
         self.state = _new(torch.zeros, stream, max(n, 16), dtype=torch.uint8, device=dev)
         self.weights = _new(torch.full, stream, (B, N), 1.0 / N, dtype=torch.float32, device=dev)
         self.applied = _new(torch.zeros, stream, B, dtype=torch.int32, device=dev)

@@ -189,7 +189,7 @@ def new_pool(pages, kv_heads, head_dim, layers=None, device=None):
     if head_dim not in (64, 128):
         raise ValueError("head_dim must be 64 or 128, got %r" % (head_dim,))
     shape = (pages, kv_heads, 68 * head_dim)
-    return torch.zeros(shape if layers is None else (layers,) + shape, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(shape if layers is None else (layers,) + shape, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def new_attention_workspace(N, q_heads, kv_heads, head_dim, device=None):
@@ -197,13 +197,13 @@ def new_attention_workspace(N, q_heads, kv_heads, head_dim, device=None):
     n = int(_lib().spec_cache_attention_workspace_size(N, q_heads, kv_heads, head_dim))
     if n == 0:
         raise ValueError("unsupported sizes N=%d Hq=%d Hk=%d D=%d" % (N, q_heads, kv_heads, head_dim))
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def new_pages_workspace(sequences, pages, device=None):
     """Workspace of the pages_* calls, cache_append and cache_read, ready for its first use."""
     n = int(_lib().spec_pages_workspace_size(sequences, pages))
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def rope_frequencies(rotary_dim, theta=10000.0, *, inv_freq=None, device=None):
@@ -217,7 +217,7 @@ def rope_frequencies(rotary_dim, theta=10000.0, *, inv_freq=None, device=None):
             raise ValueError("inv_freq must have rotary_dim / 2 = %d values, got %d" % (rotary_dim // 2, inv.numel()))
     high = torch.remainder(inv / (2.0 * math.pi), 1.0) * 2.0 ** 32
     low = (high - high.floor()) * 2.0 ** 32      # exact: a double's 53 bits, in two steps
-    return (high.floor().long() << 32 | low.floor().long()).to(device or "cuda")
+    return (high.floor().long() << 32 | low.floor().long()).to("cuda" if device is None else device)
 
 
 def qk_norm_rope(q, k, positions, freqs, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,

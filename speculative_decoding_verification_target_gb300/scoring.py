@@ -170,8 +170,8 @@ def new_matmul_workspace(tokens, C, K, device=None):
     if n == 0:
         raise ValueError("unsupported sizes tokens=%d C=%d K=%d" % (tokens, C, K))
     if n <= 1 << 16:
-        return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
     ws[:WS_HEADER].zero_()
     return ws
 

@@ -313,6 +313,19 @@ def test_a_mask_may_be_expanded(fake):
     assert fake[1].calls[-1][1][-5:-2] == (fake[1].calls[-1][1][-5], 0, 0)
 
 
+@pytest.mark.parametrize("new", [lambda **kw: sv.new_matmul_workspace(4, 4, 16, **kw), lambda **kw: sv.new_workspace(2, 3, 64, **kw),
+                                 lambda **kw: sv.new_pool(3, 2, 64, **kw), lambda **kw: sv.new_attention_workspace(1, 8, 2, 64, **kw),
+                                 lambda **kw: sv.new_pages_workspace(2, 3, **kw), lambda **kw: sv.HedgeFeedback(2, 3, 4, **kw)])
+def test_a_device_may_be_named_by_its_number(fake, new):
+    """The first one too, while another is the current one."""
+    t = fake[0]
+    t.cuda.device_index = 1
+    for device, index in ((0, 0), (1, 1), (None, 1)):
+        del t.made[:]
+        new(device=device)
+        assert t.made and all(x.index == index for x in t.made)
+
+
 # --------------------------------------------------------------------------------------------- the plain forms
 def test_exact_codes_against_fractions():
     from fractions import Fraction
