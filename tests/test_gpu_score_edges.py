@@ -70,6 +70,58 @@ def test_weighted_codes_on_the_middle_of_two(D):
     assert torch.equal(got, codes)
 
 
+# ---------------------------------------------------------------------------------------- infinities and NaN
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("D", [261, 2051, 8193, 16385, 32768])
+def test_infinities_and_nans_anywhere_in_a_row(D, dtype):
+    """In a row's first and last values, and amid its pieces; every row of an odd width begins elsewhere."""
+    places = (0, 1, 6, 7, 8, D // 2, D - 9, D - 8, D - 2, D - 1)
+    n = len(places)
+    x = torch.randn(2 * n, D, generator=gen(3)).to(dtype)
+    res, w = torch.randn(2 * n, D, generator=gen(4)).to(dtype), (1 + 0.2 * torch.randn(D, generator=gen(5))).to(dtype)
+    bad = x.clone()
+    for i, at in enumerate(places):
+        bad[2 * i, at] = (float("inf"), float("-inf"), float("nan"))[i % 3]
+    fine = torch.arange(2 * n) % 2 == 1
+    for r, weight in ((None, None), (res, w)):
+        c = lambda t: None if t is None else t.cuda()  # noqa: E731
+        calls = [lambda v: sv.residual_norm(v.cuda(), c(r), c(weight), quantize=True)]
+        if r is None:
+            calls.append(lambda v: sv.quantize_rows(v.cuda()))
+        for call in calls:
+            want, got = call(x), call(bad)
+            assert torch.isnan(got["scale"].cpu()[~fine]).all() and (got["out"].cpu()[~fine] == 0).all()
+            for k in ("out", "scale"):
+                assert torch.equal(got[k].cpu()[fine], want[k].cpu()[fine])
+        want, got = (sv.residual_norm(v.cuda(), c(r), c(weight))["out"].cpu() for v in (x, bad))
+        assert torch.equal(got[fine], want[fine]) and torch.isfinite(got[fine]).all()
+        # with an infinity the row is infinitely long: 0 beside it, and NaN in its place; with a NaN all of it is
+        for i, at in enumerate(places):
+            row = got[2 * i]
+            if i % 3 == 2:
+                assert torch.isnan(row).all()
+            else:
+                rest = torch.cat([row[:at], row[at + 1:]])
+                assert torch.isnan(row[at]) and (rest == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("rows,D", [(1217, 96), (700, 2048), (2000, 301), (1500, 2051), (400, 8192)])
+def test_many_rows_of_other_types(rows, D, dtype):
+    """Threads that take several rows one after the other."""
+    x, res = (torch.randn(rows, D, generator=gen(s)).to(dtype) for s in (6, 7))
+    w = (1 + 0.2 * torch.randn(D, generator=gen(8))).to(dtype)
+    r, p, inv, v = su.norm(x, res, w, 1e-5)
+    codes, s = su.exact_codes(p)
+    got = sv.residual_norm(x.cuda(), res.cuda(), w.cuda(), 1e-5, quantize=True)
+    assert torch.equal(got["residual"].cpu(), r) and torch.equal(got["out"].cpu(), codes)
+    assert ((got["scale"].cpu().double() - s * inv).abs() <= su.inv_tol(D) * s * inv).all()
+    got = sv.residual_norm(x.cuda(), res.cuda(), w.cuda(), 1e-5)
+    assert torch.equal(got["residual"].cpu(), r)
+    assert ((got["out"].cpu().double() - v).abs() <= su.half_step(v, dtype) * (1 + 2.0 ** -8) + su.inv_tol(D) * v.abs()).all()
+    assert torch.equal(sv.quantize_rows(x.cuda())["out"].cpu(), su.exact_codes(x.float())[0])
+
+
 # ----------------------------------------------------------------------------------------------------- product
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("C,K", [(257, 512), (300, 4096), (200, 301)])
@@ -161,3 +213,25 @@ def test_a_repetition_divides(V, dtype):
     rep = reps[:, None, None]
     want = torch.where(seen, torch.where(y > 0, y / rep, y * rep), y)
     assert torch.equal(got, want.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("masked", [False, True])
+def test_as_many_listed_tokens_as_there_may_be(masked, dtype):
+    """1024 tokens with a bias and 64 others among the drafts, all in one part of the vocabulary; enough sequences that it is one."""
+    B, R, V, n = 608, 65, 1500, 1024
+    g = gen(13)
+    order = torch.randperm(V, generator=g).int()
+    x = torch.randn(B, R, V, device="cuda", generator=torch.Generator("cuda").manual_seed(14)).to(dtype)
+    a = dict(tokens=order[n:n + R - 1].expand(B, -1).contiguous(), bias_tokens=order[:n].expand(B, -1).contiguous(),
+             bias=4 * torch.randn(B, n, generator=g), history=torch.randint(0, V, (B, 40), generator=g, dtype=torch.int32),
+             lengths=torch.full((B,), 40, dtype=torch.int32), prompt=torch.full((B,), 13, dtype=torch.int32),
+             repetition=1 + torch.rand(B, generator=g), frequency=torch.rand(B, generator=g), presence=torch.rand(B, generator=g))
+    if masked:
+        a["mask"] = torch.randint(-2 ** 31, 2 ** 31, (1, R, (V + 31) // 32), generator=g).int().expand(B, -1, -1)
+    got = sv.process_logits(x, **{k: v.cuda() for k, v in a.items()})["out"]
+    for b in (0, 303, B - 1):
+        want, tol, same = su.logits(x[b:b + 1].cpu(), **{k: v[b:b + 1] for k, v in a.items()})
+        out, fine = got[b:b + 1].cpu(), torch.isfinite(want)
+        assert torch.equal(out[same], x[b:b + 1].cpu()[same]) and torch.equal(torch.isfinite(out), fine)
+        assert ((out.double() - want).abs() <= tol + su.half_step(want, dtype) * (1 + 2.0 ** -8))[fine].all()
