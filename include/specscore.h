@@ -17,6 +17,7 @@
  * on `stream`; every call can be captured into a CUDA graph. Arguments that the host can see are checked before anything
  * is launched (SPEC_ERR_INVALID, SPEC_ERR_UNSUPPORTED; message in spec_score_last_error()). Empty calls (no tokens, no
  * rows, no channels) do nothing. No call needs its data aligned beyond its type; rows that all begin on 16 bytes are faster.
+ * B <= 65535, N <= 1048576 (R below), B N <= 4194304, C <= 1048576.
  * Outputs may not overlap the inputs, but for those that are named as possibly the same. An output's rows must not overlap.
  */
 #ifndef SPECSCORE_H
@@ -49,7 +50,8 @@ typedef struct {
  * dtype), or in 8 bits (out_type = SPEC_INT8): with p = r w rounded to fp32 (exact for bf16 and fp16) and m the
  * row's largest |p|, each code is the integer nearest to 127 p / m, even on ties, decided exactly; 0 where m = 0. scale
  * (device float [B, N]) receives m / 127 / sqrt(mean(r^2) + eps): v is about code times scale. A row with an infinity or a NaN
- * in p gets codes 0 and the scale NaN. Sums in fp32: a row whose squares' sum passes 3.4e38 counts as infinitely long.
+ * in p gets codes 0 and the scale NaN. Sums in fp32: a row whose squares' sum passes 3.4e38 counts as infinitely long, and squares below
+ * 1e-38 lose digits or all (which matters where eps is as small).
  * dtype: SPEC_BF16, SPEC_FP16 or SPEC_FP32. residual_out may be x or residual, out (not in 8 bits) may be x or
  * residual; not both the same. 1 <= D <= SPEC_SCORE_MAX_D. */
 spec_status spec_residual_norm(const spec_rows* x, const spec_rows* residual, int dtype, int B, int N, int D,
@@ -79,12 +81,12 @@ spec_status spec_int8_matmul(const spec_rows* a, const float* a_scale, const voi
  *   y = y - frequency[b] n - (n > 0 ? presence[b] : 0),
  *   y = -inf                                            where bit (token % 32) of mask[b, j, token / 32] is 0,
  * in fp32, rounded once; the quotient of bf16 logits is y times the rounded 1 / repetition[b]. Each part is left out where its
- * pointer is NULL. history: device int32 [B, L] with lengths [B] and prompt
- * [B] (NULL: all output); a length is taken as at least 0 and at most L. tokens: device int32 [B, T], T >= R - 1. Tokens outside
- * [0, V) are passed over, so -1 pads. bias_tokens: device int32 [B, biases], bias: device float of the same shape; of entries with
- * the same token the last counts. repetition (> 0), frequency, presence: device float [B]. mask: device 32-bit words, the
- * rows' ceil(V / 32) contiguous, with any strides (0: one mask for several rows); bits past V are not looked at. A row whose
- * mask allows nothing is -inf throughout: no row to verify. out may be logits. R <= SPEC_SCORE_MAX_ROWS, V <= 262144. */
+ * pointer is NULL. history: device int32 [B, L] with lengths [B] and prompt [B] (NULL: all output); a length is taken as at least 0
+ * and at most L. tokens: device int32 [B, T], T >= R - 1. Tokens outside [0, V) are passed over, so -1 pads. bias_tokens: device int32
+ * [B, biases], bias: device float of the same shape; of entries with the same token the last counts. repetition (> 0), frequency,
+ * presence: device float [B]. mask: device 32-bit words, the rows' ceil(V / 32) contiguous, with any strides (0: one mask for several
+ * rows); bits past V are not looked at. A row whose mask allows nothing is -inf throughout: no row to verify. out may be logits.
+ * R <= SPEC_SCORE_MAX_ROWS, V <= 262144. */
 spec_status spec_process_logits(const spec_rows* logits, int dtype, int B, int R, int V, const int32_t* tokens, int T,
                                 const int32_t* history, const int32_t* lengths, const int32_t* prompt, int L,
                                 const float* repetition, const float* frequency, const float* presence,

@@ -92,7 +92,7 @@ __device__ __forceinline__ void words_of(const unsigned* s_word, int v, int from
 // go by, 16 bytes of a row at a time, and all rows at a place one behind the other, since the table says the same to them: bandwidth
 // bounds that. A piece without a bit is copied, with the mask; in the others every value goes through the one formula, which leaves
 // those that nothing is said of as they are. Listed tokens come last, each by itself. 128 sequences of 21 rows of 151936 in bf16 with
-// histories of up to 32768 tokens take 291 us, 84% of the copy rate; 64 of 6 rows of 128256 with masks and biases 62.3 us (49%), where
+// histories of up to 32768 tokens take 292 us, 84% of the copy rate; 64 of 6 rows of 128256 with masks and biases 61.8 us (49%), where
 // the table, made once for six rows, and the masks count for more.
 template <class T, bool MASK>
 __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __grid_constant__ LogitsParams p) {

@@ -13,7 +13,7 @@ struct MatmulParams {
     int k_warps;      // of a CTA's eight: 1, 2, 4 or 8
 };
 
-constexpr int MV_WARPS = 8, MV_CH = 4, MV_SMS = 152;
+constexpr int MV_WARPS = 8, MV_CH = 4, MV_SMS = 152;      // SMs of the card that the rule for k_warps was measured on
 
 // 16 codes at p, of which `valid` are there; the others are 0. Without alignment only words that hold a valid code are read.
 template <bool ALIGNED>
@@ -45,7 +45,7 @@ __device__ __forceinline__ float scaled_sum(int sum, float scale, bool biased, f
 
 // A warp takes four channels and up to TOKENS tokens, its lanes 16 of K each; k_warps of a CTA's warps share their K. Integer
 // products four at a time (dp4a, 64 lanes a cycle and SM; the tensor cores' own integer products are no faster here), whole sums in 32
-// bits, so their order does not matter. The weights' bytes bound one token (128256 channels of 4096 in 78.4 us, the copy rate), the
+// bits, so their order does not matter. The weights' bytes bound one token (128256 channels of 4096 in 79.8 us, the copy rate), the
 // products eight.
 template <class T, int TOKENS, bool ALIGNED>
 __global__ void __launch_bounds__(MV_WARPS * 32) matvec_kernel(const __grid_constant__ MatmulParams p) {

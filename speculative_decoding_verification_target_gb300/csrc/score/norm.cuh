@@ -142,7 +142,8 @@ __device__ __forceinline__ void join_row(float& sum, float& top, int from, int w
 // A row is in the registers of tpr threads, SLOTS pieces each, between its one read and its one write; the next row of these
 // threads is on its way meanwhile, and the weights stay. Bandwidth bounds many rows, latency few: there a row has more threads.
 // FULL: with a residual, a weight or a norm; else codes of the rows as they are, with half the registers. 16384 rows of 4096 in bf16,
-// with all of it, take 78.4 us (90% of the copy rate), 8192 rows of 14336 as they are 79.3 us (66%; instruction issue and the row's barrier).
+// with all of it, take 78.8 us (89% of the copy rate), 8192 rows of 14336 as they are 79.6 us (66%; instruction issue, at 16.9 a value, and
+// the row's barrier). With four pieces to codes, bf16's 128 registers spill 24 bytes, and 16-bit types' 64 without a norm 32.
 template <class T, bool CODES, int SLOTS, bool VEC, bool FULL>
 __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __grid_constant__ NormParams p) {
     using P = Piece<T, VEC>;
@@ -257,7 +258,8 @@ __global__ void __launch_bounds__(512, FULL ? 1 : 2) norm_rows_kernel(const __gr
 
 // 16-bit rows of which each begins elsewhere within 16 bytes, but all of a token's alike, as those of an odd width do: pieces of 16
 // bytes from the row's first such place on, and up to seven single values at either end, one a thread. The weights come from shared
-// memory, shifted by the row's place. 5001 rows of 2051 in fp16 take 22.6 us (value by value 27.6).
+// memory, shifted by the row's place. 5001 rows of 2051 in fp16 take 22.7 us on the device (value by value 27.6), 8192 rows of 4099 in bf16
+// 60.0 us, to codes, which are stored byte by byte, 70.7 (floors 40.2 and 35.2).
 template <class T, bool CODES, int SLOTS>
 __global__ void __launch_bounds__(512) norm_peel_kernel(const __grid_constant__ NormParams p) {
     using P = Piece<T, true>;
@@ -401,7 +403,8 @@ __global__ void __launch_bounds__(512) norm_peel_kernel(const __grid_constant__ 
     }
 }
 
-// Rows that do not fit in registers: read twice, the second time from the caches.
+// Rows that do not fit in registers: read twice, the second time from the caches, a value a load. 2048 fp32 rows of 16384 to codes take
+// 116.5 us, 1024 bf16 rows of 32768 110 us (floors 65.2 and 35.1).
 template <class T, bool CODES>
 __global__ void __launch_bounds__(512) norm_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 s_part[2][32];

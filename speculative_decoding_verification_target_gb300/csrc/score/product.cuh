@@ -205,8 +205,10 @@ struct Unit {
 // MAP: the codes' rows are on 16 bytes, and copies bring them; else the warps that turn them fetch them themselves, 16 bytes a lane.
 // HERE: up to 32 tokens, one tile of them, whose codes the same warps fetch and turn, a step of theirs ahead: one launch.
 // split > 1: the CTAs of a cluster share a tile's K, and add their integers through one another's shared memory.
-// 384 tokens, 128256 channels of 4096 take 240 us, 1.68 P operations a second, 86% of what a library product in bf16 reaches; 8192
-// tokens, 14336 channels of 4096 561 us, 88%.
+// A few passes behind one another, 384 tokens over 128256 channels of 4096 take 246 us, 1.64 P operations a second, 84% of what a library
+// product in bf16 reaches in a burst; 8192 tokens over 14336 channels of 4096 550 us, 90%. Launched for seconds on end, under the power
+// limit, 270 and 603 us, 85% and 91% of what the library sustains. 384 tokens over a layer's 14336 x 4096 take 39.5 us (C x K), over
+// 4096 x 14336 54.2, over 4096 x 4096 20.5; the floors are 23.2, 23.2 and 6.6.
 template <class T, bool PAIR, bool MAP, bool HERE>
 __global__ void __launch_bounds__(PR_THREADS, 1) product_kernel(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char dynamic[];

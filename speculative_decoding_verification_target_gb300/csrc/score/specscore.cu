@@ -121,7 +121,8 @@ int sm_count() {
 }
 
 // ---------------------------------------------------------------------------------------- norm and codes
-// Rows of one value short of 16 bytes anywhere go value by value.
+// Rows that begin and end on 16 bytes throughout, and codes on as many values. Of the others, 16-bit rows that begin alike take what
+// pieces they hold (norm_peel_kernel), the rest go value by value.
 bool whole_pieces(const NormParams& p, size_t e, bool codes, int B) {
     const int per = 16 / static_cast<int>(e);
     auto fits = [&](const Rows& t, size_t bytes) {

@@ -222,8 +222,8 @@ def _ints(t, name, shape, d):
 def process_logits(logits, *, tokens=None, history=None, lengths=None, prompt=None, repetition=None, frequency=None,
                    presence=None, bias_tokens=None, bias=None, mask=None, out=None, stream=None):
     """Logits [B, R, V] (bf16 or fp32) as they are sampled from: biases (bias_tokens int32 [B, n], bias float32 [B, n]), the
-    penalties repetition, frequency and presence (float32 [B]) over each sequence's history (int32 [B, L], with lengths and
-    prompt, int32 [B]) and the drafts before a row (tokens int32 [B, T], T >= R - 1), and a grammar's mask (int32 [B, R, ceil(V / 32)],
+    penalties repetition, frequency and presence (float32 [B]) over each sequence's history (int32 [B, L], with lengths and, if part
+    of it is a prompt, prompt, int32 [B]) and the drafts before a row (tokens int32 [B, T], T >= R - 1), and a grammar's mask (int32 [B, R, ceil(V / 32)],
     or expanded to it). out may be logits. Returns dict(out)."""
     if logits.dim() != 3:
         raise ValueError("logits must be [B, R, V], got %s" % (tuple(logits.shape),))
