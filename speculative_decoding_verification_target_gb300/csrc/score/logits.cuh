@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(LG_THREADS, LG_CTAS) logits_kernel(const __gri
     // rounded reciprocal and times what that lacks, joined by one rounding. Repetitions near either end of fp32's range, whose
     // reciprocals are not whole, divide, value by value. Before bf16's rounding the reciprocal alone does: its half step of fp32 is a
     // 2^16th of the half step behind it, the second product costs 5% to 9% of a call, and a division for the ends 2% to 4%.
-    const float rest = fmaf(-rep, per_rep, 1.f) / rep;
+    const float rest = fmaf(-rep, per_rep, 1.f) * per_rep;
     const bool known = E == 8 || (rep >= 5.4210109e-20f && rep <= 1.8446744e19f);      // 2^-64, 2^64
     auto simple = [&](float x, unsigned w) {
         const float off = __uint_as_float(w);
